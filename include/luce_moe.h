@@ -79,8 +79,15 @@ typedef struct {
     uint8_t qs[128];     /* 256 4-bit codes (see luce_moe_glu_q4k)       */
 } luce_block_q4_k;
 
+/* Element types of the operators that take more than one (int8 decode head). */
+typedef enum {
+    LUCE_F32 = 0,
+    LUCE_BF16 = 1,
+    LUCE_F16 = 2
+} luce_dtype;
+
 /* Device fault bits (luce_get_fault). */
-#define LUCE_FAULT_BAD_ID 0x1u  /* a route id >= E was seen and skipped          */
+#define LUCE_FAULT_BAD_ID 0x1u  /* a route id >= E, or a token id >= V, was seen and skipped */
 #define LUCE_FAULT_TIMEOUT 0x2u /* a bounded device wait gave up (never expected) */
 #define LUCE_FAULT_DESYNC 0x4u  /* a device-wide barrier of luce_moe_layer gave up: its count is out of step
                                    with the grid, so zero the `sync` word before the next call */
@@ -373,6 +380,111 @@ LUCE_API luce_status luce_add_rmsnorm_router(const float *x, const float *residu
  */
 LUCE_API luce_status luce_ep_mask(const int32_t *ids, int64_t n, int e0, int e1, int32_t *ids_out, void *stream);
 LUCE_API luce_status luce_add_f32(const float *a, const float *b, float *out, int64_t n, void *stream);
+
+/* ------------------------------------------------------------------------
+ * luce_quantize_i8 / luce_rmsnorm_i8 / luce_add_rmsnorm_i8 -- rows to int8
+ * codes with one fp32 scale per row, the operands of luce_linear_i8: of the
+ * row itself (activations; or weights, a channel to a row), of its RMS norm,
+ * or of the RMS norm of the residual sum.
+ *
+ * luce_quantize_i8, row by row (fp32 operations, each rounded to nearest):
+ *   m = max_i |x_i|    d = m / 127    q_i = round(x_i / d)    scale = d
+ * (halves away from zero, within [-127, 127]; a row whose d is zero has codes
+ * and scale zero).  The value of a code is q_i * scale.
+ * luce_rmsnorm_i8: the same of p_i = x_i * gamma_i, and
+ *   scale = d * r,   r = 1 / sqrt(mean_i x_i^2 + eps)
+ * so that q_i * scale stands for x_i r gamma_i.  The factor r is common to
+ * the row and does not enter the codes: they depend on no sum, and are the
+ * same bits whatever the order in which the squares are added (fp32).
+ * luce_add_rmsnorm_i8: first s_i = x_i + residual_i (one fp32 addition,
+ * rounded to the element type, as it is stored), then luce_rmsnorm_i8 of s.
+ * A row with a NaN or an infinity among the values that are quantized has
+ * codes zero and scale NaN: NaN reaches every product with the row, and no
+ * code is undefined.  Squares that overflow fp32 give r = 0, as in
+ * luce_rmsnorm_router.
+ *
+ *   x, residual, x_sum [T][H] of `dtype`, aligned to the element; x_sum may
+ *     be NULL (not stored), or x or residual itself (the stream updated in
+ *     place); any other overlap with x or residual is refused
+ *   gamma [H] fp32    eps >= 0, finite
+ *   q [T][H] int8 out    scale [T] fp32 out; neither may overlap an input
+ * Requires 1 <= H <= 65536, T >= 0 (residual may be NULL only when T == 0).
+ * Any alignment and any H is served; rows that start 16-byte aligned in every
+ * array are the fastest.
+ */
+LUCE_API luce_status luce_quantize_i8(const void *x, luce_dtype dtype, int T, int H, int8_t *q, float *scale,
+                                      void *stream);
+LUCE_API luce_status luce_rmsnorm_i8(const void *x, luce_dtype dtype, const float *gamma, float eps, int T, int H,
+                                     int8_t *q, float *scale, void *stream);
+LUCE_API luce_status luce_add_rmsnorm_i8(const void *x, const void *residual, void *x_sum, luce_dtype dtype,
+                                         const float *gamma, float eps, int T, int H, int8_t *q, float *scale,
+                                         void *stream);
+
+/* ------------------------------------------------------------------------
+ * luce_linear_i8 -- a dense product of int8 activations with int8 weights,
+ * scales per token and per output channel (a projection, or the vocabulary
+ * head whose logits luce_logits_process and luce_argmax read):
+ *   isum[t][n] = sum_k xq[t][k] * wq[n][k]                        (exact int32)
+ *   out[t][n]  = isum[t][n] * (x_scale[t] * w_scale[n]) (+ bias[n])
+ * in fp32 (isum converted, the product of the scales, the product with it and
+ * the addition each rounded once), then rounded to out_dtype.  The sum is
+ * exact, so a token's row has the same bits in every batch, whichever of the
+ * kernels serves it.
+ *
+ *   xq [T][K], wq [N][K] int8 (any code, -128 too), 16-byte aligned
+ *   x_scale [T], w_scale [N] fp32    bias [N] fp32 or NULL
+ *   out [T][N] of out_dtype, its rows ld_out elements apart (ld_out >= N;
+ *     what lies between the rows is left as it was), aligned to the element
+ * Requires K % 16 == 0, 16 <= K <= 65536, N >= 1, T >= 0, N and T below 2^24.
+ * Under programmatic launch (luce_set_pdl) the kernel may read wq before it
+ * waits for the previous kernel, so that kernel must not write it.
+ */
+LUCE_API luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq, const float *w_scale,
+                                    const float *bias, int T, int N, int K, void *out, luce_dtype out_dtype,
+                                    int64_t ld_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * luce_logits_process -- what stands between a step's logits and the pick of
+ * its tokens: penalties for repeated tokens, biases, and a grammar's mask, in
+ * one pass over the logits.  Per row r and token v, in fp32 and this order:
+ *   l = logits[r][v]
+ *   repetition:  if v is among hist[r][0 .. hist_len[r]):
+ *                  l = l > 0 ? l / repetition[r] : l * repetition[r]
+ *   frequency and presence:  c = times v is among
+ *                  hist[r][prompt_len[r] .. hist_len[r]) (what was generated);
+ *                  if c > 0: l = l - (c * frequency[r] + presence[r])
+ *   bias:        if bias_ids[r][j] == v: l = l + bias_vals[r][j]; an id that
+ *                  is listed twice takes its last entry
+ *   mask:        if the row has a mask m and bit v % 32 of
+ *                  mask[m][v / 32] is clear: l = -infinity (whatever l was)
+ *   out[r][v] = l
+ * A row whose mask allows nothing is -infinity throughout; a NaN stays NaN
+ * unless it is masked.
+ *
+ *   logits [R][V] of `dtype`, rows ld_logits elements apart (ld_logits >= V)
+ *   out [R][V] fp32, rows ld_out apart (ld_out >= V; what lies between the
+ *     rows is left as it was); may be logits itself when dtype is LUCE_F32
+ *     and ld_out == ld_logits (in place); any other overlap is refused
+ *   hist [R][ld_hist] int32 token ids, hist_len [R] int32: both or neither
+ *     NULL; lengths are taken as within [0, ld_hist].  Ids < 0 are padding and
+ *     count for nothing; ids >= V are skipped and raise LUCE_FAULT_BAD_ID
+ *   prompt_len [R] int32 or NULL (zero)
+ *   repetition, frequency, presence [R] fp32, each NULL for none (1, 0, 0)
+ *   bias_ids [R][n_bias] int32, bias_vals [R][n_bias] fp32, ids < 0 unused,
+ *     ids >= V skipped with the fault bit; n_bias == 0 for none
+ *   mask [n_masks][ld_mask] 32-bit words, ld_mask >= ceil(V / 32), or NULL
+ *   mask_rows [R] int32: the mask of row r, < 0 for none (>= n_masks: none,
+ *     with the fault bit); NULL when row r has mask r (n_masks >= R)
+ * Requires 1 <= V < 2^31, 0 <= R <= 65535, ld_hist and n_bias below 2^30,
+ * arrays aligned to their elements.  No workspace; deterministic (the counts
+ * are whole numbers, kept in shared memory per stretch of the vocabulary).
+ */
+LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, int R, int64_t V, int64_t ld_logits,
+                                         const int32_t *hist, int64_t ld_hist, const int32_t *hist_len,
+                                         const int32_t *prompt_len, const float *repetition, const float *frequency,
+                                         const float *presence, const int32_t *bias_ids, const float *bias_vals,
+                                         int n_bias, const uint32_t *mask, int n_masks, int64_t ld_mask,
+                                         const int32_t *mask_rows, float *out, int64_t ld_out, void *stream);
 
 /* ------------------------------------------------------------------------
  * luce_moe_prep -- luce_route_topk, luce_quantize_q8_1 (K = H) and

@@ -20,6 +20,9 @@ LUCE_OK = 0
 LUCE_ERR_INVALID_ARG = 1
 LUCE_ERR_UNSUPPORTED = 2
 LUCE_ERR_CUDA = 3
+LUCE_F32 = 0
+LUCE_BF16 = 1
+LUCE_F16 = 2
 LUCE_FAULT_BAD_ID = 0x1
 LUCE_FAULT_TIMEOUT = 0x2
 LUCE_FAULT_DESYNC = 0x4
@@ -60,6 +63,12 @@ def lib() -> ctypes.CDLL:
             "luce_add_f32": [P, P, P, i64, P],
             "luce_moe_glu_q4k": [P, P, P, P, P, P, i32, i32, i32, i32, i32, f32, P, P, P],
             "luce_moe_down_combine_q4k": [P, P, P, P, P, i32, i32, i32, i32, i32, P, P],
+            "luce_quantize_i8": [P, i32, i32, i32, P, P, P],
+            "luce_rmsnorm_i8": [P, i32, P, f32, i32, i32, P, P, P],
+            "luce_add_rmsnorm_i8": [P, P, P, i32, P, f32, i32, i32, P, P, P],
+            "luce_linear_i8": [P, P, P, P, P, i32, i32, i32, P, i32, i64, P],
+            "luce_logits_process": [P, i32, i32, i64, i64, P, i64, P, P, P, P, P, P, P, i32, P, i32, i64, P, P, i64,
+                                    P],
         }
         for name, args in sigs.items():
             fn = getattr(L, name)
@@ -269,6 +278,156 @@ def luce_moe_down_combine_q4k(w_down, ws_down, hq, ids, weights, E: int, H: int,
         _ptr(weights, f32, "weights"), T, k, E, H, I, _ptr(out, f32, "out"), _stream(stream)))
 
 
+# ----------------------------------------------------------------------------- int8 decode head
+# These entry points check shapes as well, and run on the device that holds
+# their tensors, on its current stream unless one is given.
+_DTYPE = {torch.float32: LUCE_F32, torch.bfloat16: LUCE_BF16, torch.float16: LUCE_F16}
+_FLOATS = frozenset(_DTYPE)
+_F32, _I8, _I32, _WORDS = frozenset({torch.float32}), frozenset({torch.int8}), frozenset({torch.int32}), \
+    frozenset({torch.int32, torch.uint32})
+
+
+def _addr(t, dtypes, shape, dev, name) -> int:
+    """data_ptr of a contiguous CUDA tensor of one of `dtypes`, of `shape`, on device `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _rows(t, dtypes, shape, dev, name) -> tuple[int, int]:
+    """(data_ptr, row stride) of a CUDA matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    R, C = shape
+    step, inner = t.stride()
+    if C > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (step if R > 1 else C)
+
+
+def _matrix(t, name) -> tuple[int, int, int]:
+    """(rows, columns, device) of a CUDA matrix."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    R, C = t.shape
+    return R, C, t.get_device()
+
+
+def _call(fn: str, dev: int, stream, *args) -> None:
+    """The library call on device `dev`, on `stream` or the device's current stream."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
+    if stream is None:
+        s = torch.cuda.current_stream().cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+        s = stream.cuda_stream
+    else:
+        s = int(stream)
+    status = getattr(lib(), fn)(*args, s)
+    if status != LUCE_OK:
+        raise LuceError(fn, status)
+
+
+def luce_quantize_i8(x, q, scale, stream=None) -> None:
+    """x [T, H] fp32, bf16 or fp16 -> q [T, H] int8, scale [T] fp32 (q * scale stands for x)."""
+    T, H, dev = _matrix(x, "x")
+    _call("luce_quantize_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"), _DTYPE[x.dtype], T, H,
+          _addr(q, _I8, (T, H), dev, "q"), _addr(scale, _F32, (T,), dev, "scale"))
+
+
+def luce_rmsnorm_i8(x, gamma, eps: float, q, scale, stream=None) -> None:
+    """x [T, H], gamma [H] fp32 -> the int8 codes and scales of the RMS norm of x."""
+    T, H, dev = _matrix(x, "x")
+    _call("luce_rmsnorm_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"), _DTYPE[x.dtype],
+          _addr(gamma, _F32, (H,), dev, "gamma"), eps, T, H, _addr(q, _I8, (T, H), dev, "q"),
+          _addr(scale, _F32, (T,), dev, "scale"))
+
+
+def luce_add_rmsnorm_i8(x, residual, x_sum, gamma, eps: float, q, scale, stream=None) -> None:
+    """x, residual [T, H] of one type -> x_sum = x + residual (or None; may be x or residual itself),
+    then luce_rmsnorm_i8 of the sum."""
+    T, H, dev = _matrix(x, "x")
+    own = (x.dtype,)
+    _call("luce_add_rmsnorm_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"),
+          _addr(residual, own, (T, H), dev, "residual"),
+          None if x_sum is None else _addr(x_sum, own, (T, H), dev, "x_sum"), _DTYPE[x.dtype],
+          _addr(gamma, _F32, (H,), dev, "gamma"), eps, T, H, _addr(q, _I8, (T, H), dev, "q"),
+          _addr(scale, _F32, (T,), dev, "scale"))
+
+
+def luce_linear_i8(xq, x_scale, wq, w_scale, bias, out, stream=None) -> None:
+    """xq [T, K], wq [N, K] int8, x_scale [T], w_scale [N], bias [N] (or None) fp32 -> out [T, N]
+    fp32, bf16 or fp16 (its rows may be apart: a slice of wider rows)."""
+    T, K, dev = _matrix(xq, "xq")
+    N = _matrix(wq, "wq")[0]
+    o, ldo = _rows(out, _FLOATS, (T, N), dev, "out")
+    _call("luce_linear_i8", dev, stream, _addr(xq, _I8, (T, K), dev, "xq"),
+          _addr(x_scale, _F32, (T,), dev, "x_scale"), _addr(wq, _I8, (N, K), dev, "wq"),
+          _addr(w_scale, _F32, (N,), dev, "w_scale"),
+          None if bias is None else _addr(bias, _F32, (N,), dev, "bias"), T, N, K, o, _DTYPE[out.dtype], ldo)
+
+
+def luce_logits_process(logits, out, hist=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
+                        presence=None, bias_ids=None, bias_vals=None, mask=None, mask_rows=None,
+                        stream=None) -> None:
+    """logits [R, V] fp32, bf16 or fp16 -> out [R, V] fp32 (may be logits itself): penalties for the
+    tokens of hist [R, L] (hist_len [R]; prompt_len [R] of them the prompt's), biases
+    bias_ids / bias_vals [R, n], masks [M, words] of 32 tokens a word (mask_rows [R], or row r
+    takes mask r).  Each group may be left out."""
+    R, V, dev = _matrix(logits, "logits")
+    lp, ldl = _rows(logits, _FLOATS, (R, V), dev, "logits")
+    op, ldo = _rows(out, _F32, (R, V), dev, "out")
+    hp, ldh, hl = None, 0, None
+    if hist is not None:
+        if hist_len is None:
+            raise ValueError("hist needs hist_len")
+        ldh = _matrix(hist, "hist")[1]
+        hp, hl = _addr(hist, _I32, (R, ldh), dev, "hist"), _addr(hist_len, _I32, (R,), dev, "hist_len")
+        if ldh == 0:
+            hp = hl = prompt_len = None
+    elif hist_len is not None or prompt_len is not None:
+        raise ValueError("hist_len and prompt_len need hist")
+    nb, bi, bv = 0, None, None
+    if bias_ids is not None:
+        nb = _matrix(bias_ids, "bias_ids")[1]
+        bi, bv = _addr(bias_ids, _I32, (R, nb), dev, "bias_ids"), _addr(bias_vals, _F32, (R, nb), dev, "bias_vals")
+    elif bias_vals is not None:
+        raise ValueError("bias_vals needs bias_ids")
+    mp, nm, ldm = None, 0, 0
+    if mask is not None:
+        nm, ldm = _matrix(mask, "mask")[:2]
+        mp = _addr(mask, _WORDS, (nm, ldm), dev, "mask")
+    elif mask_rows is not None:
+        raise ValueError("mask_rows needs mask")
+
+    def per_row(t, dtypes, name):
+        return None if t is None else _addr(t, dtypes, (R,), dev, name)
+
+    _call("luce_logits_process", dev, stream, lp, _DTYPE[logits.dtype], R, V, ldl, hp, ldh, hl,
+          per_row(prompt_len, _I32, "prompt_len"), per_row(repetition, _F32, "repetition"),
+          per_row(frequency, _F32, "frequency"), per_row(presence, _F32, "presence"), bi, bv, nb, mp, nm, ldm,
+          per_row(mask_rows, _I32, "mask_rows"), op, ldo)
+
+
 def luce_get_fault() -> int:
     bits = ctypes.c_uint(0)
     _check("luce_get_fault", lib().luce_get_fault(ctypes.byref(bits)))
@@ -284,5 +443,7 @@ __all__ = ["LuceError", "lib", "status_string", "luce_route_topk", "luce_quantiz
            "luce_moe_down_combine", "luce_argmax", "luce_argmax_workspace_bytes", "luce_argmax_noalloc",
            "luce_argmax_shard", "luce_argmax_pick", "luce_rmsnorm_router", "luce_add_rmsnorm_router", "luce_ep_mask", "luce_add_f32",
            "luce_moe_glu_q4k", "luce_moe_down_combine_q4k",
+           "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process",
+           "LUCE_F32", "LUCE_BF16", "LUCE_F16",
            "luce_get_fault", "luce_version", "LUCE_OK", "LUCE_ERR_INVALID_ARG", "LUCE_ERR_UNSUPPORTED",
            "LUCE_ERR_CUDA", "LUCE_FAULT_BAD_ID", "LUCE_FAULT_TIMEOUT", "LUCE_FAULT_DESYNC"]

@@ -617,6 +617,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_layer_flat(unsigned int *bits);
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_tc(unsigned int *bits);
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_q4k(unsigned int *bits);
+extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_logits(unsigned int *bits);
 
 namespace luce_host {
 Tuning g_tuning;
@@ -680,8 +681,9 @@ extern "C" luce_status luce_get_fault(unsigned int *bits)
     cudaError_t e5 = luce_internal_fault_q4k(bits);
     cudaError_t e6 = luce_internal_fault_layer_flat(bits);
     cudaError_t e7 = luce_internal_fault_tc(bits);
+    cudaError_t e8 = luce_internal_fault_logits(bits);
     return (e1 == cudaSuccess && e2 == cudaSuccess && e3 == cudaSuccess && e4 == cudaSuccess && e5 == cudaSuccess &&
-            e6 == cudaSuccess && e7 == cudaSuccess)
+            e6 == cudaSuccess && e7 == cudaSuccess && e8 == cudaSuccess)
                ? LUCE_OK
                : LUCE_ERR_CUDA;
 }

@@ -6,6 +6,10 @@ pages' order on one stream: route select + weights, q8_1 quantization of
 the FFN input, expert grouping (one fused launch for the first three when
 it fits one CTA), gate/up pair + SwiGLU, down + combine.
 Allocation is torch's; all arithmetic is in libluce_moe's kernels.
+
+:class:`LinearI8` is an int8 projection with its weights, :class:`GreedyHead`
+the end of a decode or verify step: final norm, vocabulary product, penalties
+and masks, greedy tokens.
 """
 from __future__ import annotations
 
@@ -83,3 +87,51 @@ class Argmax:
     def run(self, logits, stream=None):
         B.luce_argmax(logits, self.idx, self.val, self.workspace, stream)
         return self.idx, self.val
+
+
+class LinearI8:
+    """An int8 projection: weights [N, K] with a scale per output channel, and an optional bias."""
+
+    def __init__(self, wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None):
+        self.wq, self.w_scale, self.bias = wq, w_scale, bias
+        self.N, self.K = wq.shape
+
+    @classmethod
+    def from_float(cls, w: torch.Tensor, bias: torch.Tensor | None = None) -> "LinearI8":
+        """Quantizes w [N, K] (fp32, bf16 or fp16), a channel to a row, by the rule of luce_quantize_i8."""
+        wq = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+        scale = torch.empty(w.shape[0], dtype=torch.float32, device=w.device)
+        B.luce_quantize_i8(w, wq, scale)
+        return cls(wq, scale, bias)
+
+    def run(self, xq, x_scale, out, stream=None) -> torch.Tensor:
+        B.luce_linear_i8(xq, x_scale, self.wq, self.w_scale, self.bias, out, stream)
+        return out
+
+
+class GreedyHead:
+    """The end of a step for R rows (tokens, or the columns of a verify step): the residual sum's
+    RMS norm in int8, the vocabulary product, penalties, biases and masks, the greedy tokens.
+
+    Owns every buffer; `run` makes four launches and returns (idx [R] int32, val [R] fp32)."""
+
+    def __init__(self, R: int, gamma: torch.Tensor, eps: float, head: LinearI8):
+        if head.K != gamma.numel():
+            raise ValueError(f"the head takes {head.K} values, the norm gives {gamma.numel()}")
+        dev = gamma.device
+        self.R, self.gamma, self.eps, self.head = R, gamma, float(eps), head
+        self.q = torch.empty((R, head.K), dtype=torch.int8, device=dev)
+        self.scale = torch.empty(R, dtype=torch.float32, device=dev)
+        self.logits = torch.empty((R, head.N), dtype=torch.float32, device=dev)
+        self.argmax = Argmax(R, head.N, device=dev)
+
+    def run(self, x, residual=None, x_sum=None, stream=None, **process):
+        """x (+ residual) [R, K]; `process` are the keyword arguments of luce_logits_process."""
+        if residual is not None:
+            B.luce_add_rmsnorm_i8(x, residual, x_sum, self.gamma, self.eps, self.q, self.scale, stream)
+        else:
+            B.luce_rmsnorm_i8(x, self.gamma, self.eps, self.q, self.scale, stream)
+        self.head.run(self.q, self.scale, self.logits, stream)
+        if process:
+            B.luce_logits_process(self.logits, self.logits, stream=stream, **process)
+        return self.argmax.run(self.logits, stream)
