@@ -618,6 +618,7 @@ extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_tc(unsigned int *bits);
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_q4k(unsigned int *bits);
 extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_logits(unsigned int *bits);
+extern "C" __attribute__((visibility("hidden"))) cudaError_t luce_internal_fault_linear(unsigned int *bits);
 
 namespace luce_host {
 Tuning g_tuning;
@@ -682,8 +683,9 @@ extern "C" luce_status luce_get_fault(unsigned int *bits)
     cudaError_t e6 = luce_internal_fault_layer_flat(bits);
     cudaError_t e7 = luce_internal_fault_tc(bits);
     cudaError_t e8 = luce_internal_fault_logits(bits);
+    cudaError_t e9 = luce_internal_fault_linear(bits);
     return (e1 == cudaSuccess && e2 == cudaSuccess && e3 == cudaSuccess && e4 == cudaSuccess && e5 == cudaSuccess &&
-            e6 == cudaSuccess && e7 == cudaSuccess && e8 == cudaSuccess)
+            e6 == cudaSuccess && e7 == cudaSuccess && e8 == cudaSuccess && e9 == cudaSuccess)
                ? LUCE_OK
                : LUCE_ERR_CUDA;
 }
