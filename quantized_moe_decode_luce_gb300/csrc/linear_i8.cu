@@ -79,74 +79,87 @@ __global__ void __launch_bounds__(WARPS * 32)
 // Exactness.  tcgen05.mma has no int8 kind on this GPU, so the codes go in as
 // fp16: every code is an exact fp16 number, and the partial sums of up to 1024
 // products (at most 1024 * 2^14 = 2^24) are exact fp32 integers.  Every CHUNK
-// stages the accumulator is read back, converted to int32 and added to the
-// int32 sums that the worker threads hold, and the next chunk starts from
+// units an accumulator is read back, converted to int32 and added to the
+// int32 sums that the epilogue warps hold, and the next chunk starts from
 // zero: the result is the int32 sum, bit for bit.
 //
 // Operands.  A = 128 weight rows per CTA, converted into tensor memory (a
 // thread writes its own lane's row); B = the tokens, converted into shared
 // memory in the tensor core's 128-byte-swizzled K-major layout; D[channel,
-// token].  Weights cross HBM and shared memory as int8 and are converted once
-// per token tile.  With CG = 2 a CTA pair shares one 256-channel tile: each
-// CTA converts its own 128 weight rows and half of the tokens, so the tokens'
-// shared-memory traffic per MMA halves, which is what bounds wide tiles (per
-// 64 values of K a CTA moves 8 + 8 KB of weights and, for 128 of its own
-// token rows, 8 + 8 + 16 + 16 KB of tokens through a 128 B/clock shared
-// memory, 512 clocks against the MMAs' 536).
+// token].  Codes cross HBM and L2 as int8 and are converted once per tile.
+// What bounds a tile is the 128 B/clock of shared memory: per 64 values of K,
+// 8 + 8 KB of weights in and out, and 8 + 8 + 16 + 16 KB for 128 token rows
+// (raw in and out, converted in and out to the tensor core).  A CTA pair
+// (CG = 2) shares a tile of 256 channels, so that each CTA holds only half of
+// the tokens: 512 clocks for 256 tokens, whose MMAs take 512 too, and 320 for
+// up to 128 tokens, where the weights' 8 KB take 356 clocks of HBM.
 //
-// HALVES = 2 splits a tile of up to 256 tokens in two accumulators whose
-// chunks end at different stages, so that one is read back while the MMAs of
-// the other run; with HALVES = 1 (up to 128 tokens) the two accumulator slots
-// alternate chunk by chunk.
+// Reading an accumulator back takes 64 to 128 values per thread, bound by the
+// float-to-int conversions (16 a clock and SM: about 1000 clocks for 128
+// columns), so it overlaps MMAs: up to 128 tokens the two accumulator slots
+// alternate chunk by chunk; beyond, a tile has two halves of up to 128 tokens
+// (HALVES = 2), a slot each, whose chunks end half a chunk apart, and the MMAs
+// go through blocks of BLOCK units one half at a time, in an order that leaves
+// two blocks of the other half between a chunk's end and its slot's next use.
 //
-// Few tiles: SK CTA groups of one cluster split K among them and add their
+// Few tiles: sk CTA groups of one cluster split K among them and add their
 // int32 sums through distributed shared memory (any split gives the same
 // bits).
 //
-// Roles: warps 0-15 convert (warp w: lane quarter w & 3, a quarter of the
-// stage's K; a share of the token rows), read accumulators back and store;
-// warp 16 issues the TMA tiles, warp 17 the MMAs (of the pair, in its leader).
+// Roles: warp 0 issues the TMA tiles, warp 1 the MMAs (of the pair, in its
+// leader); GROUPS groups of four warps convert, every GROUPS-th unit each (a
+// warp its lane quarter of A and a quarter of B); eight epilogue warps read
+// accumulators back (lane quarter w & 3, half of the columns) and store, while
+// the next tile's products run.  The epilogue's sums need more registers than
+// an even share, so warpgroups trade them with setmaxnreg; the shares add up
+// to no more than the launch's (static_assert below).
 // Every wait is bounded: a role that gives up raises LUCE_FAULT_TIMEOUT and
 // the CTA's abort flag, the others leave at their next wait, copies and MMAs
 // in flight are waited for (bounded) and tensor memory is freed.
-constexpr int SK_MAX = 8;          // CTAs of one cluster at most
-constexpr int KS = 128;            // K values of one stage
-constexpr int CHUNK = 1024 / KS;   // stages whose sums fit fp32
-constexpr int RM = 128;            // weight rows per CTA
-constexpr int WORKERS = 16;        // warps
-constexpr int TMA_WARP = WORKERS, MMA_WARP = WORKERS + 1;
-constexpr int TC_THREADS = (WORKERS + 2) * 32;
+constexpr int SK_MAX = 8;        // CTAs of one cluster at most
+constexpr int KU = 128;          // K values of a unit: a TMA stage, what a group converts, and eight MMAs per half
+constexpr int CHUNK = 1024 / KU; // units whose sums fit fp32
+constexpr int BLOCK = 2;         // (half a chunk is two blocks)
+constexpr int RM = 128;          // weight rows per CTA
+constexpr int ROWS = 64;         // token rows per half and CTA, at most
+constexpr int TMA_WARP = 0, MMA_WARP = 1, CONV_WARP0 = 4, EPI_WARPS = 8;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int RA = 4;              // converted stages: A slots of 64 columns in tensor memory, B slots in shared memory
-constexpr uint32_t D_COL = RA * 64;
-constexpr int LAG = 2;             // stages converted past a chunk's end before it is read back (at most RB)
+constexpr int ACOLS = KU / 2;    // tensor-memory columns of a unit of A
+constexpr uint32_t D_COL = 256;
+constexpr int REGS_MISC = 40;
+constexpr int PITCH = RM + 4;    // of the int32 sums [token][channel] in shared memory, without bank conflicts
 
-template <int CG_, int HALVES_, int ROWS_, int NS_, int RB_> struct Cfg {
-    static constexpr int CG = CG_, HALVES = HALVES_;
-    static constexpr int ROWS = ROWS_;           // token rows per half and CTA, at most
-    static constexpr int NS = NS_, RB = RB_;     // raw stages, converted stages (A and B slots)
-    static constexpr int DCOLS = ROWS * CG;      // columns of one accumulator slot
-    static constexpr int CPW = DCOLS / 4;        // accumulator columns per worker warp
-    static constexpr int RAW_W = RM * KS;        // raw weights of a stage
-    static constexpr int RAW_X = HALVES * ROWS * KS;
-    static constexpr int RAW = RAW_W + RAW_X;
-    static constexpr int ATOM = ROWS * 128;      // 64 K values of one half's rows
-    static constexpr int BST = HALVES * 2 * ATOM;
+template <int CG_, int HALVES_, int GROUPS_, int NS_, int RB_, int LAUNCH_REGS, int REGS_CONV_, int REGS_EPI_> struct Cfg {
+    static constexpr int CG = CG_, HALVES = HALVES_, GROUPS = GROUPS_;
+    static constexpr int NS = NS_, RB = RB_; // raw stages, converted units (A and B slots)
+    static constexpr int REGS_CONV = REGS_CONV_, REGS_EPI = REGS_EPI_;
+    static constexpr int EPI_WARP0 = CONV_WARP0 + 4 * GROUPS;
+    static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+    static constexpr int DCOLS = ROWS * CG;  // columns of an accumulator slot
+    static constexpr int ECOLS = DCOLS / 2;  // of an epilogue warp
+    static constexpr int RAW_W = RM * KU, RAW_X = ROWS * KU;
+    static constexpr int RAW = RAW_W + HALVES * RAW_X;
+    static constexpr int BATOM = ROWS * 128; // 64 values of K of one half's tokens, fp16
+    static constexpr int BHALF = 2 * BATOM;
+    static constexpr int BST = HALVES * BHALF;
     static constexpr int SMEM = NS * RAW + RB * BST + 1024;
-    static constexpr int PART = HALVES * DCOLS * RM * 4; // the int32 sums of a CTA
-    static_assert(LAG <= RB && RB <= RA && D_COL + 2 * DCOLS <= TMEM_COLS, "tensor memory");
-    static_assert(RAW % 1024 == 0 && BST % 1024 == 0 && ATOM % 1024 == 0, "swizzle atoms");
-    static_assert(PART <= NS * RAW + RB * BST && SMEM <= 232448, "shared memory");
-    static_assert(CPW == 16 || CPW == 32, "accumulator columns");
+    static_assert(RB * ACOLS <= (int)D_COL && D_COL + 2 * DCOLS <= TMEM_COLS, "tensor memory");
+    static_assert(RAW % 1024 == 0 && BHALF % 1024 == 0, "swizzle atoms");
+    static_assert(HALVES * DCOLS * PITCH * 4 <= NS * RAW + RB * BST && SMEM <= 232448, "shared memory");
+    static_assert(NS > GROUPS && RB > GROUPS && (HALVES == 1 || RB >= 2 * BLOCK), "slots");
+    static_assert(128 * REGS_MISC + 128 * GROUPS * REGS_CONV + 256 * REGS_EPI <= THREADS * LAUNCH_REGS &&
+                      THREADS * LAUNCH_REGS <= 65536,
+                  "register shares");
 };
 
 struct TcArgs {
-    CUtensorMap tw, tx; // int8 [N][K], box 128 x 128; int8 [T][K], box (nh / CG) x 128; 128-byte swizzle
+    CUtensorMap tw, tx; // int8 [N][K], box 128 x 128; int8 [T][K], box 128 x rows; 128-byte swizzle
     const float *xs, *ws, *bias;
     void *out;
     int64_t ldo;
-    int T, N, stages; // stages of the whole K
-    int nh;           // tokens per half (a multiple of 16 CG)
+    int T, N, units;  // units of the whole K
+    int xbox;         // token rows of a box
+    int nb, nh[2];    // tokens of a tile, and of its halves (multiples of 16, of 32 for a pair)
     int mt, tiles;    // channel tiles, tiles in all (channel tiles fastest)
     int sk;           // CTA groups along K
 };
@@ -253,49 +266,63 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Waits.  Barriers that the peer CTA arrives on need the cluster's scope.
-template <bool CLUSTER> __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity, uint32_t ns)
+// Waits.  Barriers that the peer CTA arrives on need the cluster's scope.  A
+// poll parks the thread in hardware for a while; the timer, which is slow to
+// read, is looked at every 64 polls only.
+template <bool CLUSTER> __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity)
 {
     uint32_t ok;
     if constexpr (CLUSTER)
         asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+                     : "r"(smem_addr(bar)), "r"(parity)
                      : "memory");
     else
         asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}"
                      : "=r"(ok)
-                     : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+                     : "r"(smem_addr(bar)), "r"(parity)
                      : "memory");
     return ok != 0;
 }
 
 template <bool CLUSTER> __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
 {
-    if (try_wait<CLUSTER>(bar, parity, 0))
-        return true;
-    const unsigned long long t0 = global_timer_ns();
-    for (;;) {
-        if (try_wait<CLUSTER>(bar, parity, 10000))
+    unsigned long long t0 = 0;
+    for (uint32_t i = 1;; i++) {
+        if (try_wait<CLUSTER>(bar, parity))
             return true;
-        if (*abort_flag)
-            return false;
-        if (global_timer_ns() - t0 > WAIT_LIMIT_NS) {
-            *abort_flag = 1;
-            atomicOr(&g_fault_word, LUCE_FAULT_TIMEOUT);
-            return false;
+        if ((i & 63u) == 0) {
+            if (*abort_flag)
+                return false;
+            const unsigned long long t = global_timer_ns();
+            if (t0 == 0)
+                t0 = t;
+            if (t - t0 > WAIT_LIMIT_NS) {
+                *abort_flag = 1;
+                atomicOr(&g_fault_word, LUCE_FAULT_TIMEOUT);
+                return false;
+            }
         }
     }
 }
 
+// A wait for what is in flight when the CTA leaves: bounded, whatever the abort flag says.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
+{
+    const unsigned long long t0 = global_timer_ns();
+    while (!try_wait<false>(bar, parity) && global_timer_ns() - t0 < WAIT_LIMIT_NS)
+        ;
+}
+
 // The same for a whole warp, one answer for every lane (.sync.aligned instructions follow).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
 {
-    return __all_sync(0xffffffffu, tc_wait<false>(bar, parity, abort_flag));
+    return __all_sync(0xffffffffu, tc_wait<CLUSTER>(bar, parity, abort_flag));
 }
 
 // One arrival on the barrier at `bar` of cluster CTA `rank`.
@@ -306,8 +333,16 @@ template <int CG> __device__ __forceinline__ void arrive_on(uint64_t *bar, uint3
     } else {
         uint32_t remote;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(bar)), "r"(rank));
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
     }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -333,21 +368,21 @@ template <int R> struct Ring {
     }
 };
 
-// Whether an accumulator's chunk starts, or ends, at stage i of n: half 0
-// restarts every CHUNK stages, half 1 half a chunk earlier.
-template <int HALVES> __device__ __forceinline__ bool chunk_starts(int h, int i)
+// Whether half h's chunk starts, or ends, at unit u of nu: half 0 restarts
+// every CHUNK units, half 1 half a chunk earlier.
+template <int HALVES> __device__ __forceinline__ bool chunk_starts(int h, int u)
 {
-    const int o = HALVES == 2 && h == 1 ? CHUNK / 2 : 0;
-    return i == 0 || (i + o) % CHUNK == 0;
+    return u == 0 || ((u + (HALVES == 2 && h == 1 ? CHUNK / 2 : 0)) & (CHUNK - 1)) == 0;
 }
-template <int HALVES> __device__ __forceinline__ bool chunk_ends(int h, int i, int n)
+template <int HALVES> __device__ __forceinline__ bool chunk_ends(int h, int u, int nu)
 {
-    return i == n - 1 || chunk_starts<HALVES>(h, i + 1);
+    return u == nu - 1 || chunk_starts<HALVES>(h, u + 1);
 }
 
-template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1) k_linear_i8_tc(const __grid_constant__ TcArgs a)
+template <class C, typename TO>
+__global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_constant__ TcArgs a)
 {
-    constexpr int CG = C::CG, HALVES = C::HALVES, NS = C::NS, RB = C::RB, CPW = C::CPW;
+    constexpr int CG = C::CG, HALVES = C::HALVES, GROUPS = C::GROUPS, NS = C::NS, RB = C::RB, ECOLS = C::ECOLS;
     extern __shared__ uint8_t smraw[];
     __shared__ uint64_t full[NS], rfree[NS], afull[RB], sfree[RB], dfull[2], dfree[2], drain;
     __shared__ uint32_t tmem_base;
@@ -355,7 +390,7 @@ template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1)
     volatile int *abort_flag = &abort_word;
     const uint32_t sm = (smem_addr(smraw) + 1023u) & ~1023u;
     const uint32_t smb = sm + NS * C::RAW;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int csize = CG * a.sk;
     const uint32_t rank = csize > 1 ? cluster_rank() : 0;
     const uint32_t pr = rank % CG, leader = rank - pr; // place in the pair, the pair's leader
@@ -365,15 +400,15 @@ template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < NS; i++) {
             mbar_init(&full[i], 1);
-            mbar_init(&rfree[i], WORKERS);
+            mbar_init(&rfree[i], 4);
         }
         for (int i = 0; i < RB; i++) {
-            mbar_init(&afull[i], WORKERS * CG);
+            mbar_init(&afull[i], 4 * CG);
             mbar_init(&sfree[i], 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dfree[i], WORKERS * CG);
+            mbar_init(&dfree[i], EPI_WARPS * CG);
         }
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -399,144 +434,222 @@ template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1)
 
     // this CTA's tiles: cluster c takes tiles c, c + clusters, ...; its share of K
     const int c0 = (int)(blockIdx.x / (unsigned)csize), cstep = (int)(gridDim.x / (unsigned)csize);
-    const int s0 = (int)((long long)a.stages * kg / a.sk), s1 = (int)((long long)a.stages * (kg + 1) / a.sk);
-    const int ns = s1 - s0; // (the host keeps sk <= stages, so that ns >= 1)
-    const int nh = a.nh, xr = nh / CG;
+    const int u0 = (int)((long long)a.units * kg / a.sk), u1 = (int)((long long)a.units * (kg + 1) / a.sk);
+    const int nu = u1 - u0; // (the host keeps sk <= units, so that nu >= 1)
+    auto w_row = [&](int tile) { return ((tile % a.mt) * CG + (int)pr) * RM; };
+    auto x_tile = [&](int tile) { return (tile / a.mt) * a.nb; };
 
-    if (warp == TMA_WARP) {
-        if (lane == 0) {
-            const uint32_t bytes = (uint32_t)(C::RAW_W + HALVES * xr * KS);
-            Ring<NS> r;
-            int issued = 0;
-            auto load_x = [&](uint32_t slot, int st, int tile) {
-                const int t0 = (tile / a.mt) * (nh * HALVES);
-#pragma unroll
-                for (int h = 0; h < HALVES; h++)
-                    tma_2d(sm + slot * C::RAW + C::RAW_W + h * (C::ROWS * KS), &a.tx, (s0 + st) * KS,
-                           t0 + h * nh + (int)pr * xr, &full[slot]);
+    if (warp < CONV_WARP0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MISC));
+        // Both loops run warp-wide, with uniform control flow, and elect one lane
+        // where something is issued: the operands then stay in uniform registers.
+        if (warp == TMA_WARP) {
+            const uint32_t bytes = (uint32_t)(C::RAW_W + HALVES * a.xbox * KU);
+            auto load_w = [&](uint32_t slot, int st, int wr) {
+                mbar_arrive_expect_tx(&full[slot], bytes);
+                tma_2d(sm + slot * C::RAW, &a.tw, (u0 + st) * KU, wr, &full[slot]);
+            };
+            auto load_x = [&](uint32_t slot, int st, int xt) {
+                tma_2d(sm + slot * C::RAW + C::RAW_W, &a.tx, (u0 + st) * KU, xt + (int)pr * (a.nh[0] / CG), &full[slot]);
+                if constexpr (HALVES == 2)
+                    tma_2d(sm + slot * C::RAW + C::RAW_W + C::RAW_X, &a.tx, (u0 + st) * KU,
+                           xt + a.nh[0] + (int)pr * (a.nh[1] / CG), &full[slot]);
             };
             // the first tile's weights do not depend on the previous kernel
-            const int early = c0 < a.tiles ? min(ns, NS) : 0;
-            for (int st = 0; st < early; st++) {
-                mbar_arrive_expect_tx(&full[st], bytes);
-                tma_2d(sm + st * C::RAW, &a.tw, (s0 + st) * KS, ((c0 % a.mt) * CG + (int)pr) * RM, &full[st]);
-            }
+            const int early = c0 < a.tiles ? min(nu, NS) : 0;
+            if (elect_one())
+                for (int st = 0; st < early; st++)
+                    load_w((uint32_t)st, st, w_row(c0));
             pdl_wait();
-            for (int st = 0; st < early; st++)
-                load_x((uint32_t)st, st, c0);
+            if (elect_one())
+                for (int st = 0; st < early; st++)
+                    load_x((uint32_t)st, st, x_tile(c0));
+            Ring<NS> r;
+            int issued = 0;
             bool ok = true;
             for (int tile = c0; tile < a.tiles && ok; tile += cstep) {
-                for (int st = 0; st < ns; st++, r.next(), issued++) {
+                const int wr = w_row(tile), xt = x_tile(tile);
+                for (int st = 0; st < nu; st++, r.next(), issued++) {
                     if (issued < early)
                         continue;
-                    if (!(ok = tc_wait<false>(&rfree[r.slot], r.phase ^ 1, abort_flag)))
+                    if (!(ok = tc_wait_warp(&rfree[r.slot], r.phase ^ 1, abort_flag)))
                         break;
-                    mbar_arrive_expect_tx(&full[r.slot], bytes);
-                    tma_2d(sm + r.slot * C::RAW, &a.tw, (s0 + st) * KS, ((tile % a.mt) * CG + (int)pr) * RM, &full[r.slot]);
-                    load_x(r.slot, st, tile);
+                    if (elect_one()) {
+                        load_w(r.slot, st, wr);
+                        load_x(r.slot, st, xt);
+                    }
                 }
             }
             if (!ok || *abort_flag) {
                 // the copies in flight land before the CTA leaves: the last NS stages issued
-                for (int g = max(0, issued - NS); g < issued; g++) {
-                    const unsigned long long t = global_timer_ns();
-                    while (!try_wait<false>(&full[g % NS], (uint32_t)(g / NS) & 1, 1000) &&
-                           !try_wait<false>(&full[g % NS], ((uint32_t)(g / NS) & 1) ^ 1, 0) &&
-                           global_timer_ns() - t < WAIT_LIMIT_NS)
-                        ;
-                }
+                for (int g = max(0, issued - NS); g < issued; g++)
+                    wait_out(&full[g % NS], (uint32_t)(g / NS) & 1);
             }
-        }
-        __syncwarp();
-    } else if (warp == MMA_WARP) {
-        pdl_wait();
-        if (lane == 0 && pr == 0) {
-            const uint32_t idesc = (1u << 4) | ((uint32_t)(nh >> 3) << 17) | ((uint32_t)(RM * CG >> 4) << 24);
-            Ring<RB> ar;
-            uint32_t dphase = 0;         // bit s: phase of accumulator slot s
+        } else if (warp == MMA_WARP && pr == 0) {
+            constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(RM * CG >> 4) << 24); // fp16 x fp16 -> fp32
+            const uint32_t idesc0 = IDESC | ((uint32_t)(a.nh[0] >> 3) << 17), idesc1 = IDESC | ((uint32_t)(a.nh[1] >> 3) << 17);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t desc0 = sw128_desc(smb);
+            uint32_t pos = 0, phase = 0; // ring position of the block's first unit
+            uint32_t dphase = 3;         // bit s: parity of slot s's next wait
             uint32_t slot = 0;           // (one half: the slots alternate)
             bool ok = true;
             for (int tile = c0; tile < a.tiles && ok; tile += cstep) {
-                for (int st = 0; st < ns && ok; st++, ar.next()) {
-                    if (!(ok = tc_wait<CG == 2>(&afull[ar.slot], ar.phase, abort_flag)))
-                        break;
-                    tc_fence_after();
-                    const uint32_t bs = smb + ar.slot * C::BST, as = tmem + ar.slot * 64;
-                    // the half whose accumulator is being read back goes second
-                    const int first = HALVES == 2 && (chunk_starts<HALVES>(0, st) && st > 0) ? 1 : 0;
-#pragma unroll
-                    for (int hh = 0; hh < HALVES; hh++) {
+                for (int b = 0; b * BLOCK < nu && ok; b++) {
+                    const int n = min(BLOCK, nu - b * BLOCK);
+                    // half 0 restarts at blocks 0, 4, 8 .., half 1 at 2, 6 ..: the half that does not goes first
+                    const int first = HALVES == 2 && b > 0 && (b & 3) < 2 ? 1 : 0;
+#pragma unroll 1
+                    for (int hh = 0; hh < HALVES && ok; hh++) {
                         const int h = HALVES == 2 ? hh ^ first : 0;
-                        const bool fresh = chunk_starts<HALVES>(h, st);
-                        const uint32_t ds = HALVES == 2 ? (uint32_t)h : slot;
-                        if (fresh) {
-                            if (!(ok = tc_wait<CG == 2>(&dfree[ds], ((dphase >> ds) & 1) ^ 1, abort_flag)))
+                        const uint32_t idesc = h ? idesc1 : idesc0;
+                        uint32_t at = pos, ph = phase;
+#pragma unroll 1
+                        for (int j = 0; j < n; j++) {
+                            const int u = b * BLOCK + j;
+                            const bool fresh = chunk_starts<HALVES>(h, u);
+                            const uint32_t ds = HALVES == 2 ? (uint32_t)h : slot;
+                            if (fresh) {
+                                if (!(ok = tc_wait_warp<CG == 2>(&dfree[ds], (dphase >> ds) & 1, abort_flag)))
+                                    break;
+                                dphase ^= 1u << ds;
+                            }
+                            if (hh == 0 && !(ok = tc_wait_warp<CG == 2>(&afull[at], ph, abort_flag)))
                                 break;
                             tc_fence_after();
-                            dphase ^= 1u << ds;
-                        }
+                            const uint32_t as = tm + at * ACOLS, dd = tm + D_COL + ds * C::DCOLS;
+                            const uint64_t bd = desc0 + ((at * C::BST + (uint32_t)h * C::BHALF) >> 4);
+                            const bool ends = chunk_ends<HALVES>(h, u, nu);
+                            if (elect_one()) {
+                                mma_ts<CG>(dd, as, bd, idesc, !fresh);
 #pragma unroll
-                        for (int k = 0; k < KS / 16; k++)
-                            mma_ts<CG>(tmem + D_COL + ds * C::DCOLS, as + 8 * k,
-                                       sw128_desc(bs + h * 2 * C::ATOM + (k >> 2) * C::ATOM + (k & 3) * 32), idesc,
-                                       !(fresh && k == 0));
-                        if (chunk_ends<HALVES>(h, st, ns)) {
-                            mma_commit<CG>(&dfull[ds], pair_mask);
-                            if (HALVES == 1)
+                                for (int k = 1; k < KU / 16; k++)
+                                    mma_ts<CG>(dd, as + 8 * k, bd + ((k >> 2) * C::BATOM >> 4) + 2 * (k & 3), idesc, true);
+                                if (hh == HALVES - 1)
+                                    mma_commit<CG>(&sfree[at], pair_mask);
+                                if (ends)
+                                    mma_commit<CG>(&dfull[ds], pair_mask);
+                            }
+                            if (HALVES == 1 && ends)
                                 slot ^= 1;
+                            if (++at == RB) {
+                                at = 0;
+                                ph ^= 1;
+                            }
+                        }
+                        if (hh == HALVES - 1) {
+                            pos = at;
+                            phase = ph;
                         }
                     }
-                    if (ok)
-                        mma_commit<CG>(&sfree[ar.slot], pair_mask);
                 }
             }
             // every MMA issued has completed before the tensor memory is freed
-            mma_commit_here<CG>(&drain);
-            const unsigned long long t = global_timer_ns();
-            while (!try_wait<false>(&drain, 0, 10000) && global_timer_ns() - t < WAIT_LIMIT_NS)
-                ;
+            if (elect_one())
+                mma_commit_here<CG>(&drain);
+            wait_out(&drain, 0);
         }
         __syncwarp();
-    } else {
-        pdl_wait();
-        const int q = warp & 3, kq = warp >> 2; // lane quarter; quarter of a stage's K, of an accumulator's columns
-        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        if (a.sk > 1)
+            cluster_sync_all(); // (the epilogue's exchange)
+    } else if (warp < C::EPI_WARP0) {
+        // ------------------------------------------------------------ converters
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+        const int q = warp & 3, grp = (warp - CONV_WARP0) >> 2;
         const int row = 32 * q + lane;
-        // weights: 16-byte chunks 2 kq and 2 kq + 1 of this row, swizzled by the TMA
-        const uint32_t w0 = (uint32_t)(row * KS + (((2 * kq) ^ (row & 7)) << 4));
-        const uint32_t w1 = (uint32_t)(row * KS + (((2 * kq + 1) ^ (row & 7)) << 4));
-        // tokens: a unit is 8 rows x 64 values; a quarter-warp takes rows p and
-        // p ^ 5 and four chunks, which touches all banks once in the raw tile
-        // and once in the converted one
+        const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16);
+        // tokens: a warp's step is 8 rows x 128 values; a quarter-warp takes rows
+        // p and p ^ 5 and four 16-byte chunks, which touches every bank once in
+        // the raw tile and once in the converted one
         const int xrow = ((lane >> 2) & 1) ? ((lane >> 3) ^ 5) : (lane >> 3), xc = lane & 3;
-        const int units = HALVES * (xr >> 3) * 2;
-        Ring<NS> rr;
-        Ring<RB> ar;
-        int acc[HALVES][CPW];
-        uint32_t dph = 0; // bit s: phase of accumulator slot s
-        uint32_t slot = 0;
-        const int lag = min(LAG, ns);
-        int done_tile = -1; // tile whose last chunks are still to be read back
+        const uint32_t x_d0 = (uint32_t)(xrow * 128 + (((2 * xc) ^ xrow) << 4));
+        const uint32_t x_d1 = (uint32_t)(xrow * 128 + (((2 * xc + 1) ^ xrow) << 4));
+        const int mytiles = c0 < a.tiles ? (a.tiles - c0 + cstep - 1) / cstep : 0;
+        const int total = mytiles * nu; // units of all tiles, in order
+        uint32_t rslot = (uint32_t)grp, rphase = 0, aslot = (uint32_t)grp, aphase = 1;
+        for (int g = grp; g < total; g += GROUPS) {
+            if (!tc_wait_warp(&full[rslot], rphase, abort_flag) || !tc_wait_warp(&sfree[aslot], aphase, abort_flag))
+                break;
+            tc_fence_after();
+            const uint32_t raw = sm + rslot * C::RAW, bst = smb + aslot * C::BST;
+#pragma unroll
+            for (int c0 = 0; c0 < 8; c0 += 4) {
+                uint4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    v[c] = lds128(raw + row * KU + (((c0 + c) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t h8[8];
+                    codes16(v[c], h8);
+                    tmem_st8(ta + aslot * ACOLS + 8 * (c0 + c), h8);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < HALVES; h++) {
+                const int steps = a.nh[h] / (8 * CG);
+#pragma unroll 1
+                for (int v = q; v < steps; v += 4) {
+                    const uint32_t s = raw + C::RAW_W + h * C::RAW_X + v * (8 * KU) + (uint32_t)(xrow * KU);
+                    const uint32_t d = bst + h * C::BHALF + v * 1024;
+                    const uint4 v0 = lds128(s + ((xc ^ xrow) << 4)), v1 = lds128(s + (((4 + xc) ^ xrow) << 4));
+                    uint32_t h8[8];
+                    codes16(v0, h8);
+                    sts128(d + x_d0, h8[0], h8[1], h8[2], h8[3]);
+                    sts128(d + x_d1, h8[4], h8[5], h8[6], h8[7]);
+                    codes16(v1, h8);
+                    sts128(d + C::BATOM + x_d0, h8[0], h8[1], h8[2], h8[3]);
+                    sts128(d + C::BATOM + x_d1, h8[4], h8[5], h8[6], h8[7]);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // the tensor core reads the tokens
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                arrive_on<CG>(&afull[aslot], leader);
+                mbar_arrive(&rfree[rslot]);
+            }
+            if ((rslot += GROUPS) >= NS) {
+                rslot -= NS;
+                rphase ^= 1;
+            }
+            if ((aslot += GROUPS) >= RB) {
+                aslot -= RB;
+                aphase ^= 1;
+            }
+        }
+        if (a.sk > 1)
+            cluster_sync_all();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
+        pdl_wait();
+        const int q = warp & 3, eh = (warp - C::EPI_WARP0) >> 2;
+        const int row = 32 * q + lane, col0 = eh * ECOLS;
+        const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + D_COL + col0;
+        uint32_t dphase = 0, slot = 0;
         bool ok = true;
-
-        // reads accumulator `ds` back into acc[h] (set, or added to)
-        auto read_back = [&](int h, uint32_t ds, bool set) {
-            if (!tc_wait_warp(&dfull[ds], (dph >> ds) & 1, abort_flag))
+        int acc[HALVES][ECOLS];
+        // accumulator slot `ds` into the sums of half h (set, or added to)
+        auto read_back = [&](int (&s)[ECOLS], uint32_t ds, bool set) {
+            if (!tc_wait_warp(&dfull[ds], (dphase >> ds) & 1, abort_flag))
                 return false;
             tc_fence_after();
-            dph ^= 1u << ds;
+            dphase ^= 1u << ds;
 #pragma unroll
-            for (int c = 0; c < CPW; c += 16) {
+            for (int c = 0; c < ECOLS; c += 16) {
                 uint32_t v[16];
-                tmem_ld16(tl + D_COL + ds * C::DCOLS + kq * CPW + c, v);
+                tmem_ld16(td + ds * C::DCOLS + c, v);
                 tmem_wait_ld();
+                if (set) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int x = __float2int_rn(__uint_as_float(v[i]));
-                    if (h == 0 || HALVES == 1)
-                        acc[0][c + i] = set ? x : acc[0][c + i] + x;
-                    else
-                        acc[HALVES - 1][c + i] = set ? x : acc[HALVES - 1][c + i] + x;
+                    for (int i = 0; i < 16; i++)
+                        s[c + i] = __float2int_rn(__uint_as_float(v[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        s[c + i] += __float2int_rn(__uint_as_float(v[i]));
                 }
             }
             tc_fence_before();
@@ -545,138 +658,101 @@ template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1)
                 arrive_on<CG>(&dfree[ds], leader);
             return true;
         };
-        auto store_tile = [&](int tile) {
-            const int n = ((tile % a.mt) * CG + (int)pr) * RM + row;
-            const int t0 = (tile / a.mt) * (nh * HALVES);
-            if (n < a.N) {
-                const float wsn = a.ws[n];
-                TO *o = static_cast<TO *>(a.out) + n;
-#pragma unroll
-                for (int h = 0; h < HALVES; h++)
-#pragma unroll
-                    for (int c = 0; c < CPW; c++) {
-                        const int j = kq * CPW + c, t = t0 + h * nh + j;
-                        if (j < nh && t < a.T)
-                            store_out(o + (size_t)t * a.ldo, epilogue(acc[h][c], __ldg(a.xs + t), wsn, a.bias, n));
-                    }
-            }
-        };
-        // the chunks that ended at stage i of a tile (n stages)
-        auto read_backs = [&](int i) {
-#pragma unroll
-            for (int h = 0; h < HALVES; h++)
-                if (chunk_ends<HALVES>(h, i, ns)) {
-                    const int start = HALVES == 2 && h == 1 ? CHUNK / 2 : CHUNK;
-                    if (!read_back(h, HALVES == 2 ? (uint32_t)h : slot, i < start))
-                        return false;
-                    if (HALVES == 1)
-                        slot ^= 1;
-                }
-            return true;
-        };
-
         for (int tile = c0; tile < a.tiles && ok; tile += cstep) {
-            for (int st = 0; st < ns; st++, rr.next(), ar.next()) {
-                if (!(ok = tc_wait_warp(&full[rr.slot], rr.phase, abort_flag)))
-                    break;
-                if (!(ok = tc_wait_warp(&sfree[ar.slot], ar.phase ^ 1, abort_flag)))
-                    break;
-                tc_fence_after();
-                const uint32_t raw = sm + rr.slot * C::RAW, bst = smb + ar.slot * C::BST;
-                {
-                    const uint4 v0 = lds128(raw + w0), v1 = lds128(raw + w1);
-                    uint32_t h8[8];
-                    codes16(v0, h8);
-                    tmem_st8(tl + ar.slot * 64 + kq * 16, h8);
-                    codes16(v1, h8);
-                    tmem_st8(tl + ar.slot * 64 + kq * 16 + 8, h8);
-                }
-                for (int u = warp; u < units; u += WORKERS) {
-                    const int at = u & 1, grp = u >> 1;              // 64-value atom, 8-row group
-                    const int h = HALVES == 2 ? grp / (xr >> 3) : 0; // half
-                    const int r8 = (HALVES == 2 ? grp % (xr >> 3) : grp) * 8;
-                    const uint32_t src = raw + C::RAW_W + h * (C::ROWS * KS) + (r8 + xrow) * KS +
-                                         (((4 * at + xc) ^ xrow) << 4);
-                    const uint32_t dst = bst + h * 2 * C::ATOM + at * C::ATOM + (r8 + xrow) * 128;
-                    uint32_t h8[8];
-                    codes16(lds128(src), h8);
-                    sts128(dst + (((2 * xc) ^ xrow) << 4), h8[0], h8[1], h8[2], h8[3]);
-                    sts128(dst + (((2 * xc + 1) ^ xrow) << 4), h8[4], h8[5], h8[6], h8[7]);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); // the tensor core reads the tokens
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive_on<CG>(&afull[ar.slot], leader);
-                    mbar_arrive(&rfree[rr.slot]);
-                }
-                // what ended `lag` stages ago, so that the MMAs have converted stages ahead of them meanwhile
-                if (st >= lag) {
-                    if (!(ok = read_backs(st - lag)))
-                        break;
-                } else if (done_tile >= 0) {
-                    if (!(ok = read_backs(ns - lag + st)))
-                        break;
-                    if (st == lag - 1)
-                        store_tile(done_tile);
-                }
-            }
-            done_tile = tile;
-        }
-        for (int i = ns - lag; i < ns && ok && done_tile >= 0; i++)
-            ok = read_backs(i);
-        if (ok && done_tile >= 0) {
-            if (a.sk == 1) {
-                store_tile(done_tile);
+            // the chunks in the order in which they end
+            if constexpr (HALVES == 1) {
+                for (int u = 0; u < nu && ok; u += CHUNK, slot ^= 1)
+                    ok = read_back(acc[0], slot, u == 0);
             } else {
-                // the int32 sums, [half][token][channel], where the stages were
-                int *part = reinterpret_cast<int *>(smraw + (sm - smem_addr(smraw)));
+                for (int u = CHUNK / 2 - 1; u < nu - 1 && ok; u += CHUNK / 2) {
+                    if ((u & (CHUNK - 1)) == CHUNK - 1)
+                        ok = read_back(acc[0], 0, u == CHUNK - 1);
+                    else
+                        ok = read_back(acc[HALVES - 1], 1, u == CHUNK / 2 - 1);
+                }
+                ok = ok && read_back(acc[0], 0, nu <= CHUNK) && read_back(acc[HALVES - 1], 1, nu <= CHUNK / 2);
+            }
+            if (!ok)
+                break;
+            const int n = w_row(tile) + row;
+            if (a.sk > 1) {
+                // (one tile per cluster) the int32 sums, where the stages were
 #pragma unroll
                 for (int h = 0; h < HALVES; h++)
 #pragma unroll
-                    for (int c = 0; c < CPW; c++)
-                        part[(h * C::DCOLS + kq * CPW + c) * RM + row] = acc[h][c];
+                    for (int c = 0; c < ECOLS; c++)
+                        asm volatile("st.shared.s32 [%0], %1;" ::"r"(sm + ((h * C::DCOLS + col0 + c) * PITCH + row) * 4),
+                                     "r"(acc[h][c])
+                                     : "memory");
+            } else {
+                // a thread holds tokens of one channel: a warp stores 32 channels of
+                // a token; the tokens' scales come from the lanes that loaded them
+                const bool live = n < a.N;
+                const float wsn = live ? a.ws[n] : 0.0f, bn = live && a.bias ? a.bias[n] : 0.0f;
+                const bool add = a.bias != nullptr;
+#pragma unroll
+                for (int h = 0; h < HALVES; h++) {
+                    const int t0 = x_tile(tile) + h * a.nh[0] + col0, nt = min(a.nh[h] - col0, a.T - t0);
+                    TO *o = static_cast<TO *>(a.out) + (size_t)t0 * a.ldo + n;
+#pragma unroll
+                    for (int c0 = 0; c0 < ECOLS; c0 += 32) {
+                        if (c0 >= nt)
+                            break;
+                        const float xl = c0 + lane < nt ? a.xs[t0 + c0 + lane] : 0.0f;
+#pragma unroll
+                        for (int c = 0; c < 32; c++) {
+                            const float f = __fmul_rn(__shfl_sync(0xffffffffu, xl, c), wsn);
+                            float v = __fmul_rn((float)acc[h][c0 + c], f);
+                            if (add)
+                                v = __fadd_rn(v, bn);
+                            if (live && c0 + c < nt)
+                                store_out(o, v);
+                            o += a.ldo;
+                        }
+                    }
+                }
             }
         }
-    }
-
-    if (a.sk > 1) {
-        // every group's sums are in shared memory; each group adds its share of the tokens
-        __syncwarp();
-        cluster_sync_all();
-        const int tile = c0; // (one tile per cluster)
-        const int n0 = ((tile % a.mt) * CG + (int)pr) * RM, t0 = (tile / a.mt) * (nh * HALVES);
-        const int nt = min(nh * HALVES, a.T - t0);
-        const int quads = RM / 4;
-        if (!abort_word) {
-            for (int i = tid; i < ((nt - kg + a.sk - 1) / a.sk) * quads; i += TC_THREADS) {
-                const int j = kg + (i / quads) * a.sk, r4 = (i % quads) * 4; // token of the tile, four channels
-                const int col = HALVES == 2 && j >= nh ? C::DCOLS + j - nh : j;
-                int4 s = make_int4(0, 0, 0, 0);
-                for (int g = 0; g < a.sk; g++) {
-                    uint32_t remote;
-                    int4 v;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                                 : "=r"(remote)
-                                 : "r"(sm + (uint32_t)((col * RM + r4) * 4)), "r"((uint32_t)(g * CG) + pr));
-                    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "r"(remote)
-                                 : "memory");
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
+        if (a.sk > 1) {
+            // every group's sums are in shared memory: each group adds its share of the tile's tokens
+            __syncwarp();
+            cluster_sync_all();
+            const int n0 = w_row(c0), t0 = x_tile(c0);
+            const int nt = min(a.nb, a.T - t0);
+            constexpr int QUADS = RM / 4; // four channels to a thread
+            for (int i = tid - C::EPI_WARP0 * 32; i < ((nt - kg + a.sk - 1) / a.sk) * QUADS && ok; i += EPI_WARPS * 32) {
+                const int t = kg + (i / QUADS) * a.sk, n = 4 * (i % QUADS);
+                const int col = HALVES == 2 && t >= a.nh[0] ? C::DCOLS + t - a.nh[0] : t;
+                const uint32_t at = sm + (uint32_t)(col * PITCH + n) * 4;
+                int4 v[SK_MAX / CG];
+#pragma unroll
+                for (int g = 0; g < SK_MAX / CG; g++) { // (all in flight together)
+                    v[g] = make_int4(0, 0, 0, 0);
+                    if (g < a.sk) {
+                        uint32_t remote;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                     : "=r"(remote)
+                                     : "r"(at), "r"((uint32_t)(g * CG) + pr));
+                        asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[g].x), "=r"(v[g].y), "=r"(v[g].z), "=r"(v[g].w)
+                                     : "r"(remote)
+                                     : "memory");
+                    }
                 }
-                const int t = t0 + j, n = n0 + r4;
-                const float xst = a.xs[t];
-                TO *o = static_cast<TO *>(a.out) + (size_t)t * a.ldo + n;
-                const int sv[4] = {s.x, s.y, s.z, s.w};
+                const float xst = a.xs[t0 + t];
+                int s[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int g = 0; g < SK_MAX / CG; g++) {
+                    s[0] += v[g].x;
+                    s[1] += v[g].y;
+                    s[2] += v[g].z;
+                    s[3] += v[g].w;
+                }
+                TO *o = static_cast<TO *>(a.out) + (size_t)(t0 + t) * a.ldo + n0 + n;
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (n + e < a.N)
-                        store_out(o + e, epilogue(sv[e], xst, a.ws[n + e], a.bias, n + e));
+                    if (n0 + n + e < a.N)
+                        store_out(o + e, epilogue(s[e], xst, a.ws[n0 + n + e], a.bias, n0 + n + e));
             }
         }
     }
@@ -694,9 +770,9 @@ template <class C, typename TO> __global__ void __launch_bounds__(TC_THREADS, 1)
     }
 }
 
-using CfgSmall = Cfg<1, 1, 64, 6, 4>; // up to 64 tokens to a tile, one CTA
-using CfgPair = Cfg<2, 1, 64, 6, 4>;  // up to 128, a CTA pair
-using CfgWide = Cfg<2, 2, 64, 4, 3>;  // up to 256, a CTA pair
+using CfgOne = Cfg<1, 1, 3, 6, 4, 80, 56, 104>;  // up to 64 tokens to a tile, one CTA
+using CfgPair = Cfg<2, 1, 3, 6, 4, 80, 56, 136>; // up to 128, a CTA pair
+using CfgWide = Cfg<2, 2, 2, 3, 4, 96, 48, 168>; // up to 256, a CTA pair
 
 // ---------------------------------------------------------------------------
 // Host side.
@@ -729,7 +805,7 @@ bool map_codes(CUtensorMap *m, const int8_t *base, int rows, int K, int box_rows
         return false;
     const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)K};
-    const cuuint32_t box[2] = {KS, (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {KU, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -738,7 +814,7 @@ bool map_codes(CUtensorMap *m, const int8_t *base, int rows, int K, int box_rows
 
 template <class C, typename TO>
 luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
-                      int N, int K, TO *out, int64_t ldo, int nh, int sk, cudaStream_t stream)
+                      int N, int K, TO *out, int64_t ldo, int tile_tokens, int sk, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
     auto kern = k_linear_i8_tc<C, TO>;
@@ -750,15 +826,19 @@ luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const
     a.ldo = ldo;
     a.T = T;
     a.N = N;
-    a.stages = (K + KS - 1) / KS;
-    a.nh = nh;
-    a.mt = (N + RM * C::CG - 1) / (RM * C::CG);
-    const int64_t tt = ((int64_t)T + nh * C::HALVES - 1) / (nh * C::HALVES);
-    if (a.mt * tt > INT_MAX / SK_MAX)
+    a.units = (K + KU - 1) / KU;
+    a.nb = tile_tokens;
+    a.nh[0] = C::HALVES == 2 ? std::min(tile_tokens, C::DCOLS) : tile_tokens;
+    a.nh[1] = tile_tokens - a.nh[0];
+    a.xbox = a.nh[0] / C::CG; // (the second half's box reads rows that no MMA uses when it is narrower)
+    const int64_t mt = ((int64_t)N + RM * C::CG - 1) / (RM * C::CG);
+    const int64_t tt = ((int64_t)T + tile_tokens - 1) / tile_tokens;
+    if (mt * tt > INT_MAX / SK_MAX)
         return LUCE_ERR_UNSUPPORTED;
-    a.tiles = (int)(a.mt * tt);
+    a.mt = (int)mt;
+    a.tiles = (int)(mt * tt);
     a.sk = sk;
-    if (!map_codes(&a.tw, wq, N, K, RM) || !map_codes(&a.tx, xq, T, K, nh / C::CG))
+    if (!map_codes(&a.tw, wq, N, K, RM) || !map_codes(&a.tx, xq, T, K, a.xbox))
         return LUCE_ERR_CUDA;
     if (limit.raise(kern, C::SMEM) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -768,7 +848,7 @@ luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const
     const int clusters = sk > 1 ? a.tiles : std::min(a.tiles, luce_host::sm_count() / C::CG);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    luce_host::make_config(cfg, attr, dim3((unsigned)(clusters * csize)), dim3(TC_THREADS), C::SMEM, stream);
+    luce_host::make_config(cfg, attr, dim3((unsigned)(clusters * csize)), dim3(C::THREADS), C::SMEM, stream);
     if (csize > 1) {
         cudaLaunchAttribute &c = attr[cfg.numAttrs++];
         c.id = cudaLaunchAttributeClusterDimension;
@@ -794,29 +874,32 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
     if (T > TPW) {
-        // token tiles of at most 64, 128 or 256, all of one width
-        const int stages = (K + KS - 1) / KS;
-        auto width = [](int tokens, int most) { // tokens of a tile, a multiple of 16, all tiles alike
-            const int n = (tokens + most - 1) / most;
-            return ((tokens + n - 1) / n + 15) & ~15;
-        };
-        auto split = [&](int64_t ctas, int cg) { // groups along K while SMs are idle
+        const int units = (K + KU - 1) / KU, sms = luce_host::sm_count();
+        auto split = [&](int64_t tiles, int cg) { // groups along K while SMs are idle
             int sk = 1;
-            while (sk * 2 * cg <= SK_MAX && ctas * sk * 2 <= luce_host::sm_count() && sk * 2 <= stages)
+            while (sk * 2 * cg <= SK_MAX && tiles * cg * sk * 2 <= sms && sk * 2 <= units)
                 sk *= 2;
             return sk;
         };
-        const int64_t mt = ((int64_t)N + RM - 1) / RM;
-        if (T <= 64) {
-            const int nh = width(T, 64);
-            return launch_tc<CfgSmall>(xq, xs, wq, ws, bias, T, N, K, out, ldo, nh, split(mt, 1), stream);
+        if (T <= ROWS) {
+            const int64_t tiles = ((int64_t)N + RM - 1) / RM;
+            return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 15) & ~15, split(tiles, 1), stream);
         }
-        if (T <= 128) {
-            const int nh = width(T, 128);
-            return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, nh, split((mt + 1) / 2 * 2, 2), stream);
+        const int64_t mt = ((int64_t)N + 2 * RM - 1) / (2 * RM);
+        if (T <= 2 * ROWS)
+            return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 31) & ~31, split(mt, 2), stream);
+        // tiles of at most 256 tokens: the width with the least rounds x width
+        int best = 4 * ROWS;
+        int64_t cost = INT64_MAX;
+        for (int w = 4 * ROWS; w > 2 * ROWS; w -= 32) {
+            const int64_t tiles = mt * (((int64_t)T + w - 1) / w), rounds = (tiles + sms / 2 - 1) / (sms / 2);
+            if (rounds * w < cost) {
+                cost = rounds * w;
+                best = w;
+            }
         }
-        const int nh = (width(T, 256) / 2 + 15) & ~15, tt = (T + 2 * nh - 1) / (2 * nh);
-        return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, nh, split((mt + 1) / 2 * 2 * tt, 2), stream);
+        const int64_t tiles = mt * (((int64_t)T + best - 1) / best);
+        return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, best, split(tiles, 2), stream);
     }
     const int64_t nb = ((int64_t)N + WARPS - 1) / WARPS;
     // tokens in slices of at most 65,535 tiles, the grid's limit in y
