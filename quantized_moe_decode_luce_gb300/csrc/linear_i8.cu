@@ -33,42 +33,115 @@ __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_out(__half *p, float v) { *p = __float2half_rn(v); }
 
-// One warp per output channel and up to TPW tokens: the lanes walk K in
-// 16-byte steps with dp4a, then a butterfly.
-constexpr int WARPS = 8;
-constexpr int TPW = 8;
+// ---------------------------------------------------------------------------
+// Few tokens (T of them, nt live): a stream of the weights through dp4a.
+//
+// What bounds it is the weights' way from HBM, and for small matrices the
+// latency of getting there.  A warp takes VR channels and a slice of K, 16
+// bytes a lane and load, VU x VR loads in flight (4 KB) with the next batch
+// requested before the current one is used; the tokens' codes come through L1
+// (VR channels share each load).  Where there are too few channels to fill the
+// GPU, the wk warps of a row group split K and add their int32 sums through
+// shared memory (exact, so any split gives the same bits).
+constexpr int VR = 4;      // channels of a warp
+constexpr int V_WARPS = 8; // warps of a CTA
 
-template <typename TO>
-__global__ void __launch_bounds__(WARPS * 32)
-    k_linear_i8_rows(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
-                     int N, int K, TO *out, int64_t ldo)
+__device__ __forceinline__ uint4 ldg_stream(const void *p)
 {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Sums over a warp's lanes of V values (a power of two): each step sends half
+// of the values one way and keeps the other half.  Lane l ends with the sum of
+// value l >> log2(32 / V), in every lane that shares it.
+template <int V> __device__ __forceinline__ int warp_sums(int (&v)[V], int lane)
+{
+    int o = 16;
+#pragma unroll
+    for (int n = V; n > 1; n >>= 1, o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n / 2; i++) {
+            const int keep = up ? v[i + n / 2] : v[i], give = up ? v[i] : v[i + n / 2];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    int s = v[0];
+    for (; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+template <int T, int VU, typename TO>
+__global__ void __launch_bounds__(V_WARPS * 32)
+    k_linear_i8_vec(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int nt,
+                    int N, int K, int wk, TO *out, int64_t ldo)
+{
+    constexpr int V = VR * T;
+    __shared__ int part[V_WARPS][V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = V_WARPS / wk, kw = warp % wk; // row groups of the CTA, this warp's place along K
+    const int64_t n0 = ((int64_t)blockIdx.x * groups + warp / wk) * VR;
+    const int slice = ((K >> 4) + wk - 1) / wk << 4;
+    const int k1 = min(K, (kw + 1) * slice);
+    const int8_t *w[VR];
+#pragma unroll
+    for (int r = 0; r < VR; r++)
+        w[r] = wq + (size_t)min(n0 + r, (int64_t)N - 1) * K;
+    uint4 cur[VU][VR];
+    auto load = [&](uint4 (&b)[VU][VR], int k) {
+#pragma unroll
+        for (int u = 0; u < VU; u++)
+#pragma unroll
+            for (int r = 0; r < VR; r++)
+                b[u][r] = k + 512 * u < k1 ? ldg_stream(w[r] + k + 512 * u) : make_uint4(0, 0, 0, 0);
+    };
+    load(cur, kw * slice + 16 * lane); // the weights do not depend on the previous kernel
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int t0 = blockIdx.y * TPW, nt = min(TPW, T - t0);
-    const int K16 = K >> 4;
-    for (int64_t n = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5); n < N; n += (int64_t)gridDim.x * WARPS) {
-        int acc[TPW] = {};
-        const int4 *wr = reinterpret_cast<const int4 *>(wq + (size_t)n * K);
-        for (int i = lane; i < K16; i += 32) {
-            const int4 w = wr[i];
+    int acc[V] = {};
+    for (int k0 = kw * slice; k0 < k1; k0 += 512 * VU) {
+        const int k = k0 + 16 * lane;
+        uint4 next[VU][VR];
+        load(next, k + 512 * VU);
 #pragma unroll
-            for (int t = 0; t < TPW; t++) {
-                if (t < nt) {
-                    const int4 v = reinterpret_cast<const int4 *>(xq + (size_t)(t0 + t) * K)[i];
-                    acc[t] = __dp4a(w.x, v.x, acc[t]);
-                    acc[t] = __dp4a(w.y, v.y, acc[t]);
-                    acc[t] = __dp4a(w.z, v.z, acc[t]);
-                    acc[t] = __dp4a(w.w, v.w, acc[t]);
+        for (int u = 0; u < VU; u++) {
+            if (k + 512 * u < k1) {
+#pragma unroll
+                for (int t = 0; t < T; t++) {
+                    const int4 x = *reinterpret_cast<const int4 *>(xq + (size_t)min(t, nt - 1) * K + k + 512 * u);
+#pragma unroll
+                    for (int r = 0; r < VR; r++) {
+                        int s = acc[r * T + t];
+                        s = __dp4a((int)cur[u][r].x, x.x, s);
+                        s = __dp4a((int)cur[u][r].y, x.y, s);
+                        s = __dp4a((int)cur[u][r].z, x.z, s);
+                        acc[r * T + t] = __dp4a((int)cur[u][r].w, x.w, s);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int t = 0; t < TPW; t++) {
-            const int s = warp_sum_i(acc[t]);
-            if (lane == 0 && t < nt)
-                store_out(out + (size_t)(t0 + t) * ldo + n, epilogue(s, xs[t0 + t], ws[n], bias, (int)n));
+        for (int u = 0; u < VU; u++)
+#pragma unroll
+            for (int r = 0; r < VR; r++)
+                cur[u][r] = next[u][r];
+    }
+    const int s = warp_sums<V>(acc, lane);
+    if (lane % (32 / V) == 0)
+        part[warp][lane / (32 / V)] = s;
+    __syncthreads();
+    // value r T + t of each row group, in its order along the output row
+    for (int i = threadIdx.x; i < groups * V; i += V_WARPS * 32) {
+        const int t = i / (groups * VR), c = i % (groups * VR), g = c / VR, r = c % VR;
+        const int64_t n = ((int64_t)blockIdx.x * groups + g) * VR + r;
+        if (n < N && t < nt) {
+            int sum = 0;
+            for (int j = 0; j < wk; j++)
+                sum += part[g * wk + j][r * T + t];
+            store_out(out + (size_t)t * ldo + n, epilogue(sum, xs[t], ws[n], bias, (int)n));
         }
     }
 }
@@ -812,11 +885,31 @@ bool map_codes(CUtensorMap *m, const int8_t *base, int rows, int K, int box_rows
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How many clusters of a size a device holds at once (of one kernel; asked once per size and device).
+struct ClusterLimit {
+    std::atomic<int> known[64][SK_MAX + 1];
+    template <class Kernel> int get(Kernel kern, const cudaLaunchConfig_t &cfg, int csize)
+    {
+        int dev = 0, n = 0;
+        const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+        if (keep && (n = known[dev][csize].load(std::memory_order_relaxed)) > 0)
+            return n - 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        if (keep)
+            known[dev][csize].store(n + 1, std::memory_order_relaxed);
+        return n;
+    }
+};
+
 template <class C, typename TO>
 luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
-                      int N, int K, TO *out, int64_t ldo, int tile_tokens, int sk, cudaStream_t stream)
+                      int N, int K, TO *out, int64_t ldo, int tile_tokens, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
+    static ClusterLimit clusters_at_once;
     auto kern = k_linear_i8_tc<C, TO>;
     TcArgs a;
     a.xs = xs;
@@ -837,24 +930,36 @@ luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const
         return LUCE_ERR_UNSUPPORTED;
     a.mt = (int)mt;
     a.tiles = (int)(mt * tt);
-    a.sk = sk;
     if (!map_codes(&a.tw, wq, N, K, RM) || !map_codes(&a.tx, xq, T, K, a.xbox))
         return LUCE_ERR_CUDA;
     if (limit.raise(kern, C::SMEM) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_UNSUPPORTED;
     }
-    const int csize = C::CG * sk;
-    const int clusters = sk > 1 ? a.tiles : std::min(a.tiles, luce_host::sm_count() / C::CG);
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    luce_host::make_config(cfg, attr, dim3((unsigned)(clusters * csize)), dim3(C::THREADS), C::SMEM, stream);
-    if (csize > 1) {
-        cudaLaunchAttribute &c = attr[cfg.numAttrs++];
-        c.id = cudaLaunchAttributeClusterDimension;
-        c.val.clusterDim.x = (unsigned)csize;
-        c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    luce_host::make_config(cfg, attr, dim3((unsigned)C::CG), dim3(C::THREADS), C::SMEM, stream);
+    cudaLaunchAttribute &cluster = attr[cfg.numAttrs];
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    // groups along K while all tiles' clusters are resident at once: a second
+    // round costs more than the split gains (100 x 4096 x 4096: clusters of 8 CTAs, of
+    // which not all 16 fit, 24.7 us; clusters of 4 16.9 us; pairs alone 18.5 us)
+    a.sk = 1;
+    for (int sk = 2; sk * C::CG <= SK_MAX && sk <= a.units && (int64_t)a.tiles * sk * C::CG <= luce_host::sm_count(); sk *= 2) {
+        cudaLaunchConfig_t query = cfg;
+        query.gridDim = dim3((unsigned)(sk * C::CG));
+        query.numAttrs = cfg.numAttrs + 1;
+        cluster.val.clusterDim.x = (unsigned)(sk * C::CG);
+        if (a.tiles > clusters_at_once.get(kern, query, sk * C::CG))
+            break;
+        a.sk = sk;
     }
+    const int csize = C::CG * a.sk;
+    const int clusters = a.sk > 1 ? a.tiles : std::min(a.tiles, luce_host::sm_count() / C::CG);
+    cfg.gridDim = dim3((unsigned)(clusters * csize));
+    cluster.val.clusterDim.x = (unsigned)csize;
+    cfg.numAttrs += csize > 1;
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
         (void)cudaGetLastError();
         limit.forget();
@@ -869,51 +974,50 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return p < q + nb && q < p + na;
 }
 
+template <int T, int VU, typename TO>
+luce_status launch_vec(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int nt,
+                       int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
+{
+    const int64_t rows = ((int64_t)N + VR - 1) / VR;
+    int wk = 1; // warps along K while fewer than 24 warps to an SM are busy and a slice keeps a full batch
+    while (wk < V_WARPS && rows * wk < (int64_t)24 * luce_host::sm_count() && K / (2 * wk) >= 512 * VU)
+        wk *= 2;
+    const int groups = V_WARPS / wk;
+    return luce_host::launch(k_linear_i8_vec<T, VU, TO>, dim3((unsigned)((rows + groups - 1) / groups)), dim3(V_WARPS * 32), 0,
+                             stream, xq, xs, wq, ws, bias, nt, N, K, wk, out, ldo);
+}
+
 template <typename TO>
 luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
-    if (T > TPW) {
-        const int units = (K + KU - 1) / KU, sms = luce_host::sm_count();
-        auto split = [&](int64_t tiles, int cg) { // groups along K while SMs are idle
-            int sk = 1;
-            while (sk * 2 * cg <= SK_MAX && tiles * cg * sk * 2 <= sms && sk * 2 <= units)
-                sk *= 2;
-            return sk;
-        };
-        if (T <= ROWS) {
-            const int64_t tiles = ((int64_t)N + RM - 1) / RM;
-            return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 15) & ~15, split(tiles, 1), stream);
+    // a stream of the weights for up to four tokens, and for up to eight while the
+    // weights are few: beyond 64 MB the products bound it (5 x 129280 x 4096:
+    // 105 us, tensor cores 87.6 us; 8 x 8192 x 4096: 11.0 against 13.5 us)
+    if (T == 1)
+        return launch_vec<1, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
+    if (T == 2)
+        return launch_vec<2, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
+    if (T <= 4)
+        return launch_vec<4, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
+    if (T <= 8 && (int64_t)N * K <= (int64_t)64 << 20)
+        return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
+    if (T <= ROWS)
+        return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 15) & ~15, stream);
+    if (T <= 2 * ROWS)
+        return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 31) & ~31, stream);
+    // tiles of at most 256 tokens: the width with the least rounds x width
+    const int64_t mt = ((int64_t)N + 2 * RM - 1) / (2 * RM), pairs = luce_host::sm_count() / 2;
+    int best = 4 * ROWS;
+    int64_t cost = INT64_MAX;
+    for (int w = 4 * ROWS; w > 2 * ROWS; w -= 32) {
+        const int64_t tiles = mt * (((int64_t)T + w - 1) / w), rounds = (tiles + pairs - 1) / pairs;
+        if (rounds * w < cost) {
+            cost = rounds * w;
+            best = w;
         }
-        const int64_t mt = ((int64_t)N + 2 * RM - 1) / (2 * RM);
-        if (T <= 2 * ROWS)
-            return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 31) & ~31, split(mt, 2), stream);
-        // tiles of at most 256 tokens: the width with the least rounds x width
-        int best = 4 * ROWS;
-        int64_t cost = INT64_MAX;
-        for (int w = 4 * ROWS; w > 2 * ROWS; w -= 32) {
-            const int64_t tiles = mt * (((int64_t)T + w - 1) / w), rounds = (tiles + sms / 2 - 1) / (sms / 2);
-            if (rounds * w < cost) {
-                cost = rounds * w;
-                best = w;
-            }
-        }
-        const int64_t tiles = mt * (((int64_t)T + best - 1) / best);
-        return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, best, split(tiles, 2), stream);
     }
-    const int64_t nb = ((int64_t)N + WARPS - 1) / WARPS;
-    // tokens in slices of at most 65,535 tiles, the grid's limit in y
-    for (int t0 = 0; t0 < T;) {
-        const int n = std::min(T - t0, 65535 * TPW);
-        const luce_status st =
-            luce_host::launch(k_linear_i8_rows<TO>, dim3((unsigned)nb, (unsigned)((n + TPW - 1) / TPW)),
-                              dim3(WARPS * 32), 0, stream, xq + (size_t)t0 * K, xs + t0, wq, ws, bias, n, N, K,
-                              out + (size_t)t0 * ldo, ldo);
-        if (st != LUCE_OK)
-            return st;
-        t0 += n;
-    }
-    return LUCE_OK;
+    return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, best, stream);
 }
 
 } // namespace
