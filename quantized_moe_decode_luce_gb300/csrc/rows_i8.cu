@@ -25,67 +25,313 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-constexpr int THREADS = 256;
-
-// One CTA per row, two passes over it: the row's sum of squares and its
-// largest |p|, then the codes.
-template <typename TX>
-__global__ void __launch_bounds__(THREADS)
-    k_rows_i8(const TX *x, const TX *res, TX *xsum, const float *gamma, float eps, int T, int H, int8_t *q,
-              float *scale)
+// The larger of m and |v|; a NaN stays.
+__device__ __forceinline__ float max_abs(float m, float v)
 {
-    __shared__ float s_ss[THREADS / 32];
-    __shared__ uint32_t s_m[THREADS / 32];
-    pdl_wait();
-    pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int t = blockIdx.x; t < T; t += gridDim.x) {
-        const size_t row = (size_t)t * H;
-        float ss = 0.0f;
-        uint32_t m = 0;
-        for (int i = threadIdx.x; i < H; i += THREADS) {
-            float v = to_f32(x[row + i]);
-            if (res)
-                v = to_f32(from_f32<TX>(__fadd_rn(v, to_f32(res[row + i]))));
-            const float p = gamma ? __fmul_rn(v, gamma[i]) : v;
-            ss = fmaf(v, v, ss);
-            m = max(m, __float_as_uint(p) & 0x7fffffffu); // |p| as ordered bits: a NaN lies above infinity
-        }
-        ss = warp_sum(ss);
-        m = __reduce_max_sync(0xffffffffu, m);
-        __syncthreads(); // (the previous row's totals have been read)
-        if (lane == 0) {
-            s_ss[warp] = ss;
-            s_m[warp] = m;
-        }
-        __syncthreads();
-        ss = 0.0f;
-        m = 0;
-        for (int w = 0; w < THREADS / 32; w++) {
-            ss += s_ss[w];
-            m = max(m, s_m[w]);
-        }
-        const bool finite = m < 0x7f800000u;
-        const float d = __fdiv_rn(__uint_as_float(m), 127.0f);
-        for (int i = threadIdx.x; i < H; i += THREADS) {
-            float v = to_f32(x[row + i]);
-            if (res) {
-                const TX s = from_f32<TX>(__fadd_rn(v, to_f32(res[row + i])));
-                v = to_f32(s);
-                if (xsum)
-                    xsum[row + i] = s;
-            }
-            const float p = gamma ? __fmul_rn(v, gamma[i]) : v;
-            const float c = fminf(fmaxf(roundf(__fdiv_rn(p, d)), -127.0f), 127.0f);
-            q[row + i] = finite && d > 0.0f ? (int8_t)c : (int8_t)0;
-        }
-        if (threadIdx.x == 0) {
-            float sc = d;
-            if (gamma)
-                sc = __fmul_rn(d, __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps))));
-            scale[t] = finite ? sc : NAN;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+// Sum of squares and largest |p| of a row over its threads: `lanes` of a warp, or the whole block.
+template <bool NORM> __device__ __forceinline__ void row_totals(float &ss, float &m, int lanes)
+{
+    __shared__ float s_ss[32];
+    __shared__ uint32_t s_m[32];
+    uint32_t mb = __float_as_uint(m); // ordered like the values, which are not negative; a NaN lies above infinity
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o < lanes) {
+            if (NORM)
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lanes < 32)
+                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
         }
     }
+    if (lanes >= 32)
+        mb = __reduce_max_sync(0xffffffffu, mb);
+    if (lanes > 32) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) {
+            if (NORM)
+                s_ss[warp] = ss;
+            s_m[warp] = mb;
+        }
+        __syncthreads();
+        if (NORM)
+            ss = warp_sum(lane < warps ? s_ss[lane] : 0.0f);
+        mb = __reduce_max_sync(0xffffffffu, lane < warps ? s_m[lane] : 0u);
+    }
+    m = __uint_as_float(mb);
+}
+
+__device__ __forceinline__ int code_of(float p, float d)
+{
+    return (int)fminf(fmaxf(roundf(__fdiv_rn(p, d)), -127.0f), 127.0f);
+}
+
+// Codes of V values, four to a word.  round(fl(p / d)) is the whole number
+// nearest p rinv wherever that is not within 1e-4 of half way between two
+// (|p / d| <= 127.0001, and rinv = fl(1 / d) moves it by less than 2e-5), which
+// four operations per value find: the sum with 1.5 2^23 rounds to a whole
+// number and leaves it in the low bits.  Chunks with a value near half way (or
+// a d whose reciprocal overflows: the distance is then a NaN) divide.  Division
+// throughout took 54.9 us for 8191 x 4096 bf16 rows with a residual.
+template <int V> __device__ __forceinline__ void codes_of(const float (&p)[V], float d, float rinv, uint32_t (&w)[V / 4])
+{
+    constexpr float M = 12582912.0f;
+    uint32_t u[V];
+    bool near_half = false;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        const float r = fmaf(p[i], rinv, M);
+        u[i] = __float_as_uint(r);
+        near_half |= !(fabsf(fmaf(p[i], rinv, -__fsub_rn(r, M))) <= 0.4999f);
+    }
+    if (near_half) {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            u[i] = (uint32_t)code_of(p[i], d);
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+        w[i / 4] = __byte_perm(__byte_perm(u[i], u[i + 1], 0x0040), __byte_perm(u[i + 2], u[i + 3], 0x0040), 0x5410);
+}
+
+__device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, bool norm, bool finite)
+{
+    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
+    return !finite ? NAN : norm ? __fmul_rn(d, r) : d;
+}
+
+// ---------------------------------------------------------------------------
+// A row in registers: NCH chunks of 16 bytes of x per thread, read once (with
+// the residual beside them), codes written once.  Bound by HBM for many rows, whose 32 values a thread spread
+// what every thread does once (the totals, three divisions) thin: with 16 the
+// 8191 x 4096 bf16 rows of luce_quantize_i8 took 33 us.  For few rows it is
+// latency: one chunk a thread, all loads at once, one barrier.
+//
+// blockDim.x threads to a row: 8, 16 or 32 lanes of a warp (blockDim.y rows to
+// the block, no barrier), or the block.
+//
+// ALIGNED: every row starts 16-byte aligned in every array.  Otherwise chunk j
+// holds the elements j V - a .. j V - a + V - 1 of the row, a the row's offset
+// in x from a 16-byte boundary (the residual and the sum share it: checked by
+// the host), the first and last chunk element by element; the codes, whose
+// rows lie at other offsets, go through shared memory and leave in 16-byte
+// stores.
+template <typename TX, int NCH, bool ALIGNED, bool NORM>
+__global__ void __launch_bounds__(1024)
+    k_rows_i8(const TX *x, const TX *res, TX *xsum, const float *__restrict__ gamma, float eps, int T, int H, int8_t *q,
+              float *scale)
+{
+    constexpr int V = 16 / sizeof(TX);
+    extern __shared__ __align__(16) uint32_t codes[]; // [rows of the block][pitch] (unaligned rows)
+    pdl_wait();
+    pdl_trigger();
+    const int t = blockIdx.x * blockDim.y + threadIdx.y, lanes = blockDim.x;
+    const bool live_row = t < T;
+    const size_t row = (size_t)(live_row ? t : 0) * H;
+    const int n = live_row ? H : 0;
+    const int a = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(x + row) & 15) / sizeof(TX));
+    const bool in_place = !ALIGNED && (xsum == x || xsum == res) && xsum != nullptr;
+    union Chunk {
+        uint4 w;
+        TX e[V];
+    };
+    Chunk cx[NCH], cr[NCH];
+    auto load = [&](Chunk &c, const TX *p, int e0) { // elements e0 .. e0 + V - 1 of the row
+        if (ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n) {
+            c.w = *reinterpret_cast<const uint4 *>(p + e0);
+        } else {
+            c.w = make_uint4(0, 0, 0, 0);
+            if (!ALIGNED && e0 + V > 0 && e0 < n) {
+                // a chunk over the row's end: whole where the neighbouring row fills it (and
+                // nothing is stored to it meanwhile), its other elements set to zero
+                if (!in_place && (long long)row + e0 >= 0 && row + e0 + V <= (size_t)T * H) {
+                    c.w = *reinterpret_cast<const uint4 *>(p + e0);
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        if (e0 + i < 0 || e0 + i >= n)
+                            c.e[i] = from_f32<TX>(0.0f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        if (e0 + i >= 0 && e0 + i < n)
+                            c.e[i] = p[e0 + i];
+                }
+            }
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < NCH; c++)
+        load(cx[c], x + row, (int)(threadIdx.x + c * lanes) * V - a);
+    if (res) {
+#pragma unroll
+        for (int c = 0; c < NCH; c++)
+            load(cr[c], res + row, (int)(threadIdx.x + c * lanes) * V - a);
+    }
+    // p of chunk c: its values times gamma (elements behind the row's ends are zero)
+    auto scaled = [&](const Chunk &c, int e0, bool whole, float (&p)[V]) {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            p[i] = to_f32(c.e[i]);
+        if constexpr (NORM) {
+            if (ALIGNED) {
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < V; i += 4) {
+                        const float4 g = __ldg(reinterpret_cast<const float4 *>(gamma + e0 + i));
+                        p[i] = __fmul_rn(p[i], g.x);
+                        p[i + 1] = __fmul_rn(p[i + 1], g.y);
+                        p[i + 2] = __fmul_rn(p[i + 2], g.z);
+                        p[i + 3] = __fmul_rn(p[i + 3], g.w);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if (whole || (e0 + i >= 0 && e0 + i < n))
+                        p[i] = __fmul_rn(p[i], __ldg(gamma + e0 + i));
+            }
+        }
+    };
+    float ss = 0.0f, m = 0.0f;
+    float p[NORM ? NCH : 1][V];
+#pragma unroll
+    for (int c = 0; c < NCH; c++) {
+        const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
+        const bool whole = ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n;
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                cx[c].e[i] = from_f32<TX>(__fadd_rn(to_f32(cx[c].e[i]), to_f32(cr[c].e[i])));
+        }
+        if (xsum) {
+            if (whole) {
+                *reinterpret_cast<uint4 *>(xsum + row + e0) = cx[c].w;
+            } else if (!ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if (e0 + i >= 0 && e0 + i < n)
+                        xsum[row + e0 + i] = cx[c].e[i];
+            }
+        }
+        float pc[V];
+        scaled(cx[c], e0, whole, pc);
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            if (NORM) {
+                const float v = to_f32(cx[c].e[i]);
+                ss = fmaf(v, v, ss);
+                p[NORM ? c : 0][i] = pc[i];
+            }
+            m = max_abs(m, pc[i]);
+        }
+    }
+    row_totals<NORM>(ss, m, lanes);
+    const bool finite = m < INFINITY;
+    const float d = __fdiv_rn(m, 127.0f);
+    const bool live = finite && d > 0.0f;
+    const float rinv = __fdiv_rn(1.0f, d);
+    if (threadIdx.x == 0 && live_row)
+        scale[t] = scale_of(d, ss, H, eps, NORM, finite);
+    int8_t *qr = q + row;
+    const int pitch = (H + 32) / 16 * 4; // words
+    uint32_t *buf = codes + threadIdx.y * pitch;
+#pragma unroll
+    for (int c = 0; c < NCH; c++) {
+        const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
+        const bool whole = ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n;
+        uint32_t w[V / 4] = {};
+        if (live) {
+            if constexpr (NORM) {
+                codes_of<V>(p[c], d, rinv, w);
+            } else {
+                float pc[V];
+                scaled(cx[c], e0, whole, pc);
+                codes_of<V>(pc, d, rinv, w);
+            }
+        }
+        if (e0 < n) {
+            if (ALIGNED) {
+                if constexpr (V == 4)
+                    *reinterpret_cast<uint32_t *>(qr + e0) = w[0];
+                else
+                    *reinterpret_cast<uint2 *>(qr + e0) = make_uint2(w[0], w[V / 4 - 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 4; i++)
+                    buf[(e0 + a) / 4 + i] = w[i]; // (byte e + a of the buffer is element e)
+            }
+        }
+    }
+    if (!ALIGNED) {
+        if (lanes <= 32)
+            __syncwarp();
+        else
+            __syncthreads();
+        // 16-byte pieces of the row at 16-byte boundaries of q: piece i starts at element 16 i - b
+        const int b = (int)(reinterpret_cast<uintptr_t>(qr) & 15);
+        for (int i = threadIdx.x; 16 * i < b + n; i += lanes) {
+            const int e = 16 * i - b, s = e + a; // first element, its byte in the buffer
+            if (e >= 0 && e + 16 <= n) {
+                const uint32_t *src = buf + (s >> 2);
+                uint32_t w[5];
+#pragma unroll
+                for (int k = 0; k < 5; k++)
+                    w[k] = src[k]; // (the last one may lie behind the row, within the pitch)
+                const uint32_t sh = 8 * (s & 3);
+                *reinterpret_cast<uint4 *>(qr + e) =
+                    make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                               __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+            } else {
+                const int8_t *bytes = reinterpret_cast<const int8_t *>(buf);
+                for (int k = max(e, 0); k < min(e + 16, n); k++)
+                    qr[k] = bytes[k + a];
+            }
+        }
+    }
+}
+
+// Any row: one block per row, two passes over it (rows longer than the
+// registers of a block hold, or a residual at another offset than x).
+constexpr int THREADS = 512;
+
+template <typename TX>
+__global__ void __launch_bounds__(THREADS)
+    k_rows_i8_any(const TX *x, const TX *res, TX *xsum, const float *gamma, float eps, int T, int H, int8_t *q,
+                  float *scale)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int t = blockIdx.x;
+    const size_t row = (size_t)t * H;
+    auto value = [&](int i) {
+        const float v = to_f32(x[row + i]);
+        return res ? from_f32<TX>(__fadd_rn(v, to_f32(res[row + i]))) : x[row + i];
+    };
+    float ss = 0.0f, m = 0.0f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < H; i += THREADS) {
+        const float v = to_f32(value(i));
+        ss = fmaf(v, v, ss);
+        m = max_abs(m, gamma ? __fmul_rn(v, gamma[i]) : v);
+    }
+    row_totals<true>(ss, m, THREADS);
+    const bool finite = m < INFINITY;
+    const float d = __fdiv_rn(m, 127.0f);
+    const bool live = finite && d > 0.0f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < H; i += THREADS) {
+        const TX s = value(i);
+        const float v = to_f32(s);
+        if (xsum)
+            xsum[row + i] = s;
+        q[row + i] = live ? (int8_t)code_of(gamma ? __fmul_rn(v, gamma[i]) : v, d) : (int8_t)0;
+    }
+    if (threadIdx.x == 0)
+        scale[t] = scale_of(d, ss, H, eps, gamma != nullptr, finite);
 }
 
 constexpr int H_MAX = 65536;
@@ -96,13 +342,58 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return p < q + nb && q < p + na;
 }
 
-template <typename TX>
-luce_status run_rows(const void *x, const void *res, void *xsum, const float *gamma, float eps, int T, int H,
-                     int8_t *q, float *scale, void *stream)
+template <typename TX, int NCH>
+luce_status launch_rows(const TX *x, const TX *res, TX *xsum, const float *gamma, float eps, int T, int H, int8_t *q,
+                        float *scale, int threads, bool aligned_rows, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)T;
-    return luce_host::launch(k_rows_i8<TX>, dim3(grid), dim3(THREADS), 0, luce_host::as_stream(stream),
-                             (const TX *)x, (const TX *)res, (TX *)xsum, gamma, eps, T, H, q, scale);
+    const int rows = threads <= 32 ? 256 / threads : 1;
+    const dim3 grid((unsigned)((T + rows - 1) / rows)), block((unsigned)threads, (unsigned)rows);
+    const size_t smem = aligned_rows ? 0 : (size_t)rows * ((H + 32) / 16 * 16);
+    auto run = [&](auto kern) {
+        return luce_host::launch(kern, grid, block, smem, stream, x, res, xsum, gamma, eps, T, H, q, scale);
+    };
+    if (gamma)
+        return aligned_rows ? run(k_rows_i8<TX, NCH, true, true>) : run(k_rows_i8<TX, NCH, false, true>);
+    return aligned_rows ? run(k_rows_i8<TX, NCH, true, false>) : run(k_rows_i8<TX, NCH, false, false>);
+}
+
+template <typename TX>
+luce_status run_rows(const void *vx, const void *vres, void *vsum, const float *gamma, float eps, int T, int H,
+                     int8_t *q, float *scale, void *vstream)
+{
+    using luce_host::aligned;
+    constexpr int V = 16 / sizeof(TX);
+    const TX *x = (const TX *)vx, *res = (const TX *)vres;
+    TX *xsum = (TX *)vsum;
+    cudaStream_t stream = luce_host::as_stream(vstream);
+    const bool al = H % V == 0 && aligned(x, 16) && (!res || aligned(res, 16)) && (!xsum || aligned(xsum, 16)) &&
+                    (!gamma || aligned(gamma, 16)) && aligned(q, V);
+    auto off = [](const void *p) { return reinterpret_cast<uintptr_t>(p) & 15; };
+    const bool one_offset = (!res || off(res) == off(x)) && (!xsum || off(xsum) == off(x));
+    const int chunks = al ? H / V : (H + V - 1) / V + 1; // 16-byte pieces of a row
+    // one chunk a thread for few rows, or rows that a warp holds; 32 values for many (fp32 with a
+    // gamma: 16, whose loads are enough in flight; 8191 x 4096: 64.9 us, with 32 82.6 us)
+    const int sms = luce_host::sm_count();
+    int nch = T <= 2 * sms || chunks <= 32 ? 1 : T < 16 * sms || (gamma && V == 4) ? 16 / V : 32 / V;
+    while (nch < 32 / V && chunks > 1024 * nch)
+        nch *= 2;
+    if (!one_offset || chunks > 1024 * nch)
+        return luce_host::launch(k_rows_i8_any<TX>, dim3((unsigned)T), dim3(THREADS), 0, stream, x, res, xsum, gamma,
+                                 eps, T, H, q, scale);
+    const int need = (chunks + nch - 1) / nch;
+    int threads = need > 32 ? (need + 31) & ~31 : 8;
+    while (threads < need)
+        threads *= 2;
+    switch (nch) {
+    case 1:
+        return launch_rows<TX, 1>(x, res, xsum, gamma, eps, T, H, q, scale, threads, al, stream);
+    case 2:
+        return launch_rows<TX, 2>(x, res, xsum, gamma, eps, T, H, q, scale, threads, al, stream);
+    case 4:
+        return launch_rows<TX, 4>(x, res, xsum, gamma, eps, T, H, q, scale, threads, al, stream);
+    default:
+        return launch_rows<TX, 32 / V>(x, res, xsum, gamma, eps, T, H, q, scale, threads, al, stream);
+    }
 }
 
 // the three entry points: gamma is NULL for the plain rows, res and xsum for those without a residual
