@@ -48,45 +48,56 @@ struct LogitsArgs {
 };
 
 constexpr int THREADS = 512;
-constexpr int NB = 4; // vectors of logits of a thread in flight
+constexpr int NB = 2; // steps of a thread in flight, and as many requested behind them
+constexpr int HB = 4; // history loads of a thread in flight (four tokens each)
 
 // What a slot of shared memory holds for its token: twice the number of
-// generated occurrences, the low bit set if the token is among the prompt's.
+// generated occurrences, the low bit set if the token is among the prompt's
+// (the two never touch each other's bits, so their order does not matter).
 // Sixteen bits are enough while a row has at most 32,767 tokens.
 template <bool S16> struct Slots {
-    uint32_t *w;
+    uint32_t base; // shared address
     __device__ __forceinline__ uint32_t get(int at) const
     {
-        return S16 ? reinterpret_cast<const uint16_t *>(w)[at] : w[at];
+        uint32_t v;
+        if (S16) {
+            uint16_t h;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(base + 2 * at));
+            v = h;
+        } else {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(base + 4 * at));
+        }
+        return v;
     }
     __device__ __forceinline__ void put(int at, uint32_t v) const
     {
         if (S16)
-            reinterpret_cast<uint16_t *>(w)[at] = (uint16_t)v;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(base + 2 * at), "h"((uint16_t)v) : "memory");
         else
-            w[at] = v;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + 4 * at), "r"(v) : "memory");
     }
-    __device__ __forceinline__ void add(int at, uint32_t v) const
+    // one more generated (no carry between sixteen-bit slots: at most 65,535), or among the prompt's; if `live`
+    template <bool PROMPT> __device__ __forceinline__ void count(int at, bool live) const
     {
-        if (S16)
-            atomicAdd(w + (at >> 1), v << (16 * (at & 1))); // (no carry: at most 65,535)
+        const uint32_t addr = base + (S16 ? (2 * at) & ~3 : 4 * at);
+        const uint32_t v = (PROMPT ? 1u : 2u) << (S16 ? 16 * (at & 1) : 0);
+        if (PROMPT)
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.or.b32 [%0], %1;\n\t}" ::"r"(addr),
+                         "r"(v), "r"((uint32_t)live)
+                         : "memory");
         else
-            atomicAdd(w + at, v);
-    }
-    __device__ __forceinline__ void set_low(int at) const
-    {
-        if (S16)
-            atomicOr(w + (at >> 1), 1u << (16 * (at & 1)));
-        else
-            atomicOr(w + at, 1u);
+            asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0], %1;\n\t}" ::"r"(addr),
+                         "r"(v), "r"((uint32_t)live)
+                         : "memory");
     }
     __device__ __forceinline__ void raise(int at, uint32_t v) const // the larger of the slot and v
     {
+        extern __shared__ __align__(16) uint32_t slot_words[];
         if (!S16) {
-            atomicMax(w + at, v);
+            atomicMax(slot_words + at, v);
             return;
         }
-        uint32_t *p = w + (at >> 1), old = *p;
+        uint32_t *p = slot_words + (at >> 1), old = *p;
         const int sh = 16 * (at & 1);
         while (((old >> sh) & 0xffffu) < v) {
             const uint32_t seen = atomicCAS(p, old, (old & ~(0xffffu << sh)) | v << sh);
@@ -95,65 +106,80 @@ template <bool S16> struct Slots {
             old = seen;
         }
     }
-    // four slots from `at` (a multiple of four)
-    __device__ __forceinline__ uint4 get4(int at) const
+    // the slots of N tokens from `at` (a multiple of N)
+    template <int N> __device__ __forceinline__ void get_n(int at, uint32_t (&c)[N]) const
     {
-        if (!S16)
-            return *reinterpret_cast<const uint4 *>(w + at);
-        const uint2 v = *reinterpret_cast<const uint2 *>(w + (at >> 1));
-        return make_uint4(v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16);
+        if constexpr (N == 1) {
+            c[0] = get(at);
+        } else if constexpr (S16) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                uint32_t x, y;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(base + 2 * (at + i)));
+                c[i] = x & 0xffffu;
+                c[i + 1] = x >> 16;
+                c[i + 2] = y & 0xffffu;
+                c[i + 3] = y >> 16;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(c[i]), "=r"(c[i + 1]), "=r"(c[i + 2]), "=r"(c[i + 3])
+                             : "r"(base + 4 * (at + i)));
+        }
     }
 };
 
-__device__ __forceinline__ float penalized(float l, uint32_t c, float rep, float freq, float pres)
+// l / rep, correctly rounded, from rinv = fl(1 / rep): Markstein's sequence, a
+// product, its exact remainder and one correction.  Results outside the range
+// where no intermediate can over- or underflow (zero, infinities and NaNs
+// among them) divide.
+__device__ __forceinline__ float divided(float l, float rep, float rinv)
 {
-    l = l > 0.0f ? __fdiv_rn(l, rep) : __fmul_rn(l, rep);
-    if (c >> 1)
-        l = __fsub_rn(l, __fadd_rn(__fmul_rn((float)(c >> 1), freq), pres));
-    return l;
+    const float q = __fmul_rn(l, rinv);
+    const float s = fmaf(fmaf(-q, rep, l), rinv, q);
+    const float m = fabsf(s);
+    return m > 1e-25f && m < 1e25f ? s : __fdiv_rn(l, rep);
 }
 
-// VEC logits a step and thread: 4 where every row starts aligned, else 1.
+template <bool S16>
+__device__ __forceinline__ float penalized(float l, uint32_t c, float rep, float rinv, float freq, float pres)
+{
+    const float p = l > 0.0f ? divided(l, rep, rinv) : __fmul_rn(l, rep);
+    const uint32_t k = c >> 1;
+    // (at most 32,767: exact in the low bits of 2^23)
+    const float f = S16 ? __fsub_rn(__uint_as_float(0x4b000000u | k), 8388608.0f) : (float)k;
+    const float g = k ? __fsub_rn(p, __fadd_rn(__fmul_rn(f, freq), pres)) : p;
+    return c ? g : l;
+}
+
+// VEC logits a step and thread: 16 bytes, or one.  A row may start `sh`
+// elements behind a boundary of VEC elements (the same for logits and out:
+// checked by the host), so a stretch is gone through in steps that start at
+// boundaries, u = v + sh, whose first and last may be partial.
 template <typename TL, int VEC, bool S16>
-__global__ void __launch_bounds__(THREADS) k_logits_process(const LogitsArgs a, int stretch)
+__global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch)
 {
     extern __shared__ __align__(16) uint32_t slot_words[];
-    const Slots<S16> slots{slot_words};
+    const Slots<S16> slots{smem_addr(slot_words)}; // (slot u is that of token c0 + u - sh)
     const int r = blockIdx.y, tid = threadIdx.x;
     const int64_t c0 = (int64_t)blockIdx.x * stretch;
     const int nc = (int)min((int64_t)stretch, a.V - c0);
     struct alignas(VEC * sizeof(TL)) In {
         TL e[VEC];
     };
-    struct alignas(VEC * 4) Out {
-        float e[VEC];
-    };
+    float *o = a.out + (size_t)r * a.ldo + c0;
+    const int sh = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(o) >> 2) & (VEC - 1));
     // slots to zero (they do not depend on the previous kernel)
     if (a.hist) {
-        const int words = S16 ? (nc + 1) / 2 : nc;
+        const int words = S16 ? (nc + sh + 1) / 2 : nc + sh;
         for (int i = tid; 4 * i < words; i += THREADS)
             reinterpret_cast<uint4 *>(slot_words)[i] = make_uint4(0, 0, 0, 0);
     }
     pdl_wait();
     pdl_trigger();
     const TL *lr = static_cast<const TL *>(a.logits) + (size_t)r * a.ldl + c0;
-    float *o = a.out + (size_t)r * a.ldo + c0;
-    In in[NB];
-    auto load = [&](int v0) {
-#pragma unroll
-        for (int i = 0; i < NB; i++) {
-            const int v = v0 + (tid + i * THREADS) * VEC;
-            if (v + VEC <= nc) {
-                in[i] = *reinterpret_cast<const In *>(lr + v);
-            } else if (VEC > 1) {
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    if (v + e < nc)
-                        in[i].e[e] = lr[v + e];
-            }
-        }
-    };
-    load(0);
     const uint32_t *mr = nullptr;
     bool bad = false;
     if (a.mask) {
@@ -163,98 +189,162 @@ __global__ void __launch_bounds__(THREADS) k_logits_process(const LogitsArgs a, 
         else if (m >= 0)
             mr = a.mask + (size_t)m * a.ldm + (c0 >> 5); // (c0 is a multiple of 32)
     }
-    float rep = 1.0f, freq = 0.0f, pres = 0.0f;
-    if (a.hist) {
-        __syncthreads();
-        const int len = (int)min((int64_t)max(a.hist_len[r], 0), a.ldh);
-        const int plen = a.prompt_len ? a.prompt_len[r] : 0;
-        rep = a.rep ? a.rep[r] : 1.0f;
-        freq = a.freq ? a.freq[r] : 0.0f;
-        pres = a.pres ? a.pres[r] : 0.0f;
-        const int32_t *h = a.hist + (size_t)r * a.ldh;
-        const bool first = blockIdx.x == 0;
-        auto count = [&](int32_t id, int i) {
-            const uint32_t at = (uint32_t)(id - (int32_t)c0);
-            if (id >= 0 && at < (uint32_t)nc) {
-                if (i < plen)
-                    slots.set_low((int)at);
-                else
-                    slots.add((int)at, 2u);
+    auto allowed = [&](int v) { return (mr[v >> 5] >> (v & 31)) & 1u; };
+    // a batch: the logits of NB steps and the mask bits of their tokens
+    struct Batch {
+        In in[NB];
+        uint32_t bits[NB];
+    };
+    auto load = [&](Batch &b, int u0) {
+#pragma unroll
+        for (int i = 0; i < NB; i++) {
+            const int v = u0 + (tid + i * THREADS) * VEC - sh;
+            b.bits[i] = 0xffffffffu;
+            if (v >= 0 && v + VEC <= nc) {
+                b.in[i] = *reinterpret_cast<const In *>(lr + v);
+                if (mr) {
+                    b.bits[i] = mr[v >> 5] >> (v & 31);
+                    if (VEC > 1 && sh != 0 && (v & 31) > 32 - VEC)
+                        b.bits[i] |= mr[(v >> 5) + 1] << (32 - (v & 31));
+                }
+            } else if (VEC > 1 && v + VEC > 0 && v < nc) {
+                if (mr)
+                    b.bits[i] = 0;
+#pragma unroll
+                for (int e = 0; e < VEC; e++)
+                    if (v + e >= 0 && v + e < nc) {
+                        b.in[i].e[e] = lr[v + e];
+                        if (mr)
+                            b.bits[i] |= allowed(v + e) << e;
+                    }
             }
-            if (first)
-                bad |= id >= a.V;
-        };
-        const int head = (int)(((16 - (reinterpret_cast<uintptr_t>(h) & 15)) & 15) / 4); // tokens before a 16-byte boundary
-        if (tid < min(head, len))
-            count(h[tid], tid);
-        const int quads = len > head ? (len - head) >> 2 : 0;
+        }
+    };
+    Batch cur;
+    load(cur, 0);
+    float rep = 1.0f, rinv = 1.0f, freq = 0.0f, pres = 0.0f;
+    if (a.hist) {
+        const int32_t *h = a.hist + (size_t)r * a.ldh;
+        // tokens before a 16-byte boundary, quads from there, and a rest; the first
+        // quads are requested before the length is known (they lie within ld_hist)
+        const int head = (int)((4 - ((reinterpret_cast<uintptr_t>(h) >> 2) & 3)) & 3);
         const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
-        constexpr int HB = 4; // loads in flight
-        for (int q0 = 0; q0 < quads; q0 += HB * THREADS) {
-            int4 t[HB];
+        const int all_quads = a.ldh > head ? (int)((a.ldh - head) >> 2) : 0;
+        int4 t[HB];
+        auto request = [&](int q0, int quads) {
 #pragma unroll
             for (int i = 0; i < HB; i++) {
                 const int q = q0 + i * THREADS + tid;
                 t[i] = q < quads ? h4[q] : make_int4(-1, -1, -1, -1);
             }
+        };
+        request(0, all_quads);
+        const int len = (int)min((int64_t)max(a.hist_len[r], 0), a.ldh);
+        const int plen = a.prompt_len ? a.prompt_len[r] : 0;
+        rep = a.rep ? a.rep[r] : 1.0f;
+        freq = a.freq ? a.freq[r] : 0.0f;
+        pres = a.pres ? a.pres[r] : 0.0f;
+        rinv = __fdiv_rn(1.0f, rep);
+        const int32_t lo = (int32_t)c0;
+        int32_t top = -1; // the largest id seen
+        // (c0 + nc <= V < 2^31, so that one unsigned comparison also leaves out negative ids)
+        auto prompt = [&](int32_t id) {
+            top = max(top, id);
+            const uint32_t at = (uint32_t)(id - lo);
+            slots.template count<true>((int)at + sh, at < (uint32_t)nc);
+        };
+        auto made = [&](int32_t id) {
+            top = max(top, id);
+            const uint32_t at = (uint32_t)(id - lo);
+            slots.template count<false>((int)at + sh, at < (uint32_t)nc);
+        };
+        auto one = [&](int32_t id, int i) {
+            if (i >= len)
+                return;
+            if (i < plen)
+                prompt(id);
+            else
+                made(id);
+        };
+        __syncthreads();
+        if (tid < min(head, len))
+            one(h[tid], tid);
+        const int quads = len > head ? (len - head) >> 2 : 0;
+        for (int q0 = 0; q0 < quads;) {
 #pragma unroll
             for (int i = 0; i < HB; i++) {
-                const int at = head + 4 * (q0 + i * THREADS + tid);
-                count(t[i].x, at);
-                count(t[i].y, at + 1);
-                count(t[i].z, at + 2);
-                count(t[i].w, at + 3);
-            }
-        }
-        const int tail = head + 4 * quads + tid;
-        if (tail < len && tid < 4)
-            count(h[tail], tail);
-        __syncthreads();
-    }
-    for (int v0 = 0; v0 < nc; v0 += NB * THREADS * VEC) {
-        if (v0 > 0)
-            load(v0);
+                const int q = q0 + i * THREADS + tid, at = head + 4 * q;
+                if (q >= quads)
+                    break;
+                const int32_t id[4] = {t[i].x, t[i].y, t[i].z, t[i].w};
+                if (at + 4 <= plen) {
 #pragma unroll
-        for (int i = 0; i < NB; i++) {
-            const int v = v0 + (tid + i * THREADS) * VEC;
-            if (v >= nc)
-                break;
-            Out w;
+                    for (int k = 0; k < 4; k++)
+                        prompt(id[k]);
+                } else if (at >= plen) {
 #pragma unroll
-            for (int e = 0; e < VEC; e++)
-                w.e[e] = to_f32(in[i].e[e]);
-            if (a.hist) {
-                if constexpr (VEC == 4) {
-                    const uint4 c = slots.get4(v);
-                    if (c.x | c.y | c.z | c.w) {
-                        const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-                        for (int e = 0; e < VEC; e++)
-                            if (cs[e])
-                                w.e[e] = penalized(w.e[e], cs[e], rep, freq, pres);
-                    }
+                    for (int k = 0; k < 4; k++)
+                        made(id[k]);
                 } else {
-                    const uint32_t c = slots.get(v);
-                    if (c)
-                        w.e[0] = penalized(w.e[0], c, rep, freq, pres);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        one(id[k], at + k);
                 }
             }
-            if (mr) {
-                const uint32_t bits = mr[v >> 5] >> (v & 31);
+            q0 += HB * THREADS;
+            if (q0 < quads)
+                request(q0, quads);
+        }
+        const int rest = head + 4 * quads + tid;
+        if (tid < 4 && rest < len && len > head)
+            one(h[rest], rest);
+        bad |= top >= a.V;
+        __syncthreads();
+    }
+    for (int u0 = 0; u0 < nc + sh; u0 += NB * THREADS * VEC) {
+        Batch next;
+        load(next, u0 + NB * THREADS * VEC);
+#pragma unroll
+        for (int i = 0; i < NB; i++) {
+            const int u = u0 + (tid + i * THREADS) * VEC, v = u - sh;
+            if (v >= nc)
+                break;
+            float w[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; e++)
+                w[e] = to_f32(cur.in[i].e[e]);
+            if (a.hist) {
+                uint32_t c[VEC], any = 0;
+                slots.template get_n<VEC>(u, c);
 #pragma unroll
                 for (int e = 0; e < VEC; e++)
-                    if (!((bits >> e) & 1u))
-                        w.e[e] = -INFINITY;
+                    any |= c[e];
+                if (any) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e++)
+                        w[e] = penalized<S16>(w[e], c[e], rep, rinv, freq, pres);
+                }
             }
-            if (v + VEC <= nc) {
-                *reinterpret_cast<Out *>(o + v) = w;
+#pragma unroll
+            for (int e = 0; e < VEC; e++)
+                if (!((cur.bits[i] >> e) & 1u))
+                    w[e] = -INFINITY;
+            if (v >= 0 && v + VEC <= nc) {
+                if constexpr (VEC == 1) {
+                    o[v] = w[0];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 4)
+                        *reinterpret_cast<float4 *>(o + v + e) = make_float4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < VEC; e++)
-                    if (v + e < nc)
-                        o[v + e] = w.e[e];
+                    if (v + e >= 0 && v + e < nc)
+                        o[v + e] = w[e];
             }
         }
+        cur = next;
     }
     if (a.nbias) {
         // the slots now find each id's last entry, which adds its bias to the
@@ -275,7 +365,7 @@ __global__ void __launch_bounds__(THREADS) k_logits_process(const LogitsArgs a, 
         each([&](int at, int) { slots.put(at, 0); });
         each([&](int at, int j) { slots.raise(at, (uint32_t)j + 1u); });
         each([&](int at, int j) {
-            if (slots.get(at) == (uint32_t)j + 1u && !(mr && !((mr[at >> 5] >> (at & 31)) & 1u)))
+            if (slots.get(at) == (uint32_t)j + 1u && (!mr || allowed(at)))
                 o[at] = __fadd_rn(o[at], vals[j]);
         });
     }
@@ -288,7 +378,7 @@ luce_status launch_logits(const LogitsArgs &a, int R, int stretch, cudaStream_t 
 {
     static luce_host::SmemLimit limit;
     auto kern = k_logits_process<TL, VEC, S16>;
-    const size_t smem = a.hist || a.nbias ? ((size_t)stretch * (S16 ? 2 : 4) + 15) / 16 * 16 : 0;
+    const size_t smem = a.hist || a.nbias ? ((size_t)(stretch + 2 * VEC) * (S16 ? 2 : 4) + 15) / 16 * 16 : 0;
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
@@ -309,10 +399,11 @@ template <typename TL> luce_status run_logits(const LogitsArgs &a, int R, cudaSt
     const int64_t fill = std::max<int64_t>(1, 2 * luce_host::sm_count() / R);
     const int64_t n = std::max((a.V + most - 1) / most, std::min(fill, (a.V + 511) / 512));
     const int stretch = (int)(((a.V + n - 1) / n + 31) & ~(int64_t)31);
-    const bool vec = luce_host::aligned(a.logits, 4 * sizeof(TL)) && luce_host::aligned(a.out, 16) &&
-                     (R == 1 || (a.ldl % 4 == 0 && a.ldo % 4 == 0));
-    if (vec)
-        return s16 ? launch_logits<TL, 4, true>(a, R, stretch, stream) : launch_logits<TL, 4, false>(a, R, stretch, stream);
+    // 16 bytes of logits at a step where a row of logits and of out lie at the same place between boundaries of V
+    constexpr int VEC = 16 / sizeof(TL);
+    auto place = [](const void *p, size_t es) { return (int64_t)(reinterpret_cast<uintptr_t>(p) / es); };
+    if ((place(a.logits, sizeof(TL)) - place(a.out, 4)) % VEC == 0 && (R == 1 || (a.ldl - a.ldo) % VEC == 0))
+        return s16 ? launch_logits<TL, VEC, true>(a, R, stretch, stream) : launch_logits<TL, VEC, false>(a, R, stretch, stream);
     return s16 ? launch_logits<TL, 1, true>(a, R, stretch, stream) : launch_logits<TL, 1, false>(a, R, stretch, stream);
 }
 
