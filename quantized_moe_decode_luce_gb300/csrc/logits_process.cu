@@ -159,7 +159,7 @@ __device__ __forceinline__ float penalized(float l, uint32_t c, float rep, float
 // checked by the host), so a stretch is gone through in steps that start at
 // boundaries, u = v + sh, whose first and last may be partial.
 template <typename TL, int VEC, bool S16>
-__global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch)
+__global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch, int mask_at)
 {
     extern __shared__ __align__(16) uint32_t slot_words[];
     const Slots<S16> slots{smem_addr(slot_words)}; // (slot u is that of token c0 + u - sh)
@@ -189,34 +189,26 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         else if (m >= 0)
             mr = a.mask + (size_t)m * a.ldm + (c0 >> 5); // (c0 is a multiple of 32)
     }
-    auto allowed = [&](int v) { return (mr[v >> 5] >> (v & 31)) & 1u; };
-    // a batch: the logits of NB steps and the mask bits of their tokens
+    // the mask's words behind the slots, one word of padding before them
+    uint32_t *mw = slot_words + mask_at;
+    if (mr)
+        for (int i = tid; i < (nc + 31) >> 5; i += THREADS)
+            mw[1 + i] = mr[i];
+    // a batch: the logits of NB steps
     struct Batch {
         In in[NB];
-        uint32_t bits[NB];
     };
     auto load = [&](Batch &b, int u0) {
 #pragma unroll
         for (int i = 0; i < NB; i++) {
             const int v = u0 + (tid + i * THREADS) * VEC - sh;
-            b.bits[i] = 0xffffffffu;
             if (v >= 0 && v + VEC <= nc) {
                 b.in[i] = *reinterpret_cast<const In *>(lr + v);
-                if (mr) {
-                    b.bits[i] = mr[v >> 5] >> (v & 31);
-                    if (VEC > 1 && sh != 0 && (v & 31) > 32 - VEC)
-                        b.bits[i] |= mr[(v >> 5) + 1] << (32 - (v & 31));
-                }
             } else if (VEC > 1 && v + VEC > 0 && v < nc) {
-                if (mr)
-                    b.bits[i] = 0;
 #pragma unroll
                 for (int e = 0; e < VEC; e++)
-                    if (v + e >= 0 && v + e < nc) {
+                    if (v + e >= 0 && v + e < nc)
                         b.in[i].e[e] = lr[v + e];
-                        if (mr)
-                            b.bits[i] |= allowed(v + e) << e;
-                    }
             }
         }
     };
@@ -299,8 +291,10 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         if (tid < 4 && rest < len && len > head)
             one(h[rest], rest);
         bad |= top >= a.V;
-        __syncthreads();
     }
+    __syncthreads();
+    const int32_t bias_id = tid < a.nbias ? a.bias_ids[(size_t)r * a.nbias + tid] : -1; // (the first of a thread's)
+    const float bias_val = tid < a.nbias ? a.bias_vals[(size_t)r * a.nbias + tid] : 0.0f;
     for (int u0 = 0; u0 < nc + sh; u0 += NB * THREADS * VEC) {
         Batch next;
         load(next, u0 + NB * THREADS * VEC);
@@ -325,11 +319,31 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
                         w[e] = penalized<S16>(w[e], c[e], rep, rinv, freq, pres);
                 }
             }
+            if (mr) {
+                const int at = (v >> 5) + 1;
+                const uint32_t bits = __funnelshift_r(mw[at], mw[at + 1], v & 31);
 #pragma unroll
-            for (int e = 0; e < VEC; e++)
-                if (!((cur.bits[i] >> e) & 1u))
-                    w[e] = -INFINITY;
-            if (v >= 0 && v + VEC <= nc) {
+                for (int e = 0; e < VEC; e++)
+                    if (!((bits >> e) & 1u))
+                        w[e] = -INFINITY;
+            }
+            const int vw = v - (tid & 31) * VEC; // the warp's first
+            if (VEC == 8 && vw >= 0 && vw + 32 * VEC <= nc) {
+                // neighbouring lanes swap halves, so that each store writes whole sectors
+                const bool odd = tid & 1;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float give = odd ? w[e] : w[e + VEC / 2];
+                    const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                    if (odd)
+                        w[e] = got;
+                    else
+                        w[e + VEC / 2] = got;
+                }
+                float *p = o + v + (odd ? -VEC / 2 : 0);
+                *reinterpret_cast<float4 *>(p) = make_float4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<float4 *>(p + VEC) = make_float4(w[VEC / 2], w[VEC / 2 + 1], w[VEC / 2 + 2], w[VEC / 2 + 3]);
+            } else if (v >= 0 && v + VEC <= nc) {
                 if constexpr (VEC == 1) {
                     o[v] = w[0];
                 } else {
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         const float *vals = a.bias_vals + (size_t)r * a.nbias;
         auto each = [&](auto &&f) {
             for (int j = tid; j < a.nbias; j += THREADS) {
-                const int32_t id = ids[j];
+                const int32_t id = j == tid ? bias_id : ids[j];
                 const uint32_t at = (uint32_t)(id - (int32_t)c0);
                 if (id >= 0 && at < (uint32_t)nc)
                     f((int)at, j);
@@ -365,8 +379,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         each([&](int at, int) { slots.put(at, 0); });
         each([&](int at, int j) { slots.raise(at, (uint32_t)j + 1u); });
         each([&](int at, int j) {
-            if (slots.get(at) == (uint32_t)j + 1u && (!mr || allowed(at)))
-                o[at] = __fadd_rn(o[at], vals[j]);
+            if (slots.get(at) == (uint32_t)j + 1u && (!mr || ((mw[1 + (at >> 5)] >> (at & 31)) & 1u)))
+                o[at] = __fadd_rn(o[at], j == tid ? bias_val : vals[j]);
         });
     }
     if (bad && blockIdx.x == 0)
@@ -378,13 +392,14 @@ luce_status launch_logits(const LogitsArgs &a, int R, int stretch, cudaStream_t 
 {
     static luce_host::SmemLimit limit;
     auto kern = k_logits_process<TL, VEC, S16>;
-    const size_t smem = a.hist || a.nbias ? ((size_t)(stretch + 2 * VEC) * (S16 ? 2 : 4) + 15) / 16 * 16 : 0;
+    const size_t slots = a.hist || a.nbias ? ((size_t)(stretch + 2 * VEC) * (S16 ? 2 : 4) + 15) / 16 * 16 : 0;
+    const size_t smem = slots + (a.mask ? ((size_t)stretch / 32 + 3) * 4 : 0);
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
     const luce_status st = luce_host::launch(kern, dim3((unsigned)((a.V + stretch - 1) / stretch), (unsigned)R),
-                                             dim3(THREADS), smem, stream, a, stretch);
+                                             dim3(THREADS), smem, stream, a, stretch, (int)(slots / 4));
     if (st != LUCE_OK)
         limit.forget();
     return st;
