@@ -287,36 +287,41 @@ _F32, _I8, _I32, _WORDS = frozenset({torch.float32}), frozenset({torch.int8}), f
     frozenset({torch.int32, torch.uint32})
 
 
-def _addr(t, dtypes, shape, dev, name) -> int:
-    """data_ptr of a contiguous CUDA tensor of one of `dtypes`, of `shape`, on device `dev`."""
+# torch's own call behind torch.cuda.current_stream(dev).cuda_stream, without
+# the Stream object around it (0.1 against 2.9 us, of a call of 9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _refuse(t, dtypes, shape, dev, name, rows=False):
+    """Raises what is wrong with `t`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have contiguous rows" if rows else f"{name} must be contiguous")
+
+
+def _addr(t, dtypes, shape, dev, name) -> int:
+    """data_ptr of a contiguous CUDA tensor of one of `dtypes`, of `shape`, on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, dtypes, shape, dev, name)
 
 
 def _rows(t, dtypes, shape, dev, name) -> tuple[int, int]:
     """(data_ptr, row stride) of a CUDA matrix whose rows are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    R, C = shape
-    step, inner = t.stride()
-    if C > 1 and inner != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), (step if R > 1 else C)
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        step, inner = t.stride()
+        if inner == 1 or shape[1] == 1:
+            return t.data_ptr(), (step if shape[0] > 1 else shape[1])
+    _refuse(t, dtypes, shape, dev, name, rows=True)
 
 
 def _matrix(t, name) -> tuple[int, int, int]:
@@ -335,14 +340,14 @@ def _call(fn: str, dev: int, stream, *args) -> None:
         with torch.cuda.device(dev):
             return _call(fn, dev, stream, *args)
     if stream is None:
-        s = torch.cuda.current_stream().cuda_stream
+        s = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device.index != dev:
             raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
         s = stream.cuda_stream
     else:
         s = int(stream)
-    status = getattr(lib(), fn)(*args, s)
+    status = getattr(_LIB or lib(), fn)(*args, s)
     if status != LUCE_OK:
         raise LuceError(fn, status)
 
