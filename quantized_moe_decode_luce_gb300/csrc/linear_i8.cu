@@ -22,12 +22,10 @@ using namespace luce;
 
 // The epilogue of every kernel of this file: four roundings to fp32 at most,
 // then the output type's, so that all of them give the same bits.
-__device__ __forceinline__ float epilogue(int isum, float xs, float ws, const float *bias, int n)
+__device__ __forceinline__ float epilogue(int isum, float xs, float ws, bool add, float bias)
 {
-    float v = __fmul_rn((float)isum, __fmul_rn(xs, ws));
-    if (bias)
-        v = __fadd_rn(v, bias[n]);
-    return v;
+    const float v = __fmul_rn((float)isum, __fmul_rn(xs, ws));
+    return add ? __fadd_rn(v, bias) : v;
 }
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
@@ -141,7 +139,7 @@ __global__ void __launch_bounds__(V_WARPS * 32)
             int sum = 0;
             for (int j = 0; j < wk; j++)
                 sum += part[g * wk + j][r * T + t];
-            store_out(out + (size_t)t * ldo + n, epilogue(sum, xs[t], ws[n], bias, (int)n));
+            store_out(out + (size_t)t * ldo + n, epilogue(sum, xs[t], ws[n], bias != nullptr, bias ? bias[n] : 0.0f));
         }
     }
 }
@@ -190,6 +188,7 @@ __global__ void __launch_bounds__(V_WARPS * 32)
 // the CTA's abort flag, the others leave at their next wait, copies and MMAs
 // in flight are waited for (bounded) and tensor memory is freed.
 constexpr int SK_MAX = 8;        // CTAs of one cluster at most
+constexpr int EARLY = 2;         // stages of the first tile requested ahead of the CTA's other preparations
 constexpr int KU = 128;          // K values of a unit: a TMA stage, what a group converts, and eight MMAs per half
 constexpr int CHUNK = 1024 / KU; // units whose sums fit fp32
 constexpr int BLOCK = 2;         // (half a chunk is two blocks)
@@ -234,7 +233,7 @@ struct TcArgs {
     int xbox;         // token rows of a box
     int nb, nh[2];    // tokens of a tile, and of its halves (multiples of 16, of 32 for a pair)
     int mt, tiles;    // channel tiles, tiles in all (channel tiles fastest)
-    int sk;           // CTA groups along K
+    int sk;           // CTA groups along K (a power of two)
 };
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
@@ -424,6 +423,8 @@ __device__ __forceinline__ uint32_t cluster_rank()
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -470,11 +471,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
     const int kg = (int)rank / CG;                      // place along K
     const uint16_t pair_mask = (uint16_t)(3u << leader);
 
-    if (tid == 0) {
-        for (int i = 0; i < NS; i++) {
-            mbar_init(&full[i], 1);
-            mbar_init(&rfree[i], 4);
+    // this CTA's tiles: cluster c takes tiles c, c + clusters, ...; its share of K
+    const int c0 = (int)(blockIdx.x / (unsigned)csize), cstep = (int)(gridDim.x / (unsigned)csize);
+    const int u0 = (int)((long long)a.units * kg / a.sk), u1 = (int)((long long)a.units * (kg + 1) / a.sk);
+    const int nu = u1 - u0; // (the host keeps sk <= units, so that nu >= 1)
+    auto w_row = [&](int tile) { return ((tile % a.mt) * CG + (int)pr) * RM; };
+    auto x_tile = [&](int tile) { return (tile / a.mt) * a.nb; };
+    const uint32_t bytes = (uint32_t)(C::RAW_W + HALVES * a.xbox * KU);
+    auto load_w = [&](uint32_t slot, int st, int wr) {
+        mbar_arrive_expect_tx(&full[slot], bytes);
+        tma_2d(sm + slot * C::RAW, &a.tw, (u0 + st) * KU, wr, &full[slot]);
+    };
+    auto load_x = [&](uint32_t slot, int st, int xt) {
+        tma_2d(sm + slot * C::RAW + C::RAW_W, &a.tx, (u0 + st) * KU, xt + (int)pr * (a.nh[0] / CG), &full[slot]);
+        if constexpr (HALVES == 2)
+            tma_2d(sm + slot * C::RAW + C::RAW_W + C::RAW_X, &a.tx, (u0 + st) * KU,
+                   xt + a.nh[0] + (int)pr * (a.nh[1] / CG), &full[slot]);
+    };
+    const int early = c0 < a.tiles ? min(nu, EARLY) : 0; // stages requested before anything else is set up
+
+    if (warp == TMA_WARP) {
+        // the first stages: their barriers are this CTA's own, and the weights do
+        // not depend on the previous kernel
+        if (elect_one()) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tw)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tx)) : "memory");
+            for (int i = 0; i < NS; i++)
+                mbar_init(&full[i], 1);
+            fence_mbar_init();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            for (int st = 0; st < early; st++)
+                load_w((uint32_t)st, st, w_row(c0));
         }
+        pdl_wait();
+        if (elect_one())
+            for (int st = 0; st < early; st++)
+                load_x((uint32_t)st, st, x_tile(c0));
+    }
+    if (tid == CONV_WARP0 * 32) {
+        for (int i = 0; i < NS; i++)
+            mbar_init(&rfree[i], 4);
         for (int i = 0; i < RB; i++) {
             mbar_init(&afull[i], 4 * CG);
             mbar_init(&sfree[i], 1);
@@ -500,43 +536,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
     }
     tc_fence_before();
     __syncthreads();
+    // the cluster's CTAs run and their barriers are initialised (made visible by
+    // fence.mbarrier_init) before any remote access: each role waits for that
+    // where it first needs it
     if (csize > 1)
-        cluster_sync_all(); // the peers' barriers are initialised before any remote arrival
+        cluster_arrive_relaxed();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-
-    // this CTA's tiles: cluster c takes tiles c, c + clusters, ...; its share of K
-    const int c0 = (int)(blockIdx.x / (unsigned)csize), cstep = (int)(gridDim.x / (unsigned)csize);
-    const int u0 = (int)((long long)a.units * kg / a.sk), u1 = (int)((long long)a.units * (kg + 1) / a.sk);
-    const int nu = u1 - u0; // (the host keeps sk <= units, so that nu >= 1)
-    auto w_row = [&](int tile) { return ((tile % a.mt) * CG + (int)pr) * RM; };
-    auto x_tile = [&](int tile) { return (tile / a.mt) * a.nb; };
 
     if (warp < CONV_WARP0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MISC));
         // Both loops run warp-wide, with uniform control flow, and elect one lane
         // where something is issued: the operands then stay in uniform registers.
         if (warp == TMA_WARP) {
-            const uint32_t bytes = (uint32_t)(C::RAW_W + HALVES * a.xbox * KU);
-            auto load_w = [&](uint32_t slot, int st, int wr) {
-                mbar_arrive_expect_tx(&full[slot], bytes);
-                tma_2d(sm + slot * C::RAW, &a.tw, (u0 + st) * KU, wr, &full[slot]);
-            };
-            auto load_x = [&](uint32_t slot, int st, int xt) {
-                tma_2d(sm + slot * C::RAW + C::RAW_W, &a.tx, (u0 + st) * KU, xt + (int)pr * (a.nh[0] / CG), &full[slot]);
-                if constexpr (HALVES == 2)
-                    tma_2d(sm + slot * C::RAW + C::RAW_W + C::RAW_X, &a.tx, (u0 + st) * KU,
-                           xt + a.nh[0] + (int)pr * (a.nh[1] / CG), &full[slot]);
-            };
-            // the first tile's weights do not depend on the previous kernel
-            const int early = c0 < a.tiles ? min(nu, NS) : 0;
-            if (elect_one())
-                for (int st = 0; st < early; st++)
-                    load_w((uint32_t)st, st, w_row(c0));
-            pdl_wait();
-            if (elect_one())
-                for (int st = 0; st < early; st++)
-                    load_x((uint32_t)st, st, x_tile(c0));
             Ring<NS> r;
             int issued = 0;
             bool ok = true;
@@ -559,6 +571,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                     wait_out(&full[g % NS], (uint32_t)(g / NS) & 1);
             }
         } else if (warp == MMA_WARP && pr == 0) {
+            if constexpr (CG == 2)
+                cluster_wait();
             constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(RM * CG >> 4) << 24); // fp16 x fp16 -> fp32
             const uint32_t idesc0 = IDESC | ((uint32_t)(a.nh[0] >> 3) << 17), idesc1 = IDESC | ((uint32_t)(a.nh[1] >> 3) << 17);
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -623,6 +637,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             wait_out(&drain, 0);
         }
         __syncwarp();
+        if (csize > 1 && !(CG == 2 && warp == MMA_WARP && pr == 0))
+            cluster_wait();
         if (a.sk > 1)
             cluster_sync_all(); // (the epilogue's exchange)
     } else if (warp < C::EPI_WARP0) {
@@ -639,8 +655,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
         const uint32_t x_d1 = (uint32_t)(xrow * 128 + (((2 * xc + 1) ^ xrow) << 4));
         const int mytiles = c0 < a.tiles ? (a.tiles - c0 + cstep - 1) / cstep : 0;
         const int total = mytiles * nu; // units of all tiles, in order
+        bool peers_ready = csize == 1;
         uint32_t rslot = (uint32_t)grp, rphase = 0, aslot = (uint32_t)grp, aphase = 1;
         for (int g = grp; g < total; g += GROUPS) {
+            // A parity names a phase only to who knows the one before it to be over.
+            // The slot's last stage belonged to this group only if GROUPS divides NS;
+            // else it may still be on its way (TMA tiles land out of order), so its
+            // conversion is waited for first.  (That of the stage before it is over:
+            // the stage this group converted last was requested after it.)
+            if (NS % GROUPS != 0 && !tc_wait_warp(&rfree[rslot], rphase ^ 1, abort_flag))
+                break;
             if (!tc_wait_warp(&full[rslot], rphase, abort_flag) || !tc_wait_warp(&sfree[aslot], aphase, abort_flag))
                 break;
             tc_fence_after();
@@ -679,6 +703,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
+            if (!peers_ready) {
+                cluster_wait();
+                peers_ready = true;
+            }
             if (lane == 0) {
                 arrive_on<CG>(&afull[aslot], leader);
                 mbar_arrive(&rfree[rslot]);
@@ -692,12 +720,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                 aphase ^= 1;
             }
         }
+        __syncwarp();
+        if (!peers_ready)
+            cluster_wait();
         if (a.sk > 1)
             cluster_sync_all();
     } else {
         // ------------------------------------------------------------ epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_EPI));
         pdl_wait();
+        if (csize > 1)
+            cluster_wait();
         const int q = warp & 3, eh = (warp - C::EPI_WARP0) >> 2;
         const int row = 32 * q + lane, col0 = eh * ECOLS;
         const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + D_COL + col0;
@@ -774,10 +807,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                         const float xl = c0 + lane < nt ? a.xs[t0 + c0 + lane] : 0.0f;
 #pragma unroll
                         for (int c = 0; c < 32; c++) {
-                            const float f = __fmul_rn(__shfl_sync(0xffffffffu, xl, c), wsn);
-                            float v = __fmul_rn((float)acc[h][c0 + c], f);
-                            if (add)
-                                v = __fadd_rn(v, bn);
+                            const float v = epilogue(acc[h][c0 + c], __shfl_sync(0xffffffffu, xl, c), wsn, add, bn);
                             if (live && c0 + c < nt)
                                 store_out(o, v);
                             o += a.ldo;
@@ -787,16 +817,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             }
         }
         if (a.sk > 1) {
-            // every group's sums are in shared memory: each group adds its share of the tile's tokens
+            // every group's sums are in shared memory: each group adds its share of
+            // the tile's tokens, a thread four channels (its scales are requested
+            // before the wait for the other groups)
+            constexpr int QUADS = RM / 4, STEP = EPI_WARPS * 32 / QUADS; // tokens at once
+            const int e0 = tid - C::EPI_WARP0 * 32, n = w_row(c0) + 4 * (e0 % QUADS), t0 = x_tile(c0);
+            const int nt = min(a.nb, a.T - t0);
+            float wsn[4], bn[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                wsn[e] = n + e < a.N ? a.ws[n + e] : 0.0f;
+                bn[e] = a.bias && n + e < a.N ? a.bias[n + e] : 0.0f;
+            }
+            int t = kg + (e0 / QUADS) * a.sk;
+            float xst = t < nt ? a.xs[t0 + t] : 0.0f;
             __syncwarp();
             cluster_sync_all();
-            const int n0 = w_row(c0), t0 = x_tile(c0);
-            const int nt = min(a.nb, a.T - t0);
-            constexpr int QUADS = RM / 4; // four channels to a thread
-            for (int i = tid - C::EPI_WARP0 * 32; i < ((nt - kg + a.sk - 1) / a.sk) * QUADS && ok; i += EPI_WARPS * 32) {
-                const int t = kg + (i / QUADS) * a.sk, n = 4 * (i % QUADS);
+            for (; t < nt && ok; t += STEP * a.sk) {
                 const int col = HALVES == 2 && t >= a.nh[0] ? C::DCOLS + t - a.nh[0] : t;
-                const uint32_t at = sm + (uint32_t)(col * PITCH + n) * 4;
+                const uint32_t at = sm + (uint32_t)(col * PITCH + 4 * (e0 % QUADS)) * 4;
                 int4 v[SK_MAX / CG];
 #pragma unroll
                 for (int g = 0; g < SK_MAX / CG; g++) { // (all in flight together)
@@ -812,7 +851,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                                      : "memory");
                     }
                 }
-                const float xst = a.xs[t0 + t];
+                const float xnow = xst;
+                if (t + STEP * a.sk < nt)
+                    xst = a.xs[t0 + t + STEP * a.sk];
                 int s[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int g = 0; g < SK_MAX / CG; g++) {
@@ -821,11 +862,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                     s[2] += v[g].z;
                     s[3] += v[g].w;
                 }
-                TO *o = static_cast<TO *>(a.out) + (size_t)(t0 + t) * a.ldo + n0 + n;
+                TO *o = static_cast<TO *>(a.out) + (size_t)(t0 + t) * a.ldo + n;
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (n0 + n + e < a.N)
-                        store_out(o + e, epilogue(s[e], xst, a.ws[n0 + n + e], a.bias, n0 + n + e));
+                    if (n + e < a.N)
+                        store_out(o + e, epilogue(s[e], xnow, wsn[e], a.bias != nullptr, bn[e]));
             }
         }
     }

@@ -235,6 +235,29 @@ def test_linear_into_a_slice_of_wider_rows(T):
     check_linear(T, 128, 512, f16, gap=128)
 
 
+@pytest.mark.parametrize("T", [5, 40, 100, 300])
+def test_linear_many_tiles_and_launches(T):
+    # several tiles per CTA, launches back to back: stages, slots and accumulators
+    # go round many times (weights from memory, whose tiles land in any order)
+    N, K, n = 60000, 2048, 4
+    g = torch.Generator(device="cuda").manual_seed(T)
+    wq = torch.empty((n, N, K), dtype=torch.int8, device="cuda").random_(-127, 128, generator=g)
+    xq = codes(T, K, 3).cuda()
+    xs, ws = torch.rand(T, generator=gen(5)).cuda(), torch.rand(N, generator=gen(6)).cuda()
+    out = torch.empty((n, T, N), device="cuda")
+    for r in range(20):
+        for i in range(n):
+            B.luce_linear_i8(xq, xs, wq[i], ws, None, out[i])
+        if r in (0, 19):
+            first = out.clone() if r == 0 else first
+    torch.cuda.synchronize()
+    assert torch.equal(out, first)
+    for i in range(n):
+        at = torch.randint(0, N, (200,), generator=gen(i)).cuda()
+        at[:4] = torch.tensor([0, 127, 128, N - 1])
+        same(out[i][:, at], O.linear_i8(xq.cpu(), xs.cpu(), wq[i][at].cpu(), ws[at].cpu(), None, f32))
+
+
 def test_linear_rows_do_not_depend_on_the_batch():
     N, K, T = 700, 2048, 300
     xq, wq = codes(T, K, 3), codes(N, K, 4)
