@@ -10,10 +10,13 @@ library has not been built, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
+from .build import CALL as CALL_PATH
 from .build import LIB as LIB_PATH
 
 LUCE_OK = 0
@@ -28,6 +31,7 @@ LUCE_FAULT_TIMEOUT = 0x2
 LUCE_FAULT_DESYNC = 0x4
 
 _LIB = None
+_fast = None  # the call module, loaded with the library
 
 
 class LuceError(RuntimeError):
@@ -86,8 +90,22 @@ def lib() -> ctypes.CDLL:
         L.luce_get_fault.restype = ctypes.c_int
         L.luce_version.argtypes = []
         L.luce_version.restype = ctypes.c_int
+        _load_call_module(L)
         _LIB = L
     return _LIB
+
+
+def _load_call_module(L) -> None:
+    """The module that makes the common calls of the int8 head without Python in between."""
+    global _fast
+    if not os.path.exists(CALL_PATH):
+        raise RuntimeError(f"{CALL_PATH} is not built: run quantized_moe_decode_luce_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("luce_call", CALL_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("luce_call", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+        "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process")))
+    _fast = module
 
 
 def status_string(status: int) -> str:
@@ -280,7 +298,9 @@ def luce_moe_down_combine_q4k(w_down, ws_down, hq, ids, weights, E: int, H: int,
 
 # ----------------------------------------------------------------------------- int8 decode head
 # These entry points check shapes as well, and run on the device that holds
-# their tensors, on its current stream unless one is given.
+# their tensors, on its current stream unless one is given.  The common call
+# (that stream, the current device, nothing to object to) goes through the call
+# module in one step; it leaves every other call (-1) to the code here.
 _DTYPE = {torch.float32: LUCE_F32, torch.bfloat16: LUCE_BF16, torch.float16: LUCE_F16}
 _FLOATS = frozenset(_DTYPE)
 _F32, _I8, _I32, _WORDS = frozenset({torch.float32}), frozenset({torch.int8}), frozenset({torch.int32}), \
@@ -354,6 +374,10 @@ def _call(fn: str, dev: int, stream, *args) -> None:
 
 def luce_quantize_i8(x, q, scale, stream=None) -> None:
     """x [T, H] fp32, bf16 or fp16 -> q [T, H] int8, scale [T] fp32 (q * scale stands for x)."""
+    if stream is None and _fast is not None:
+        status = _fast.quantize_i8(x, q, scale)
+        if status >= 0:
+            return _check("luce_quantize_i8", status)
     T, H, dev = _matrix(x, "x")
     _call("luce_quantize_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"), _DTYPE[x.dtype], T, H,
           _addr(q, _I8, (T, H), dev, "q"), _addr(scale, _F32, (T,), dev, "scale"))
@@ -361,6 +385,10 @@ def luce_quantize_i8(x, q, scale, stream=None) -> None:
 
 def luce_rmsnorm_i8(x, gamma, eps: float, q, scale, stream=None) -> None:
     """x [T, H], gamma [H] fp32 -> the int8 codes and scales of the RMS norm of x."""
+    if stream is None and _fast is not None:
+        status = _fast.rmsnorm_i8(x, gamma, eps, q, scale)
+        if status >= 0:
+            return _check("luce_rmsnorm_i8", status)
     T, H, dev = _matrix(x, "x")
     _call("luce_rmsnorm_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"), _DTYPE[x.dtype],
           _addr(gamma, _F32, (H,), dev, "gamma"), eps, T, H, _addr(q, _I8, (T, H), dev, "q"),
@@ -370,6 +398,10 @@ def luce_rmsnorm_i8(x, gamma, eps: float, q, scale, stream=None) -> None:
 def luce_add_rmsnorm_i8(x, residual, x_sum, gamma, eps: float, q, scale, stream=None) -> None:
     """x, residual [T, H] of one type -> x_sum = x + residual (or None; may be x or residual itself),
     then luce_rmsnorm_i8 of the sum."""
+    if stream is None and _fast is not None:
+        status = _fast.add_rmsnorm_i8(x, residual, x_sum, gamma, eps, q, scale)
+        if status >= 0:
+            return _check("luce_add_rmsnorm_i8", status)
     T, H, dev = _matrix(x, "x")
     own = (x.dtype,)
     _call("luce_add_rmsnorm_i8", dev, stream, _addr(x, _FLOATS, (T, H), dev, "x"),
@@ -382,6 +414,10 @@ def luce_add_rmsnorm_i8(x, residual, x_sum, gamma, eps: float, q, scale, stream=
 def luce_linear_i8(xq, x_scale, wq, w_scale, bias, out, stream=None) -> None:
     """xq [T, K], wq [N, K] int8, x_scale [T], w_scale [N], bias [N] (or None) fp32 -> out [T, N]
     fp32, bf16 or fp16 (its rows may be apart: a slice of wider rows)."""
+    if stream is None and _fast is not None:
+        status = _fast.linear_i8(xq, x_scale, wq, w_scale, bias, out)
+        if status >= 0:
+            return _check("luce_linear_i8", status)
     T, K, dev = _matrix(xq, "xq")
     N = _matrix(wq, "wq")[0]
     o, ldo = _rows(out, _FLOATS, (T, N), dev, "out")
@@ -398,6 +434,11 @@ def luce_logits_process(logits, out, hist=None, hist_len=None, prompt_len=None, 
     tokens of hist [R, L] (hist_len [R]; prompt_len [R] of them the prompt's), biases
     bias_ids / bias_vals [R, n], masks [M, words] of 32 tokens a word (mask_rows [R], or row r
     takes mask r).  Each group may be left out."""
+    if stream is None and _fast is not None:
+        status = _fast.logits_process(logits, out, hist, hist_len, prompt_len, repetition, frequency, presence,
+                                      bias_ids, bias_vals, mask, mask_rows)
+        if status >= 0:
+            return _check("luce_logits_process", status)
     R, V, dev = _matrix(logits, "logits")
     lp, ldl = _rows(logits, _FLOATS, (R, V), dev, "logits")
     op, ldo = _rows(out, _F32, (R, V), dev, "out")

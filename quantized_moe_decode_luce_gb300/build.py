@@ -1,4 +1,5 @@
-"""Build libluce_moe.so in-tree with nvcc for sm_103a (GB300).
+"""Build libluce_moe.so in-tree with nvcc for sm_103a (GB300), and beside it the
+module that makes the common calls of the int8 head (g++, torch's headers).
 
 The translation units are compiled in parallel and linked into
 ``quantized_moe_decode_luce_gb300/lib/libluce_moe.so``.  Release flags only:
@@ -20,6 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libluce_moe.so")
 SOURCES = ["small_ops.cu", "glu_pair.cu", "down_combine.cu", "moe_layer.cu", "moe_layer_flat.cu", "edge_ops.cu",
            "q4k_ops.cu", "moe_tc.cu", "rows_i8.cu", "linear_i8.cu", "logits_process.cu"]
+CALL = os.path.join(LIBDIR, "luce_call.so")
+CALL_SOURCE = "fastcall.cpp"
 HEADERS = ["common.cuh", os.path.join("..", "..", "include", "luce_moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-Xptxas", "-warn-spills"]
@@ -39,6 +42,20 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def call_command(source: str, target: str) -> list[str]:
+    """The g++ command for the call module, against this Python and this torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    lib = os.path.join(root, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(root, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), source,
+            "-o", target, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if stale) and return the path of libluce_moe.so."""
     os.makedirs(LIBDIR, exist_ok=True)
@@ -53,16 +70,24 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + headers + [__file__]):
             jobs.append([nvcc(), *ARCH, *NVCC_FLAGS, "-c", s, "-o", o])
 
+    call = os.path.join(CSRC, CALL_SOURCE)
+    tmp_call = CALL + f".tmp{os.getpid()}"
+    new_call = force or _stale(CALL, [call, headers[-1], __file__])
+    if new_call:
+        jobs.append(call_command(call, tmp_call))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compilation failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose:
             sys.stderr.write(r.stderr)
         return r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, jobs))
+    if new_call:
+        os.replace(tmp_call, CALL)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])

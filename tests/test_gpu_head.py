@@ -534,6 +534,61 @@ def test_calls_on_a_given_stream_and_under_programmatic_launch(T):
     same(l, O.logits_process(ref, **{k: v.cpu() for k, v in kw.items()}))
 
 
+def test_both_ways_of_calling_are_one(monkeypatch):
+    # the call module takes the common call, the Python code the others: the same results
+    x, gamma = rows_input(5, 200, bf16, 1).cuda(), (torch.rand(200, generator=gen(2)) + 0.5).cuda()
+    res = rows_input(5, 200, bf16, 3).cuda()
+    wq, ws = codes(64, 208, 4).cuda(), torch.rand(64, generator=gen(5)).cuda()
+    xq, xs = codes(5, 208, 6).cuda(), torch.rand(5, generator=gen(7)).cuda()
+    c = {k: v.cuda() for k, v in logits_case(5, 64, hist=9, bias=3, mask=True).items()}
+    logits = c.pop("logits")
+
+    def everything():
+        new = lambda *s, dt=f32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+        outs = [new(5, 200, dt=torch.int8), new(5), new(5, 200, dt=torch.int8), new(5), new(5, 200, dt=bf16),
+                new(5, 200, dt=torch.int8), new(5), new(5, 64), new(5, 70, dt=f16)[:, :64], new(5, 64), new(5, 64)]
+        B.luce_quantize_i8(x, outs[0], outs[1])
+        B.luce_rmsnorm_i8(x, gamma, 1e-5, outs[2], outs[3])
+        B.luce_add_rmsnorm_i8(x, res, outs[4], gamma, 1e-5, outs[5], outs[6])
+        B.luce_linear_i8(xq, xs, wq, ws, None, outs[7])
+        B.luce_linear_i8(xq, xs, wq, ws, ws, outs[8])
+        B.luce_logits_process(logits, outs[9], **c)
+        B.luce_logits_process(logits, outs[10])
+        torch.cuda.synchronize()
+        return outs
+
+    calls = []
+    fast = B._fast
+    assert fast is not None
+
+    class Counting:
+        def __getattr__(self, name):
+            def call(*a):
+                calls.append(getattr(fast, name)(*a))
+                return calls[-1]
+            return call
+
+    monkeypatch.setattr(B, "_fast", Counting())
+    first = everything()
+    assert calls == [0] * 7  # every one of these is a common call
+    monkeypatch.setattr(B, "_fast", None)
+    for a, b in zip(first, everything()):
+        same(a, b)
+    monkeypatch.setattr(B, "_fast", fast)
+    # what the module leaves alone: other kinds, shapes and layouts
+    s = torch.zeros(5, device="cuda")
+    q = torch.zeros((5, 200), dtype=torch.int8, device="cuda")
+    assert fast.quantize_i8(x, q, s[:4]) == -1 and fast.quantize_i8(x.cpu(), q, s) == -1
+    assert fast.quantize_i8(x.t(), q, s) == -1 and fast.quantize_i8(x, q.float(), s) == -1
+    assert fast.quantize_i8(None, q, s) == -1 and fast.quantize_i8(x, q) == -1
+    assert fast.rmsnorm_i8(x, gamma, 1, q, s) == -1 and fast.rmsnorm_i8(x, gamma[:9], 1e-5, q, s) == -1
+    assert fast.linear_i8(xq, xs, wq[:, :192], ws, None, first[7]) == -1
+    assert fast.logits_process(logits, logits, *[None] * 9, s.int()) == -1
+    assert fast.rmsnorm_i8(x, gamma, -1.0, q, s) == B.LUCE_ERR_INVALID_ARG  # the library's own refusals come through
+    with pytest.raises(B.LuceError):
+        B.luce_rmsnorm_i8(x, gamma, -1.0, q, s)
+
+
 def test_bindings_check_shapes():
     x = torch.zeros((4, 64), device="cuda")
     q, s = torch.zeros((4, 64), dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
