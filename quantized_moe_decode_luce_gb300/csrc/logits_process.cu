@@ -48,7 +48,10 @@ struct LogitsArgs {
 };
 
 constexpr int THREADS = 512;
-constexpr int NB = 2; // steps of a thread in flight, and as many requested behind them
+// steps of a thread in flight, and as many requested behind them (a step of
+// 16-bit logits is eight tokens, of fp32 four; 256 rows: 90 and 49 us, with two
+// and one 95 and 59)
+template <typename TL> constexpr int NB_OF = sizeof(TL) == 4 ? 2 : 1;
 constexpr int HB = 4; // history loads of a thread in flight (four tokens each)
 
 // What a slot of shared memory holds for its token: twice the number of
@@ -131,27 +134,37 @@ template <bool S16> struct Slots {
     }
 };
 
-// l / rep, correctly rounded, from rinv = fl(1 / rep): Markstein's sequence, a
-// product, its exact remainder and one correction.  Results outside the range
-// where no intermediate can over- or underflow (zero, infinities and NaNs
-// among them) divide.
-__device__ __forceinline__ float divided(float l, float rep, float rinv)
+// The penalties of N tokens whose slots hold c, without a branch in the common
+// case.  l / rep, correctly rounded, comes from rinv = fl(1 / rep) by Markstein's
+// sequence: a product, its exact remainder and one correction.  Where a result
+// lies outside the range in which no intermediate can over- or underflow
+// (zero, infinities and NaNs among them), all N divide.
+template <bool S16, int N>
+__device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], float rep, float rinv, float freq,
+                                         float pres)
 {
-    const float q = __fmul_rn(l, rinv);
-    const float s = fmaf(fmaf(-q, rep, l), rinv, q);
-    const float m = fabsf(s);
-    return m > 1e-25f && m < 1e25f ? s : __fdiv_rn(l, rep);
-}
-
-template <bool S16>
-__device__ __forceinline__ float penalized(float l, uint32_t c, float rep, float rinv, float freq, float pres)
-{
-    const float p = l > 0.0f ? divided(l, rep, rinv) : __fmul_rn(l, rep);
-    const uint32_t k = c >> 1;
-    // (at most 32,767: exact in the low bits of 2^23)
-    const float f = S16 ? __fsub_rn(__uint_as_float(0x4b000000u | k), 8388608.0f) : (float)k;
-    const float g = k ? __fsub_rn(p, __fadd_rn(__fmul_rn(f, freq), pres)) : p;
-    return c ? g : l;
+    float p[N];
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+        const float l = w[e], q = __fmul_rn(l, rinv);
+        const float s = fmaf(fmaf(-q, rep, l), rinv, q), m = fabsf(s);
+        p[e] = l > 0.0f ? s : __fmul_rn(l, rep);
+        odd |= l > 0.0f && !(m > 1e-25f && m < 1e25f);
+    }
+    if (odd) {
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            p[e] = w[e] > 0.0f ? __fdiv_rn(w[e], rep) : __fmul_rn(w[e], rep);
+    }
+#pragma unroll
+    for (int e = 0; e < N; e++) {
+        const uint32_t k = c[e] >> 1;
+        // (at most 32,767: exact in the low bits of 2^23)
+        const float f = S16 ? __fsub_rn(__uint_as_float(0x4b000000u | k), 8388608.0f) : (float)k;
+        const float g = __fsub_rn(p[e], __fadd_rn(__fmul_rn(f, freq), pres));
+        w[e] = k ? g : c[e] ? p[e] : w[e];
+    }
 }
 
 // VEC logits a step and thread: 16 bytes, or one.  A row may start `sh`
@@ -162,6 +175,7 @@ template <typename TL, int VEC, bool S16>
 __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch, int mask_at)
 {
     extern __shared__ __align__(16) uint32_t slot_words[];
+    constexpr int NB = NB_OF<TL>;
     const Slots<S16> slots{smem_addr(slot_words)}; // (slot u is that of token c0 + u - sh)
     const int r = blockIdx.y, tid = threadIdx.x;
     const int64_t c0 = (int64_t)blockIdx.x * stretch;
@@ -313,11 +327,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
 #pragma unroll
                 for (int e = 0; e < VEC; e++)
                     any |= c[e];
-                if (any) {
-#pragma unroll
-                    for (int e = 0; e < VEC; e++)
-                        w[e] = penalized<S16>(w[e], c[e], rep, rinv, freq, pres);
-                }
+                if (any)
+                    penalize<S16, VEC>(w, c, rep, rinv, freq, pres);
             }
             if (mr) {
                 const int at = (v >> 5) + 1;
