@@ -59,7 +59,8 @@ constexpr int HB = 4; // history loads of a thread in flight (four tokens each)
 // (the two never touch each other's bits, so their order does not matter).
 // Sixteen bits are enough while a row has at most 32,767 tokens.
 template <bool S16> struct Slots {
-    uint32_t base; // shared address
+    uint32_t base;   // shared address
+    uint32_t *words; // the same
     __device__ __forceinline__ uint32_t get(int at) const
     {
         uint32_t v;
@@ -95,12 +96,11 @@ template <bool S16> struct Slots {
     }
     __device__ __forceinline__ void raise(int at, uint32_t v) const // the larger of the slot and v
     {
-        extern __shared__ __align__(16) uint32_t slot_words[];
         if (!S16) {
-            atomicMax(slot_words + at, v);
+            atomicMax(words + at, v);
             return;
         }
-        uint32_t *p = slot_words + (at >> 1), old = *p;
+        uint32_t *p = words + (at >> 1), old = *p;
         const int sh = 16 * (at & 1);
         while (((old >> sh) & 0xffffu) < v) {
             const uint32_t seen = atomicCAS(p, old, (old & ~(0xffffu << sh)) | v << sh);
@@ -172,11 +172,12 @@ __device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], 
 // checked by the host), so a stretch is gone through in steps that start at
 // boundaries, u = v + sh, whose first and last may be partial.
 template <typename TL, int VEC, bool S16>
-__global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch, int mask_at)
+__global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch, int mask_at, int bias_at)
 {
     extern __shared__ __align__(16) uint32_t slot_words[];
     constexpr int NB = NB_OF<TL>;
-    const Slots<S16> slots{smem_addr(slot_words)}; // (slot u is that of token c0 + u - sh)
+    const Slots<S16> slots{smem_addr(slot_words), slot_words}; // (slot u is that of token c0 + u - sh)
+    const Slots<S16> places{smem_addr(slot_words + bias_at), slot_words + bias_at}; // a token's last bias entry, from one on; if bias_at > 0
     const int r = blockIdx.y, tid = threadIdx.x;
     const int64_t c0 = (int64_t)blockIdx.x * stretch;
     const int nc = (int)min((int64_t)stretch, a.V - c0);
@@ -186,11 +187,13 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     float *o = a.out + (size_t)r * a.ldo + c0;
     const int sh = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(o) >> 2) & (VEC - 1));
     // slots to zero (they do not depend on the previous kernel)
-    if (a.hist) {
-        const int words = S16 ? (nc + sh + 1) / 2 : nc + sh;
+    const int words = S16 ? (nc + sh + 1) / 2 : nc + sh;
+    if (a.hist)
         for (int i = tid; 4 * i < words; i += THREADS)
             reinterpret_cast<uint4 *>(slot_words)[i] = make_uint4(0, 0, 0, 0);
-    }
+    if (bias_at)
+        for (int i = tid; 4 * i < words; i += THREADS)
+            reinterpret_cast<uint4 *>(places.words)[i] = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_trigger();
     const TL *lr = static_cast<const TL *>(a.logits) + (size_t)r * a.ldl + c0;
@@ -229,6 +232,24 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     Batch cur;
     load(cur, 0);
     float rep = 1.0f, rinv = 1.0f, freq = 0.0f, pres = 0.0f;
+    const int32_t *ids = a.bias_ids + (size_t)r * a.nbias;
+    const float *vals = a.bias_vals + (size_t)r * a.nbias;
+    const int32_t bias_id = tid < a.nbias ? ids[tid] : -1; // (the first of a thread's)
+    const float bias_val = tid < a.nbias ? vals[tid] : 0.0f;
+    // f(u, j) for the bias entries j whose token lies in the stretch
+    auto biases = [&](auto &&f) {
+        for (int j = tid; j < a.nbias; j += THREADS) {
+            const int32_t id = j == tid ? bias_id : ids[j];
+            const uint32_t at = (uint32_t)(id - (int32_t)c0);
+            if (at < (uint32_t)nc)
+                f((int)at, j);
+            bad |= id >= a.V;
+        }
+    };
+    auto find_places = [&] {
+        if (bias_at)
+            biases([&](int at, int j) { places.raise(at + sh, (uint32_t)j + 1u); });
+    };
     if (a.hist) {
         const int32_t *h = a.hist + (size_t)r * a.ldh;
         // tokens before a 16-byte boundary, quads from there, and a rest; the first
@@ -273,6 +294,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
                 made(id);
         };
         __syncthreads();
+        find_places();
         if (tid < min(head, len))
             one(h[tid], tid);
         const int quads = len > head ? (len - head) >> 2 : 0;
@@ -305,10 +327,11 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         if (tid < 4 && rest < len && len > head)
             one(h[rest], rest);
         bad |= top >= a.V;
+    } else if (bias_at) {
+        __syncthreads();
+        find_places();
     }
     __syncthreads();
-    const int32_t bias_id = tid < a.nbias ? a.bias_ids[(size_t)r * a.nbias + tid] : -1; // (the first of a thread's)
-    const float bias_val = tid < a.nbias ? a.bias_vals[(size_t)r * a.nbias + tid] : 0.0f;
     for (int u0 = 0; u0 < nc + sh; u0 += NB * THREADS * VEC) {
         Batch next;
         load(next, u0 + NB * THREADS * VEC);
@@ -329,6 +352,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
                     any |= c[e];
                 if (any)
                     penalize<S16, VEC>(w, c, rep, rinv, freq, pres);
+            }
+            if (bias_at) {
+                uint32_t j[VEC];
+                places.template get_n<VEC>(u, j);
+#pragma unroll
+                for (int e = 0; e < VEC; e++)
+                    if (j[e])
+                        w[e] = __fadd_rn(w[e], vals[j[e] - 1]);
             }
             if (mr) {
                 const int at = (v >> 5) + 1;
@@ -371,25 +402,15 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         }
         cur = next;
     }
-    if (a.nbias) {
-        // the slots now find each id's last entry, which adds its bias to the
-        // value stored above unless the token is masked
-        const int32_t *ids = a.bias_ids + (size_t)r * a.nbias;
-        const float *vals = a.bias_vals + (size_t)r * a.nbias;
-        auto each = [&](auto &&f) {
-            for (int j = tid; j < a.nbias; j += THREADS) {
-                const int32_t id = j == tid ? bias_id : ids[j];
-                const uint32_t at = (uint32_t)(id - (int32_t)c0);
-                if (id >= 0 && at < (uint32_t)nc)
-                    f((int)at, j);
-                bad |= id >= a.V;
-            }
-            __syncthreads();
-        };
+    if (a.nbias && !bias_at) {
+        // no room for the places: the slots now find each id's last entry, which
+        // adds its bias to the value stored above unless the token is masked
         __syncthreads();
-        each([&](int at, int) { slots.put(at, 0); });
-        each([&](int at, int j) { slots.raise(at, (uint32_t)j + 1u); });
-        each([&](int at, int j) {
+        biases([&](int at, int) { slots.put(at, 0); });
+        __syncthreads();
+        biases([&](int at, int j) { slots.raise(at, (uint32_t)j + 1u); });
+        __syncthreads();
+        biases([&](int at, int j) {
             if (slots.get(at) == (uint32_t)j + 1u && (!mr || ((mw[1 + (at >> 5)] >> (at & 31)) & 1u)))
                 o[at] = __fadd_rn(o[at], j == tid ? bias_val : vals[j]);
         });
@@ -403,14 +424,19 @@ luce_status launch_logits(const LogitsArgs &a, int R, int stretch, cudaStream_t 
 {
     static luce_host::SmemLimit limit;
     auto kern = k_logits_process<TL, VEC, S16>;
-    const size_t slots = a.hist || a.nbias ? ((size_t)(stretch + 2 * VEC) * (S16 ? 2 : 4) + 15) / 16 * 16 : 0;
-    const size_t smem = slots + (a.mask ? ((size_t)stretch / 32 + 3) * 4 : 0);
+    const size_t table = ((size_t)(stretch + 2 * VEC) * (S16 ? 2 : 4) + 15) / 16 * 16;
+    const size_t masks = a.mask ? ((size_t)stretch / 32 + 3) * 4 : 0;
+    // slots; the biases' places beside them while two CTAs still fit an SM; the mask's words
+    const bool beside = a.nbias && 2 * table + masks <= 110 * 1024;
+    const size_t bias_at = beside ? table : 0, mask_at = bias_at + (a.hist || a.nbias ? table : 0);
+    const size_t smem = mask_at + masks;
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
     const luce_status st = luce_host::launch(kern, dim3((unsigned)((a.V + stretch - 1) / stretch), (unsigned)R),
-                                             dim3(THREADS), smem, stream, a, stretch, (int)(slots / 4));
+                                             dim3(THREADS), smem, stream, a, stretch, (int)(mask_at / 4),
+                                             (int)(bias_at / 4));
     if (st != LUCE_OK)
         limit.forget();
     return st;
@@ -423,7 +449,7 @@ template <typename TL> luce_status run_logits(const LogitsArgs &a, int R, cudaSt
     // while that leaves SMs idle, 512 tokens at least, of one length
     const int64_t most = (size_t)100 * 1024 / (s16 ? 2 : 4);
     const int64_t fill = std::max<int64_t>(1, 2 * luce_host::sm_count() / R);
-    const int64_t n = std::max((a.V + most - 1) / most, std::min(fill, (a.V + 511) / 512));
+    const int64_t n = std::max((a.V + most - 1) / most, std::min(fill, (a.V + 1023) / 1024));
     const int stretch = (int)(((a.V + n - 1) / n + 31) & ~(int64_t)31);
     // 16 bytes of logits at a step where a row of logits and of out lie at the same place between boundaries of V
     constexpr int VEC = 16 / sizeof(TL);
