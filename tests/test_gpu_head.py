@@ -401,6 +401,37 @@ def test_logits_one_token_again_and_again(V, hist):
     check_logits(c)
 
 
+@pytest.mark.parametrize("hist", [32767, 32768, 40000])
+@pytest.mark.parametrize("V", [200, 60001])
+def test_logits_the_longest_histories_of_either_slot_width(V, hist):
+    # sixteen-bit slots end at 32,767 tokens: all of them one token, and all others
+    c = logits_case(3, V, hist=hist, prompt=0, bias=2)
+    c["hist"][0] = V - 1
+    c["hist"][1] = torch.arange(hist) % V
+    c["hist_len"][:] = hist
+    check_logits(c)
+    c["prompt_len"] = torch.tensor([hist, hist - 1, hist + 5], dtype=torch.int32)
+    check_logits(c)
+
+
+@pytest.mark.parametrize("V,nbias,hist", [(300, 2000, 5), (50000, 2000, None), (140000, 40, 9), (3000, 65534, 5), (3000, 65535, None)])
+def test_logits_many_biases_and_no_room_for_their_places(V, nbias, hist):
+    # ids many times over: the last entry counts, in either slot width, beside the counts or behind them
+    R = 320 if V == 140000 else 2
+    check_logits(logits_case(R, V, bf16 if V == 140000 else f32, hist=hist, prompt=2, bias=nbias, mask=True))
+
+
+def test_logits_repetition_of_extreme_values():
+    V = 64
+    l = torch.tensor([1e-44, 3e-39, 1.2e-38, 3e38, 1.0, -1e-44, -3e38, 7.0] * 8)
+    for rep in (1e-30, 0.3, 3.0, 1e30, 0.0, math.inf):
+        c = logits_case(1, V, hist=V, prompt=V)
+        c["logits"][0], c["hist"][0] = l, torch.arange(V, dtype=torch.int32)
+        c["hist_len"][:] = V
+        c["repetition"] = torch.tensor([rep])
+        check_logits({k: v for k, v in c.items() if k not in ("frequency", "presence")})
+
+
 @pytest.mark.allow_fault
 def test_logits_ids_out_of_range_are_skipped_and_raise_the_fault_bit():
     V = 5000
@@ -502,6 +533,23 @@ def test_head_captured_and_replayed_on_two_streams():
     for hd, (l, i) in zip(heads, want):
         same(hd.logits, l)
         assert torch.equal(hd.argmax.idx, i)
+
+
+@pytest.mark.parametrize("T", [3, 20, 100, 300])
+def test_linear_captured_with_split_products(T):
+    # clusters that split K, captured without a warm-up call of this shape and replayed
+    xq, wq = codes(T, 4096, 1).cuda(), codes(384, 4096, 2).cuda()
+    xs, ws = torch.rand(T, generator=gen(3)).cuda(), torch.rand(384, generator=gen(4)).cuda()
+    out = torch.zeros((T, 384), dtype=f16, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.luce_linear_i8(xq, xs, wq, ws, None, out)
+    ref = O.linear_i8(xq.cpu(), xs.cpu(), wq.cpu(), ws.cpu(), None, f16)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        same(out, ref)
 
 
 @pytest.mark.parametrize("T", [1, 20, 300])
