@@ -57,7 +57,9 @@ constexpr int HB = 4; // history loads of a thread in flight (four tokens each)
 // What a slot of shared memory holds for its token: twice the number of
 // generated occurrences, the low bit set if the token is among the prompt's
 // (the two never touch each other's bits, so their order does not matter).
-// Sixteen bits are enough while a row has at most 32,767 tokens.
+// Sixteen bits hold 32,767 occurrences: enough for rows of up to SHORT tokens,
+// whose last token is kept apart when all of them were generated.
+constexpr int SHORT = 32768;
 template <bool S16> struct Slots {
     uint32_t base;   // shared address
     uint32_t *words; // the same
@@ -160,7 +162,7 @@ __device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], 
 #pragma unroll
     for (int e = 0; e < N; e++) {
         const uint32_t k = c[e] >> 1;
-        // (at most 32,767: exact in the low bits of 2^23)
+        // (at most SHORT: exact in the low bits of 2^23)
         const float f = S16 ? __fsub_rn(__uint_as_float(0x4b000000u | k), 8388608.0f) : (float)k;
         const float g = __fsub_rn(p[e], __fadd_rn(__fmul_rn(f, freq), pres));
         w[e] = k ? g : c[e] ? p[e] : w[e];
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     Batch cur;
     load(cur, 0);
     float rep = 1.0f, rinv = 1.0f, freq = 0.0f, pres = 0.0f;
+    int apart = -VEC; // slot of the generated token that no slot counts, if any
     const int32_t *ids = a.bias_ids + (size_t)r * a.nbias;
     const float *vals = a.bias_vals + (size_t)r * a.nbias;
     const int32_t bias_id = tid < a.nbias ? ids[tid] : -1; // (the first of a thread's)
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
             }
         };
         request(0, all_quads);
-        const int len = (int)min((int64_t)max(a.hist_len[r], 0), a.ldh);
+        int len = (int)min((int64_t)max(a.hist_len[r], 0), a.ldh);
         const int plen = a.prompt_len ? a.prompt_len[r] : 0;
         rep = a.rep ? a.rep[r] : 1.0f;
         freq = a.freq ? a.freq[r] : 0.0f;
@@ -274,6 +277,11 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         rinv = __fdiv_rn(1.0f, rep);
         const int32_t lo = (int32_t)c0;
         int32_t top = -1; // the largest id seen
+        if (S16 && len == SHORT && plen <= 0) {
+            top = h[--len];
+            const uint32_t at = (uint32_t)(top - lo);
+            apart = at < (uint32_t)nc ? (int)at + sh : -VEC;
+        }
         // (c0 + nc <= V < 2^31, so that one unsigned comparison also leaves out negative ids)
         auto prompt = [&](int32_t id) {
             top = max(top, id);
@@ -347,6 +355,11 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
             if (a.hist) {
                 uint32_t c[VEC], any = 0;
                 slots.template get_n<VEC>(u, c);
+                if (S16 && (uint32_t)(apart - u) < (uint32_t)VEC) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e++)
+                        c[e] += u + e == apart ? 2u : 0u;
+                }
 #pragma unroll
                 for (int e = 0; e < VEC; e++)
                     any |= c[e];
@@ -444,7 +457,7 @@ luce_status launch_logits(const LogitsArgs &a, int R, int stretch, cudaStream_t 
 
 template <typename TL> luce_status run_logits(const LogitsArgs &a, int R, cudaStream_t stream)
 {
-    const bool s16 = a.ldh <= 32767 && a.nbias <= 65534; // counts, and the biases' places, fit sixteen bits
+    const bool s16 = a.ldh <= SHORT && a.nbias <= 65534; // counts, and the biases' places, fit sixteen bits
     // as few stretches as shared memory allows with two CTAs to an SM, more
     // while that leaves SMs idle, 512 tokens at least, of one length
     const int64_t most = (size_t)100 * 1024 / (s16 ? 2 : 4);

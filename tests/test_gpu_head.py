@@ -401,10 +401,10 @@ def test_logits_one_token_again_and_again(V, hist):
     check_logits(c)
 
 
-@pytest.mark.parametrize("hist", [32767, 32768, 40000])
+@pytest.mark.parametrize("hist", [32767, 32768, 32769, 40000])
 @pytest.mark.parametrize("V", [200, 60001])
 def test_logits_the_longest_histories_of_either_slot_width(V, hist):
-    # sixteen-bit slots end at 32,767 tokens: all of them one token, and all others
+    # sixteen-bit slots count 32,767 of a token: rows of one token alone, and of all others
     c = logits_case(3, V, hist=hist, prompt=0, bias=2)
     c["hist"][0] = V - 1
     c["hist"][1] = torch.arange(hist) % V
