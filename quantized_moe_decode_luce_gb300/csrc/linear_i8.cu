@@ -36,11 +36,14 @@ __device__ __forceinline__ void store_out(__half *p, float v) { *p = __float2hal
 //
 // What bounds it is the weights' way from HBM, and for small matrices the
 // latency of getting there.  A warp takes VR channels and a slice of K, 16
-// bytes a lane and load, VU x VR loads in flight (4 KB) with the next batch
-// requested before the current one is used; the tokens' codes come through L1
-// (VR channels share each load).  Where there are too few channels to fill the
-// GPU, the wk warps of a row group split K and add their int32 sums through
-// shared memory (exact, so any split gives the same bits).
+// bytes a lane and load; the wk warps of a row group split K and add their
+// int32 sums through shared memory (exact, so any split gives the same bits).
+// Slices are one batch of VU x VR loads wherever eight warps are enough for K:
+// every load is then in flight at once, and without the registers for a next
+// batch four CTAs fit an SM instead of two (1 x 129280 x 4096: 74.0 us, 7.16
+// TB/s; with slices of 4096 and the next batch requested ahead, which longer
+// rows still do, 79.3 us; 1 x 4096 x 4096: 4.7 against 6.2 us).  The tokens'
+// codes come through L1 (VR channels share each load).
 constexpr int VR = 4;      // channels of a warp
 constexpr int V_WARPS = 8; // warps of a CTA
 
@@ -72,7 +75,7 @@ template <int V> __device__ __forceinline__ int warp_sums(int (&v)[V], int lane)
     return s;
 }
 
-template <int T, int VU, typename TO>
+template <int T, int VU, bool MORE, typename TO>
 __global__ void __launch_bounds__(V_WARPS * 32)
     k_linear_i8_vec(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int nt,
                     int N, int K, int wk, TO *out, int64_t ldo)
@@ -100,10 +103,7 @@ __global__ void __launch_bounds__(V_WARPS * 32)
     pdl_wait();
     pdl_trigger();
     int acc[V] = {};
-    for (int k0 = kw * slice; k0 < k1; k0 += 512 * VU) {
-        const int k = k0 + 16 * lane;
-        uint4 next[VU][VR];
-        load(next, k + 512 * VU);
+    auto use = [&](int k) {
 #pragma unroll
         for (int u = 0; u < VU; u++) {
             if (k + 512 * u < k1) {
@@ -121,11 +121,21 @@ __global__ void __launch_bounds__(V_WARPS * 32)
                 }
             }
         }
+    };
+    if constexpr (MORE) {
+        for (int k0 = kw * slice; k0 < k1; k0 += 512 * VU) {
+            const int k = k0 + 16 * lane;
+            uint4 next[VU][VR];
+            load(next, k + 512 * VU);
+            use(k);
 #pragma unroll
-        for (int u = 0; u < VU; u++)
+            for (int u = 0; u < VU; u++)
 #pragma unroll
-            for (int r = 0; r < VR; r++)
-                cur[u][r] = next[u][r];
+                for (int r = 0; r < VR; r++)
+                    cur[u][r] = next[u][r];
+        }
+    } else {
+        use(kw * slice + 16 * lane);
     }
     const int s = warp_sums<V>(acc, lane);
     if (lane % (32 / V) == 0)
@@ -1020,12 +1030,16 @@ luce_status launch_vec(const int8_t *xq, const float *xs, const int8_t *wq, cons
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
     const int64_t rows = ((int64_t)N + VR - 1) / VR;
-    int wk = 1; // warps along K while fewer than 24 warps to an SM are busy and a slice keeps a full batch
-    while (wk < V_WARPS && rows * wk < (int64_t)24 * luce_host::sm_count() && K / (2 * wk) >= 512 * VU)
+    int wk = 1; // as many warps along K as leave a slice of one batch
+    while (wk < V_WARPS && K / wk > 512 * VU)
         wk *= 2;
-    const int groups = V_WARPS / wk;
-    return luce_host::launch(k_linear_i8_vec<T, VU, TO>, dim3((unsigned)((rows + groups - 1) / groups)), dim3(V_WARPS * 32), 0,
-                             stream, xq, xs, wq, ws, bias, nt, N, K, wk, out, ldo);
+    const int groups = V_WARPS / wk, slice = ((K >> 4) + wk - 1) / wk << 4;
+    const dim3 grid((unsigned)((rows + groups - 1) / groups)), block(V_WARPS * 32);
+    auto run = [&](auto kern) {
+        return luce_host::launch(kern, grid, block, 0, stream, xq, xs, wq, ws, bias, nt, N, K, wk, out, ldo);
+    };
+    // (a slice of one batch: without the registers for the next, more CTAs to an SM)
+    return slice > 512 * VU ? run(k_linear_i8_vec<T, VU, true, TO>) : run(k_linear_i8_vec<T, VU, false, TO>);
 }
 
 template <typename TO>
@@ -1033,15 +1047,15 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
     // a stream of the weights for up to four tokens, and for up to eight while the
-    // weights are few: beyond 64 MB the products bound it (5 x 129280 x 4096:
-    // 105 us, tensor cores 87.6 us; 8 x 8192 x 4096: 11.0 against 13.5 us)
+    // weights are few: beyond 40 MB the sums of eight tokens bound it (8 x 8192 x
+    // 4096: 11.8 us, tensor cores 12.9; 8 x 16384 x 4096: 21.1 against 17.2)
     if (T == 1)
         return launch_vec<1, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
     if (T == 2)
         return launch_vec<2, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
     if (T <= 4)
         return launch_vec<4, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (T <= 8 && (int64_t)N * K <= (int64_t)64 << 20)
+    if (T <= 8 && (int64_t)N * K <= (int64_t)40 << 20)
         return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
     if (T <= ROWS)
         return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 15) & ~15, stream);
