@@ -33,6 +33,20 @@ __device__ __forceinline__ float max_abs(float m, float v)
     return r;
 }
 
+// The same of two 16-bit values at once (as m, v's bits without their signs).
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t v, __nv_bfloat16)
+{
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v & 0x7fff7fffu));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t v, __half)
+{
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(v & 0x7fff7fffu));
+    return r;
+}
+
 // Sum of squares and largest |p| of a row over its threads: `lanes` of a warp, or the whole block.
 template <bool NORM> __device__ __forceinline__ void row_totals(float &ss, float &m, int lanes)
 {
@@ -76,7 +90,7 @@ __device__ __forceinline__ int code_of(float p, float d)
 // four operations per value find: the sum with 1.5 2^23 rounds to a whole
 // number and leaves it in the low bits.  Chunks with a value near half way (or
 // a d whose reciprocal overflows: the distance is then a NaN) divide.  Division
-// throughout took 54.9 us for 8191 x 4096 bf16 rows with a residual.
+// throughout took 54.9 us for 8191 x 4096 bf16 rows with a residual, this 42.3.
 template <int V> __device__ __forceinline__ void codes_of(const float (&p)[V], float d, float rinv, uint32_t (&w)[V / 4])
 {
     constexpr float M = 12582912.0f;
@@ -108,7 +122,8 @@ __device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, b
 // A row in registers: NCH chunks of 16 bytes of x per thread, read once (with
 // the residual beside them), codes written once.  Bound by HBM for many rows, whose 32 values a thread spread
 // what every thread does once (the totals, three divisions) thin: with 16 the
-// 8191 x 4096 bf16 rows of luce_quantize_i8 took 33 us.  For few rows it is
+// 8191 x 4096 bf16 rows of luce_quantize_i8 took 33 us instead of 24, and with
+// their largest value found two at a time 21.7.  For few rows it is
 // latency: one chunk a thread, all loads at once, one barrier.
 //
 // blockDim.x threads to a row: 8, 16 or 32 lanes of a warp (blockDim.y rows to
@@ -119,7 +134,8 @@ __device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, b
 // in x from a 16-byte boundary (the residual and the sum share it: checked by
 // the host), the first and last chunk element by element; the codes, whose
 // rows lie at other offsets, go through shared memory and leave in 16-byte
-// stores.
+// stores (8191 x 4099 fp32 rows: 36.8 us, aligned ones of 4096 27.5; stores of
+// 4 or 8 bytes took longer).
 template <typename TX, int NCH, bool ALIGNED, bool NORM>
 __global__ void __launch_bounds__(1024)
     k_rows_i8(const TX *x, const TX *res, TX *xsum, const float *__restrict__ gamma, float eps, int T, int H, int8_t *q,
@@ -134,6 +150,7 @@ __global__ void __launch_bounds__(1024)
     const size_t row = (size_t)(live_row ? t : 0) * H;
     const int n = live_row ? H : 0;
     const int a = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(x + row) & 15) / sizeof(TX));
+    const bool gamma16 = (reinterpret_cast<uintptr_t>(gamma) & 15) == 0;
     const bool in_place = !ALIGNED && (xsum == x || xsum == res) && xsum != nullptr;
     union Chunk {
         uint4 w;
@@ -188,6 +205,22 @@ __global__ void __launch_bounds__(1024)
                         p[i + 3] = __fmul_rn(p[i + 3], g.w);
                     }
                 }
+            } else if (whole && gamma16 && e0 + V + 4 <= n) {
+                // the 16-byte pieces of gamma around the chunk, moved down by the row's e0 mod 4 (8191 x
+                // 4099 bf16 rows with a residual: 65.0 us, with loads of single elements 71.2)
+                const int s = e0 & 3;
+                float g[V + 4];
+#pragma unroll
+                for (int i = 0; i < V + 4; i += 4) {
+                    const float4 w = __ldg(reinterpret_cast<const float4 *>(gamma + (e0 - s) + i));
+                    g[i] = w.x, g[i + 1] = w.y, g[i + 2] = w.z, g[i + 3] = w.w;
+                }
+#pragma unroll
+                for (int i = 0; i < V + 2; i++)
+                    g[i] = s & 1 ? g[i + 1] : g[i];
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    p[i] = __fmul_rn(p[i], s & 2 ? g[i + 2] : g[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; i++)
@@ -197,6 +230,7 @@ __global__ void __launch_bounds__(1024)
         }
     };
     float ss = 0.0f, m = 0.0f;
+    uint32_t mm = 0;
     float p[NORM ? NCH : 1][V];
 #pragma unroll
     for (int c = 0; c < NCH; c++) {
@@ -226,8 +260,19 @@ __global__ void __launch_bounds__(1024)
                 ss = fmaf(v, v, ss);
                 p[NORM ? c : 0][i] = pc[i];
             }
-            m = max_abs(m, pc[i]);
+            if (!ALIGNED || NORM || V == 4)
+                m = max_abs(m, pc[i]);
         }
+        if constexpr (ALIGNED && !NORM && V == 8) {
+            mm = max_abs2(mm, cx[c].w.x, TX());
+            mm = max_abs2(mm, cx[c].w.y, TX());
+            mm = max_abs2(mm, cx[c].w.z, TX());
+            mm = max_abs2(mm, cx[c].w.w, TX());
+        }
+    }
+    if constexpr (ALIGNED && !NORM && V == 8) {
+        const TX *h = reinterpret_cast<const TX *>(&mm);
+        m = max_abs(to_f32(h[0]), to_f32(h[1]));
     }
     row_totals<NORM>(ss, m, lanes);
     const bool finite = m < INFINITY;
