@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -48,10 +49,10 @@ struct LogitsArgs {
 };
 
 constexpr int THREADS = 512;
-// steps of a thread in flight, and as many requested behind them (a step of
-// 16-bit logits is eight tokens, of fp32 four; 256 rows: 90 and 49 us, with two
-// and one 95 and 59)
-template <typename TL> constexpr int NB_OF = sizeof(TL) == 4 ? 2 : 1;
+// steps of four logits in flight for each thread, and as many requested behind
+// them (256 bf16 rows of 129280 with 4096 history tokens: 44.5 us, with two 46.5;
+// eight 16-bit logits to a step, whose stores then need a swap between lanes, 46.7)
+constexpr int NB = 3;
 constexpr int HB = 4; // history loads of a thread in flight (four tokens each)
 
 // What a slot of shared memory holds for its token: twice the number of
@@ -136,25 +137,33 @@ template <bool S16> struct Slots {
     }
 };
 
+// Logits from LOW to below HIGH, over a penalty from 2^-40 to 2^40, go through
+// Markstein's division below without any result that over- or underflows.
+constexpr uint32_t LOW = 0x20000000u; // 2^-63
+constexpr int HIGH = 0x60000000;      // 2^65
+
 // The penalties of N tokens whose slots hold c, without a branch in the common
 // case.  l / rep, correctly rounded, comes from rinv = fl(1 / rep) by Markstein's
-// sequence: a product, its exact remainder and one correction.  Where a result
-// lies outside the range in which no intermediate can over- or underflow
-// (zero, infinities and NaNs among them), all N divide.
+// sequence: a product, its exact remainder and one correction (6000 penalties
+// over all 2^23 significands of a logit gave no other quotient).  Where one of
+// the logits is +0, or positive and below `low` or not below HIGH, all N divide
+// (low is LOW, or above all floats where rep is out of range).
 template <bool S16, int N>
-__device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], float rep, float rinv, float freq,
-                                         float pres)
+__device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], float rep, float rinv, uint32_t low,
+                                         float freq, float pres)
 {
     float p[N];
-    bool odd = false;
+    uint32_t lowest = ~0u; // of the bits: negative values lie above all positive ones,
+    int highest = 0;       // and, signed, below
 #pragma unroll
     for (int e = 0; e < N; e++) {
         const float l = w[e], q = __fmul_rn(l, rinv);
-        const float s = fmaf(fmaf(-q, rep, l), rinv, q), m = fabsf(s);
+        const float s = fmaf(fmaf(-q, rep, l), rinv, q);
         p[e] = l > 0.0f ? s : __fmul_rn(l, rep);
-        odd |= l > 0.0f && !(m > 1e-25f && m < 1e25f);
+        lowest = min(lowest, __float_as_uint(l));
+        highest = max(highest, __float_as_int(l));
     }
-    if (odd) {
+    if (lowest < low || highest >= HIGH) {
 #pragma unroll
         for (int e = 0; e < N; e++)
             p[e] = w[e] > 0.0f ? __fdiv_rn(w[e], rep) : __fmul_rn(w[e], rep);
@@ -169,23 +178,51 @@ __device__ __forceinline__ void penalize(float (&w)[N], const uint32_t (&c)[N], 
     }
 }
 
-// VEC logits a step and thread: 16 bytes, or one.  A row may start `sh`
+// N logits as they lie in memory, in whole words.
+template <typename TL, int N> struct Raw {
+    static constexpr int W = N * sizeof(TL) / 4;
+    uint32_t w[W ? W : 1];
+    __device__ __forceinline__ void load(const TL *p)
+    {
+        if constexpr (W == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else if constexpr (W == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            w[0] = x.x, w[1] = x.y;
+        } else if constexpr (W == 1)
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+    __device__ __forceinline__ void values(float (&v)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            if constexpr (sizeof(TL) == 4)
+                v[i] = __uint_as_float(w[i]);
+            else if constexpr (std::is_same_v<TL, __half>)
+                v[i] = __half2float(__ushort_as_half((unsigned short)(w[i / 2] >> 16 * (i & 1))));
+            else
+                v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        }
+    }
+};
+
+// VEC logits a step and thread: four, or one.  A row may start `sh`
 // elements behind a boundary of VEC elements (the same for logits and out:
 // checked by the host), so a stretch is gone through in steps that start at
-// boundaries, u = v + sh, whose first and last may be partial.
+// boundaries, u = v + sh; the tokens before the first whole step and behind the
+// last go one to a thread.
 template <typename TL, int VEC, bool S16>
 __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs a, int stretch, int mask_at, int bias_at)
 {
     extern __shared__ __align__(16) uint32_t slot_words[];
-    constexpr int NB = NB_OF<TL>;
     const Slots<S16> slots{smem_addr(slot_words), slot_words}; // (slot u is that of token c0 + u - sh)
     const Slots<S16> places{smem_addr(slot_words + bias_at), slot_words + bias_at}; // a token's last bias entry, from one on; if bias_at > 0
     const int r = blockIdx.y, tid = threadIdx.x;
     const int64_t c0 = (int64_t)blockIdx.x * stretch;
     const int nc = (int)min((int64_t)stretch, a.V - c0);
-    struct alignas(VEC * sizeof(TL)) In {
-        TL e[VEC];
-    };
     float *o = a.out + (size_t)r * a.ldo + c0;
     const int sh = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(o) >> 2) & (VEC - 1));
     // slots to zero (they do not depend on the previous kernel)
@@ -215,24 +252,25 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
             mw[1 + i] = mr[i];
     // a batch: the logits of NB steps
     struct Batch {
-        In in[NB];
+        Raw<TL, VEC> in[NB];
     };
     auto load = [&](Batch &b, int u0) {
 #pragma unroll
         for (int i = 0; i < NB; i++) {
             const int v = u0 + (tid + i * THREADS) * VEC - sh;
-            if (v >= 0 && v + VEC <= nc) {
-                b.in[i] = *reinterpret_cast<const In *>(lr + v);
-            } else if (VEC > 1 && v + VEC > 0 && v < nc) {
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    if (v + e >= 0 && v + e < nc)
-                        b.in[i].e[e] = lr[v + e];
-            }
+            if (v >= 0 && v + VEC <= nc)
+                b.in[i].load(lr + v);
         }
     };
     Batch cur;
     load(cur, 0);
+    int edge = -1; // the thread's token outside the whole steps
+    if (VEC > 1 && tid < 2 * VEC) {
+        const int head = min((VEC - sh) & (VEC - 1), nc), tail = max((nc + sh) / VEC * VEC - sh, head);
+        edge = tid < VEC ? (tid < head ? tid : -1) : tail + tid - VEC < nc ? tail + tid - VEC : -1;
+    }
+    const float edge_value = edge >= 0 ? to_f32(lr[edge]) : 0.0f;
+    uint32_t low = LOW;
     float rep = 1.0f, rinv = 1.0f, freq = 0.0f, pres = 0.0f;
     int apart = -VEC; // slot of the generated token that no slot counts, if any
     const int32_t *ids = a.bias_ids + (size_t)r * a.nbias;
@@ -275,6 +313,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         freq = a.freq ? a.freq[r] : 0.0f;
         pres = a.pres ? a.pres[r] : 0.0f;
         rinv = __fdiv_rn(1.0f, rep);
+        low = rep >= 0x1p-40f && rep <= 0x1p40f ? LOW : ~0u;
         const int32_t lo = (int32_t)c0;
         int32_t top = -1; // the largest id seen
         if (S16 && len == SHORT && plen <= 0) {
@@ -340,80 +379,62 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         find_places();
     }
     __syncthreads();
+    // the N logits of slots u ..
+    auto finish = [&](auto &w, int u) {
+        constexpr int N = sizeof(w) / sizeof(float);
+        if (a.hist) {
+            uint32_t c[N], any = 0;
+            slots.template get_n<N>(u, c);
+            if (S16 && (uint32_t)(apart - u) < (uint32_t)N) {
+#pragma unroll
+                for (int e = 0; e < N; e++)
+                    c[e] += u + e == apart ? 2u : 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                any |= c[e];
+            if (any)
+                penalize<S16, N>(w, c, rep, rinv, low, freq, pres);
+        }
+        if (bias_at) {
+            uint32_t j[N];
+            places.template get_n<N>(u, j);
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (j[e])
+                    w[e] = __fadd_rn(w[e], vals[j[e] - 1]);
+        }
+        if (mr) {
+            const int v = u - sh, at = (v >> 5) + 1;
+            const uint32_t bits = N == 1 ? mw[at] >> (v & 31) : __funnelshift_r(mw[at], mw[at + 1], v & 31);
+#pragma unroll
+            for (int e = 0; e < N; e++)
+                if (!((bits >> e) & 1u))
+                    w[e] = -INFINITY;
+        }
+    };
     for (int u0 = 0; u0 < nc + sh; u0 += NB * THREADS * VEC) {
         Batch next;
         load(next, u0 + NB * THREADS * VEC);
 #pragma unroll
         for (int i = 0; i < NB; i++) {
             const int u = u0 + (tid + i * THREADS) * VEC, v = u - sh;
-            if (v >= nc)
-                break;
+            if (v < 0 || v + VEC > nc)
+                continue;
             float w[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; e++)
-                w[e] = to_f32(cur.in[i].e[e]);
-            if (a.hist) {
-                uint32_t c[VEC], any = 0;
-                slots.template get_n<VEC>(u, c);
-                if (S16 && (uint32_t)(apart - u) < (uint32_t)VEC) {
-#pragma unroll
-                    for (int e = 0; e < VEC; e++)
-                        c[e] += u + e == apart ? 2u : 0u;
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    any |= c[e];
-                if (any)
-                    penalize<S16, VEC>(w, c, rep, rinv, freq, pres);
-            }
-            if (bias_at) {
-                uint32_t j[VEC];
-                places.template get_n<VEC>(u, j);
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    if (j[e])
-                        w[e] = __fadd_rn(w[e], vals[j[e] - 1]);
-            }
-            if (mr) {
-                const int at = (v >> 5) + 1;
-                const uint32_t bits = __funnelshift_r(mw[at], mw[at + 1], v & 31);
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    if (!((bits >> e) & 1u))
-                        w[e] = -INFINITY;
-            }
-            const int vw = v - (tid & 31) * VEC; // the warp's first
-            if (VEC == 8 && vw >= 0 && vw + 32 * VEC <= nc) {
-                // neighbouring lanes swap halves, so that each store writes whole sectors
-                const bool odd = tid & 1;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float give = odd ? w[e] : w[e + VEC / 2];
-                    const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-                    if (odd)
-                        w[e] = got;
-                    else
-                        w[e + VEC / 2] = got;
-                }
-                float *p = o + v + (odd ? -VEC / 2 : 0);
-                *reinterpret_cast<float4 *>(p) = make_float4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<float4 *>(p + VEC) = make_float4(w[VEC / 2], w[VEC / 2 + 1], w[VEC / 2 + 2], w[VEC / 2 + 3]);
-            } else if (v >= 0 && v + VEC <= nc) {
-                if constexpr (VEC == 1) {
-                    o[v] = w[0];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 4)
-                        *reinterpret_cast<float4 *>(o + v + e) = make_float4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; e++)
-                    if (v + e >= 0 && v + e < nc)
-                        o[v + e] = w[e];
-            }
+            cur.in[i].values(w);
+            finish(w, u);
+            if constexpr (VEC == 1)
+                o[v] = w[0];
+            else
+                *reinterpret_cast<float4 *>(o + v) = make_float4(w[0], w[1], w[2], w[3]);
         }
         cur = next;
+    }
+    if (edge >= 0) {
+        float w[1] = {edge_value};
+        finish(w, edge + sh);
+        o[edge] = w[0];
     }
     if (a.nbias && !bias_at) {
         // no room for the places: the slots now find each id's last entry, which
@@ -459,13 +480,13 @@ template <typename TL> luce_status run_logits(const LogitsArgs &a, int R, cudaSt
 {
     const bool s16 = a.ldh <= SHORT && a.nbias <= 65534; // counts, and the biases' places, fit sixteen bits
     // as few stretches as shared memory allows with two CTAs to an SM, more
-    // while that leaves SMs idle, 512 tokens at least, of one length
+    // while that leaves SMs idle, 1024 tokens at least, of one length
     const int64_t most = (size_t)100 * 1024 / (s16 ? 2 : 4);
     const int64_t fill = std::max<int64_t>(1, 2 * luce_host::sm_count() / R);
     const int64_t n = std::max((a.V + most - 1) / most, std::min(fill, (a.V + 1023) / 1024));
     const int stretch = (int)(((a.V + n - 1) / n + 31) & ~(int64_t)31);
-    // 16 bytes of logits at a step where a row of logits and of out lie at the same place between boundaries of V
-    constexpr int VEC = 16 / sizeof(TL);
+    // four logits at a step where a row of logits and of out lie at the same place between boundaries of four
+    constexpr int VEC = 4;
     auto place = [](const void *p, size_t es) { return (int64_t)(reinterpret_cast<uintptr_t>(p) / es); };
     if ((place(a.logits, sizeof(TL)) - place(a.out, 4)) % VEC == 0 && (R == 1 || (a.ldl - a.ldo) % VEC == 0))
         return s16 ? launch_logits<TL, VEC, true>(a, R, stretch, stream) : launch_logits<TL, VEC, false>(a, R, stretch, stream);

@@ -432,6 +432,31 @@ def test_logits_repetition_of_extreme_values():
         check_logits({k: v for k, v in c.items() if k not in ("frequency", "presence")})
 
 
+@pytest.mark.parametrize("e", [-130, -126, -64, -63, -40, 0, 40, 64, 65, 127])
+def test_logits_repetition_at_every_magnitude(e):
+    # all four logits of a step of one magnitude, over penalties on both sides of 2^-40 and 2^40
+    V = 4096
+    reps = [2.0**-40, math.nextafter(2.0**-40, 0), 2.0**40, 2.0**40 * (1 + 2.0**-23), 1.3, 0.77, 1 + 2.0**-23, 2 - 2.0**-23]
+    c = logits_case(len(reps), V, hist=V, prompt=V // 2, seed=e + 200)
+    c["logits"] = torch.ldexp(1 + torch.rand((len(reps), V), generator=gen(e + 300)), torch.tensor(e))
+    c["logits"][:, ::97] *= -1
+    c["logits"][:, 5] = 0.0
+    c["hist"][:] = torch.arange(V, dtype=torch.int32)
+    c["hist_len"][:] = V
+    c["repetition"] = torch.tensor(reps)
+    check_logits(c)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16, f16])
+@pytest.mark.parametrize("V", [3, 4, 6, 7, 8, 9, 13])
+def test_logits_rows_of_a_few_steps(V, dtype):
+    # rows that start at every place between boundaries of four, whole steps or none in them
+    c = logits_case(9, V, dtype, hist=20, bias=4, mask=True, seed=V)
+    check_logits(c)
+    check_logits(c, gap_in=4, gap_out=8)
+    check_logits(c, gap_in=1, gap_out=1)
+
+
 @pytest.mark.allow_fault
 def test_logits_ids_out_of_range_are_skipped_and_raise_the_fault_bit():
     V = 5000
