@@ -188,50 +188,58 @@ __global__ void __launch_bounds__(1024)
         for (int c = 0; c < NCH; c++)
             load(cr[c], res + row, (int)(threadIdx.x + c * lanes) * V - a);
     }
-    // p of chunk c: its values times gamma (elements behind the row's ends are zero)
-    auto scaled = [&](const Chunk &c, int e0, bool whole, float (&p)[V]) {
+    // gamma of a chunk (one for elements behind the row's ends, which are zero)
+    auto gammas = [&](int e0, bool whole, float (&g)[V]) {
+        if (ALIGNED) {
+            if (whole) {
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            p[i] = to_f32(c.e[i]);
-        if constexpr (NORM) {
-            if (ALIGNED) {
-                if (whole) {
-#pragma unroll
-                    for (int i = 0; i < V; i += 4) {
-                        const float4 g = __ldg(reinterpret_cast<const float4 *>(gamma + e0 + i));
-                        p[i] = __fmul_rn(p[i], g.x);
-                        p[i + 1] = __fmul_rn(p[i + 1], g.y);
-                        p[i + 2] = __fmul_rn(p[i + 2], g.z);
-                        p[i + 3] = __fmul_rn(p[i + 3], g.w);
-                    }
-                }
-            } else if (whole && gamma16 && e0 + V + 4 <= n) {
-                // the 16-byte pieces of gamma around the chunk, moved down by the row's e0 mod 4 (8191 x
-                // 4099 bf16 rows with a residual: 65.0 us, with loads of single elements 71.2)
-                const int s = e0 & 3;
-                float g[V + 4];
-#pragma unroll
-                for (int i = 0; i < V + 4; i += 4) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(gamma + (e0 - s) + i));
+                for (int i = 0; i < V; i += 4) {
+                    const float4 w = __ldg(reinterpret_cast<const float4 *>(gamma + e0 + i));
                     g[i] = w.x, g[i + 1] = w.y, g[i + 2] = w.z, g[i + 3] = w.w;
                 }
-#pragma unroll
-                for (int i = 0; i < V + 2; i++)
-                    g[i] = s & 1 ? g[i + 1] : g[i];
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    p[i] = __fmul_rn(p[i], s & 2 ? g[i + 2] : g[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    if (whole || (e0 + i >= 0 && e0 + i < n))
-                        p[i] = __fmul_rn(p[i], __ldg(gamma + e0 + i));
             }
+        } else if (whole && gamma16 && e0 + V + 4 <= n) {
+            // the 16-byte pieces of gamma around the chunk, moved down by the row's e0 mod 4 (8191 x
+            // 4099 bf16 rows with a residual: 65.0 us, with loads of single elements 71.2)
+            const int s = e0 & 3;
+            float h[V + 4];
+#pragma unroll
+            for (int i = 0; i < V + 4; i += 4) {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(gamma + (e0 - s) + i));
+                h[i] = w.x, h[i + 1] = w.y, h[i + 2] = w.z, h[i + 3] = w.w;
+            }
+#pragma unroll
+            for (int i = 0; i < V + 2; i++)
+                h[i] = s & 1 ? h[i + 1] : h[i];
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                g[i] = s & 2 ? h[i + 2] : h[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                g[i] = whole || (e0 + i >= 0 && e0 + i < n) ? __ldg(gamma + e0 + i) : 1.0f;
         }
     };
+    auto scaled = [&](const Chunk &c, int e0, bool whole, float (&p)[V]) {
+        float g[V] = {};
+        if constexpr (NORM)
+            gammas(e0, whole, g);
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            p[i] = NORM ? __fmul_rn(to_f32(c.e[i]), g[i]) : to_f32(c.e[i]);
+    };
+    // few values a thread: gamma is requested beside them
+    constexpr bool EARLY = NORM && NCH * V <= 16;
+    float p[NORM ? NCH : 1][V] = {};
+    if constexpr (EARLY) {
+#pragma unroll
+        for (int c = 0; c < NCH; c++) {
+            const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
+            gammas(e0, ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n, p[c]);
+        }
+    }
     float ss = 0.0f, m = 0.0f;
     uint32_t mm = 0;
-    float p[NORM ? NCH : 1][V];
 #pragma unroll
     for (int c = 0; c < NCH; c++) {
         const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
@@ -252,7 +260,13 @@ __global__ void __launch_bounds__(1024)
             }
         }
         float pc[V];
-        scaled(cx[c], e0, whole, pc);
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                pc[i] = __fmul_rn(to_f32(cx[c].e[i]), p[c][i]);
+        } else {
+            scaled(cx[c], e0, whole, pc);
+        }
 #pragma unroll
         for (int i = 0; i < V; i++) {
             if (NORM) {
