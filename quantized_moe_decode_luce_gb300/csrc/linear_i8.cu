@@ -936,31 +936,96 @@ bool map_codes(CUtensorMap *m, const int8_t *base, int rows, int K, int box_rows
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How many clusters of a size a device holds at once (of one kernel; asked once per size and device).
-struct ClusterLimit {
-    std::atomic<int> known[64][SK_MAX + 1];
-    template <class Kernel> int get(Kernel kern, const cudaLaunchConfig_t &cfg, int csize)
+// What is asked of the runtime once per kernel and device.
+template <class C, typename TO> struct Tc {
+    static inline luce_host::SmemLimit limit;
+    static inline std::atomic<int> resident[64][SK_MAX + 1]; // clusters of a size that a device holds at once, plus one
+    static bool prepare()
     {
-        int dev = 0, n = 0;
-        const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
-        if (keep && (n = known[dev][csize].load(std::memory_order_relaxed)) > 0)
+        if (limit.raise(k_linear_i8_tc<C, TO>, C::SMEM) == cudaSuccess)
+            return true;
+        (void)cudaGetLastError();
+        return false;
+    }
+    static int clusters_at_once(int dev, int csize)
+    {
+        const bool keep = dev >= 0 && dev < 64;
+        int n = keep ? resident[dev][csize].load(std::memory_order_relaxed) : 0;
+        if (n > 0)
             return n - 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        if (!prepare())
+            return 0;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        luce_host::make_config(cfg, attr, dim3((unsigned)csize), dim3(C::THREADS), C::SMEM, nullptr);
+        cudaLaunchAttribute &cluster = attr[cfg.numAttrs++];
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim.x = (unsigned)csize;
+        cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, k_linear_i8_tc<C, TO>, &cfg) != cudaSuccess) {
             (void)cudaGetLastError();
             return 0;
         }
         if (keep)
-            known[dev][csize].store(n + 1, std::memory_order_relaxed);
+            resident[dev][csize].store(n + 1, std::memory_order_relaxed);
         return n;
+    }
+    // Groups along K, while all tiles' clusters are resident at once: a second
+    // round costs more than the split gains (100 x 4096 x 4096: clusters of 8 CTAs, of
+    // which not all 16 fit, 24.7 us; clusters of 4 16.9 us; pairs alone 18.5 us)
+    static int split(int dev, int sms, int64_t tiles, int units)
+    {
+        int sk = 1;
+        for (int s = 2; s * C::CG <= SK_MAX && s <= units && tiles * s * C::CG <= sms; s *= 2) {
+            if (tiles > clusters_at_once(dev, s * C::CG))
+                break;
+            sk = s;
+        }
+        return sk;
     }
 };
 
+// The tile of the tensor-core kernel for a product: its configuration (1, 2 or 4:
+// CfgOne, CfgPair, CfgWide) and the tokens that it covers.  What a choice takes
+// is estimated in microseconds: setup and last stores, the units that a CTA goes
+// through, its tiles' sums.  The figures are fits to 26 + 19 products of 16 to
+// 8192 tokens with every choice timed; the tile that they choose took 0.4% longer
+// than the best on average, 6% at most.  Tiles of 256 tokens for all products
+// above 128, before, took 228 us for 8192 x 4096 x 4096 (now 159), 12.8 for 512 x
+// 1024 x 1024 (7.4) and 9.5 for 137 x 88 x 800 (6.1).
+struct Plan {
+    float us = INFINITY;
+    int cfg = 0, tokens = 0;
+};
+struct Cost {
+    float setup, unit, unit_token, token; // of a launch; of a unit; a unit's share per token of the tile; its sums per token
+    float split, split_token, round;      // of the exchange between groups, per token; of a further tile of a CTA
+};
+constexpr Cost COST_ONE{3.83f, 0.333f, 0.0006f, 0.0302f, 1.09f, 0.0f, 0.38f};
+constexpr Cost COST_PAIR{5.19f, 0.346f, 0.0f, 0.0201f, 0.07f, 0.0128f, 0.54f};
+constexpr Cost COST_WIDE{5.83f, 0.616f, 0.0f, 0.0147f, -1.5f, 0.0142f, 1.7f};
+
+template <class C, typename TO>
+void consider(Plan &best, int dev, int sms, int T, int N, int K, const Cost &c, int id, int first, int last, int step)
+{
+    const int units = (K + KU - 1) / KU;
+    const int64_t mt = ((int64_t)N + RM * C::CG - 1) / (RM * C::CG);
+    for (int w = first; w <= last && w - step < T; w += step) {
+        const int64_t tiles = mt * ((T + w - 1) / w);
+        const int sk = Tc<C, TO>::split(dev, sms, tiles, units), at_once = sms / C::CG;
+        const float rounds = sk > 1 ? 1.0f : (float)((tiles + at_once - 1) / at_once);
+        const float us = c.setup + rounds * (float)((units + sk - 1) / sk) * (c.unit + c.unit_token * (float)w) +
+                         c.token * (float)w + (rounds - 1.0f) * c.round +
+                         (sk > 1 ? c.split + c.split_token * (float)w : 0.0f);
+        if (us < best.us)
+            best = Plan{us, id, w};
+    }
+}
+
 template <class C, typename TO>
 luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
-                      int N, int K, TO *out, int64_t ldo, int tile_tokens, cudaStream_t stream)
+                      int N, int K, TO *out, int64_t ldo, int tile_tokens, int dev, int sms, cudaStream_t stream)
 {
-    static luce_host::SmemLimit limit;
-    static ClusterLimit clusters_at_once;
     auto kern = k_linear_i8_tc<C, TO>;
     TcArgs a;
     a.xs = xs;
@@ -983,37 +1048,23 @@ luce_status launch_tc(const int8_t *xq, const float *xs, const int8_t *wq, const
     a.tiles = (int)(mt * tt);
     if (!map_codes(&a.tw, wq, N, K, RM) || !map_codes(&a.tx, xq, T, K, a.xbox))
         return LUCE_ERR_CUDA;
-    if (limit.raise(kern, C::SMEM) != cudaSuccess) {
-        (void)cudaGetLastError();
+    if (!Tc<C, TO>::prepare())
         return LUCE_ERR_UNSUPPORTED;
-    }
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
     luce_host::make_config(cfg, attr, dim3((unsigned)C::CG), dim3(C::THREADS), C::SMEM, stream);
     cudaLaunchAttribute &cluster = attr[cfg.numAttrs];
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-    // groups along K while all tiles' clusters are resident at once: a second
-    // round costs more than the split gains (100 x 4096 x 4096: clusters of 8 CTAs, of
-    // which not all 16 fit, 24.7 us; clusters of 4 16.9 us; pairs alone 18.5 us)
-    a.sk = 1;
-    for (int sk = 2; sk * C::CG <= SK_MAX && sk <= a.units && (int64_t)a.tiles * sk * C::CG <= luce_host::sm_count(); sk *= 2) {
-        cudaLaunchConfig_t query = cfg;
-        query.gridDim = dim3((unsigned)(sk * C::CG));
-        query.numAttrs = cfg.numAttrs + 1;
-        cluster.val.clusterDim.x = (unsigned)(sk * C::CG);
-        if (a.tiles > clusters_at_once.get(kern, query, sk * C::CG))
-            break;
-        a.sk = sk;
-    }
+    a.sk = Tc<C, TO>::split(dev, sms, a.tiles, a.units);
     const int csize = C::CG * a.sk;
-    const int clusters = a.sk > 1 ? a.tiles : std::min(a.tiles, luce_host::sm_count() / C::CG);
+    const int clusters = a.sk > 1 ? a.tiles : std::min(a.tiles, sms / C::CG);
     cfg.gridDim = dim3((unsigned)(clusters * csize));
     cluster.val.clusterDim.x = (unsigned)csize;
     cfg.numAttrs += csize > 1;
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
         (void)cudaGetLastError();
-        limit.forget();
+        Tc<C, TO>::limit.forget();
         return LUCE_ERR_CUDA;
     }
     return LUCE_OK;
@@ -1057,22 +1108,22 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
         return launch_vec<4, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
     if (T <= 8 && (int64_t)N * K <= (int64_t)40 << 20)
         return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (T <= ROWS)
-        return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 15) & ~15, stream);
-    if (T <= 2 * ROWS)
-        return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, (T + 31) & ~31, stream);
-    // tiles of at most 256 tokens: the width with the least rounds x width
-    const int64_t mt = ((int64_t)N + 2 * RM - 1) / (2 * RM), pairs = luce_host::sm_count() / 2;
-    int best = 4 * ROWS;
-    int64_t cost = INT64_MAX;
-    for (int w = 4 * ROWS; w > 2 * ROWS; w -= 32) {
-        const int64_t tiles = mt * (((int64_t)T + w - 1) / w), rounds = (tiles + pairs - 1) / pairs;
-        if (rounds * w < cost) {
-            cost = rounds * w;
-            best = w;
-        }
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LUCE_ERR_CUDA;
     }
-    return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, best, stream);
+    const int sms = luce_host::sm_count();
+    Plan plan;
+    consider<CfgOne, TO>(plan, dev, sms, T, N, K, COST_ONE, 1, 16, ROWS, 16);
+    consider<CfgPair, TO>(plan, dev, sms, T, N, K, COST_PAIR, 2, ROWS, 2 * ROWS, 32);
+    if (T > 2 * ROWS)
+        consider<CfgWide, TO>(plan, dev, sms, T, N, K, COST_WIDE, 4, 2 * ROWS + 32, 4 * ROWS, 32);
+    if (plan.cfg == 1)
+        return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
+    if (plan.cfg == 2)
+        return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
+    return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
 }
 
 } // namespace

@@ -215,6 +215,19 @@ def test_linear_working_sizes(T, N, K, dtype):
     check_linear(T, N, K, dtype, bias=T % 2 == 0)
 
 
+# few and many tiles of every width, with and without a split of K
+TILES = [(37, 165, 16), (22, 39, 352), (17, 10421, 16), (373, 19, 1936), (1281, 398, 16), (465, 18, 2752), (810, 2188, 16),
+         (697, 19, 3216), (50, 10020, 3616), (51, 4875, 5200), (475, 14942, 16), (1219, 165, 2848), (354, 16147, 16),
+         (1395, 137, 4864), (137, 13219, 800), (130, 3554, 3952), (325, 6638, 1696), (210, 12862, 1296), (232, 13600, 2128)]
+
+
+@pytest.mark.parametrize("T,N,K", TILES)
+def test_linear_tiles_of_every_width(T, N, K):
+    check_linear(T, N, K, f32, bias=True, seed=T)
+    full = lambda r, v: torch.full((r, K), v, dtype=torch.int8)  # noqa: E731
+    check_linear(T, N, K, f32, xq=full(T, 127), wq=full(N, 125))
+
+
 @pytest.mark.parametrize("K", [1008, 1024, 1040, 2048, 4096, 16384, 65536])
 @pytest.mark.parametrize("T", [1, 7, 20, 100, 300])
 def test_linear_sums_are_exact_at_the_largest_codes(T, K):
