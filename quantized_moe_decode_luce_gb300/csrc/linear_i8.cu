@@ -32,7 +32,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16 *p, float v) { *p = __fl
 __device__ __forceinline__ void store_out(__half *p, float v) { *p = __float2half_rn(v); }
 
 // ---------------------------------------------------------------------------
-// Few tokens (T of them, nt live): a stream of the weights through dp4a.
+// Few tokens (T of them at a time): a stream of the weights through dp4a.
 //
 // What bounds it is the weights' way from HBM, and for small matrices the
 // latency of getting there.  A warp takes VR channels and a slice of K, 16
@@ -82,6 +82,11 @@ __global__ void __launch_bounds__(V_WARPS * 32)
 {
     constexpr int V = VR * T;
     __shared__ int part[V_WARPS][V];
+    const int t0 = (int)blockIdx.y * T; // this CTA's tokens
+    xq += (size_t)t0 * K;
+    xs += t0;
+    out += (size_t)t0 * ldo;
+    nt = min(nt - t0, T);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = V_WARPS / wk, kw = warp % wk; // row groups of the CTA, this warp's place along K
     const int64_t n0 = ((int64_t)blockIdx.x * groups + warp / wk) * VR;
@@ -1005,6 +1010,12 @@ constexpr Cost COST_ONE{3.83f, 0.333f, 0.0006f, 0.0302f, 1.09f, 0.0f, 0.38f};
 constexpr Cost COST_PAIR{5.19f, 0.346f, 0.0f, 0.0201f, 0.07f, 0.0128f, 0.54f};
 constexpr Cost COST_WIDE{5.83f, 0.616f, 0.0f, 0.0147f, -1.5f, 0.0142f, 1.7f};
 
+// The same of the stream, eight tokens at a time: setup, and a megabyte of the
+// weights as its warps go through them (fits to ten weights of 0.1 to 8 MB and 9 to
+// 250 tokens: 16 x 1024 x 1024 2.5 us, tensor cores 6.0; 64 x 148 x 3376 3.2 and 6.8;
+// 64 x 2048 x 2048 11.8 and 8.1).
+constexpr float VUS_SETUP = 2.2f, VUS_MB = 0.28f;
+
 template <class C, typename TO>
 void consider(Plan &best, int dev, int sms, int T, int N, int K, const Cost &c, int id, int first, int last, int step)
 {
@@ -1076,16 +1087,26 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return p < q + nb && q < p + na;
 }
 
+// Warps along K, as many as leave a slice of one batch, and the slice.
+struct VecSplit {
+    int wk, slice;
+};
+VecSplit vec_split(int K, int vu)
+{
+    int wk = 1;
+    while (wk < V_WARPS && K / wk > 512 * vu)
+        wk *= 2;
+    return {wk, ((K >> 4) + wk - 1) / wk << 4};
+}
+
 template <int T, int VU, typename TO>
 luce_status launch_vec(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int nt,
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
     const int64_t rows = ((int64_t)N + VR - 1) / VR;
-    int wk = 1; // as many warps along K as leave a slice of one batch
-    while (wk < V_WARPS && K / wk > 512 * VU)
-        wk *= 2;
-    const int groups = V_WARPS / wk, slice = ((K >> 4) + wk - 1) / wk << 4;
-    const dim3 grid((unsigned)((rows + groups - 1) / groups)), block(V_WARPS * 32);
+    const VecSplit vs = vec_split(K, VU);
+    const int wk = vs.wk, slice = vs.slice, groups = V_WARPS / wk;
+    const dim3 grid((unsigned)((rows + groups - 1) / groups), (unsigned)((nt + T - 1) / T)), block(V_WARPS * 32);
     auto run = [&](auto kern) {
         return luce_host::launch(kern, grid, block, 0, stream, xq, xs, wq, ws, bias, nt, N, K, wk, out, ldo);
     };
@@ -1119,6 +1140,11 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
     consider<CfgPair, TO>(plan, dev, sms, T, N, K, COST_PAIR, 2, ROWS, 2 * ROWS, 32);
     if (T > 2 * ROWS)
         consider<CfgWide, TO>(plan, dev, sms, T, N, K, COST_WIDE, 4, 2 * ROWS + 32, 4 * ROWS, 32);
+    // few tokens and weights: the stream, eight tokens at a time
+    const VecSplit vs = vec_split(K, 1);
+    const float mb = (float)N * (float)(vs.wk * ((vs.slice + 511) / 512 * 512)) / 1e6f;
+    if (T > 8 && T <= 8 * 65535 && VUS_SETUP + VUS_MB * (float)((T + 7) / 8) * mb < plan.us)
+        return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
     if (plan.cfg == 1)
         return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
     if (plan.cfg == 2)

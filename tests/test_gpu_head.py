@@ -218,7 +218,8 @@ def test_linear_working_sizes(T, N, K, dtype):
 # few and many tiles of every width, with and without a split of K
 TILES = [(37, 165, 16), (22, 39, 352), (17, 10421, 16), (373, 19, 1936), (1281, 398, 16), (465, 18, 2752), (810, 2188, 16),
          (697, 19, 3216), (50, 10020, 3616), (51, 4875, 5200), (475, 14942, 16), (1219, 165, 2848), (354, 16147, 16),
-         (1395, 137, 4864), (137, 13219, 800), (130, 3554, 3952), (325, 6638, 1696), (210, 12862, 1296), (232, 13600, 2128)]
+         (1395, 137, 4864), (137, 13219, 800), (130, 3554, 3952), (325, 6638, 1696), (210, 12862, 1296), (232, 13600, 2128),
+         (223, 620, 16), (9, 3957, 1344), (17, 1759, 2160), (639, 58, 2224), (680, 36, 4768)]
 
 
 @pytest.mark.parametrize("T,N,K", TILES)
@@ -226,6 +227,13 @@ def test_linear_tiles_of_every_width(T, N, K):
     check_linear(T, N, K, f32, bias=True, seed=T)
     full = lambda r, v: torch.full((r, K), v, dtype=torch.int8)  # noqa: E731
     check_linear(T, N, K, f32, xq=full(T, 127), wq=full(N, 125))
+
+
+@pytest.mark.parametrize("T,N,K", [(9, 1, 16), (16, 33, 4096), (17, 500, 1040), (70, 130, 9184), (250, 64, 8192),
+                                   (524280, 2, 16), (524281, 3, 16)])
+def test_linear_eight_tokens_at_a_time(T, N, K):
+    # few weights: the last tokens fill an eighth, or all; as many eights as a grid holds, and more
+    check_linear(T, N, K, bf16, bias=True, seed=T)
 
 
 @pytest.mark.parametrize("K", [1008, 1024, 1040, 2048, 4096, 16384, 65536])
