@@ -112,28 +112,24 @@ template <bool S16> struct Slots {
             old = seen;
         }
     }
-    // the slots of N tokens from `at` (a multiple of N)
-    template <int N> __device__ __forceinline__ void get_n(int at, uint32_t (&c)[N]) const
+    // the slots of N tokens from `at` (a multiple of N), as words
+    template <int N> static constexpr int WORDS = S16 && N > 1 ? N / 2 : N;
+    template <int N> __device__ __forceinline__ void get_words(int at, uint32_t (&x)[WORDS<N>]) const
     {
-        if constexpr (N == 1) {
-            c[0] = get(at);
-        } else if constexpr (S16) {
+        if constexpr (N == 1)
+            x[0] = get(at);
+        else if constexpr (S16)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(base + 2 * at));
+        else
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(base + 4 * at));
+    }
+    template <int N> static __device__ __forceinline__ void unpack(const uint32_t (&x)[WORDS<N>], uint32_t (&c)[N])
+    {
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                uint32_t x, y;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(base + 2 * (at + i)));
-                c[i] = x & 0xffffu;
-                c[i + 1] = x >> 16;
-                c[i + 2] = y & 0xffffu;
-                c[i + 3] = y >> 16;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i += 4)
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(c[i]), "=r"(c[i + 1]), "=r"(c[i + 2]), "=r"(c[i + 3])
-                             : "r"(base + 4 * (at + i)));
-        }
+        for (int i = 0; i < N; i++)
+            c[i] = !S16 || N == 1 ? x[i] : i & 1 ? x[i / 2] >> 16 : x[i / 2] & 0xffffu;
     }
 };
 
@@ -383,26 +379,37 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     auto finish = [&](auto &w, int u) {
         constexpr int N = sizeof(w) / sizeof(float);
         if (a.hist) {
-            uint32_t c[N], any = 0;
-            slots.template get_n<N>(u, c);
-            if (S16 && (uint32_t)(apart - u) < (uint32_t)N) {
+            uint32_t x[Slots<S16>::template WORDS<N>], any = 0;
+            slots.template get_words<N>(u, x);
 #pragma unroll
-                for (int e = 0; e < N; e++)
-                    c[e] += u + e == apart ? 2u : 0u;
-            }
+            for (uint32_t word : x)
+                any |= word;
+            const bool has_apart = S16 && (uint32_t)(apart - u) < (uint32_t)N;
+            if (any || has_apart) {
+                uint32_t c[N];
+                slots.template unpack<N>(x, c);
+                if (has_apart) {
 #pragma unroll
-            for (int e = 0; e < N; e++)
-                any |= c[e];
-            if (any)
+                    for (int e = 0; e < N; e++)
+                        c[e] += u + e == apart ? 2u : 0u;
+                }
                 penalize<S16, N>(w, c, rep, rinv, low, freq, pres);
+            }
         }
         if (bias_at) {
-            uint32_t j[N];
-            places.template get_n<N>(u, j);
+            uint32_t x[Slots<S16>::template WORDS<N>], any = 0;
+            places.template get_words<N>(u, x);
 #pragma unroll
-            for (int e = 0; e < N; e++)
-                if (j[e])
-                    w[e] = __fadd_rn(w[e], vals[j[e] - 1]);
+            for (uint32_t word : x)
+                any |= word;
+            if (any) {
+                uint32_t j[N];
+                places.template unpack<N>(x, j);
+#pragma unroll
+                for (int e = 0; e < N; e++)
+                    if (j[e])
+                        w[e] = __fadd_rn(w[e], vals[j[e] - 1]);
+            }
         }
         if (mr) {
             const int v = u - sh, at = (v >> 5) + 1;
