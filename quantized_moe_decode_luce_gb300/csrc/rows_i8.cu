@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(1024)
             }
         } else if (whole && gamma16 && e0 + V + 4 <= n) {
             // the 16-byte pieces of gamma around the chunk, moved down by the row's e0 mod 4 (8191 x
-            // 4099 bf16 rows with a residual: 65.0 us, with loads of single elements 71.2)
+            // 4099 bf16 rows with a residual: 63.8 us, with loads of single elements 71.2)
             const int s = e0 & 3;
             float h[V + 4];
 #pragma unroll
@@ -431,7 +431,7 @@ luce_status run_rows(const void *vx, const void *vres, void *vsum, const float *
     const bool one_offset = (!res || off(res) == off(x)) && (!xsum || off(xsum) == off(x));
     const int chunks = al ? H / V : (H + V - 1) / V + 1; // 16-byte pieces of a row
     // one chunk a thread for few rows, or rows that a warp holds; 32 values for many (fp32 with a
-    // gamma: 16, whose loads are enough in flight; 8191 x 4096: 64.9 us, with 32 82.6 us)
+    // gamma: 16, whose loads are enough in flight; 8191 x 4096: 63.2 us, with 32 82.6 us)
     const int sms = luce_host::sm_count();
     int nch = T <= 2 * sms || chunks <= 32 ? 1 : T < 16 * sms || (gamma && V == 4) ? 16 / V : 32 / V;
     while (nch < 32 / V && chunks > 1024 * nch)
