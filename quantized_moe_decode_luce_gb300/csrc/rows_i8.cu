@@ -416,6 +416,35 @@ luce_status launch_rows(const TX *x, const TX *res, TX *xsum, const float *gamma
     return aligned_rows ? run(k_rows_i8<TX, NCH, true, false>) : run(k_rows_i8<TX, NCH, false, false>);
 }
 
+// Chunks of a thread (of V values each) for T rows of `chunks` chunks.  One
+// chunk makes the shortest way through a row, but holds many threads, whose
+// totals and divisions many rows then pay for; more chunks leave room for more
+// rows on an SM.  Every choice timed for seven widths and 200 to 8191 rows, in
+// us (one, two, four chunks; eight for fp32):
+//   quantize bf16  512 x 1024: 2.1 2.4 3.3        1024 x 14336: -  18.3 14.1
+//                  512 x 4099: 5.8 4.9 5.5        2048 x 6319: 31.3 16.4 14.2
+//   quantize fp32  512 x 1024: 2.2 2.3 2.5 3.1    2048 x 8192:  -  20.0 19.3 16.6
+//   norm bf16     4000 x 4096: 22.9 23.6 24.5     2048 x 6319: 55.4 33.2 29.6
+//   norm fp32      512 x 1024: 3.7 3.8 4.1 6.6    2048 x 4096: 21.9 21.3 18.1 23.7
+int chunks_of_a_thread(int V, bool norm, bool aligned_rows, int T, int chunks)
+{
+    const int64_t work = (int64_t)T * chunks, K = 1024;
+    if (chunks <= 32)
+        return 1; // a row to a warp, or less
+    if (norm && V == 8) {
+        if (aligned_rows)
+            return chunks <= 1024 ? 1 : 4;
+        return work <= 110 * K ? 1 : chunks <= 600 || work <= 200 * K ? 2 : 4;
+    }
+    if (norm)
+        return work <= 250 * K ? 1 : 4;
+    if (work <= (aligned_rows ? 280 : 110) * K)
+        return 1;
+    if (V == 8)
+        return (aligned_rows ? (work > 450 * K && chunks >= 512) || chunks > 1024 : work > 330 * K) ? 4 : 2;
+    return (aligned_rows ? work > 2000 * K || (work > 600 * K && chunks >= 2048) : work > 500 * K) ? 8 : 2;
+}
+
 template <typename TX>
 luce_status run_rows(const void *vx, const void *vres, void *vsum, const float *gamma, float eps, int T, int H,
                      int8_t *q, float *scale, void *vstream)
@@ -430,10 +459,7 @@ luce_status run_rows(const void *vx, const void *vres, void *vsum, const float *
     auto off = [](const void *p) { return reinterpret_cast<uintptr_t>(p) & 15; };
     const bool one_offset = (!res || off(res) == off(x)) && (!xsum || off(xsum) == off(x));
     const int chunks = al ? H / V : (H + V - 1) / V + 1; // 16-byte pieces of a row
-    // one chunk a thread for few rows, or rows that a warp holds; 32 values for many (fp32 with a
-    // gamma: 16, whose loads are enough in flight; 8191 x 4096: 63.2 us, with 32 82.6 us)
-    const int sms = luce_host::sm_count();
-    int nch = T <= 2 * sms || chunks <= 32 ? 1 : T < 16 * sms || (gamma && V == 4) ? 16 / V : 32 / V;
+    int nch = chunks_of_a_thread(V, gamma != nullptr, al, T, chunks);
     while (nch < 32 / V && chunks > 1024 * nch)
         nch *= 2;
     if (!one_offset || chunks > 1024 * nch)
