@@ -157,36 +157,61 @@ __global__ void __launch_bounds__(1024)
         TX e[V];
     };
     Chunk cx[NCH], cr[NCH];
+    auto first = [&](int c) { return (int)(threadIdx.x + c * lanes) * V - a; }; // element of the thread's chunk c
+    auto is_whole = [&](int e0) { return ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n; };
+    auto load_edge = [&](Chunk &c, const TX *p, int e0) { // those of them that lie in the row, if not all do
+        if (e0 >= n)
+            return;
+        // whole where the neighbouring row fills it (and nothing is stored to it
+        // meanwhile), its other elements set to zero
+        if (!in_place && (long long)row + e0 >= 0 && row + e0 + V <= (size_t)T * H) {
+            c.w = *reinterpret_cast<const uint4 *>(p + e0);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (e0 + i < 0 || e0 + i >= n)
+                    c.e[i] = from_f32<TX>(0.0f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (e0 + i >= 0 && e0 + i < n)
+                    c.e[i] = p[e0 + i];
+        }
+    };
     auto load = [&](Chunk &c, const TX *p, int e0) { // elements e0 .. e0 + V - 1 of the row
-        if (ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n) {
+        if (is_whole(e0)) {
             c.w = *reinterpret_cast<const uint4 *>(p + e0);
         } else {
             c.w = make_uint4(0, 0, 0, 0);
-            if (!ALIGNED && e0 + V > 0 && e0 < n) {
-                // a chunk over the row's end: whole where the neighbouring row fills it (and
-                // nothing is stored to it meanwhile), its other elements set to zero
-                if (!in_place && (long long)row + e0 >= 0 && row + e0 + V <= (size_t)T * H) {
-                    c.w = *reinterpret_cast<const uint4 *>(p + e0);
-#pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (e0 + i < 0 || e0 + i >= n)
-                            c.e[i] = from_f32<TX>(0.0f);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (e0 + i >= 0 && e0 + i < n)
-                            c.e[i] = p[e0 + i];
-                }
-            }
+            if (!ALIGNED && !NORM)
+                load_edge(c, p, e0);
         }
     };
 #pragma unroll
     for (int c = 0; c < NCH; c++)
-        load(cx[c], x + row, (int)(threadIdx.x + c * lanes) * V - a);
-    if (res) {
+        load(cx[c], x + row, first(c));
+    if (NORM && res) {
 #pragma unroll
         for (int c = 0; c < NCH; c++)
-            load(cr[c], res + row, (int)(threadIdx.x + c * lanes) * V - a);
+            load(cr[c], res + row, first(c));
+    }
+    if (!ALIGNED && NORM) {
+        // the two threads of a row that hold its edges, apart from the others (3282 x 7374
+        // fp32 rows with a residual: 60.2 us, chunk by chunk as above 68.4; luce_quantize_i8
+        // of 8191 x 4099 fp32: 39.6 and 36.8)
+        bool edge = false;
+#pragma unroll
+        for (int c = 0; c < NCH; c++)
+            edge |= !is_whole(first(c)) && first(c) < n;
+        if (edge) {
+#pragma unroll
+            for (int c = 0; c < NCH; c++) {
+                if (is_whole(first(c)))
+                    continue;
+                load_edge(cx[c], x + row, first(c));
+                if (res)
+                    load_edge(cr[c], res + row, first(c));
+            }
+        }
     }
     // gamma of a chunk (one for elements behind the row's ends, which are zero)
     auto gammas = [&](int e0, bool whole, float (&g)[V]) {
@@ -200,7 +225,7 @@ __global__ void __launch_bounds__(1024)
             }
         } else if (whole && gamma16 && e0 + V + 4 <= n) {
             // the 16-byte pieces of gamma around the chunk, moved down by the row's e0 mod 4 (8191 x
-            // 4099 bf16 rows with a residual: 63.8 us, with loads of single elements 71.2)
+            // 4099 bf16 rows with a residual: 65.0 us, with loads of single elements 71.2)
             const int s = e0 & 3;
             float h[V + 4];
 #pragma unroll
@@ -234,16 +259,16 @@ __global__ void __launch_bounds__(1024)
     if constexpr (EARLY) {
 #pragma unroll
         for (int c = 0; c < NCH; c++) {
-            const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
-            gammas(e0, ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n, p[c]);
+            const int e0 = first(c);
+            gammas(e0, is_whole(e0), p[c]);
         }
     }
     float ss = 0.0f, m = 0.0f;
     uint32_t mm = 0;
 #pragma unroll
     for (int c = 0; c < NCH; c++) {
-        const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
-        const bool whole = ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n;
+        const int e0 = first(c);
+        const bool whole = is_whole(e0);
         if (res) {
 #pragma unroll
             for (int i = 0; i < V; i++)
@@ -300,8 +325,8 @@ __global__ void __launch_bounds__(1024)
     uint32_t *buf = codes + threadIdx.y * pitch;
 #pragma unroll
     for (int c = 0; c < NCH; c++) {
-        const int e0 = (int)(threadIdx.x + c * lanes) * V - a;
-        const bool whole = ALIGNED ? e0 < n : e0 >= 0 && e0 + V <= n;
+        const int e0 = first(c);
+        const bool whole = is_whole(e0);
         uint32_t w[V / 4] = {};
         if (live) {
             if constexpr (NORM) {
