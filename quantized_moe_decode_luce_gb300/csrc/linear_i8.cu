@@ -22,9 +22,9 @@ using namespace luce;
 
 // The epilogue of every kernel of this file: four roundings to fp32 at most,
 // then the output type's, so that all of them give the same bits.
-__device__ __forceinline__ float epilogue(int isum, float xs, float ws, bool add, float bias)
+__device__ __forceinline__ float epilogue(float isum, float xs, float ws, bool add, float bias)
 {
-    const float v = __fmul_rn((float)isum, __fmul_rn(xs, ws));
+    const float v = __fmul_rn(isum, __fmul_rn(xs, ws));
     return add ? __fadd_rn(v, bias) : v;
 }
 __device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
@@ -752,6 +752,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
         uint32_t dphase = 0, slot = 0;
         bool ok = true;
         int acc[HALVES][ECOLS];
+        // K of one chunk: the accumulators are the sums, and stay floats (1860 x 113600 x
+        // 128: 186 us, converted to int32 and back 220; no gain for two halves)
+        constexpr bool AS_FLOATS = HALVES == 1; // sums are stored as floats
+        const bool raw = AS_FLOATS && a.sk == 1 && nu <= CHUNK;
         // accumulator slot `ds` into the sums of half h (set, or added to)
         auto read_back = [&](int (&s)[ECOLS], uint32_t ds, bool set) {
             if (!tc_wait_warp(&dfull[ds], (dphase >> ds) & 1, abort_flag))
@@ -763,7 +767,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                 uint32_t v[16];
                 tmem_ld16(td + ds * C::DCOLS + c, v);
                 tmem_wait_ld();
-                if (set) {
+                if (raw) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        s[c + i] = __float_as_int(__fadd_rn(__uint_as_float(v[i]), 0.0f)); // (no -0, as of an int32)
+                } else if (set) {
 #pragma unroll
                     for (int i = 0; i < 16; i++)
                         s[c + i] = __float2int_rn(__uint_as_float(v[i]));
@@ -811,6 +819,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                 const bool live = n < a.N;
                 const float wsn = live ? a.ws[n] : 0.0f, bn = live && a.bias ? a.bias[n] : 0.0f;
                 const bool add = a.bias != nullptr;
+                if (AS_FLOATS && !raw) {
+#pragma unroll
+                    for (int h = 0; h < HALVES; h++)
+#pragma unroll
+                        for (int c = 0; c < ECOLS; c++)
+                            acc[h][c] = __float_as_int((float)acc[h][c]);
+                }
 #pragma unroll
                 for (int h = 0; h < HALVES; h++) {
                     const int t0 = x_tile(tile) + h * a.nh[0] + col0, nt = min(a.nh[h] - col0, a.T - t0);
@@ -822,7 +837,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                         const float xl = c0 + lane < nt ? a.xs[t0 + c0 + lane] : 0.0f;
 #pragma unroll
                         for (int c = 0; c < 32; c++) {
-                            const float v = epilogue(acc[h][c0 + c], __shfl_sync(0xffffffffu, xl, c), wsn, add, bn);
+                            const int s = acc[h][c0 + c];
+                            const float v = epilogue(AS_FLOATS ? __int_as_float(s) : (float)s,
+                                                     __shfl_sync(0xffffffffu, xl, c), wsn, add, bn);
                             if (live && c0 + c < nt)
                                 store_out(o, v);
                             o += a.ldo;

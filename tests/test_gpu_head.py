@@ -249,6 +249,18 @@ def test_linear_sums_are_exact_at_the_largest_codes(T, K):
     check_linear(T, N, K, xq=x, wq=w)
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 40, 512), (100, 3000, 512), (100, 3000, 1040), (300, 12000, 512), (300, 12000, 1024)])
+def test_linear_sums_of_nothing_are_positive_zeros(T, N, K):
+    # zeros times negative codes: the sum's sign is an int32's, whatever the kernel
+    out = torch.empty((T, N), device="cuda")
+    ones = torch.ones(max(T, N), device="cuda")
+    x = torch.zeros((T, K), dtype=torch.int8, device="cuda")
+    w = torch.full((N, K), -7, dtype=torch.int8, device="cuda")
+    for xq, wq in ((x, w), (torch.full_like(x, -3), torch.zeros_like(w))):
+        B.luce_linear_i8(xq, ones[:T], wq, ones[:N], None, out)
+        assert torch.all(out == 0) and not torch.any(torch.signbit(out))
+
+
 @pytest.mark.parametrize("T", [1, 6, 30, 130, 280])
 def test_linear_into_a_slice_of_wider_rows(T):
     check_linear(T, 260, 512, f32, gap=12)
