@@ -788,6 +788,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             return true;
         };
         for (int tile = c0; tile < a.tiles && ok; tile += cstep) {
+            // the scales, requested before the sums are waited for
+            const int n = w_row(tile) + row;
+            const bool live = a.sk == 1 && n < a.N;
+            const float wsn = live ? a.ws[n] : 0.0f, bn = live && a.bias ? a.bias[n] : 0.0f;
+            float xl[HALVES][ECOLS / 32];
+#pragma unroll
+            for (int h = 0; h < HALVES; h++)
+#pragma unroll
+                for (int c = 0; c < ECOLS; c += 32) {
+                    const int t = h * a.nh[0] + col0 + c + lane; // (of the tile)
+                    xl[h][c / 32] = a.sk == 1 && col0 + c + lane < a.nh[h] && x_tile(tile) + t < a.T ? a.xs[x_tile(tile) + t] : 0.0f;
+                }
             // the chunks in the order in which they end
             if constexpr (HALVES == 1) {
                 for (int u = 0; u < nu && ok; u += CHUNK, slot ^= 1)
@@ -803,7 +815,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             }
             if (!ok)
                 break;
-            const int n = w_row(tile) + row;
             if (a.sk > 1) {
                 // (one tile per cluster) the int32 sums, where the stages were
 #pragma unroll
@@ -816,8 +827,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             } else {
                 // a thread holds tokens of one channel: a warp stores 32 channels of
                 // a token; the tokens' scales come from the lanes that loaded them
-                const bool live = n < a.N;
-                const float wsn = live ? a.ws[n] : 0.0f, bn = live && a.bias ? a.bias[n] : 0.0f;
                 const bool add = a.bias != nullptr;
                 if (AS_FLOATS && !raw) {
 #pragma unroll
@@ -834,12 +843,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                     for (int c0 = 0; c0 < ECOLS; c0 += 32) {
                         if (c0 >= nt)
                             break;
-                        const float xl = c0 + lane < nt ? a.xs[t0 + c0 + lane] : 0.0f;
 #pragma unroll
                         for (int c = 0; c < 32; c++) {
                             const int s = acc[h][c0 + c];
                             const float v = epilogue(AS_FLOATS ? __int_as_float(s) : (float)s,
-                                                     __shfl_sync(0xffffffffu, xl, c), wsn, add, bn);
+                                                     __shfl_sync(0xffffffffu, xl[h][c0 / 32], c), wsn, add, bn);
                             if (live && c0 + c < nt)
                                 store_out(o, v);
                             o += a.ldo;
