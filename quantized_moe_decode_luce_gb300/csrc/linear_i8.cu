@@ -248,7 +248,7 @@ struct TcArgs {
     int xbox;         // token rows of a box
     int nb, nh[2];    // tokens of a tile, and of its halves (multiples of 16, of 32 for a pair)
     int mt, tiles;    // channel tiles, tiles in all (channel tiles fastest)
-    int sk;           // CTA groups along K (a power of two)
+    int sk;           // CTA groups along K
 };
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
@@ -1002,15 +1002,15 @@ template <class C, typename TO> struct Tc {
     }
     // Groups along K, while all tiles' clusters are resident at once: a second
     // round costs more than the split gains (100 x 4096 x 4096: clusters of 8 CTAs, of
-    // which not all 16 fit, 24.7 us; clusters of 4 16.9 us; pairs alone 18.5 us)
+    // which not all 16 fit, 24.7 us; clusters of 4 16.9 us; pairs alone 18.5 us).
+    // Any number of groups that shortens the longest share (61 x 5120 x 5120, 40 tiles:
+    // three groups 12.6 us, two 14.7).
     static int split(int dev, int sms, int64_t tiles, int units)
     {
         int sk = 1;
-        for (int s = 2; s * C::CG <= SK_MAX && s <= units && tiles * s * C::CG <= sms; s *= 2) {
-            if (tiles > clusters_at_once(dev, s * C::CG))
-                break;
-            sk = s;
-        }
+        for (int s = 2; s * C::CG <= SK_MAX && s <= units && tiles * s * C::CG <= sms; s++)
+            if ((units + s - 1) / s < (units + sk - 1) / sk && tiles <= clusters_at_once(dev, s * C::CG))
+                sk = s;
         return sk;
     }
 };
