@@ -1025,7 +1025,14 @@ template <class C, typename TO> struct Tc {
 // 1024 x 1024 (7.4) and 9.5 for 137 x 88 x 800 (6.1).
 struct Plan {
     float us = INFINITY;
-    int cfg = 0, tokens = 0;
+    int cfg = 0, tokens = 0; // configuration 0 is the stream
+};
+// Where a tile's last round is not full: the channels of the whole rounds, by
+// themselves, and a guess of the time with the rest spread over all SMs.
+struct Part {
+    float guess = INFINITY;
+    Plan plan;
+    int channels = 0;
 };
 struct Cost {
     float setup, unit, unit_token, token; // of a launch; of a unit; a unit's share per token of the tile; its sums per token
@@ -1040,22 +1047,58 @@ constexpr Cost COST_WIDE{5.83f, 0.616f, 0.0f, 0.0147f, -1.5f, 0.0142f, 1.7f};
 // 250 tokens: 16 x 1024 x 1024 2.5 us, tensor cores 6.0; 64 x 148 x 3376 3.2 and 6.8;
 // 64 x 2048 x 2048 11.8 and 8.1).
 constexpr float VUS_SETUP = 2.2f, VUS_MB = 0.28f;
+constexpr float SECOND_LAUNCH = 0.95f; // what two launches may take of one's time
+
+// Warps along K, as many as leave a slice of one batch, and the slice.
+struct VecSplit {
+    int wk, slice;
+};
+VecSplit vec_split(int K, int vu)
+{
+    int wk = 1;
+    while (wk < V_WARPS && K / wk > 512 * vu)
+        wk *= 2;
+    return {wk, ((K >> 4) + wk - 1) / wk << 4};
+}
 
 template <class C, typename TO>
-void consider(Plan &best, int dev, int sms, int T, int N, int K, const Cost &c, int id, int first, int last, int step)
+void consider(Plan &best, Part &part, int dev, int sms, int T, int N, int K, const Cost &c, int id, int first, int last, int step)
 {
     const int units = (K + KU - 1) / KU;
     const int64_t mt = ((int64_t)N + RM * C::CG - 1) / (RM * C::CG);
     for (int w = first; w <= last && w - step < T; w += step) {
-        const int64_t tiles = mt * ((T + w - 1) / w);
+        const int64_t tt = (T + w - 1) / w, tiles = mt * tt;
         const int sk = Tc<C, TO>::split(dev, sms, tiles, units), at_once = sms / C::CG;
-        const float rounds = sk > 1 ? 1.0f : (float)((tiles + at_once - 1) / at_once);
-        const float us = c.setup + rounds * (float)((units + sk - 1) / sk) * (c.unit + c.unit_token * (float)w) +
-                         c.token * (float)w + (rounds - 1.0f) * c.round +
-                         (sk > 1 ? c.split + c.split_token * (float)w : 0.0f);
-        if (us < best.us)
-            best = Plan{us, id, w};
+        const int64_t rounds = sk > 1 ? 1 : (tiles + at_once - 1) / at_once;
+        const float share = (float)((units + sk - 1) / sk) * (c.unit + c.unit_token * (float)w);
+        auto time = [&](float r) {
+            return c.setup + r * share + c.token * (float)w + (r - 1.0f) * c.round +
+                   (sk > 1 ? c.split + c.split_token * (float)w : 0.0f);
+        };
+        if (time((float)rounds) < best.us)
+            best = Plan{time((float)rounds), id, w};
+        const int64_t full = tiles / at_once * at_once / tt; // channel tiles of the whole rounds
+        if (rounds > 1 && full > 0 && full < mt) {
+            const float us = time((float)(rounds - 1)), rest = (float)((mt - full) * tt) / (float)at_once;
+            if (us + c.setup + rest * share < part.guess)
+                part = Part{us + c.setup + rest * share, Plan{us, id, w}, (int)full * RM * C::CG};
+        }
     }
+}
+
+template <typename TO> Plan plan_product(int dev, int sms, int T, int N, int K, Part &part)
+{
+    Plan best;
+    consider<CfgOne, TO>(best, part, dev, sms, T, N, K, COST_ONE, 1, 16, ROWS, 16);
+    consider<CfgPair, TO>(best, part, dev, sms, T, N, K, COST_PAIR, 2, ROWS, 2 * ROWS, 32);
+    if (T > 2 * ROWS)
+        consider<CfgWide, TO>(best, part, dev, sms, T, N, K, COST_WIDE, 4, 2 * ROWS + 32, 4 * ROWS, 32);
+    const VecSplit vs = vec_split(K, 1);
+    const float mb = (float)N * (float)(vs.wk * ((vs.slice + 511) / 512 * 512)) / 1e6f;
+    const float us = VUS_SETUP + VUS_MB * (float)((T + 7) / 8) * mb;
+    if (us < best.us && T <= 8 * 65535)
+        best = Plan{us, 0, 8};
+    return best;
 }
 
 template <class C, typename TO>
@@ -1112,18 +1155,6 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return p < q + nb && q < p + na;
 }
 
-// Warps along K, as many as leave a slice of one batch, and the slice.
-struct VecSplit {
-    int wk, slice;
-};
-VecSplit vec_split(int K, int vu)
-{
-    int wk = 1;
-    while (wk < V_WARPS && K / wk > 512 * vu)
-        wk *= 2;
-    return {wk, ((K >> 4) + wk - 1) / wk << 4};
-}
-
 template <int T, int VU, typename TO>
 luce_status launch_vec(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int nt,
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
@@ -1160,21 +1191,32 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
         return LUCE_ERR_CUDA;
     }
     const int sms = luce_host::sm_count();
-    Plan plan;
-    consider<CfgOne, TO>(plan, dev, sms, T, N, K, COST_ONE, 1, 16, ROWS, 16);
-    consider<CfgPair, TO>(plan, dev, sms, T, N, K, COST_PAIR, 2, ROWS, 2 * ROWS, 32);
-    if (T > 2 * ROWS)
-        consider<CfgWide, TO>(plan, dev, sms, T, N, K, COST_WIDE, 4, 2 * ROWS + 32, 4 * ROWS, 32);
-    // few tokens and weights: the stream, eight tokens at a time
-    const VecSplit vs = vec_split(K, 1);
-    const float mb = (float)N * (float)(vs.wk * ((vs.slice + 511) / 512 * 512)) / 1e6f;
-    if (T > 8 && T <= 8 * 65535 && VUS_SETUP + VUS_MB * (float)((T + 7) / 8) * mb < plan.us)
-        return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (plan.cfg == 1)
-        return launch_tc<CfgOne>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
-    if (plan.cfg == 2)
-        return launch_tc<CfgPair>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
-    return launch_tc<CfgWide>(xq, xs, wq, ws, bias, T, N, K, out, ldo, plan.tokens, dev, sms, stream);
+    auto run = [&](const Plan &plan, int n0, int n) { // channels n0 .. n0 + n - 1
+        const int8_t *w = wq + (size_t)n0 * K;
+        const float *s = ws + n0, *b = bias ? bias + n0 : nullptr;
+        switch (plan.cfg) {
+        case 0:
+            return launch_vec<8, 1>(xq, xs, w, s, b, T, n, K, out + n0, ldo, stream);
+        case 1:
+            return launch_tc<CfgOne>(xq, xs, w, s, b, T, n, K, out + n0, ldo, plan.tokens, dev, sms, stream);
+        case 2:
+            return launch_tc<CfgPair>(xq, xs, w, s, b, T, n, K, out + n0, ldo, plan.tokens, dev, sms, stream);
+        default:
+            return launch_tc<CfgWide>(xq, xs, w, s, b, T, n, K, out + n0, ldo, plan.tokens, dev, sms, stream);
+        }
+    };
+    Part part, none;
+    const Plan plan = plan_product<TO>(dev, sms, T, N, K, part);
+    // a round that few tiles are left for: a launch of its own, whose tiles split K
+    // (9 x 21891 x 10240, 171 tiles: 46.8 us, in one launch 59.8; 512 x 5120 x 13824: 57.7 and 70.2)
+    if (part.guess < SECOND_LAUNCH * plan.us) {
+        const Plan rest = plan_product<TO>(dev, sms, T, N - part.channels, K, none);
+        if (part.plan.us + rest.us < SECOND_LAUNCH * plan.us) {
+            const luce_status st = run(part.plan, 0, part.channels);
+            return st == LUCE_OK ? run(rest, part.channels, N - part.channels) : st;
+        }
+    }
+    return run(plan, 0, N);
 }
 
 } // namespace

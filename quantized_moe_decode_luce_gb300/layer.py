@@ -113,7 +113,7 @@ class GreedyHead:
     """The end of a step for R rows (tokens, or the columns of a verify step): the residual sum's
     RMS norm in int8, the vocabulary product, penalties, biases and masks, the greedy tokens.
 
-    Owns every buffer; `run` makes four launches and returns (idx [R] int32, val [R] fp32)."""
+    Owns every buffer; `run` makes four calls and returns (idx [R] int32, val [R] fp32)."""
 
     def __init__(self, R: int, gamma: torch.Tensor, eps: float, head: LinearI8):
         if head.K != gamma.numel():

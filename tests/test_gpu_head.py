@@ -229,6 +229,13 @@ def test_linear_tiles_of_every_width(T, N, K):
     check_linear(T, N, K, f32, xq=full(T, 127), wq=full(N, 125))
 
 
+@pytest.mark.parametrize("T,N,K", [(9, 21891, 10240), (32, 20480, 5120), (70, 20480, 6144), (260, 9800, 8192)])
+def test_linear_a_last_round_of_few_tiles(T, N, K):
+    # the channels behind the whole rounds of tiles, in their own launch: bias, scales and stride go with them
+    check_linear(T, N, K, bf16, bias=True, gap=6, seed=T)
+    assert B.luce_get_fault() == 0
+
+
 @pytest.mark.parametrize("T,N,K", [(9, 1, 16), (16, 33, 4096), (17, 500, 1040), (70, 130, 9184), (250, 64, 8192),
                                    (524280, 2, 16), (524281, 3, 16)])
 def test_linear_eight_tokens_at_a_time(T, N, K):
