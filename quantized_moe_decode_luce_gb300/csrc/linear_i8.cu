@@ -1040,7 +1040,7 @@ struct Cost {
 };
 constexpr Cost COST_ONE{3.83f, 0.333f, 0.0006f, 0.0302f, 1.09f, 0.0f, 0.38f};
 constexpr Cost COST_PAIR{5.19f, 0.346f, 0.0f, 0.0201f, 0.07f, 0.0128f, 0.54f};
-constexpr Cost COST_WIDE{5.83f, 0.616f, 0.0f, 0.0147f, -1.5f, 0.0142f, 1.7f};
+constexpr Cost COST_WIDE{6.53f, 0.616f, 0.0f, 0.0147f, -1.5f, 0.0142f, 1.7f};
 
 // The same of the stream, eight tokens at a time: setup, and a megabyte of the
 // weights as its warps go through them (fits to ten weights of 0.1 to 8 MB and 9 to
