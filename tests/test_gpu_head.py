@@ -102,6 +102,20 @@ HS = [1, 2, 7, 31, 32, 33, 64, 100, 255, 516, 1000, 1024, 1025, 2048, 4096, 4099
       32768, 65536]
 
 
+# every number of chunks to a thread: few and many rows of short and long ones
+MANY = [(60, 1000), (700, 1000), (2300, 1001), (330, 758), (3600, 758), (150, 4099), (400, 4099), (900, 4099), (1100, 4096),
+        (900, 4728), (300, 6319), (260, 8192), (700, 8192), (300, 14336), (300, 16390)]
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("T,H", MANY)
+def test_many_rows_of_every_width(T, H, dtype):
+    x, gamma = rows_input(T, H, dtype, T + H), torch.randn(H, generator=gen(H))
+    check_rows(x)
+    check_rows(x, gamma, 1e-6)
+    check_rows(x, gamma, 1e-6, rows_input(T, H, dtype, T), in_place="x" if T % 2 else None)
+
+
 @pytest.mark.parametrize("dtype", [f32, bf16, f16])
 @pytest.mark.parametrize("H", HS)
 def test_quantize_rows(H, dtype):
