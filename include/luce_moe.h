@@ -436,8 +436,9 @@ LUCE_API luce_status luce_add_rmsnorm_i8(const void *x, const void *residual, vo
  *   out [T][N] of out_dtype, its rows ld_out elements apart (ld_out >= N;
  *     what lies between the rows is left as it was), aligned to the element
  * Requires K % 16 == 0, 16 <= K <= 65536, N >= 1, T >= 0, N and T below 2^24.
- * Under programmatic launch (luce_set_pdl) the kernel may read wq before it
- * waits for the previous kernel, so that kernel must not write it.
+ * Under programmatic launch (luce_set_pdl) nothing is read before the previous
+ * kernel is over: any operand may be its result, the weights that
+ * luce_quantize_i8 has just written among them.
  */
 LUCE_API luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq, const float *w_scale,
                                     const float *bias, int T, int N, int K, void *out, luce_dtype out_dtype,
@@ -561,10 +562,15 @@ LUCE_API luce_status luce_moe_layer(const float *logits, const float *bias, cons
  * dependent launch: each library kernel may then start before the previous
  * kernel on the stream has finished, run its prologue, and wait on the GPU
  * before it reads that kernel's results.  Kernels of other code never start
- * early (they do not signal), so expert weights written by any earlier
- * kernel are safe.  One extra rule holds while it is on:
- * luce_moe_down_combine reads ids, weights, offsets and routes before it
- * waits, and luce_moe_down_combine_q4k ids, weights and its weight rows, so
+ * early (they do not signal), and no kernel of the library writes Q8_0 or
+ * Q4_K blocks, which some kernels request before they wait: expert weights
+ * written by any earlier kernel are safe.  The library does write weights of
+ * luce_linear_i8 (luce_quantize_i8); luce_linear_i8, like every kernel of the
+ * int8 decode head, reads nothing before it waits.  Two extra rules hold while
+ * it is on.  luce_rmsnorm_router and luce_add_rmsnorm_router read w_router and
+ * gamma before they wait, so the launch immediately before them must not write
+ * those.  luce_moe_down_combine reads ids, weights, offsets and routes before
+ * it waits, and luce_moe_down_combine_q4k ids, weights and its weight rows, so
  * the call that produced them must not be the launch immediately before it
  * (in the order prep/group, glu_pair, down_combine, or route, glu_q4k,
  * down_combine_q4k, it never is).

@@ -104,9 +104,9 @@ __global__ void __launch_bounds__(V_WARPS * 32)
             for (int r = 0; r < VR; r++)
                 b[u][r] = k + 512 * u < k1 ? ldg_stream(w[r] + k + 512 * u) : make_uint4(0, 0, 0, 0);
     };
-    load(cur, kw * slice + 16 * lane); // the weights do not depend on the previous kernel
-    pdl_wait();
+    pdl_wait(); // (the weights too may be the previous kernel's: luce_quantize_i8 writes them)
     pdl_trigger();
+    load(cur, kw * slice + 16 * lane);
     int acc[V] = {};
     auto use = [&](int k) {
 #pragma unroll
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
     const int early = c0 < a.tiles ? min(nu, EARLY) : 0; // stages requested before anything else is set up
 
     if (warp == TMA_WARP) {
-        // the first stages: their barriers are this CTA's own, and the weights do
-        // not depend on the previous kernel
+        // the first stages: their barriers are this CTA's own; weights and tokens
+        // alike may be the previous kernel's
         if (elect_one()) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tw)) : "memory");
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tx)) : "memory");
@@ -515,13 +515,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
                 mbar_init(&full[i], 1);
             fence_mbar_init();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            for (int st = 0; st < early; st++)
-                load_w((uint32_t)st, st, w_row(c0));
         }
         pdl_wait();
         if (elect_one())
-            for (int st = 0; st < early; st++)
+            for (int st = 0; st < early; st++) {
+                load_w((uint32_t)st, st, w_row(c0));
                 load_x((uint32_t)st, st, x_tile(c0));
+            }
     }
     if (tid == CONV_WARP0 * 32) {
         for (int i = 0; i < NS; i++)
