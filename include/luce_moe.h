@@ -475,7 +475,8 @@ LUCE_API luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, cons
  *     ids >= V skipped with the fault bit; n_bias == 0 for none
  *   mask [n_masks][ld_mask] 32-bit words, ld_mask >= ceil(V / 32), or NULL
  *   mask_rows [R] int32: the mask of row r, < 0 for none (>= n_masks: none,
- *     with the fault bit); NULL when row r has mask r (n_masks >= R)
+ *     with the fault bit); NULL when row r has mask r (n_masks >= R).  With
+ *     no masks at all (mask NULL) it may be given if n_masks == 0
  * Requires 1 <= V < 2^31, 0 <= R <= 65535, ld_hist and n_bias below 2^30,
  * arrays aligned to their elements.  No workspace; deterministic (the counts
  * are whole numbers, kept in shared memory per stretch of the vocabulary).

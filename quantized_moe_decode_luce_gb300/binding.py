@@ -462,6 +462,9 @@ def luce_logits_process(logits, out, hist=None, hist_len=None, prompt_len=None, 
     if mask is not None:
         nm, ldm = _matrix(mask, "mask")[:2]
         mp = _addr(mask, _WORDS, (nm, ldm), dev, "mask")
+        # an empty tensor has no address, by which the library would know that there is a mask
+        if (nm > 0 and ldm == 0) or (nm == 0 and R > 0 and mask_rows is None):
+            raise LuceError("luce_logits_process", LUCE_ERR_INVALID_ARG)
     elif mask_rows is not None:
         raise ValueError("mask_rows needs mask")
 

@@ -234,6 +234,7 @@ PyObject *logits_process(PyObject *, PyObject *const *p, Py_ssize_t n)
             const at::Tensor *m = a.tensor(p[10], 2);
             nm = a.size(m, 0);
             ldm = a.size(m, 1);
+            a.ok = a.ok && nm > 0 && ldm > 0; // (no masks, or masks without words: binding.py)
             mp = a.data(p[10], a.ok && m->scalar_type() == ScalarType::UInt32 ? ScalarType::UInt32 : ScalarType::Int, nm, ldm);
         } else {
             a.ok = a.ok && p[11] == Py_None;

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     const TL *lr = static_cast<const TL *>(a.logits) + (size_t)r * a.ldl + c0;
     const uint32_t *mr = nullptr;
     bool bad = false;
-    if (a.mask) {
+    if (a.mask || a.mask_rows) {
         const int m = a.mask_rows ? a.mask_rows[r] : r;
         if (m >= a.nmasks)
             bad = true;
@@ -523,7 +523,7 @@ extern "C" luce_status luce_logits_process(const void *logits, luce_dtype dtype,
     if (n_bias < 0 || n_bias >= LIM || (hist && (ld_hist < 0 || ld_hist >= LIM)) || (mask && ld_mask < (V + 31) / 32) ||
         (mask && (n_masks < 1 || ld_mask > 8 * LIM || (!mask_rows && n_masks < R))))
         return LUCE_ERR_INVALID_ARG;
-    if ((hist == nullptr) != (hist_len == nullptr) || (!hist && prompt_len) || (!mask && mask_rows))
+    if ((hist == nullptr) != (hist_len == nullptr) || (!hist && prompt_len) || (!mask && mask_rows && n_masks != 0))
         return LUCE_ERR_INVALID_ARG;
     if (R == 0)
         return LUCE_OK;

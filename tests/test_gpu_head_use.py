@@ -9,7 +9,7 @@ import torch
 from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from quantized_moe_decode_luce_gb300.layer import LinearI8
-from test_gpu_head import _lib, _no_device_faults, codes, f32, gen, same  # noqa: F401  (fixtures of every test here)
+from test_gpu_head import (_lib, _no_device_faults, codes, f32, gen, logits_case, same)  # noqa: F401  (fixtures too)
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +44,40 @@ def test_weights_quantized_just_before_their_product(T, N, K, pdl):
     for i in range(20):
         same(outs[i], refs[i % 2])
     same(last, refs[0])
+
+
+# ----------------------------------------------------------------------------- masks
+@pytest.fixture(params=["call module", "python"])
+def both_ways(request, monkeypatch):
+    if request.param == "python":
+        monkeypatch.setattr(B, "_fast", None)
+
+
+def test_logits_masks_that_hold_nothing_are_refused(both_ways):
+    # an empty tensor is a mask all the same: a step with a grammar does not run without it
+    x, out = torch.randn((3, 64), generator=gen(1)).cuda(), torch.full((3, 64), 7.0, device="cuda")
+    rows = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for shape, mask_rows in (((0, 2), None), ((0, 0), None), ((3, 0), None), ((3, 0), rows), ((3, 1), rows), ((2, 2), None)):
+        mask = torch.zeros(shape, dtype=torch.int32, device="cuda")
+        with pytest.raises(B.LuceError):
+            B.luce_logits_process(x, out, mask=mask, mask_rows=mask_rows)
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0)
+    B.luce_logits_process(x[:0], out[:0], mask=torch.zeros((0, 2), dtype=torch.int32, device="cuda"))  # no rows: nothing
+
+
+@pytest.mark.allow_fault
+@pytest.mark.parametrize("groups", [(), ("hist", "bias")])
+def test_logits_rows_without_a_mask_need_no_masks(groups, both_ways):
+    V = 5000
+    c = logits_case(3, V, hist=30 if "hist" in groups else None, bias=4 if "bias" in groups else 0)
+    want = O.logits_process(**c)
+    kw = {k: v.cuda() for k, v in c.items()}
+    out = torch.empty((3, V), device="cuda")
+    for words in ((V + 31) // 32, 0):
+        none = torch.zeros((0, words), dtype=torch.int32, device="cuda")
+        for rows, fault in (([-1, -1, -1], 0), ([-1, 0, -1], B.LUCE_FAULT_BAD_ID)):
+            out.fill_(9.0)
+            B.luce_logits_process(out=out, mask=none, mask_rows=torch.tensor(rows, dtype=torch.int32, device="cuda"), **kw)
+            same(out, want)
+            assert B.luce_get_fault() == fault
