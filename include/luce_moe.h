@@ -393,6 +393,7 @@ LUCE_API luce_status luce_add_f32(const float *a, const float *b, float *out, in
  * and scale zero).  The value of a code is q_i * scale.
  * luce_rmsnorm_i8: the same of p_i = x_i * gamma_i, and
  *   scale = d * r,   r = 1 / sqrt(mean_i x_i^2 + eps)
+ * (zero where d is zero, whatever r is: eps may be zero, and so may a row),
  * so that q_i * scale stands for x_i r gamma_i.  The factor r is common to
  * the row and does not enter the codes: they depend on no sum, and are the
  * same bits whatever the order in which the squares are added (fp32).

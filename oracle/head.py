@@ -42,7 +42,8 @@ def rows_i8(x: torch.Tensor, gamma=None, eps: float = 0.0, residual=None):
     q = round_half_away(_fl(torch.where(live[:, None], p, torch.zeros_like(p)) / dd)).clamp(-127, 127)
     scale = d
     if gamma is not None:
-        scale = d / torch.sqrt(v.square().mean(dim=1) + float(torch.tensor(eps, dtype=f32)))
+        r2 = v.square().mean(dim=1) + float(torch.tensor(eps, dtype=f32))
+        scale = torch.where(d > 0, d / torch.sqrt(r2), d)  # (a row whose d is zero has scale zero, without 0 / 0)
     scale = torch.where(finite, scale, torch.full_like(scale, math.nan))
     return q.to(torch.int8), scale, s
 

@@ -112,10 +112,11 @@ template <int V> __device__ __forceinline__ void codes_of(const float (&p)[V], f
         w[i / 4] = __byte_perm(__byte_perm(u[i], u[i + 1], 0x0040), __byte_perm(u[i + 2], u[i + 3], 0x0040), 0x5410);
 }
 
+// (a row of zeros has scale zero whatever r is: 1 / 0 when eps is zero too)
 __device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, bool norm, bool finite)
 {
     const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
-    return !finite ? NAN : norm ? __fmul_rn(d, r) : d;
+    return !finite ? NAN : norm && d > 0.0f ? __fmul_rn(d, r) : d;
 }
 
 // ---------------------------------------------------------------------------

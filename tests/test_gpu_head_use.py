@@ -9,7 +9,8 @@ import torch
 from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from quantized_moe_decode_luce_gb300.layer import LinearI8
-from test_gpu_head import (_lib, _no_device_faults, codes, f32, gen, logits_case, same)  # noqa: F401  (fixtures too)
+from test_gpu_head import (_lib, _no_device_faults, bf16, check_rows, codes, f16, f32, gen,  # noqa: F401
+                           logits_case, rows_input, same)  # (the fixtures hold for every test here)
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +82,19 @@ def test_logits_rows_without_a_mask_need_no_masks(groups, both_ways):
             B.luce_logits_process(out=out, mask=none, mask_rows=torch.tensor(rows, dtype=torch.int32, device="cuda"), **kw)
             same(out, want)
             assert B.luce_get_fault() == fault
+
+
+# ----------------------------------------------------------------------------- rows
+@pytest.mark.parametrize("dtype", [f32, bf16, f16])
+@pytest.mark.parametrize("H", [32, 100, 2048, 4099, 20000, 65536])
+def test_rows_of_zeros_without_an_epsilon(H, dtype):
+    # codes and scale are zero; the row's neighbours are what they are anyway
+    x = rows_input(5, H, dtype, H)
+    x[1], x[3] = 0.0, -0.0
+    gamma = torch.rand(H, generator=gen(5)) + 0.5
+    check_rows(x, gamma, 0.0)
+    check_rows(x, gamma, 0.0, -x, in_place="new")  # every sum is a zero
+    check_rows(x, torch.zeros(H), 0.0)
+    q, s = torch.empty((5, H), dtype=torch.int8, device="cuda"), torch.empty(5, device="cuda")
+    B.luce_rmsnorm_i8(x.cuda(), gamma.cuda(), 0.0, q, s)
+    assert torch.all(s[[1, 3, 4]] == 0) and not torch.any(q[[1, 3, 4]]) and torch.all(s[[0, 2]] > 0)
