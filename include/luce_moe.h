@@ -402,7 +402,9 @@ LUCE_API luce_status luce_add_f32(const float *a, const float *b, float *out, in
  * A row with a NaN or an infinity among the values that are quantized has
  * codes zero and scale NaN: NaN reaches every product with the row, and no
  * code is undefined.  Squares that overflow fp32 give r = 0, as in
- * luce_rmsnorm_router.
+ * luce_rmsnorm_router; rows whose squares fall below its range (they need an
+ * eps below 2^-120 to matter) are summed again in 64 bits, by a second launch
+ * that calls with such an eps make.
  *
  *   x, residual, x_sum [T][H] of `dtype`, aligned to the element; x_sum may
  *     be NULL (not stored), or x or residual itself (the stream updated in

@@ -112,11 +112,17 @@ template <int V> __device__ __forceinline__ void codes_of(const float (&p)[V], f
         w[i / 4] = __byte_perm(__byte_perm(u[i], u[i + 1], 0x0040), __byte_perm(u[i + 2], u[i + 3], 0x0040), 0x5410);
 }
 
+// Squares below the normal range keep 2^-150 of error each, and so does their
+// mean: nothing to a mean (with eps) of TINY or more, but too much below it,
+// where r itself leaves the range of fp32.  Such a row's scale is left at
+// infinity for k_tiny_rows, which follows where eps is below TINY.
+constexpr float TINY = 0x1p-120f;
+
 // (a row of zeros has scale zero whatever r is: 1 / 0 when eps is zero too)
 __device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, bool norm, bool finite)
 {
-    const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)H), eps)));
-    return !finite ? NAN : norm && d > 0.0f ? __fmul_rn(d, r) : d;
+    const float r2 = __fadd_rn(__fdiv_rn(ss, (float)H), eps), r = __fdiv_rn(1.0f, __fsqrt_rn(r2));
+    return !finite ? NAN : norm && d > 0.0f ? (r2 < TINY ? INFINITY : __fmul_rn(d, r)) : d;
 }
 
 // ---------------------------------------------------------------------------
@@ -419,6 +425,39 @@ __global__ void __launch_bounds__(THREADS)
         scale[t] = scale_of(d, ss, H, eps, gamma != nullptr, finite);
 }
 
+// The scales of normed rows that the kernels above left at infinity, a warp to
+// a row: squares in 64 bits, whose range holds those of all fp32 numbers.  Rare:
+// one look at every scale is what it costs a call with such a small eps.
+constexpr int TINY_WARPS = 8;
+
+template <typename TX>
+__global__ void __launch_bounds__(TINY_WARPS * 32)
+    k_tiny_rows(const TX *x, const TX *res, const TX *xsum, const float *gamma, float eps, int T, int H, float *scale)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int64_t t = (int64_t)blockIdx.x * TINY_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (t >= T || scale[t] != INFINITY)
+        return;
+    const size_t row = (size_t)t * H;
+    double ss = 0.0;
+    float m = 0.0f;
+    for (int i = lane; i < H; i += 32) {
+        const float v = xsum  ? to_f32(xsum[row + i])
+                        : res ? to_f32(from_f32<TX>(__fadd_rn(to_f32(x[row + i]), to_f32(res[row + i]))))
+                              : to_f32(x[row + i]);
+        ss += (double)v * (double)v;
+        m = fmaxf(m, fabsf(__fmul_rn(v, gamma[i])));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    m = warp_max(m);
+    if (lane == 0)
+        scale[t] = (float)((double)__fdiv_rn(m, 127.0f) / sqrt(ss / H + (double)eps));
+}
+
 constexpr int H_MAX = 65536;
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
@@ -469,6 +508,14 @@ int chunks_of_a_thread(int V, bool norm, bool aligned_rows, int T, int chunks)
     if (V == 8)
         return (aligned_rows ? (work > 450 * K && chunks >= 512) || chunks > 1024 : work > 330 * K) ? 4 : 2;
     return (aligned_rows ? work > 2000 * K || (work > 600 * K && chunks >= 2048) : work > 500 * K) ? 8 : 2;
+}
+
+template <typename TX>
+luce_status launch_tiny_rows(const TX *x, const TX *res, const TX *xsum, const float *gamma, float eps, int T, int H,
+                             float *scale, cudaStream_t stream)
+{
+    const dim3 grid((unsigned)(((int64_t)T + TINY_WARPS - 1) / TINY_WARPS));
+    return luce_host::launch(k_tiny_rows<TX>, grid, dim3(TINY_WARPS * 32), 0, stream, x, res, xsum, gamma, eps, T, H, scale);
 }
 
 template <typename TX>
@@ -540,13 +587,21 @@ luce_status rows_i8(const void *x, const void *res, void *xsum, luce_dtype dtype
         (gamma && (overlap(q, nq, gamma, ng) || overlap(scale, ns, gamma, ng) ||
                    (xsum && overlap(xsum, nx, gamma, ng)))))
         return LUCE_ERR_INVALID_ARG;
+    auto run = [&](auto element) {
+        using TX = decltype(element);
+        const luce_status st = run_rows<TX>(x, res, xsum, gamma, eps, T, H, q, scale, stream);
+        if (st != LUCE_OK || !gamma || eps >= TINY)
+            return st;
+        return launch_tiny_rows<TX>((const TX *)x, (const TX *)res, (const TX *)xsum, gamma, eps, T, H, scale,
+                                    luce_host::as_stream(stream));
+    };
     switch (dtype) {
     case LUCE_F32:
-        return run_rows<float>(x, res, xsum, gamma, eps, T, H, q, scale, stream);
+        return run(float());
     case LUCE_BF16:
-        return run_rows<__nv_bfloat16>(x, res, xsum, gamma, eps, T, H, q, scale, stream);
+        return run(__nv_bfloat16());
     case LUCE_F16:
-        return run_rows<__half>(x, res, xsum, gamma, eps, T, H, q, scale, stream);
+        return run(__half());
     }
     return LUCE_ERR_INVALID_ARG;
 }

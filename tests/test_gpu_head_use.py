@@ -98,3 +98,18 @@ def test_rows_of_zeros_without_an_epsilon(H, dtype):
     q, s = torch.empty((5, H), dtype=torch.int8, device="cuda"), torch.empty(5, device="cuda")
     B.luce_rmsnorm_i8(x.cuda(), gamma.cuda(), 0.0, q, s)
     assert torch.all(s[[1, 3, 4]] == 0) and not torch.any(q[[1, 3, 4]]) and torch.all(s[[0, 2]] > 0)
+
+
+@pytest.mark.parametrize("in_place", ["x", "residual", "new", None])
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("H", [32, 100, 2048, 4099, 20000, 65536])
+def test_rows_whose_squares_fall_out_of_range(H, dtype, in_place):
+    # values on both sides of where their squares leave the normal range (2^-63) and vanish
+    # (2^-75), and down to the smallest numbers: the scale is the definition's whatever eps is
+    es = [-20, -58, -60, -62, -64, -70, -74, -76, -90, -110, -120]
+    x, r = (torch.ldexp(rows_input(len(es) + 2, H, f32, s), torch.tensor(es + [0, -100])[:, None]).to(dtype)
+            for s in (H, H + 1))
+    gamma = torch.rand(H, generator=gen(5)) + 0.5
+    for eps in (0.0, 1e-42, 2.0 ** -121, 2.0 ** -119, 1e-30):
+        check_rows(x, gamma, eps)
+        check_rows(x, gamma, eps, r, in_place=in_place)
