@@ -13,11 +13,12 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
-from .build import CALL as CALL_PATH
 from .build import LIB as LIB_PATH
+from .build import call_path
 
 LUCE_OK = 0
 LUCE_ERR_INVALID_ARG = 1
@@ -31,7 +32,7 @@ LUCE_FAULT_TIMEOUT = 0x2
 LUCE_FAULT_DESYNC = 0x4
 
 _LIB = None
-_fast = None  # the call module, loaded with the library
+_fast = None  # the call module, loaded with the library; None where there is none
 
 
 class LuceError(RuntimeError):
@@ -96,13 +97,17 @@ def lib() -> ctypes.CDLL:
 
 
 def _load_call_module(L) -> None:
-    """The module that makes the common calls of the int8 head without Python in between."""
+    """The module that makes the common calls of the int8 head without Python in between.  The code
+    below serves every call without it, a few microseconds of host time slower."""
     global _fast
-    if not os.path.exists(CALL_PATH):
-        raise RuntimeError(f"{CALL_PATH} is not built: run quantized_moe_decode_luce_gb300.build.build()")
-    loader = importlib.machinery.ExtensionFileLoader("luce_call", CALL_PATH)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("luce_call", loader))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("luce_call", call_path())
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("luce_call", loader))
+        loader.exec_module(module)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"no call module (run quantized_moe_decode_luce_gb300.build.build()): {e}", RuntimeWarning,
+                      stacklevel=3)
+        return
     module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
         "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process")))
     _fast = module

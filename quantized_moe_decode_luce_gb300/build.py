@@ -1,5 +1,6 @@
 """Build libluce_moe.so in-tree with nvcc for sm_103a (GB300), and beside it the
-module that makes the common calls of the int8 head (g++, torch's headers).
+module that makes the common calls of the int8 head (g++, torch's headers),
+which is an addition: without it every call goes through binding.py.
 
 The translation units are compiled in parallel and linked into
 ``quantized_moe_decode_luce_gb300/lib/libluce_moe.so``.  Release flags only:
@@ -10,9 +11,11 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -21,7 +24,6 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(LIBDIR, "libluce_moe.so")
 SOURCES = ["small_ops.cu", "glu_pair.cu", "down_combine.cu", "moe_layer.cu", "moe_layer_flat.cu", "edge_ops.cu",
            "q4k_ops.cu", "moe_tc.cu", "rows_i8.cu", "linear_i8.cu", "logits_process.cu"]
-CALL = os.path.join(LIBDIR, "luce_call.so")
 CALL_SOURCE = "fastcall.cpp"
 HEADERS = ["common.cuh", os.path.join("..", "..", "include", "luce_moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -40,6 +42,13 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def call_path() -> str:
+    """The call module of this Python and this torch: it is tied to both, so both stand in its name."""
+    import torch
+    version = re.sub(r"[^0-9A-Za-z.]+", "_", torch.__version__)
+    return os.path.join(LIBDIR, f"luce_call.{sys.implementation.cache_tag}.torch-{version}.so")
 
 
 def call_command(source: str, target: str) -> list[str]:
@@ -70,12 +79,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + headers + [__file__]):
             jobs.append([nvcc(), *ARCH, *NVCC_FLAGS, "-c", s, "-o", o])
 
-    call = os.path.join(CSRC, CALL_SOURCE)
-    tmp_call = CALL + f".tmp{os.getpid()}"
-    new_call = force or _stale(CALL, [call, headers[-1], __file__])
-    if new_call:
-        jobs.append(call_command(call, tmp_call))
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -84,10 +87,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return r
 
+    def build_call():
+        # (no torch, no headers, no compiler: the library does without the module)
+        target = None
+        try:
+            target = call_path()
+            source = os.path.join(CSRC, CALL_SOURCE)
+            if force or _stale(target, [source, headers[-1], __file__]):
+                tmp = target + f".tmp{os.getpid()}"
+                run(call_command(source, tmp))
+                os.replace(tmp, target)
+        except (ImportError, OSError, RuntimeError) as e:
+            if target is not None and os.path.exists(target):
+                os.remove(target)  # one of an older source
+            warnings.warn(f"the call module is not built, calls of the int8 head go through binding.py: {e}",
+                          RuntimeWarning, stacklevel=2)
+
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        call = ex.submit(build_call)
         list(ex.map(run, jobs))
-    if new_call:
-        os.replace(tmp_call, CALL)
+        call.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])

@@ -1,11 +1,14 @@
 """How the int8 decode head is called and built, where no GPU is needed: host
 checks of its entry points, the bindings and the call module."""
 import ctypes
+import os
+import sys
 
 import pytest
 import torch
 
 from oracle import head as O
+from quantized_moe_decode_luce_gb300 import binding as Bd
 from quantized_moe_decode_luce_gb300 import build as B
 
 vp, ci, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
@@ -37,3 +40,60 @@ def test_a_row_of_zeros_has_scale_zero_without_an_epsilon():
     assert abs(float(s[1]) * 127 - 8 ** 0.5) < 1e-6  # 4 / sqrt(16 / 8)
     q, s, _ = O.rows_i8(x, torch.zeros(8), 0.0)
     assert torch.all(s == 0) and torch.all(q == 0)
+
+
+# ----------------------------------------------------------------------------- the call module
+@pytest.fixture
+def unloaded(monkeypatch, lib):
+    monkeypatch.setattr(Bd, "_LIB", None)
+    monkeypatch.setattr(Bd, "_fast", None)
+
+
+def test_the_library_loads_with_its_call_module(unloaded):
+    assert Bd.lib().luce_version() > 0 and Bd._fast is not None
+
+
+@pytest.mark.parametrize("what", ["missing", "not a module", "another library"])
+def test_the_library_loads_without_the_call_module(what, unloaded, monkeypatch, tmp_path):
+    path = tmp_path / "luce_call.so"
+    if what == "not a module":
+        path.write_bytes(b"no shared object")
+    monkeypatch.setattr(Bd, "call_path", lambda: B.LIB if what == "another library" else str(path))
+    with pytest.warns(RuntimeWarning, match="call module"):
+        L = Bd.lib()
+    assert Bd._fast is None and L.luce_version() > 0 and Bd.status_string(1) == "invalid argument"
+    x = torch.zeros((2, 64))
+    with pytest.raises(TypeError):  # the bindings are there, and look at their arguments themselves
+        Bd.luce_quantize_i8(x, x, x)
+    with pytest.raises(TypeError):
+        Bd.luce_logits_process(x, x)
+
+
+def test_the_call_module_is_named_after_what_it_is_tied_to(monkeypatch):
+    here = B.call_path()
+    assert sys.implementation.cache_tag in here and os.path.dirname(here) == B.LIBDIR and os.path.exists(here)
+    monkeypatch.setattr(torch, "__version__", "9.9.9+cu000")
+    assert B.call_path() not in (here,) and not os.path.exists(B.call_path())
+
+
+@pytest.mark.parametrize("what", ["compiler", "torch"])
+def test_the_build_does_without_the_call_module(what, lib, monkeypatch, tmp_path):
+    path = tmp_path / "luce_call.so"
+    path.write_bytes(b"an older one")
+    os.utime(path, (1, 1))
+
+    def none(*a):
+        raise ImportError("no torch")
+    monkeypatch.setattr(B, "call_path", none if what == "torch" else lambda: str(path))
+    monkeypatch.setattr(B, "call_command", lambda s, t: ["false"])
+    with pytest.warns(RuntimeWarning, match="call module"):
+        assert B.build() == B.LIB
+    assert os.path.exists(B.LIB) and path.exists() == (what == "torch")  # an older source's does not stay
+
+
+def test_the_build_makes_the_call_module(lib, monkeypatch, tmp_path):
+    path = tmp_path / "luce_call.so"
+    monkeypatch.setattr(B, "call_path", lambda: str(path))
+    monkeypatch.setattr(B, "call_command", lambda s, t: ["cp", s, t])
+    B.build()
+    assert path.exists() and os.listdir(tmp_path) == ["luce_call.so"]
