@@ -11,6 +11,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <exception>
+
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -99,16 +101,32 @@ struct Args {
 };
 
 // A call's status for Python; whatever goes wrong on the way leaves the call to binding.py.
+// (No catch of everything: a thread that the interpreter ends at its exit unwinds through here.)
 template <class F> PyObject *result(F &&call)
 {
     int status = -1;
     try {
         status = call();
-    } catch (...) {
+    } catch (const std::exception &) {
         PyErr_Clear();
         status = -1;
     }
     return PyLong_FromLong(status);
+}
+
+// The library's function, without the interpreter's lock (as ctypes calls it): a
+// launch may wait for a full queue, or for a host function that needs Python.
+// The caller holds references to the tensors meanwhile.
+template <class F, class... A> int unlocked(F f, A... args)
+{
+    int status = -1;
+    PyThreadState *state = PyEval_SaveThread();
+    try {
+        status = (int)f(args...);
+    } catch (const std::exception &) {
+    }
+    PyEval_RestoreThread(state);
+    return status;
 }
 
 bool number(PyObject *o, float &v)
@@ -132,7 +150,7 @@ PyObject *quantize_i8(PyObject *, PyObject *const *p, Py_ssize_t n)
         void *q = a.data(p[1], ScalarType::Char, T, H), *s = a.data(p[2], ScalarType::Float, T);
         const int t = a.small(T), h = a.small(H);
         void *stream = a.stream();
-        return a.ok ? (int)f_quantize(x->data_ptr(), dt, t, h, (int8_t *)q, (float *)s, stream) : -1;
+        return a.ok ? unlocked(f_quantize, x->data_ptr(), dt, t, h, (int8_t *)q, (float *)s, stream) : -1;
     });
 }
 
@@ -151,7 +169,7 @@ PyObject *rmsnorm_i8(PyObject *, PyObject *const *p, Py_ssize_t n)
              *s = a.data(p[4], ScalarType::Float, T);
         const int t = a.small(T), h = a.small(H);
         void *stream = a.stream();
-        return a.ok ? (int)f_rmsnorm(x->data_ptr(), dt, (const float *)g, eps, t, h, (int8_t *)q, (float *)s, stream)
+        return a.ok ? unlocked(f_rmsnorm, x->data_ptr(), dt, (const float *)g, eps, t, h, (int8_t *)q, (float *)s, stream)
                     : -1;
     });
 }
@@ -173,7 +191,7 @@ PyObject *add_rmsnorm_i8(PyObject *, PyObject *const *p, Py_ssize_t n)
              *s = a.data(p[6], ScalarType::Float, T);
         const int t = a.small(T), h = a.small(H);
         void *stream = a.stream();
-        return a.ok ? (int)f_add_rmsnorm(x->data_ptr(), r, sum, dt, (const float *)g, eps, t, h, (int8_t *)q,
+        return a.ok ? unlocked(f_add_rmsnorm, x->data_ptr(), r, sum, dt, (const float *)g, eps, t, h, (int8_t *)q,
                                          (float *)s, stream)
                     : -1;
     });
@@ -195,7 +213,7 @@ PyObject *linear_i8(PyObject *, PyObject *const *p, Py_ssize_t n)
              *b = a.data_or_none(p[4], ScalarType::Float, N);
         const int t = a.small(T), nn = a.small(N), k = a.small(K);
         void *stream = a.stream();
-        return a.ok ? (int)f_linear((const int8_t *)xq, (const float *)xs, (const int8_t *)wq, (const float *)ws,
+        return a.ok ? unlocked(f_linear, (const int8_t *)xq, (const float *)xs, (const int8_t *)wq, (const float *)ws,
                                     (const float *)b, t, nn, k, out, dt, ldo, stream)
                     : -1;
     });
@@ -244,7 +262,7 @@ PyObject *logits_process(PyObject *, PyObject *const *p, Py_ssize_t n)
              *mr = a.data_or_none(p[11], ScalarType::Int, R);
         const int r = a.small(R), b = a.small(nb), m = a.small(nm);
         void *stream = a.stream();
-        return a.ok ? (int)f_logits(lp, dt, r, V, ldl, (const int32_t *)hp, ldh, (const int32_t *)hl, (const int32_t *)pl,
+        return a.ok ? unlocked(f_logits, lp, dt, r, V, ldl, (const int32_t *)hp, ldh, (const int32_t *)hl, (const int32_t *)pl,
                                     (const float *)rep, (const float *)fr, (const float *)pr, (const int32_t *)bi,
                                     (const float *)bv, b, (const uint32_t *)mp, m, ldm, (const int32_t *)mr, (float *)op,
                                     ldo, stream)

@@ -3,11 +3,20 @@ launches that start early, streams and threads, the tile of every product --
 against the definitions in 64 bits (oracle/head.py), with the helpers and
 bounds of test_gpu_head.py.
 """
+import ctypes
+import importlib.machinery
+import importlib.util
+import shutil
+import subprocess
+import threading
+import time
+
 import pytest
 import torch
 
 from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as B
+from quantized_moe_decode_luce_gb300 import build as BLD
 from quantized_moe_decode_luce_gb300.layer import LinearI8
 from test_gpu_head import (_lib, _no_device_faults, bf16, check_rows, codes, f16, f32, gen,  # noqa: F401
                            logits_case, rows_input, same)  # (the fixtures hold for every test here)
@@ -113,3 +122,40 @@ def test_rows_whose_squares_fall_out_of_range(H, dtype, in_place):
     for eps in (0.0, 1e-42, 2.0 ** -121, 2.0 ** -119, 1e-30):
         check_rows(x, gamma, eps)
         check_rows(x, gamma, eps, r, in_place=in_place)
+
+
+# ----------------------------------------------------------------------------- threads
+WAITER = r"""
+#include <unistd.h>
+static volatile int flag;
+void set_flag(void) { flag = 1; }
+int wait_for_flag(void) /* two seconds at most */
+{
+    for (int i = 0; i < 2000 && !flag; i++)
+        usleep(1000);
+    return flag ? 0 : 3;
+}
+"""
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    # a launch may have to wait (a full queue, a host function that needs Python): the call
+    # module's function stands still here until another Python thread has run
+    source, helper, copy = tmp_path / "w.c", tmp_path / "w.so", tmp_path / "luce_call.so"
+    source.write_text(WAITER)
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", str(source), "-o", str(helper)], check=True)
+    w = ctypes.CDLL(str(helper))
+    shutil.copy(BLD.call_path(), copy)  # (a module of its own, so that the real one keeps its functions)
+    loader = importlib.machinery.ExtensionFileLoader("luce_call", str(copy))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("luce_call", loader))
+    loader.exec_module(module)
+    module.bind(*[ctypes.cast(w.wait_for_flag, ctypes.c_void_p).value] * 5)
+    x, g = torch.zeros((2, 64), device="cuda"), torch.zeros(64, device="cuda")
+    q, s = torch.zeros((2, 64), dtype=torch.int8, device="cuda"), torch.zeros(2, device="cuda")
+    other = threading.Thread(target=lambda: (time.sleep(0.05), w.set_flag()))
+    other.start()
+    assert module.quantize_i8(x, q, s) == 0
+    other.join()
+    for status in (module.rmsnorm_i8(x, g, 1e-6, q, s), module.add_rmsnorm_i8(x, x, None, g, 1e-6, q, s),
+                   module.linear_i8(q, s, q, s, None, x[:, :2]), module.logits_process(x, x, *[None] * 10)):
+        assert status == 0  # (the flag stands)
