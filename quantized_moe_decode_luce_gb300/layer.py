@@ -126,7 +126,12 @@ class GreedyHead:
         self.argmax = Argmax(R, head.N, device=dev)
 
     def run(self, x, residual=None, x_sum=None, stream=None, **process):
-        """x (+ residual) [R, K]; `process` are the keyword arguments of luce_logits_process."""
+        """x (+ residual) [R, K]; `process` are the keyword arguments of luce_logits_process.
+        Runs on the head's device, on its current stream unless one is given."""
+        dev = self.q.get_device()
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return self.run(x, residual, x_sum, stream, **process)
         if residual is not None:
             B.luce_add_rmsnorm_i8(x, residual, x_sum, self.gamma, self.eps, self.q, self.scale, stream)
         else:

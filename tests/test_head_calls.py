@@ -10,6 +10,7 @@ import torch
 from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as Bd
 from quantized_moe_decode_luce_gb300 import build as B
+from quantized_moe_decode_luce_gb300.layer import GreedyHead, LinearI8
 
 vp, ci, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 
@@ -97,3 +98,42 @@ def test_the_build_makes_the_call_module(lib, monkeypatch, tmp_path):
     monkeypatch.setattr(B, "call_command", lambda s, t: ["cp", s, t])
     B.build()
     assert path.exists() and os.listdir(tmp_path) == ["luce_call.so"]
+
+
+# ----------------------------------------------------------------------------- GreedyHead
+@pytest.fixture
+def calls(monkeypatch, lib):
+    """The library calls that a head makes, each with the device that is current, without a GPU."""
+    made, current = [], [0]
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            self.i, current[0] = current[0], self.i
+
+        def __exit__(self, *a):
+            current[0] = self.i
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for name in ("luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process", "luce_argmax"):
+        monkeypatch.setattr(Bd, name, lambda *a, name=name, **kw: made.append((name, current[0])))
+    return made
+
+
+def greedy_head():
+    w = LinearI8(torch.zeros((100, 32), dtype=torch.int8), torch.zeros(100))
+    return GreedyHead(2, torch.ones(32), 1e-6, w)
+
+
+def test_a_head_runs_on_its_own_device(calls):
+    head, x = greedy_head(), torch.zeros((2, 32))
+    here = head.q.get_device()
+    assert here != torch.cuda.current_device()
+    head.run(x, x, hist=None)
+    head.run(x)
+    assert calls == [(n, here) for n in ("luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process", "luce_argmax",
+                                         "luce_rmsnorm_i8", "luce_linear_i8", "luce_argmax")]
+    assert torch.cuda.current_device() == 0
