@@ -132,6 +132,8 @@ class GreedyHead:
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):
                 return self.run(x, residual, x_sum, stream, **process)
+        if residual is None and x_sum is not None:
+            raise ValueError("x_sum is the sum with a residual, and there is none")
         if residual is not None:
             B.luce_add_rmsnorm_i8(x, residual, x_sum, self.gamma, self.eps, self.q, self.scale, stream)
         else:

@@ -137,3 +137,10 @@ def test_a_head_runs_on_its_own_device(calls):
     assert calls == [(n, here) for n in ("luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process", "luce_argmax",
                                          "luce_rmsnorm_i8", "luce_linear_i8", "luce_argmax")]
     assert torch.cuda.current_device() == 0
+
+
+def test_a_head_without_a_residual_has_no_sum_to_store(calls):
+    head, x = greedy_head(), torch.zeros((2, 32))
+    with pytest.raises(ValueError):
+        head.run(x, None, torch.zeros((2, 32)))
+    assert calls == []  # nothing was launched
