@@ -212,7 +212,9 @@ LUCE_API luce_status luce_moe_down_combine(const luce_block_q8_0 *w_down, const 
  *
  * idx[r] = the lowest index of the maximum of logits[r][0..V) (float
  * comparison: -0 == +0 is a tie; inputs must hold no NaN); val[r] = that
- * maximum (val may be NULL).
+ * maximum (val may be NULL).  A row of -infinity has index 0.  In a row with
+ * NaNs idx[r] is the index of one of its values, not always the largest, and
+ * val[r] is that value.
  *
  *   logits [R][V] fp32          idx [R] int32 out      val [R] fp32 out or NULL
  *   workspace, workspace_bytes  device scratch of at least

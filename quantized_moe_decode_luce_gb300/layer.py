@@ -113,7 +113,12 @@ class GreedyHead:
     """The end of a step for R rows (tokens, or the columns of a verify step): the residual sum's
     RMS norm in int8, the vocabulary product, penalties, biases and masks, the greedy tokens.
 
-    Owns every buffer; `run` makes four calls and returns (idx [R] int32, val [R] fp32)."""
+    Owns every buffer, so one head runs on one stream at a time (a captured graph of it among them);
+    `run` makes four calls and returns (idx [R] int32, val [R] fp32).
+
+    val says whether a row has a token: it is -inf where the row's mask allows nothing (idx is 0), and
+    NaN or -inf where the row of x (or of the sum) holds a NaN or an infinity, which makes all its logits
+    NaN that are not masked (idx then is in range, and no pick)."""
 
     def __init__(self, R: int, gamma: torch.Tensor, eps: float, head: LinearI8):
         if head.K != gamma.numel():

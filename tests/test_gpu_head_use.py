@@ -6,6 +6,7 @@ bounds of test_gpu_head.py.
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import shutil
 import subprocess
 import threading
@@ -17,9 +18,9 @@ import torch
 from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from quantized_moe_decode_luce_gb300 import build as BLD
-from quantized_moe_decode_luce_gb300.layer import LinearI8
+from quantized_moe_decode_luce_gb300.layer import GreedyHead, LinearI8
 from test_gpu_head import (_lib, _no_device_faults, bf16, check_rows, codes, f16, f32, gen,  # noqa: F401
-                           logits_case, rows_input, same)  # (the fixtures hold for every test here)
+                           logits_case, make_head, rows_input, same)  # (the fixtures hold for every test here)
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +160,28 @@ def test_other_threads_run_while_a_call_waits(tmp_path):
     for status in (module.rmsnorm_i8(x, g, 1e-6, q, s), module.add_rmsnorm_i8(x, x, None, g, 1e-6, q, s),
                    module.linear_i8(q, s, q, s, None, x[:, :2]), module.logits_process(x, x, *[None] * 10)):
         assert status == 0  # (the flag stands)
+
+
+# ----------------------------------------------------------------------------- rows without a token
+@pytest.mark.parametrize("V", [333, 3001, 20000])
+def test_greedy_head_says_which_rows_have_no_token(V):
+    R, H = 6, 256
+    head, w, gamma = make_head(R, V, H)
+    x = torch.randn((R, H), generator=gen(2))
+    x[1, 3], x[2, 5], x[4, 7] = math.nan, -math.inf, math.inf
+    mask = torch.randint(-2**31, 2**31, (2, (V + 31) // 32), generator=gen(3)).to(torch.int32)
+    mask[0] = 0  # allows nothing
+    mask[1, 0] = -2  # (not token 0)
+    kw = dict(mask=mask.cuda(), mask_rows=torch.tensor([-1, -1, -1, 0, 1, 0], dtype=torch.int32, device="cuda"))
+    idx, val = head.run(x.cuda(), **kw)
+    clean = GreedyHead(1, gamma.cuda(), 1e-6, head.head)
+    idx0, val0 = clean.run(x[:1].cuda())
+    assert torch.equal(idx[:1], idx0) and torch.equal(val[:1], val0)  # (the neighbours do not reach it)
+    idx, val, logits = idx.cpu().long(), val.cpu(), head.logits.cpu()
+    assert torch.all((idx >= 0) & (idx < V))
+    assert torch.isnan(val[1]) and torch.isnan(val[2])
+    assert idx[3] == 0 and val[3] == -math.inf and idx[5] == 0 and val[5] == -math.inf
+    assert torch.isnan(val[4]) or val[4] == -math.inf
+    at = logits[torch.arange(R), idx]
+    assert torch.all((at == val) | (torch.isnan(at) & torch.isnan(val)))
+    assert torch.all(torch.isnan(logits[1:3])) and torch.all(torch.isnan(logits[4]) | (logits[4] == -math.inf))
