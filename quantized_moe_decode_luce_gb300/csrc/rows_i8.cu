@@ -471,7 +471,7 @@ luce_status launch_rows(const TX *x, const TX *res, TX *xsum, const float *gamma
                         float *scale, int threads, bool aligned_rows, cudaStream_t stream)
 {
     const int rows = threads <= 32 ? 256 / threads : 1;
-    const dim3 grid((unsigned)((T + rows - 1) / rows)), block((unsigned)threads, (unsigned)rows);
+    const dim3 grid((unsigned)(((int64_t)T + rows - 1) / rows)), block((unsigned)threads, (unsigned)rows);
     const size_t smem = aligned_rows ? 0 : (size_t)rows * ((H + 32) / 16 * 16);
     auto run = [&](auto kern) {
         return luce_host::launch(kern, grid, block, smem, stream, x, res, xsum, gamma, eps, T, H, q, scale);

@@ -185,3 +185,19 @@ def test_greedy_head_says_which_rows_have_no_token(V):
     at = logits[torch.arange(R), idx]
     assert torch.all((at == val) | (torch.isnan(at) & torch.isnan(val)))
     assert torch.all(torch.isnan(logits[1:3])) and torch.all(torch.isnan(logits[4]) | (logits[4] == -math.inf))
+
+
+def test_as_many_rows_as_there_may_be():
+    # 2^31 - 1 rows of one value: the count of blocks, the row numbers and the offsets at their ends
+    T = 2**31 - 1
+    x = torch.ones((T, 1), dtype=bf16, device="cuda")
+    x[-3:, 0] = torch.tensor([-2.0, 0.0, 3.0], dtype=bf16)
+    q, scale = torch.full((T + 40,), 55, dtype=torch.int8, device="cuda"), torch.full((T + 40,), 55.0, device="cuda")
+    B.luce_quantize_i8(x, q[:T].view(T, 1), scale[:T])
+    torch.cuda.synchronize()
+    assert q[T - 3:T].tolist() == [-127, 0, 127] and torch.all(q[T:] == 55) and torch.all(scale[T:] == 55)
+    same(scale[T - 3:T], torch.tensor([2.0, 0.0, 3.0]) / 127)
+    for r in range(0, T - 3, 2**28):
+        end = min(r + 2**28, T - 3)
+        assert torch.all(q[r:end] == 127) and torch.all(scale[r:end] == scale[0])
+    assert scale[0] == torch.tensor(1.0) / 127
