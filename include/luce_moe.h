@@ -448,6 +448,14 @@ LUCE_API luce_status luce_add_rmsnorm_i8(const void *x, const void *residual, vo
 LUCE_API luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, const int8_t *wq, const float *w_scale,
                                     const float *bias, int T, int N, int K, void *out, luce_dtype out_dtype,
                                     int64_t ld_out, void *stream);
+/* The kernels that luce_linear_i8 takes for a product on the current device
+ * (for tests and tuning; launches nothing).  Launch i = 0 and 1 of a product:
+ *   plan[4 i]      0 the stream of the weights, 1 tiles of one CTA (up to 64
+ *                  tokens), 2 of a CTA pair (up to 128), 4 of a CTA pair (up to 256)
+ *   plan[4 i + 1]  tokens of a tile, or that the stream takes at once
+ *   plan[4 i + 2]  groups along K
+ *   plan[4 i + 3]  channels; zero where there is no such launch */
+LUCE_API luce_status luce_linear_i8_plan(int T, int N, int K, luce_dtype out_dtype, int *plan);
 
 /* ------------------------------------------------------------------------
  * luce_logits_process -- what stands between a step's logits and the pick of

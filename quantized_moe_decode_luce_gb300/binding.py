@@ -72,6 +72,7 @@ def lib() -> ctypes.CDLL:
             "luce_rmsnorm_i8": [P, i32, P, f32, i32, i32, P, P, P],
             "luce_add_rmsnorm_i8": [P, P, P, i32, P, f32, i32, i32, P, P, P],
             "luce_linear_i8": [P, P, P, P, P, i32, i32, i32, P, i32, i64, P],
+            "luce_linear_i8_plan": [i32, i32, i32, i32, P],
             "luce_logits_process": [P, i32, i32, i64, i64, P, i64, P, P, P, P, P, P, P, i32, P, i32, i64, P, P, i64,
                                     P],
         }
@@ -432,6 +433,15 @@ def luce_linear_i8(xq, x_scale, wq, w_scale, bias, out, stream=None) -> None:
           None if bias is None else _addr(bias, _F32, (N,), dev, "bias"), T, N, K, o, _DTYPE[out.dtype], ldo)
 
 
+def luce_linear_i8_plan(T: int, N: int, K: int, dtype=torch.float32) -> list[tuple[int, int, int, int]]:
+    """What luce_linear_i8 launches for a product on the current device: (kernel, tokens of a tile,
+    groups along K, channels) of one or two launches; kernel 0 is the stream of the weights, 1, 2 and 4
+    are tiles of up to 64, 128 and 256 tokens."""
+    plan = (ctypes.c_int * 8)()
+    _check("luce_linear_i8_plan", lib().luce_linear_i8_plan(T, N, K, _DTYPE[dtype], plan))
+    return [tuple(plan[i:i + 4]) for i in (0, 4) if plan[i + 3]]
+
+
 def luce_logits_process(logits, out, hist=None, hist_len=None, prompt_len=None, repetition=None, frequency=None,
                         presence=None, bias_ids=None, bias_vals=None, mask=None, mask_rows=None,
                         stream=None) -> None:
@@ -497,7 +507,7 @@ __all__ = ["LuceError", "lib", "status_string", "luce_route_topk", "luce_quantiz
            "luce_moe_down_combine", "luce_argmax", "luce_argmax_workspace_bytes", "luce_argmax_noalloc",
            "luce_argmax_shard", "luce_argmax_pick", "luce_rmsnorm_router", "luce_add_rmsnorm_router", "luce_ep_mask", "luce_add_f32",
            "luce_moe_glu_q4k", "luce_moe_down_combine_q4k",
-           "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process",
-           "LUCE_F32", "LUCE_BF16", "LUCE_F16",
+           "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_linear_i8_plan",
+           "luce_logits_process", "LUCE_F32", "LUCE_BF16", "LUCE_F16",
            "luce_get_fault", "luce_version", "LUCE_OK", "LUCE_ERR_INVALID_ARG", "LUCE_ERR_UNSUPPORTED",
            "LUCE_ERR_CUDA", "LUCE_FAULT_BAD_ID", "LUCE_FAULT_TIMEOUT", "LUCE_FAULT_DESYNC"]

@@ -1170,21 +1170,58 @@ luce_status launch_vec(const int8_t *xq, const float *xs, const int8_t *wq, cons
     return slice > 512 * VU ? run(k_linear_i8_vec<T, VU, true, TO>) : run(k_linear_i8_vec<T, VU, false, TO>);
 }
 
+// The launches of a product: one, or the channels of the whole rounds of tiles
+// and the rest.
+struct Launches {
+    Plan plan[2];
+    int channels[2] = {0, 0};
+};
+
+template <typename TO> Launches choose(int dev, int sms, int T, int N, int K)
+{
+    Launches c;
+    Part part, none;
+    const Plan plan = plan_product<TO>(dev, sms, T, N, K, part);
+    // a round that few tiles are left for: a launch of its own, whose tiles split K
+    // (9 x 21891 x 10240, 171 tiles: 46.8 us, in one launch 59.8; 512 x 5120 x 13824: 57.7 and 70.2)
+    if (part.guess < SECOND_LAUNCH * plan.us) {
+        const Plan rest = plan_product<TO>(dev, sms, T, N - part.channels, K, none);
+        if (part.plan.us + rest.us < SECOND_LAUNCH * plan.us) {
+            c.plan[0] = part.plan;
+            c.plan[1] = rest;
+            c.channels[0] = part.channels;
+            c.channels[1] = N - part.channels;
+            return c;
+        }
+    }
+    c.plan[0] = plan;
+    c.channels[0] = N;
+    return c;
+}
+
+// Tokens that a warp of the stream takes at once where the stream serves all
+// products, else 0: up to four tokens, and up to eight while the weights are
+// few: beyond 40 MB the sums of eight tokens bound it (8 x 8192 x 4096: 11.8 us,
+// tensor cores 12.9; 8 x 16384 x 4096: 21.1 against 17.2).
+int stream_tokens(int T, int N, int K)
+{
+    return T <= 2 ? T : T <= 4 ? 4 : T <= 8 && (int64_t)N * K <= (int64_t)40 << 20 ? 8 : 0;
+}
+
 template <typename TO>
 luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, const float *ws, const float *bias, int T,
                        int N, int K, TO *out, int64_t ldo, cudaStream_t stream)
 {
-    // a stream of the weights for up to four tokens, and for up to eight while the
-    // weights are few: beyond 40 MB the sums of eight tokens bound it (8 x 8192 x
-    // 4096: 11.8 us, tensor cores 12.9; 8 x 16384 x 4096: 21.1 against 17.2)
-    if (T == 1)
+    switch (stream_tokens(T, N, K)) {
+    case 1:
         return launch_vec<1, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (T == 2)
+    case 2:
         return launch_vec<2, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (T <= 4)
+    case 4:
         return launch_vec<4, 2>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
-    if (T <= 8 && (int64_t)N * K <= (int64_t)40 << 20)
+    case 8:
         return launch_vec<8, 1>(xq, xs, wq, ws, bias, T, N, K, out, ldo, stream);
+    }
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -1205,18 +1242,49 @@ luce_status run_linear(const int8_t *xq, const float *xs, const int8_t *wq, cons
             return launch_tc<CfgWide>(xq, xs, w, s, b, T, n, K, out + n0, ldo, plan.tokens, dev, sms, stream);
         }
     };
-    Part part, none;
-    const Plan plan = plan_product<TO>(dev, sms, T, N, K, part);
-    // a round that few tiles are left for: a launch of its own, whose tiles split K
-    // (9 x 21891 x 10240, 171 tiles: 46.8 us, in one launch 59.8; 512 x 5120 x 13824: 57.7 and 70.2)
-    if (part.guess < SECOND_LAUNCH * plan.us) {
-        const Plan rest = plan_product<TO>(dev, sms, T, N - part.channels, K, none);
-        if (part.plan.us + rest.us < SECOND_LAUNCH * plan.us) {
-            const luce_status st = run(part.plan, 0, part.channels);
-            return st == LUCE_OK ? run(rest, part.channels, N - part.channels) : st;
-        }
+    const Launches c = choose<TO>(dev, sms, T, N, K);
+    const luce_status st = run(c.plan[0], 0, c.channels[0]);
+    return st == LUCE_OK && c.channels[1] ? run(c.plan[1], c.channels[0], c.channels[1]) : st;
+}
+
+// What luce_linear_i8_plan says of one launch.
+template <typename TO> void describe(const Plan &plan, int channels, int dev, int sms, int T, int K, int *d)
+{
+    const int units = (K + KU - 1) / KU;
+    auto tiles = [&](int rows) { return (((int64_t)channels + rows - 1) / rows) * (((int64_t)T + plan.tokens - 1) / plan.tokens); };
+    d[0] = plan.cfg;
+    d[1] = plan.tokens;
+    d[2] = plan.cfg == 0   ? vec_split(K, 1).wk
+           : plan.cfg == 1 ? Tc<CfgOne, TO>::split(dev, sms, tiles(RM), units)
+           : plan.cfg == 2 ? Tc<CfgPair, TO>::split(dev, sms, tiles(2 * RM), units)
+                           : Tc<CfgWide, TO>::split(dev, sms, tiles(2 * RM), units);
+    d[3] = channels;
+}
+
+template <typename TO> luce_status describe_product(int T, int N, int K, int *d)
+{
+    if (const int n = stream_tokens(T, N, K)) {
+        d[1] = n;
+        d[2] = vec_split(K, n == 8 ? 1 : 2).wk;
+        d[3] = N;
+        return LUCE_OK;
     }
-    return run(plan, 0, N);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LUCE_ERR_CUDA;
+    }
+    const int sms = luce_host::sm_count();
+    const Launches c = choose<TO>(dev, sms, T, N, K);
+    for (int i = 0; i < 2 && c.channels[i]; i++)
+        describe<TO>(c.plan[i], c.channels[i], dev, sms, T, K, d + 4 * i);
+    return LUCE_OK;
+}
+
+bool bad_sizes(int T, int N, int K, luce_dtype out_dtype)
+{
+    return T < 0 || T >= (1 << 24) || N < 1 || N >= (1 << 24) || K < 16 || K > 65536 || K % 16 != 0 ||
+           (out_dtype != LUCE_F32 && out_dtype != LUCE_BF16 && out_dtype != LUCE_F16);
 }
 
 } // namespace
@@ -1226,9 +1294,7 @@ extern "C" luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, co
                                       int64_t ld_out, void *stream)
 {
     using luce_host::aligned;
-    if (T < 0 || T >= (1 << 24) || N < 1 || N >= (1 << 24) || K < 16 || K > 65536 || K % 16 != 0 || ld_out < N ||
-        ld_out > ((int64_t)1 << 32) ||
-        (out_dtype != LUCE_F32 && out_dtype != LUCE_BF16 && out_dtype != LUCE_F16))
+    if (bad_sizes(T, N, K, out_dtype) || ld_out < N || ld_out > ((int64_t)1 << 32))
         return LUCE_ERR_INVALID_ARG;
     if (T == 0)
         return LUCE_OK;
@@ -1249,6 +1315,24 @@ extern "C" luce_status luce_linear_i8(const int8_t *xq, const float *x_scale, co
         return run_linear(xq, x_scale, wq, w_scale, bias, T, N, K, (__nv_bfloat16 *)out, ld_out, st);
     case LUCE_F16:
         return run_linear(xq, x_scale, wq, w_scale, bias, T, N, K, (__half *)out, ld_out, st);
+    }
+    return LUCE_ERR_INVALID_ARG;
+}
+
+extern "C" luce_status luce_linear_i8_plan(int T, int N, int K, luce_dtype out_dtype, int *plan)
+{
+    if (!plan || bad_sizes(T, N, K, out_dtype))
+        return LUCE_ERR_INVALID_ARG;
+    std::fill_n(plan, 8, 0);
+    if (T == 0)
+        return LUCE_OK;
+    switch (out_dtype) {
+    case LUCE_F32:
+        return describe_product<float>(T, N, K, plan);
+    case LUCE_BF16:
+        return describe_product<__nv_bfloat16>(T, N, K, plan);
+    case LUCE_F16:
+        return describe_product<__half>(T, N, K, plan);
     }
     return LUCE_ERR_INVALID_ARG;
 }

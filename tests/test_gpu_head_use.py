@@ -57,6 +57,172 @@ def test_weights_quantized_just_before_their_product(T, N, K, pdl):
     same(last, refs[0])
 
 
+# ----------------------------------------------------------------------------- the product's tiles
+# Products by the kernels that they take, in one launch or two.  The choice is an estimate of time; each test below asks for it, so that none runs another kernel unseen.
+TILES = [  # T, N, K, [(kernel, tokens of a tile, K split)]
+    (10, 9788, 1056, [(1, 16, False)]), (10, 7521, 528, [(1, 16, True)]), (9, 8589, 16, [(1, 16, False)]),
+    (1246, 131, 1040, [(1, 32, False)]), (18, 1418, 2704, [(1, 32, True)]), (17, 9732, 16, [(1, 32, False)]),
+    (33, 10219, 1088, [(1, 48, False)]), (35, 1422, 2704, [(1, 48, True)]),
+    (49, 10871, 1056, [(1, 64, False)]), (356, 129, 3904, [(1, 64, True)]), (49, 30303, 16, [(1, 64, False)]),
+    (52, 9857, 3632, [(2, 64, False)]), (49, 6965, 5280, [(2, 64, True)]),
+    (66, 9982, 1184, [(2, 96, False)]), (67, 3311, 2896, [(2, 96, True)]), (261, 23338, 16, [(2, 96, False)]),
+    (98, 10483, 1152, [(2, 128, False)]), (98, 4909, 2224, [(2, 128, True)]), (202, 24999, 16, [(2, 128, False)]),
+    (139, 14096, 2080, [(4, 160, False)]), (147, 5091, 3264, [(4, 160, True)]), (4879, 258, 3200, [(4, 160, False)]),
+    (161, 13370, 2960, [(4, 192, False)]), (168, 5041, 3808, [(4, 192, True)]),
+    (195, 12849, 2768, [(4, 224, False)]), (207, 4731, 4496, [(4, 224, True)]), (223, 7087, 15776, [(4, 224, True)]),
+    (229, 13044, 3456, [(4, 256, False)]), (1242, 781, 5328, [(4, 256, True)]), (1968, 53319, 1040, [(4, 256, False)]),
+    (9, 20278, 1632, [(1, 16, False), (0, 8, True)]), (10, 21035, 4656, [(1, 16, False), (1, 16, True)]),
+    (51, 25907, 7584, [(1, 64, False), (2, 64, True)]), (69, 19595, 2272, [(2, 96, False), (0, 8, True)]),
+    (189, 9915, 3008, [(2, 96, False), (1, 32, True)]), (65, 22772, 5056, [(2, 96, False), (2, 96, True)]),
+    (149, 12937, 13296, [(2, 96, False), (4, 160, True)]), (139, 19469, 4944, [(4, 160, False), (0, 8, True)]),
+    (173, 19772, 5104, [(4, 192, False), (1, 48, True)]), (130, 21998, 5184, [(4, 160, False), (2, 96, True)]),
+    (134, 24353, 9024, [(4, 160, False), (4, 160, True)])]
+SPLIT = {1: [t for t in TILES if t[3] == [(1, 64, True)]], 2: [t for t in TILES if t[3] == [(2, 96, True)]],
+         4: [t for t in TILES if t[3] == [(4, 160, True)]]}
+
+
+def assert_plan(T, N, K, dtype, want):
+    plan = B.luce_linear_i8_plan(T, N, K, dtype)
+    assert [(kernel, tokens, groups > 1) for kernel, tokens, groups, _ in plan] == want, (
+        f"{T} x {N} x {K} takes {plan} now: another product is needed for {want}")
+    assert sum(channels for *_, channels in plan) == N
+
+
+def definition(xq, xs, wq, ws, b, dtype):
+    """oracle/head.py's product on tensors of the GPU (64 bits there too), a slice of the channels at a time."""
+    N, K = wq.shape
+    out = torch.empty((xq.shape[0], N), dtype=dtype, device="cuda")
+    step = max(1, min((1 << 28) // K, (1 << 25) // xq.shape[0]))
+    for n in range(0, N, step):
+        e = min(n + step, N)
+        out[:, n:e] = O.linear_i8(xq, xs, wq[n:e], ws[n:e], None if b is None else b[n:e], dtype)
+    return out
+
+
+def product(T, N, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    xq, wq = (torch.randint(-128, 128, (r, K), generator=g, dtype=torch.int8, device="cuda") for r in (T, N))
+    xs, ws = (torch.rand(r, generator=g, device="cuda") * 0.01 for r in (T, N))
+    return xq, xs, wq, ws, torch.randn(N, generator=g, device="cuda")
+
+
+def run_product(xq, xs, wq, ws, b, dtype, gap=0):
+    T, N = xq.shape[0], wq.shape[0]
+    wide = torch.full((T + 1, N + gap), 77.0, dtype=dtype, device="cuda")
+    B.luce_linear_i8(xq, xs, wq, ws, b, wide[:T, :N])
+    assert torch.all(wide[:, N:] == 77.0) and torch.all(wide[T:] == 77.0)
+    return wide[:T, :N]
+
+
+def equal(out, ref):
+    bad = out != ref
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} differ, first at {tuple(bad.nonzero()[0].tolist())}"
+
+
+def test_the_tiles_above_are_all_there_are():
+    one = {p[0] for *_, p in TILES if len(p) == 1}
+    widths = {1: (16, 32, 48, 64), 2: (64, 96, 128), 4: (160, 192, 224, 256)}
+    assert one == {(k, w, split) for k in widths for w in widths[k] for split in (False, True)}
+    first = {(p[0][0], p[1][0]) for *_, p in TILES if len(p) == 2}
+    assert {a for a, _ in first} == {1, 2, 4} and {b for _, b in first} == {0, 1, 2, 4}
+
+
+@pytest.mark.parametrize("T,N,K,plan", TILES)
+def test_linear_every_kernel_and_tile(T, N, K, plan):
+    dtype = [f32, bf16, f16][(T + N) % 3]
+    assert_plan(T, N, K, dtype, plan)
+    xq, xs, wq, ws, b = product(T, N, K, T + N)
+    b = b if N % 2 else None
+    equal(run_product(xq, xs, wq, ws, b, dtype, gap=T % 5), definition(xq, xs, wq, ws, b, dtype))
+
+
+# unsplit, with chunks of 1024 values that are full, a little short and a little over
+FULL = [(9, 9933, 1008, 1), (9, 9757, 1024, 1), (49, 10871, 1056, 1), (9, 9792, 2048, 1), (65, 9864, 1008, 2),
+        (4968, 129, 1024, 2), (66, 9884, 1040, 2), (4961, 130, 2048, 2), (1968, 53319, 1040, 4), (131, 29948, 2048, 4),
+        (130, 13109, 2064, 4), (4907, 266, 4096, 4)]
+
+
+@pytest.mark.parametrize("T,N,K,kernel", FULL + [(*t[:3], k) for k in SPLIT for t in SPLIT[k]])
+def test_linear_the_largest_sums_on_every_kernel(T, N, K, kernel):
+    # chunks that add up to 2^24 (-128 x -128), and the largest sums of low bits
+    p = B.luce_linear_i8_plan(T, N, K)
+    assert len(p) == 1 and p[0][0] == kernel and (p[0][2] > 1) == ((T, N, K, kernel) not in FULL)
+    xs, ws = torch.rand(T, device="cuda") * 0.01, torch.rand(N, device="cuda") * 0.01
+    full = lambda r, v: torch.full((r, K), v, dtype=torch.int8, device="cuda")  # noqa: E731
+    for x, w in ((-128, -128), (127, 127), (-128, 127)):
+        out = run_product(full(T, x), xs, full(N, w), ws, None, f32)
+        isum = torch.tensor(float(x * w * K), device="cuda")  # (below 2^31; rounded once)
+        equal(out, isum * (xs[:, None] * ws[None, :]))
+    x, w = full(T, 127), full(N, -128)
+    x[:, ::2], w[:, 1::3] = -127, 125
+    equal(run_product(x, xs, w, ws, None, f32), definition(x, xs, w, ws, None, f32))
+
+
+CHAIN = [(49, 10871, 1056, [(1, 64, False)]), (66, 9982, 1184, [(2, 96, False)]), (139, 14096, 2080, [(4, 160, False)]),
+         (35, 1422, 2704, [(1, 48, True)]), (98, 4909, 2224, [(2, 128, True)]), (147, 5091, 3264, [(4, 160, True)]),
+         (10, 21035, 4656, [(1, 16, False), (1, 16, True)]), (130, 21998, 5184, [(4, 160, False), (2, 96, True)])]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T,N,K,plan", CHAIN)
+def test_chains_of_launches_that_start_early(T, N, K, plan, captured, pdl):
+    # each reads what the one before wrote, and every buffer is written again in the next turn
+    assert_plan(T, N, K, f32, plan)
+    xs_in = [torch.randn((T, K), generator=gen(s)) for s in (1, 2)]
+    wf = [torch.randn((N, K), generator=gen(s)).cuda() for s in (3, 4)]
+    xd = [x.cuda() for x in xs_in]
+    c = logits_case(T, N, hist=20)
+    kw = {k: v.cuda() for k, v in c.items() if k != "logits"}
+    q, s = torch.empty((T, K), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    wq, ws = torch.empty((N, K), dtype=torch.int8, device="cuda"), torch.empty(N, device="cuda")
+    out, ls = torch.empty((T, N), device="cuda"), torch.zeros((4, T, N), device="cuda")
+    torch.cuda.synchronize()
+
+    def turns():
+        for i in range(4):
+            B.luce_quantize_i8(xd[i % 2], q, s)
+            B.luce_quantize_i8(wf[i // 2], wq, ws)
+            B.luce_linear_i8(q, s, wq, ws, None, out)
+            B.luce_logits_process(out, ls[i], **kw)
+
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            turns()
+        for _ in range(3):
+            g.replay()
+    else:
+        turns()
+    torch.cuda.synchronize()
+    for i in range(4):
+        qr, sr, _ = O.rows_i8(xd[i % 2])
+        wr, wsr, _ = O.rows_i8(wf[i // 2])
+        ref = definition(qr, sr.to(f32), wr, wsr.to(f32), None, f32)
+        if i == 3:
+            equal(out, ref)
+        same(ls[i], O.logits_process(ref.cpu(), **{k: v for k, v in c.items() if k != "logits"}))
+
+
+def test_split_products_on_two_streams_at_once():
+    # clusters that split K and wide ones, of two streams between one another
+    cases = [(T, N, K) for k in SPLIT for T, N, K, _ in SPLIT[k]] + [(139, 14096, 2080), (130, 21998, 5184)]
+    data = [product(*c, seed=i) for i, c in enumerate(cases)]
+    refs = [definition(*d, f32) for d in data]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(r) for r in refs] for _ in streams]
+    torch.cuda.synchronize()
+    for turn in range(5):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                for i in range(len(cases)):
+                    j = (i + k * 2 + turn) % len(cases)
+                    B.luce_linear_i8(*data[j], outs[k][j])
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, r in zip(o, refs):
+            equal(a, r)
+
+
 # ----------------------------------------------------------------------------- masks
 @pytest.fixture(params=["call module", "python"])
 def both_ways(request, monkeypatch):

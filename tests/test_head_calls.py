@@ -32,6 +32,18 @@ def test_mask_rows_without_masks(lib):
     assert call(0x20000, 0, 0x10000) == 1 and call(0x20000, 2, 0x10000) == 0
 
 
+def test_linear_plan_refusals(lib):
+    f, plan = lib.luce_linear_i8_plan, (ci * 8)(*[9] * 8)
+    f.argtypes = [ci, ci, ci, ci, vp]
+    for T, N, K, dtype in ((-1, 8, 16, 0), (1 << 24, 8, 16, 0), (1, 0, 16, 0), (1, 1 << 24, 16, 0), (1, 8, 24, 0),
+                           (1, 8, 0, 0), (1, 8, 65552, 0), (1, 8, 16, 3)):
+        assert f(T, N, K, dtype, plan) == 1
+    assert f(1, 8, 16, 0, None) == 1 and list(plan) == [9] * 8
+    assert f(0, 8, 16, 0, plan) == 0 and list(plan) == [0] * 8
+    for T, tokens in ((1, 1), (2, 2), (3, 4), (4, 4), (5, 8), (8, 8)):  # (a choice that asks no device)
+        assert f(T, 100, 4096, 1, plan) == 0 and list(plan) == [0, tokens, 8 if tokens == 8 else 4, 100, 0, 0, 0, 0]
+
+
 # ----------------------------------------------------------------------------- definitions
 def test_a_row_of_zeros_has_scale_zero_without_an_epsilon():
     x = torch.zeros((2, 8))
