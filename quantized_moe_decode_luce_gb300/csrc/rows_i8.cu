@@ -8,6 +8,7 @@
 // sum, and r = 1 / sqrt(mean x^2 + eps) enters the scale alone.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -510,6 +511,30 @@ int chunks_of_a_thread(int V, bool norm, bool aligned_rows, int T, int chunks)
     return (aligned_rows ? work > 2000 * K || (work > 600 * K && chunks >= 2048) : work > 500 * K) ? 8 : 2;
 }
 
+// Whether five chunks of a thread pay where four would do.  The blocks of both
+// have 64 registers a thread (unaligned bf16 rows 56), 1024 threads to an SM:
+// five chunks do where the rows then take fewer rounds of blocks.  Aligned bf16 rows spill with five: never
+// when normed, else only where a second block fits an SM for it.  us with four
+// and five: quantize bf16 4096 x 4099 17.2 16.2, 8191 x 5120 26.4 27.1, 4096 x
+// 20480 71.7 58.4; fp16 8191 x 5120 26.2 24.0, 4096 x 20480 73.5 50.9; norm
+// bf16 1024 x 6319 13.0 13.9, 8191 x 6319 66.7 63.1, 8191 x 10240 69.8 95.7;
+// fp16 8191 x 10240 64.3 59.7, 4096 x 15360 52.9 56.7, 4096 x 20480 91.4 66.2.
+template <typename TX> bool five_chunks(bool norm, bool aligned_rows, int T, int chunks)
+{
+    constexpr bool BF16 = std::is_same_v<TX, __nv_bfloat16>;
+    const int resident = BF16 && !norm && !aligned_rows ? 65536 / 56 : 1024;                 // threads of an SM
+    auto blocks = [&](int k) { return resident / (((chunks + k - 1) / k + 31) / 32 * 32); }; // of an SM
+    if (chunks > 4 * 1024)
+        return true; // (four would not do)
+    if (BF16 && aligned_rows && (norm || blocks(4) > 1))
+        return false;
+    auto rounds = [&](int k) {
+        const int64_t at_once = (int64_t)luce_host::sm_count() * blocks(k);
+        return (T + at_once - 1) / at_once;
+    };
+    return rounds(5) < rounds(4);
+}
+
 template <typename TX>
 luce_status launch_tiny_rows(const TX *x, const TX *res, const TX *xsum, const float *gamma, float eps, int T, int H,
                              float *scale, cudaStream_t stream)
@@ -537,7 +562,7 @@ luce_status run_rows(const void *vx, const void *vres, void *vsum, const float *
         nch *= 2;
     // warps are whole: the next number of chunks where it leaves no more of them to go through in all
     auto in_all = [&](int k) { return ((chunks + k - 1) / k + 31) / 32 * k; };
-    if (V == 8 && nch == 4 && !res && in_all(5) <= in_all(4)) // (4095 x 4099 bf16: 16.1 us, with four 17.0)
+    if (V == 8 && nch == 4 && !res && in_all(5) <= in_all(4) && five_chunks<TX>(gamma != nullptr, al, T, chunks))
         nch = 5;
     if (V == 4 && nch == 4 && chunks <= 256 && in_all(2) < in_all(4)) // (3577 x 758 fp32, normed: 10.5 us, with four 12.1)
         nch = 2;

@@ -367,3 +367,13 @@ def test_as_many_rows_as_there_may_be():
         end = min(r + 2**28, T - 3)
         assert torch.all(q[r:end] == 127) and torch.all(scale[r:end] == scale[0])
     assert scale[0] == torch.tensor(1.0) / 127
+
+
+@pytest.mark.parametrize("dtype", [bf16, f16])
+@pytest.mark.parametrize("T,H", [(1024, 5120), (700, 10240), (310, 15360), (300, 20480), (100, 40960), (1000, 4099), (750, 6319),
+                                 (300, 9211), (500, 9211), (160, 20481)])
+def test_long_rows_of_sixteen_bits(T, H, dtype):
+    # four and five chunks to a thread, on both sides of where a round of blocks ends
+    x, gamma = rows_input(T, H, dtype, T + H), torch.randn(H, generator=gen(H))
+    check_rows(x)
+    check_rows(x, gamma, 1e-6)
