@@ -412,7 +412,10 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, vol
     return __all_sync(0xffffffffu, tc_wait<CLUSTER>(bar, parity, abort_flag));
 }
 
-// One arrival on the barrier at `bar` of cluster CTA `rank`.
+// One arrival on the barrier at `bar` of cluster CTA `rank`, of the cluster's
+// scope where that may be another one.  What it orders is this CTA's shared
+// memory (tensor memory has the tcgen05 fences), so the fence is restricted to
+// that: a release of everything takes 4093 x 4096 x 4096 from 87.9 to 110.7 us.
 template <int CG> __device__ __forceinline__ void arrive_on(uint64_t *bar, uint32_t rank)
 {
     if constexpr (CG == 1) {
@@ -420,7 +423,8 @@ template <int CG> __device__ __forceinline__ void arrive_on(uint64_t *bar, uint3
     } else {
         uint32_t remote;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(bar)), "r"(rank));
-        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+        asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
     }
 }
 
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
             // the stage this group converted last was requested after it.)
             if (NS % GROUPS != 0 && !tc_wait_warp(&rfree[rslot], rphase ^ 1, abort_flag))
                 break;
-            if (!tc_wait_warp(&full[rslot], rphase, abort_flag) || !tc_wait_warp(&sfree[aslot], aphase, abort_flag))
+            if (!tc_wait_warp(&full[rslot], rphase, abort_flag) || !tc_wait_warp<CG == 2>(&sfree[aslot], aphase, abort_flag))
                 break;
             tc_fence_after();
             const uint32_t raw = sm + rslot * C::RAW, bst = smb + aslot * C::BST;
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_linear_i8_tc(const __grid_con
         const bool raw = AS_FLOATS && a.sk == 1 && nu <= CHUNK;
         // accumulator slot `ds` into the sums of half h (set, or added to)
         auto read_back = [&](int (&s)[ECOLS], uint32_t ds, bool set) {
-            if (!tc_wait_warp(&dfull[ds], (dphase >> ds) & 1, abort_flag))
+            if (!tc_wait_warp<CG == 2>(&dfull[ds], (dphase >> ds) & 1, abort_flag))
                 return false;
             tc_fence_after();
             dphase ^= 1u << ds;
