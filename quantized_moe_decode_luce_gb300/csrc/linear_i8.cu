@@ -1022,9 +1022,11 @@ template <class C, typename TO> struct Tc {
 // The tile of the tensor-core kernel for a product: its configuration (1, 2 or 4:
 // CfgOne, CfgPair, CfgWide) and the tokens that it covers.  What a choice takes
 // is estimated in microseconds: setup and last stores, the units that a CTA goes
-// through, its tiles' sums.  The figures are fits to 26 + 19 products of 16 to
-// 8192 tokens with every choice timed; the tile that they choose took 0.4% longer
-// than the best on average, 6% at most.  Tiles of 256 tokens for all products
+// through, its tiles' sums.  The figures are fits to 45 products of 16 to 8192
+// tokens with every choice timed, COST_WIDE.setup to 21 more (COST_WIDE.split, a time below zero, is what the
+// fit gave, not a mechanism).  On 48 products that no fit had seen, of 9 to 3841
+// tokens, what they choose took 0.6% longer than the best choice on average, 13% at
+// most (5.08 for 4.49 us).  Tiles of 256 tokens for all products
 // above 128, before, took 228 us for 8192 x 4096 x 4096 (now 159), 12.8 for 512 x
 // 1024 x 1024 (7.4) and 9.5 for 137 x 88 x 800 (6.1).
 struct Plan {

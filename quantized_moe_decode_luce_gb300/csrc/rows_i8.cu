@@ -128,11 +128,14 @@ __device__ __forceinline__ float scale_of(float d, float ss, int H, float eps, b
 
 // ---------------------------------------------------------------------------
 // A row in registers: NCH chunks of 16 bytes of x per thread, read once (with
-// the residual beside them), codes written once.  Bound by HBM for many rows, whose 32 values a thread spread
-// what every thread does once (the totals, three divisions) thin: with 16 the
-// 8191 x 4096 bf16 rows of luce_quantize_i8 took 33 us instead of 24, and with
-// their largest value found two at a time 21.7.  For few rows it is
-// latency: one chunk a thread, all loads at once, one barrier.
+// the residual beside them), codes written once.  Many fp32 rows, and rows with
+// a residual, are bound by HBM (add + norm 8191 x 4096 fp32: 63.1 us, a plain copy
+// of the bytes 64.5); many 16-bit rows without one by instruction issue, the
+// rounding and its half-way test going value by value (quantize 8191 x 4096 bf16
+// 20.7 us, the bytes alone 14.9; normed 35.9).  The 32 values of a thread spread what
+// every thread does once (the totals, three divisions) thin: with 16 those rows
+// took 33 us instead of 24, and with their largest value found two at a time
+// 21.  For few rows it is latency: one chunk a thread, all loads at once, one barrier.
 //
 // blockDim.x threads to a row: 8, 16 or 32 lanes of a warp (blockDim.y rows to
 // the block, no barrier), or the block.
