@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
     auto biases = [&](auto &&f) {
         for (int j = tid; j < a.nbias; j += THREADS) {
             const int32_t id = j == tid ? bias_id : ids[j];
-            const uint32_t at = (uint32_t)(id - (int32_t)c0);
+            const uint32_t at = (uint32_t)id - (uint32_t)c0;
             if (at < (uint32_t)nc)
                 f((int)at, j);
             bad |= id >= a.V;
@@ -310,22 +310,22 @@ __global__ void __launch_bounds__(THREADS, 2) k_logits_process(const LogitsArgs 
         pres = a.pres ? a.pres[r] : 0.0f;
         rinv = __fdiv_rn(1.0f, rep);
         low = rep >= 0x1p-40f && rep <= 0x1p40f ? LOW : ~0u;
-        const int32_t lo = (int32_t)c0;
+        const uint32_t lo = (uint32_t)c0;
         int32_t top = -1; // the largest id seen
         if (S16 && len == SHORT && plen <= 0) {
             top = h[--len];
-            const uint32_t at = (uint32_t)(top - lo);
+            const uint32_t at = (uint32_t)top - lo;
             apart = at < (uint32_t)nc ? (int)at + sh : -VEC;
         }
         // (c0 + nc <= V < 2^31, so that one unsigned comparison also leaves out negative ids)
         auto prompt = [&](int32_t id) {
             top = max(top, id);
-            const uint32_t at = (uint32_t)(id - lo);
+            const uint32_t at = (uint32_t)id - lo;
             slots.template count<true>((int)at + sh, at < (uint32_t)nc);
         };
         auto made = [&](int32_t id) {
             top = max(top, id);
-            const uint32_t at = (uint32_t)(id - lo);
+            const uint32_t at = (uint32_t)id - lo;
             slots.template count<false>((int)at + sh, at < (uint32_t)nc);
         };
         auto one = [&](int32_t id, int i) {

@@ -19,8 +19,8 @@ from oracle import head as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from quantized_moe_decode_luce_gb300 import build as BLD
 from quantized_moe_decode_luce_gb300.layer import GreedyHead, LinearI8
-from test_gpu_head import (_lib, _no_device_faults, bf16, check_rows, codes, f16, f32, gen,  # noqa: F401
-                           logits_case, make_head, rows_input, same)  # (the fixtures hold for every test here)
+from test_gpu_head import (SCALE_TOL, _lib, _no_device_faults, bf16, check_rows, codes, f16, f32,  # noqa: F401
+                           gen, logits_case, make_head, rows_input, same)  # (the fixtures hold for every test here)
 
 pytestmark = pytest.mark.gpu
 
@@ -377,3 +377,94 @@ def test_long_rows_of_sixteen_bits(T, H, dtype):
     x, gamma = rows_input(T, H, dtype, T + H), torch.randn(H, generator=gen(H))
     check_rows(x)
     check_rows(x, gamma, 1e-6)
+
+
+# ----------------------------------------------------------------------------- the largest sizes
+@pytest.mark.parametrize("T,H,shift", [(70001, 32768, 0), (70001, 32768, 1), (525000, 4099, 0), (36000, 65536, 0)])
+def test_rows_beyond_2_31_elements(T, H, shift):
+    # the last rows are those of a small call; the first are not written by them
+    n = 5
+    x = torch.zeros(T * H + shift, dtype=bf16, device="cuda")[shift:].view(T, H)
+    ends = rows_input(2 * n, H, bf16, 3)
+    ends[n - 1] = ends[0]
+    x[:n], x[-n:] = ends[:n].cuda(), ends[n:].cuda()
+    gamma = torch.rand(H, generator=gen(5)) + 0.5
+    q, s = torch.full((T, H), 7, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    for norm in (False, True):
+        if norm:
+            B.luce_add_rmsnorm_i8(x, x, x, gamma.cuda(), 1e-6, q, s)  # (twice the rows, where they were)
+            q_ref, s_ref, sum_ref = O.rows_i8(ends, gamma, 1e-6, ends)
+            same(torch.cat([x[:n], x[-n:]]), sum_ref)
+        else:
+            B.luce_quantize_i8(x, q, s)
+            q_ref, s_ref, _ = O.rows_i8(ends)
+        same(torch.cat([q[:n], q[-n:]]), q_ref)
+        got = torch.cat([s[:n], s[-n:]]).cpu().double()
+        assert torch.all((got - s_ref).abs() <= SCALE_TOL * s_ref)
+        assert not torch.any(s[n:-n]) and not torch.any(q[T // 2 - 9:T // 2 + 9])
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 16777215, 16), (300, 9000001, 16), (40001, 60001, 32), (300001, 9001, 16)])
+def test_linear_outputs_of_the_largest_sizes(T, N, K):
+    xq, xs, wq, ws, b = product(T, N, K, T)
+    out = torch.empty((T, N), dtype=bf16, device="cuda")
+    B.luce_linear_i8(xq, xs, wq, ws, b, out)
+    for t in (slice(0, 3), slice(T // 2, T // 2 + 3), slice(T - 3, T)):
+        equal(out[t], definition(xq[t].contiguous(), xs[t], wq, ws, b, bf16))
+
+
+def test_logits_of_the_largest_vocabulary():
+    V, L = 2**31 - 1, 4096
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty((1, V), dtype=bf16, device="cuda")
+    x.normal_(generator=g)
+    hist = torch.randint(0, V, (1, L), generator=g, dtype=torch.int64, device="cuda").to(torch.int32)
+    hist[0, :6] = torch.tensor([V - 1, 0, V - 2, V - 1, -1, V - 33])
+    bias_ids = torch.tensor([[V - 1, 5, V - 4, -1]], dtype=torch.int32, device="cuda")
+    bias_vals = torch.tensor([[3.0, -2.0, 9.0, 1.0]], device="cuda")
+    mask = torch.randint(-2**31, 2**31, (1, (V + 31) // 32), generator=g, dtype=torch.int64, device="cuda").to(torch.int32)
+    row = lambda v, t=f32: torch.tensor([v], dtype=t, device="cuda")  # noqa: E731
+    kw = dict(hist=hist, hist_len=row(L, torch.int32), prompt_len=row(2, torch.int32), repetition=row(1.3), frequency=row(0.25),
+              presence=row(0.5), bias_ids=bias_ids, bias_vals=bias_vals)
+    out = torch.empty((1, V), device="cuda")
+    B.luce_logits_process(x, out, **kw, mask=mask)
+    # the tokens that anything happens to, renumbered, by the definition; the rest are the logits or masked
+    at = torch.unique(torch.cat([hist[0], bias_ids[0]]).long().clamp_(min=0))
+    where = {int(t): i for i, t in enumerate(at.tolist())}
+    small = {k: v.cpu() for k, v in kw.items()}
+    for k in ("hist", "bias_ids"):
+        small[k] = torch.tensor([[where[t] if t >= 0 else -1 for t in small[k][0].tolist()]], dtype=torch.int32)
+    ref = O.logits_process(x[:, at].cpu(), **small)
+    bit = lambda t: (mask[0, t // 32].long() >> (t % 32)) & 1  # noqa: E731
+    ref[:, bit(at).cpu() == 0] = -math.inf
+    same(out[:, at], ref)
+    out[0, at] = 0.0
+    step = 2**27
+    for v in range(0, V, step):
+        t = torch.arange(v, min(v + step, V), device="cuda")
+        want = torch.where(bit(t) == 1, x[0, t[0]:t[-1] + 1].to(f32), -math.inf)
+        want[at[(at >= t[0]) & (at <= t[-1])] - v] = 0.0
+        assert torch.equal(out[0, t[0]:t[-1] + 1], want)
+
+
+def test_logits_of_as_many_rows_as_there_may_be():
+    R, V = 65535, 40
+    c = logits_case(7, V, hist=9, bias=3, mask=True)
+    n = R // 7 + 1
+    many = {k: (v if k == "mask" else v.repeat((n,) + (1,) * (v.dim() - 1))[:R]).cuda() for k, v in c.items()}
+    out = torch.empty((R, V), device="cuda")
+    B.luce_logits_process(many.pop("logits"), out, **many)
+    same(out, O.logits_process(**c).repeat((n, 1))[:R])
+    with pytest.raises(B.LuceError):
+        B.luce_logits_process(torch.zeros((R + 1, 2), device="cuda"), torch.zeros((R + 1, 2), device="cuda"))
+
+
+@pytest.mark.parametrize("hist", [30, 40000])
+def test_logits_ids_of_the_lowest_value_are_padding(hist):
+    c = logits_case(2, 200000, hist=hist, bias=6, mask=True)
+    c["hist"][:, 5:9] = torch.tensor([-2**31, -2**31 + 1, -200000, -2**30], dtype=torch.int32)
+    c["bias_ids"][:, 3] = -2**31
+    want = O.logits_process(**c)
+    out = torch.empty((2, 200000), device="cuda")
+    B.luce_logits_process(out=out, **{k: v.cuda() for k, v in c.items()})
+    same(out, want)
