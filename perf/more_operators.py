@@ -24,27 +24,27 @@ SIZES = {"f32": 4, "bf16": 2, "f16": 2, "i8": 1}
 def listed():
     return [
         # a small projection for a single token: pure latency
-        dict(name="linear, one token", op="linear", T=1, N=2048, K=2048, group=32, zeros=False, x="bf16", out="bf16", bias=False),
+        dict(name="linear one token", op="linear", T=1, N=2048, K=2048, group=32, zeros=False, x="bf16", out="bf16", bias=False),
         # the vocabulary head for a single token, behind the int8 norm: the weights' way from memory
-        dict(name="linear, head of 1", op="linear", T=1, N=129280, K=4096, group=128, zeros=False, x="i8", out="f32", bias=False),
+        dict(name="linear head of 1", op="linear", T=1, N=129280, K=4096, group=128, zeros=False, x="i8", out="f32", bias=False),
         # the same over the verify step's columns, an odd vocabulary, fp32 activations, codes with zero points
-        dict(name="linear, odd head of 5", op="linear", T=5, N=129279, K=4096, group=64, zeros=True, x="f32", out="f32", bias=False),
+        dict(name="linear odd head of 5", op="linear", T=5, N=129279, K=4096, group=64, zeros=True, x="f32", out="f32", bias=False),
         # a small batch of decoding sequences through a projection; K that is no multiple of a whole chunk
-        dict(name="linear, batch of 16", op="linear", T=16, N=8192, K=4144, group=128, zeros=True, x="bf16", out="bf16", bias=True),
+        dict(name="linear batch of 16", op="linear", T=16, N=8192, K=4144, group=128, zeros=True, x="bf16", out="bf16", bias=True),
         # a larger batch, ragged, through a long contraction
-        dict(name="linear, batch of 61", op="linear", T=61, N=4096, K=14336, group=128, zeros=False, x="f16", out="f16", bias=False),
+        dict(name="linear batch of 61", op="linear", T=61, N=4096, K=14336, group=128, zeros=False, x="f16", out="f16", bias=False),
         # a prompt's rest through a projection of the same weights
-        dict(name="linear, chunk of 300", op="linear", T=300, N=8192, K=4096, group=64, zeros=False, x="bf16", out="bf16", bias=False),
+        dict(name="linear chunk of 300", op="linear", T=300, N=8192, K=4096, group=64, zeros=False, x="bf16", out="bf16", bias=False),
         # one sequence with every filter: latency
-        dict(name="sample, one row", op="sample", R=1, V=129280, dtype="f32", top_k=50, top_p=0.95, min_p=0.02),
+        dict(name="sample one row", op="sample", R=1, V=129280, dtype="f32", top_k=50, top_p=0.95, min_p=0.02),
         # the verify step's columns by temperature alone, odd vocabulary
-        dict(name="sample, five rows", op="sample", R=5, V=129279, dtype="f32", top_k=0, top_p=1.0, min_p=0.0),
+        dict(name="sample five rows", op="sample", R=5, V=129279, dtype="f32", top_k=0, top_p=1.0, min_p=0.0),
         # a middling batch over a small vocabulary, rows of many parameters
-        dict(name="sample, 64 short rows", op="sample", R=64, V=32000, dtype="f16", top_k=-1, top_p=-1.0, min_p=-1.0),
+        dict(name="sample 64 short rows", op="sample", R=64, V=32000, dtype="f16", top_k=-1, top_p=-1.0, min_p=-1.0),
         # a serving batch: top-k, then top-p
-        dict(name="sample, batch of 256", op="sample", R=256, V=129280, dtype="bf16", top_k=64, top_p=0.9, min_p=0.0),
+        dict(name="sample batch of 256", op="sample", R=256, V=129280, dtype="bf16", top_k=64, top_p=0.9, min_p=0.0),
         # a serving batch whose rows keep what top-p leaves of the whole vocabulary
-        dict(name="sample, top-p of 128 rows", op="sample", R=128, V=151936, dtype="f32", top_k=0, top_p=0.9, min_p=0.0),
+        dict(name="sample top-p of 128 rows", op="sample", R=128, V=151936, dtype="f32", top_k=0, top_p=0.9, min_p=0.0),
     ]
 
 
