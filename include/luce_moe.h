@@ -79,11 +79,13 @@ typedef struct {
     uint8_t qs[128];     /* 256 4-bit codes (see luce_moe_glu_q4k)       */
 } luce_block_q4_k;
 
-/* Element types of the operators that take more than one (int8 decode head). */
+/* Element types of the operators that take more than one (decode head).
+ * LUCE_I8 is one of luce_linear_w4's activations only. */
 typedef enum {
     LUCE_F32 = 0,
     LUCE_BF16 = 1,
-    LUCE_F16 = 2
+    LUCE_F16 = 2,
+    LUCE_I8 = 3
 } luce_dtype;
 
 /* Device fault bits (luce_get_fault). */
@@ -500,6 +502,92 @@ LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, i
                                          const float *presence, const int32_t *bias_ids, const float *bias_vals,
                                          int n_bias, const uint32_t *mask, int n_masks, int64_t ld_mask,
                                          const int32_t *mask_rows, float *out, int64_t ld_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * luce_quantize_w4 / luce_pack_w4 / luce_linear_w4 -- products of a few tokens
+ * with a matrix of 4-bit codes that have a scale, and optionally a zero point,
+ * per group of 32, 64 or 128 values of a row (an output channel):
+ *   w[n][k] = scale[n][k / group] * (q[n][k] - z[n][k / group])
+ *   out[t][n] = (sum_k x[t][k] * w[n][k]) (* x_scale[t]) (+ bias[n])
+ * z is 8 where there are no zero points.  The products of a group are added in
+ * fp32 (exact for int8 activations) and multiplied by the group's scale, the
+ * groups' products are added in fp32, the factor and the bias are rounded to
+ * fp32 each, then the sum to out_dtype.  The order of the sums depends on the
+ * sizes and types alone: a call gives the same bits whenever it is made.
+ *
+ * A row of codes is kept in chunks of 128 values, 64 bytes: word 4 t + j of a
+ * chunk (t, j in 0..3; 32 bits, little-endian) holds the values 32 j + 8 t + i
+ * of the chunk, i = 0..7, value i in its bits 4 (i / 2) + 16 (i % 2) .. + 3.
+ * The last chunk of a row is whole; its codes behind K count for nothing.
+ * luce_pack_w4 brings codes of any origin into this order.
+ *
+ * luce_quantize_w4 makes codes and scales of a matrix (fp32 operations, each
+ * rounded to nearest; rounding of codes is half away from zero).  Per group:
+ *   without zero points:  d = max |w| / 7,  scale = d rounded to its type,
+ *     q = round(w / scale) + 8 within [1, 15]
+ *   with them:  lo = min(0, min w), hi = max(0, max w),  d = (hi - lo) / 15,
+ *     scale = d rounded to its type, z = round(-lo / scale) within [0, 15],
+ *     q = round(w / scale) + z within [0, 15]
+ * A scale beyond its type's range is the largest finite one; where it is zero
+ * all codes are z, and z is 8 or 0.  A group with a NaN or an infinity has the
+ * scale NaN.
+ *
+ *   x [T][K] fp32, bf16, fp16 (x_scale NULL), or int8 with x_scale [T] fp32;
+ *     rows ld_x elements apart (ld_x >= K), every row 16-byte aligned
+ *   wq [N][ceil(K / 128)][64] bytes, 16-byte aligned
+ *   scale [N][ceil(K / group)] fp16 or bf16
+ *   zeros [N][ceil(K / group)] bytes 0..15 (of others the low four bits), or NULL
+ *   bias [N] fp32 or NULL
+ *   out [T][N] of out_dtype, its rows ld_out elements apart (ld_out >= N; what
+ *     lies between the rows is left as it was), aligned to the element
+ *   w [N][K] fp32, bf16 or fp16, aligned to the element    codes [N][K] bytes
+ * Requires K % 16 == 0, 16 <= K <= 65536, group 32, 64 or 128, N >= 1 (N >= 0
+ * where a matrix is made), T >= 0, N and T below 2^24; no output may overlap
+ * an input or another output.  No workspace.  Under programmatic launch
+ * nothing is read before the previous kernel is over.
+ */
+LUCE_API luce_status luce_quantize_w4(const void *w, luce_dtype dtype, int N, int K, int group, uint8_t *wq, void *scale,
+                                      luce_dtype scale_dtype, uint8_t *zeros, void *stream);
+LUCE_API luce_status luce_pack_w4(const uint8_t *codes, int N, int K, uint8_t *wq, void *stream);
+LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t ld_x, const float *x_scale,
+                                    const uint8_t *wq, const void *scale, luce_dtype scale_dtype, const uint8_t *zeros,
+                                    int group, const float *bias, int T, int N, int K, void *out, luce_dtype out_dtype,
+                                    int64_t ld_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * luce_sample -- a token per row of logits, drawn with a temperature, top-k,
+ * top-p and min-p of the row's own and one given random number.  Per row r:
+ *   M = max_v l_v    weight w_v = exp((l_v - M) / temperature[r])
+ *   tokens stand in the order of falling logits, the lower id first among equals
+ *   top_k:  the first top_k[r] tokens stay (all if it is <= 0 or >= V)
+ *   top_p:  of those, a token stays if the weights before it add up to less than
+ *           top_p[r] times the weights of all of them (the first one always;
+ *           all if top_p[r] >= 1 or NaN)
+ *   min_p:  of those, a token stays if w_v >= min_p[r] (the first one always)
+ *   Z = the weights that stay;  idx[r] = the first token, in the order of ids,
+ *   at which the weights that stay, up to and including it, exceed u[r] * Z;
+ *   prob[r] = its weight / Z
+ * A temperature that is not above zero picks the first token (prob 1), as
+ * luce_argmax does.  An infinite one weighs all tokens above -infinity alike.
+ * Tokens at -infinity have no weight and are never drawn.  A row of them alone
+ * has idx 0 and prob 0; a row with a NaN or +infinity has idx 0 and prob NaN.
+ * u[r] is taken as within [0, 1): NaN as 0, 1 and more as the last token.
+ * Weights are whole multiples of 2^-L of the row's largest (L = 62 -
+ * ceil(log2 V), at least 40), each within 2^-30 of its value relative to it or
+ * one such unit: their sums have no order, and the result is the same bits
+ * whenever the call is made.
+ *
+ *   logits [R][V] of `dtype`, rows ld_logits elements apart (ld_logits >= V),
+ *     aligned to the element
+ *   u [R] fp32    temperature, top_p, min_p [R] fp32, top_k [R] int32, each
+ *     NULL for none (temperature 1)
+ *   idx [R] int32 out    prob [R] fp32 out, or NULL; neither may overlap an
+ *     input or the other
+ * Requires 1 <= V <= 262144 (LUCE_ERR_UNSUPPORTED beyond), 0 <= R <= 65535.  No workspace.
+ */
+LUCE_API luce_status luce_sample(const void *logits, luce_dtype dtype, int R, int64_t V, int64_t ld_logits, const float *u,
+                                 const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                                 int32_t *idx, float *prob, void *stream);
 
 /* ------------------------------------------------------------------------
  * luce_moe_prep -- luce_route_topk, luce_quantize_q8_1 (K = H) and

@@ -27,6 +27,7 @@ LUCE_ERR_CUDA = 3
 LUCE_F32 = 0
 LUCE_BF16 = 1
 LUCE_F16 = 2
+LUCE_I8 = 3
 LUCE_FAULT_BAD_ID = 0x1
 LUCE_FAULT_TIMEOUT = 0x2
 LUCE_FAULT_DESYNC = 0x4
@@ -73,6 +74,9 @@ def lib() -> ctypes.CDLL:
             "luce_add_rmsnorm_i8": [P, P, P, i32, P, f32, i32, i32, P, P, P],
             "luce_linear_i8": [P, P, P, P, P, i32, i32, i32, P, i32, i64, P],
             "luce_linear_i8_plan": [i32, i32, i32, i32, P],
+            "luce_quantize_w4": [P, i32, i32, i32, i32, P, P, i32, P, P],
+            "luce_pack_w4": [P, i32, i32, P, P],
+            "luce_linear_w4": [P, i32, i64, P, P, P, i32, P, i32, P, i32, i32, i32, P, i32, i64, P],
             "luce_logits_process": [P, i32, i32, i64, i64, P, i64, P, P, P, P, P, P, P, i32, P, i32, i64, P, P, i64,
                                     P],
         }
@@ -492,6 +496,56 @@ def luce_logits_process(logits, out, hist=None, hist_len=None, prompt_len=None, 
           per_row(mask_rows, _I32, "mask_rows"), op, ldo)
 
 
+# ----------------------------------------------------------------------------- 4-bit products
+_X_DTYPE = {**_DTYPE, torch.int8: LUCE_I8}
+_XS, _HALVES, _U8 = frozenset(_X_DTYPE), frozenset({torch.float16, torch.bfloat16}), frozenset({torch.uint8})
+
+
+def _groups(K: int, group: int) -> int:
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    return -(-K // group)
+
+
+def w4_row_bytes(K: int) -> int:
+    """Bytes of a packed row of K 4-bit codes: 64 for every chunk of 128 begun."""
+    return -(-K // 128) * 64
+
+
+def luce_quantize_w4(w, group: int, wq, scale, zeros=None, stream=None) -> None:
+    """w [N, K] fp32, bf16 or fp16 -> packed codes wq [N, w4_row_bytes(K)] uint8, scale [N, ceil(K / group)]
+    fp16 or bf16, and, with zero points, zeros of scale's shape, uint8."""
+    N, K, dev = _matrix(w, "w")
+    G = _groups(K, group)
+    _call("luce_quantize_w4", dev, stream, _addr(w, _FLOATS, (N, K), dev, "w"), _DTYPE[w.dtype], N, K, group,
+          _addr(wq, _U8, (N, w4_row_bytes(K)), dev, "wq"), _addr(scale, _HALVES, (N, G), dev, "scale"),
+          _DTYPE[scale.dtype], None if zeros is None else _addr(zeros, _U8, (N, G), dev, "zeros"))
+
+
+def luce_pack_w4(codes, wq, stream=None) -> None:
+    """codes [N, K] uint8, a 4-bit code to a byte -> packed codes wq [N, w4_row_bytes(K)] uint8."""
+    N, K, dev = _matrix(codes, "codes")
+    _call("luce_pack_w4", dev, stream, _addr(codes, _U8, (N, K), dev, "codes"), N, K,
+          _addr(wq, _U8, (N, w4_row_bytes(K)), dev, "wq"))
+
+
+def luce_linear_w4(x, x_scale, wq, scale, zeros, group: int, bias, out, stream=None) -> None:
+    """x [T, K] fp32, bf16, fp16 (x_scale None), or int8 with x_scale [T] fp32; wq, scale, zeros (or None) as
+    luce_quantize_w4 leaves them; bias [N] fp32 or None -> out [T, N] fp32, bf16 or fp16.  The rows of x and out
+    may be apart (slices of wider rows)."""
+    T, K, dev = _matrix(x, "x")
+    N, G = _matrix(wq, "wq")[0], _groups(K, group)
+    xp, ldx = _rows(x, _XS, (T, K), dev, "x")
+    o, ldo = _rows(out, _FLOATS, (T, N), dev, "out")
+    if (x.dtype == torch.int8) != (x_scale is not None):
+        raise ValueError("x_scale goes with int8 activations, and only with them")
+    _call("luce_linear_w4", dev, stream, xp, _X_DTYPE[x.dtype], ldx,
+          None if x_scale is None else _addr(x_scale, _F32, (T,), dev, "x_scale"),
+          _addr(wq, _U8, (N, w4_row_bytes(K)), dev, "wq"), _addr(scale, _HALVES, (N, G), dev, "scale"),
+          _DTYPE[scale.dtype], None if zeros is None else _addr(zeros, _U8, (N, G), dev, "zeros"), group,
+          None if bias is None else _addr(bias, _F32, (N,), dev, "bias"), T, N, K, o, _DTYPE[out.dtype], ldo)
+
+
 def luce_get_fault() -> int:
     bits = ctypes.c_uint(0)
     _check("luce_get_fault", lib().luce_get_fault(ctypes.byref(bits)))
@@ -508,6 +562,6 @@ __all__ = ["LuceError", "lib", "status_string", "luce_route_topk", "luce_quantiz
            "luce_argmax_shard", "luce_argmax_pick", "luce_rmsnorm_router", "luce_add_rmsnorm_router", "luce_ep_mask", "luce_add_f32",
            "luce_moe_glu_q4k", "luce_moe_down_combine_q4k",
            "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_linear_i8_plan",
-           "luce_logits_process", "LUCE_F32", "LUCE_BF16", "LUCE_F16",
+           "luce_logits_process", "luce_quantize_w4", "luce_pack_w4", "luce_linear_w4", "w4_row_bytes", "LUCE_I8", "LUCE_F32", "LUCE_BF16", "LUCE_F16",
            "luce_get_fault", "luce_version", "LUCE_OK", "LUCE_ERR_INVALID_ARG", "LUCE_ERR_UNSUPPORTED",
            "LUCE_ERR_CUDA", "LUCE_FAULT_BAD_ID", "LUCE_FAULT_TIMEOUT", "LUCE_FAULT_DESYNC"]
