@@ -572,8 +572,8 @@ LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t l
  * Tokens at -infinity have no weight and are never drawn.  A row of them alone
  * has idx 0 and prob 0; a row with a NaN or +infinity has idx 0 and prob NaN.
  * u[r] is taken as within [0, 1): NaN as 0, 1 and more as the last token.
- * Weights are whole multiples of 2^-L of the row's largest (L = 62 -
- * ceil(log2 V), at least 40), each within 2^-30 of its value relative to it or
+ * Weights are whole multiples of 2^-L of the row's largest (L = 63 -
+ * ceil(log2 V), at least 44), each within 2^-29 of its value relative to it or
  * one such unit: their sums have no order, and the result is the same bits
  * whenever the call is made.
  *
@@ -583,7 +583,7 @@ LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t l
  *     NULL for none (temperature 1)
  *   idx [R] int32 out    prob [R] fp32 out, or NULL; neither may overlap an
  *     input or the other
- * Requires 1 <= V <= 262144 (LUCE_ERR_UNSUPPORTED beyond), 0 <= R <= 65535.  No workspace.
+ * Requires 1 <= V <= 393216 (LUCE_ERR_UNSUPPORTED beyond), 0 <= R <= 65535.  No workspace.
  */
 LUCE_API luce_status luce_sample(const void *logits, luce_dtype dtype, int R, int64_t V, int64_t ld_logits, const float *u,
                                  const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,

@@ -77,6 +77,7 @@ def lib() -> ctypes.CDLL:
             "luce_quantize_w4": [P, i32, i32, i32, i32, P, P, i32, P, P],
             "luce_pack_w4": [P, i32, i32, P, P],
             "luce_linear_w4": [P, i32, i64, P, P, P, i32, P, i32, P, i32, i32, i32, P, i32, i64, P],
+            "luce_sample": [P, i32, i32, i64, i64, P, P, P, P, P, P, P, P],
             "luce_logits_process": [P, i32, i32, i64, i64, P, i64, P, P, P, P, P, P, P, i32, P, i32, i64, P, P, i64,
                                     P],
         }
@@ -546,6 +547,22 @@ def luce_linear_w4(x, x_scale, wq, scale, zeros, group: int, bias, out, stream=N
           None if bias is None else _addr(bias, _F32, (N,), dev, "bias"), T, N, K, o, _DTYPE[out.dtype], ldo)
 
 
+# ----------------------------------------------------------------------------- sampling
+def luce_sample(logits, u, idx, prob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> None:
+    """logits [R, V] fp32, bf16 or fp16 (rows may be apart) -> idx [R] int32, a token per row drawn with u [R] fp32 in
+    [0, 1), and prob [R] fp32 (or None), its probability among those left by top_k [R] int32, top_p and min_p
+    [R] fp32 at temperature [R] fp32.  Each of the four may be left out."""
+    R, V, dev = _matrix(logits, "logits")
+    lp, ld = _rows(logits, _FLOATS, (R, V), dev, "logits")
+
+    def per_row(t, dtypes, name):
+        return None if t is None else _addr(t, dtypes, (R,), dev, name)
+
+    _call("luce_sample", dev, stream, lp, _DTYPE[logits.dtype], R, V, ld, _addr(u, _F32, (R,), dev, "u"),
+          per_row(temperature, _F32, "temperature"), per_row(top_k, _I32, "top_k"), per_row(top_p, _F32, "top_p"),
+          per_row(min_p, _F32, "min_p"), _addr(idx, _I32, (R,), dev, "idx"), per_row(prob, _F32, "prob"))
+
+
 def luce_get_fault() -> int:
     bits = ctypes.c_uint(0)
     _check("luce_get_fault", lib().luce_get_fault(ctypes.byref(bits)))
@@ -562,6 +579,6 @@ __all__ = ["LuceError", "lib", "status_string", "luce_route_topk", "luce_quantiz
            "luce_argmax_shard", "luce_argmax_pick", "luce_rmsnorm_router", "luce_add_rmsnorm_router", "luce_ep_mask", "luce_add_f32",
            "luce_moe_glu_q4k", "luce_moe_down_combine_q4k",
            "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_linear_i8_plan",
-           "luce_logits_process", "luce_quantize_w4", "luce_pack_w4", "luce_linear_w4", "w4_row_bytes", "LUCE_I8", "LUCE_F32", "LUCE_BF16", "LUCE_F16",
+           "luce_logits_process", "luce_quantize_w4", "luce_pack_w4", "luce_linear_w4", "w4_row_bytes", "luce_sample", "LUCE_I8", "LUCE_F32", "LUCE_BF16", "LUCE_F16",
            "luce_get_fault", "luce_version", "LUCE_OK", "LUCE_ERR_INVALID_ARG", "LUCE_ERR_UNSUPPORTED",
            "LUCE_ERR_CUDA", "LUCE_FAULT_BAD_ID", "LUCE_FAULT_TIMEOUT", "LUCE_FAULT_DESYNC"]

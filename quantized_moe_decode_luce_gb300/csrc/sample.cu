@@ -1,0 +1,556 @@
+// sample.cu -- a token per row of logits, drawn with a temperature, top-k,
+// top-p and min-p from a given random number (luce_sample), with its C-ABI
+// entry point.
+//
+// A cluster of CTAs takes a row: every CTA keeps a slice of it in shared
+// memory, in the logits' own type, so the row is read from memory once and
+// everything after the first pass runs on the chip.  Both filters come down to
+// a key (a logit as a whole number of the same order) that divides those that
+// stay from the rest, and a count of ties that stay, in the order of ids.  The
+// key is found digit by digit: a histogram of the keys in question, ten bits of
+// them at a time, holds counts (top-k) or weights (top-p); the CTAs' histograms
+// are added through distributed shared memory by every CTA for itself, so a
+// level costs one cluster barrier.  The draw adds the weights that stay in the
+// order of ids: lanes, warps, CTAs.
+//
+// Weights are whole numbers.  2^-z is looked up for the first eight bits
+// behind the binary point of z = (M - l) log2(e) / temperature and corrected by
+// three terms of the exponential series for the rest, which is below 2^-9, in
+// fixed point; z itself is carried in two floats, for a rounding of z would
+// shift the borders between tokens by 2^-24 of the row's weight.  Sums of whole
+// numbers have no order: atomics give the same bits every time.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+
+namespace {
+
+using namespace luce;
+namespace cg = cooperative_groups;
+
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int CL_MAX = 8;                // CTAs of a cluster at most (the portable limit)
+constexpr int DIGIT = 10, BINS = 1 << DIGIT;
+constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
+typedef unsigned long long u64;
+
+struct SampleArgs {
+    const void *logits;
+    int64_t ld;
+    int V, slice; // slice: elements of a CTA, whole vectors of every warp
+    int sh;       // the largest weight is 2^(31 + sh)
+    const float *u, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int32_t *idx;
+    float *prob;
+};
+
+// 2^(31 - j / 256), rounded.
+struct Powers {
+    uint32_t v[256];
+};
+constexpr Powers powers()
+{
+    // the 256th root of 1/2 by eight square roots (Newton's iteration)
+    double r = 0.5;
+    for (int i = 0; i < 8; i++) {
+        double s = 1.0;
+        for (int k = 0; k < 60; k++)
+            s = 0.5 * (s + r / s);
+        r = s;
+    }
+    Powers p{};
+    double x = 2147483648.0;
+    for (int j = 0; j < 256; j++, x *= r)
+        p.v[j] = (uint32_t)(x + 0.5);
+    return p;
+}
+__device__ constexpr Powers POWERS = powers();
+
+// ---------------------------------------------------------------------------
+// Logits as whole numbers of the same order; both zeros are one.  Everything
+// at or below the key of -infinity counts as -infinity (NaN never gets here).
+template <typename TL> struct Key;
+template <> struct Key<float> {
+    static constexpr uint32_t NONE = 0x007fffffu;
+    static __device__ __forceinline__ uint32_t of(float v)
+    {
+        const uint32_t b = __float_as_uint(v + 0.0f);
+        return b & 0x80000000u ? ~b : b | 0x80000000u;
+    }
+    static __device__ __forceinline__ float value(uint32_t k)
+    {
+        return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+    }
+    static __device__ __forceinline__ uint32_t at_least(float v) { return of(v); } // the smallest key of a logit >= v
+};
+struct Key16 {
+    static __device__ __forceinline__ uint32_t of_bits(uint32_t b)
+    {
+        b = b == 0x8000u ? 0u : b;
+        return b & 0x8000u ? b ^ 0xffffu : b | 0x8000u;
+    }
+    static __device__ __forceinline__ uint16_t bits(uint32_t k) { return (uint16_t)(k & 0x8000u ? k & 0x7fffu : k ^ 0xffffu); }
+};
+template <> struct Key<__half> : Key16 {
+    static constexpr uint32_t NONE = 0x03ffu;
+    static __device__ __forceinline__ uint32_t of(__half v) { return of_bits(__half_as_ushort(v)); }
+    static __device__ __forceinline__ float value(uint32_t k) { return __half2float(__ushort_as_half(bits(k))); }
+    static __device__ __forceinline__ uint32_t at_least(float v) { return of(__float2half_ru(v)); }
+};
+template <> struct Key<__nv_bfloat16> : Key16 {
+    static constexpr uint32_t NONE = 0x007fu;
+    static __device__ __forceinline__ uint32_t of(__nv_bfloat16 v) { return of_bits(__bfloat16_as_ushort(v)); }
+    static __device__ __forceinline__ float value(uint32_t k) { return __bfloat162float(__ushort_as_bfloat16(bits(k))); }
+    static __device__ __forceinline__ uint32_t at_least(float v) { return of(__float2bfloat16_ru(v)); }
+};
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename TL> __device__ __forceinline__ TL minus_infinity();
+template <> __device__ __forceinline__ float minus_infinity<float>() { return -INFINITY; }
+template <> __device__ __forceinline__ __half minus_infinity<__half>() { return __ushort_as_half(0xfc00); }
+template <> __device__ __forceinline__ __nv_bfloat16 minus_infinity<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
+
+// The weight of a logit: 2^(31 + sh - z), z = (M - l) c, in whole numbers.
+// (M and l are taken as quarters, so that their difference cannot overflow.)
+struct Weigh {
+    float M4, c_hi, c_lo; // M / 4, 4 c in two floats
+    int sh;
+    const uint2 *table; // 2^(31 - j / 256) as a whole number and as a float
+    __device__ __forceinline__ u64 operator()(float l) const
+    {
+        const float b = -0.25f * l, d = M4 + b;
+        const float bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
+        const float zh = fminf(d * c_hi, 64.0f);
+        const float zl = fmaf(d, c_hi, -zh) + fmaf(d, c_lo, e * c_hi);
+        const float magic = 49152.0f; // steps of 2^-8 at 2^15
+        const float t = zh + magic;
+        const int n = __float_as_int(t) - __float_as_int(magic);
+        const float r = (zh - (t - magic)) + zl;
+        const float p = r * fmaf(r, fmaf(r, -0.055504109f, 0.24022651f), -0.69314718f); // ln(2)^3 / 6, ln(2)^2 / 2, ln(2)
+        const uint2 q = table[n & 255];
+        const uint32_t m = q.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(q.y), p, 12582912.0f)) - 0x4B400000);
+        return n < 64 * 256 ? ((u64)m << sh) >> (n >> 8) : 0;
+    }
+};
+
+template <typename T> __device__ __forceinline__ T warp_add(T v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <typename T> __device__ __forceinline__ T warp_scan(T v, int lane) // inclusive
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T a = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += a;
+    }
+    return v;
+}
+
+struct Shared {
+    uint2 table[256];
+    u64 hist[2][BINS];       // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
+    u64 gather[2][CL_MAX];
+    u64 warp[WARPS];
+    u64 found[4];
+    uint32_t top[CL_MAX], bad[CL_MAX];
+    uint32_t wtop[WARPS];
+    uint32_t tie;
+};
+
+template <typename TL>
+__global__ void __launch_bounds__(THREADS)
+    k_sample(const SampleArgs a)
+{
+    constexpr int VEC = 16 / sizeof(TL);
+    struct __align__(16) Vec { TL v[VEC]; };
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ Shared s;
+    TL *buf = reinterpret_cast<TL *>(smem_raw);
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks(), row = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < 256; i += THREADS)
+        s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
+    pdl_wait();
+    pdl_trigger();
+
+    // The row's slice.  Place j of the row is its element j - first, so that
+    // vectors of places start 16-byte aligned; places without an element hold -infinity.
+    const TL *logits = reinterpret_cast<const TL *>(a.logits) + (int64_t)row * a.ld;
+    const int first = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(TL));
+    const int seg = a.slice / WARPS, j0 = rank * a.slice; // places of a warp; the CTA's first
+    const int i0 = warp * seg, i1 = i0 + seg;             // this warp's places, counted from the CTA's first
+    uint32_t top = 0;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
+        const int e = j0 + i - first; // (element)
+        Vec v;
+        if (e >= 0 && e + VEC <= a.V) {
+            v = *reinterpret_cast<const Vec *>(logits + e);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; k++)
+                v.v[k] = e + k >= 0 && e + k < a.V ? logits[e + k] : minus_infinity<TL>();
+        }
+        *reinterpret_cast<Vec *>(buf + i) = v;
+#pragma unroll
+        for (int k = 0; k < VEC; k++) {
+            bad |= !(to_float(v.v[k]) < INFINITY); // NaN or +infinity
+            top = max(top, Key<TL>::of(v.v[k]));
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0)
+        s.wtop[warp] = bad ? 0xffffffffu : top; // (no logit of a good row has this key)
+    __syncthreads();
+    cl.sync(); // every CTA runs: its shared memory may be written
+    if (warp == 0) {
+        const uint32_t t = __reduce_max_sync(0xffffffffu, lane < WARPS ? s.wtop[lane] : 0u);
+        if (lane < CL)
+            cl.map_shared_rank(s.top, lane)[rank] = t;
+    }
+    cl.sync();
+    for (int i = 0; i < CL; i++)
+        top = i == 0 ? s.top[0] : max(top, s.top[i]);
+    if (top == 0xffffffffu || top <= Key<TL>::NONE) {
+        if (rank == 0 && tid == 0) {
+            a.idx[row] = 0;
+            if (a.prob)
+                a.prob[row] = top == 0xffffffffu ? __int_as_float(0x7fffffff) : 0.0f;
+        }
+        return;
+    }
+
+    const float M = Key<TL>::value(top);
+    const float temp = a.temperature ? a.temperature[row] : 1.0f;
+    const bool greedy = !(temp > 0.0f);
+    Weigh weigh{0.25f * M, 0.0f, 0.0f, a.sh, s.table};
+    uint32_t low = Key<TL>::NONE + 1; // keys below weigh nothing, or do not stay
+    if (!greedy) {
+        const double c = fmin(4.0 * 1.4426950408889634 / (double)temp, 1e38);
+        weigh.c_hi = (float)c;
+        weigh.c_lo = (float)(c - (double)weigh.c_hi);
+        const double reach = (double)M - 44.5 * (double)temp; // 44.5 > 64 ln(2)
+        if (reach > -3e38)
+            low = max(low, Key<TL>::at_least(__double2float_rd(reach)));
+    }
+
+    int phase = 0, level = 0;
+    // The sum over the CTAs of a value of each, and of those before this one.
+    auto gather = [&](u64 v, u64 &before) {
+        phase ^= 1;
+        if (tid < CL)
+            cl.map_shared_rank(s.gather[phase], tid)[rank] = v;
+        cl.sync();
+        u64 all = 0;
+        before = 0;
+        for (int i = 0; i < CL; i++) {
+            if (i == rank)
+                before = all;
+            all += s.gather[phase][i];
+        }
+        return all;
+    };
+    auto block_sum = [&](u64 v) { // of the warps' sums, which stay in s.warp
+        v = warp_add(v);
+        __syncthreads();
+        if (lane == 0)
+            s.warp[warp] = v;
+        __syncthreads();
+        u64 t = 0;
+        for (int i = 0; i < WARPS; i++)
+            t += s.warp[i];
+        return t;
+    };
+
+    // What stays: keys above `cut`, and of those at it the places up to `last`.
+    uint32_t cut = low;
+    int last = INT_MAX;
+    auto stays = [&](uint32_t key, int i) { return key > cut || (key == cut && j0 + i <= last); };
+    auto each = [&](auto &&f) {
+        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
+            const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+#pragma unroll
+            for (int k = 0; k < VEC; k++)
+                f(v.v[k], i + k);
+        }
+    };
+
+    // The place of tie number m (from 1) at the key `cut`.
+    auto locate = [&](u64 m) {
+        uint32_t n = 0;
+        each([&](TL v, int) { n += Key<TL>::of(v) == cut; });
+        u64 before;
+        const u64 mine = block_sum(n);
+        gather(mine, before);
+        if (m > before && m <= before + mine) {
+            u64 rest = m - before; // among this CTA's
+            int w = 0;
+            while (rest > s.warp[w])
+                rest -= s.warp[w++];
+            if (warp == w) {
+                for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
+                    uint32_t mask = 0;
+                    if (i < i1)
+                        for (int k = 0; k < VEC; k++)
+                            mask |= (uint32_t)(Key<TL>::of(buf[i + k]) == cut) << k;
+                    const u64 upto = warp_scan((uint32_t)__popc(mask), lane);
+                    if (upto >= rest && upto - __popc(mask) < rest) {
+                        for (u64 t = rest - (upto - __popc(mask)); t > 1; t--)
+                            mask &= mask - 1;
+                        for (int c = 0; c < CL; c++)
+                            *cl.map_shared_rank(&s.tie, c) = (uint32_t)(j0 + i + __ffs(mask) - 1);
+                    }
+                    const u64 here = __shfl_sync(0xffffffffu, upto, 31);
+                    if (here >= rest)
+                        break;
+                    rest -= here;
+                }
+            }
+        }
+        cl.sync();
+        const int at = (int)s.tie;
+        return at;
+    };
+
+    // The key at which the tokens that stay, in the order of falling logits,
+    // reach a count (top-k) or a share p of their weight (top-p): `cut` and
+    // `last` move there.
+    auto search = [&](bool by_weight, u64 want, float p) {
+        uint32_t hi = top, lo = cut;
+        u64 above = 0;
+        bool first_level = true;
+        while (true) {
+            const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
+            u64 *hist = s.hist[level & 1];
+            level++;
+            for (int i = tid; i < BINS; i += THREADS)
+                hist[i] = 0;
+            __syncthreads();
+            each([&](TL v, int i) {
+                const uint32_t key = Key<TL>::of(v);
+                if (key - lo <= hi - lo && stays(key, i))
+                    atomicAdd(hist + ((hi - key) >> shift), by_weight ? weigh(to_float(v)) : (u64)1);
+            });
+            cl.sync();
+            u64 bin[BINS / THREADS], sum = 0;
+#pragma unroll
+            for (int i = 0; i < BINS / THREADS; i++) {
+                bin[i] = 0;
+                for (int c = 0; c < CL; c++)
+                    bin[i] += cl.map_shared_rank(hist, c)[tid * (BINS / THREADS) + i];
+                sum += bin[i];
+            }
+            const u64 in_warp = warp_scan(sum, lane);
+            if (lane == 31)
+                s.warp[warp] = in_warp;
+            __syncthreads();
+            u64 upto = in_warp, total = 0;
+            for (int i = 0; i < WARPS; i++) {
+                if (i < warp)
+                    upto += s.warp[i];
+                total += s.warp[i];
+            }
+            if (first_level) {
+                first_level = false;
+                if (by_weight) {
+                    const u64 w = (u64)ceil((double)p * (double)total); // the first one always stays
+                    want = p > 0.0f ? min(max(w, (u64)1), total) : (u64)1;
+                }
+                if (want > total)
+                    return; // all stay
+            }
+            u64 at = above + upto - sum;
+#pragma unroll
+            for (int i = 0; i < BINS / THREADS; i++) {
+                if (at < want && want <= at + bin[i]) {
+                    s.found[0] = tid * (BINS / THREADS) + i;
+                    s.found[1] = at;
+                    s.found[2] = bin[i];
+                }
+                at += bin[i];
+            }
+            __syncthreads();
+            const uint32_t b = (uint32_t)s.found[0];
+            above = s.found[1];
+            const u64 in_bin = s.found[2];
+            hi -= b << shift;
+            if (shift == 0) { // one key: how many of its ties stay
+                const u64 each_one = by_weight ? weigh(Key<TL>::value(hi)) : (u64)1;
+                const u64 need = (want - above + each_one - 1) / each_one;
+                if (hi != cut) // (at the same key, those that stayed so far do)
+                    last = INT_MAX;
+                cut = hi;
+                if (need * each_one < in_bin)
+                    last = locate(need);
+                return;
+            }
+            lo = max(lo, hi - min(hi, (1u << shift) - 1));
+        }
+    };
+
+    if (greedy) {
+        cut = top;
+        last = locate(1);
+    } else {
+        const int k = a.top_k ? a.top_k[row] : 0;
+        const float p = a.top_p ? a.top_p[row] : 1.0f;
+        if (k > 0 && k < a.V)
+            search(false, (u64)k, 0.0f);
+        if (p < 1.0f)
+            search(true, 0, p);
+        const float q = a.min_p ? a.min_p[row] : 0.0f;
+        if (q > 0.0f) {
+            const double least = (double)M + (double)temp * log(fmin((double)q, 1.0));
+            const uint32_t key = least > -3e38 ? min(top, Key<TL>::at_least(__double2float_ru(least))) : 0u;
+            if (key > cut)
+                cut = key, last = INT_MAX;
+        }
+    }
+
+    // The draw.
+    u64 mine = 0, before;
+    if (greedy)
+        each([&](TL v, int i) { mine += stays(Key<TL>::of(v), i); });
+    else
+        each([&](TL v, int i) {
+            if (stays(Key<TL>::of(v), i))
+                mine += weigh(to_float(v));
+        });
+    const u64 here = block_sum(mine);
+    const u64 total = gather(here, before);
+    const float u = a.u[row];
+    const double at = u > 0.0f ? floor((double)u * (double)total) : 0.0;
+    const u64 target = at >= (double)total ? total - 1 : min((u64)at, total - 1); // of the whole numbers 0 .. total - 1
+    if (target >= before && target < before + here) {
+        u64 rest = target - before;
+        int w = 0;
+        while (rest >= s.warp[w])
+            rest -= s.warp[w++];
+        if (warp == w) {
+            for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
+                u64 x[VEC], sum = 0;
+#pragma unroll
+                for (int k = 0; k < VEC; k++) {
+                    x[k] = 0;
+                    if (i < i1 && stays(Key<TL>::of(buf[i + k]), i + k))
+                        x[k] = greedy ? (u64)1 : weigh(to_float(buf[i + k]));
+                    sum += x[k];
+                }
+                const u64 upto = warp_scan(sum, lane);
+                if (rest < upto && rest >= upto - sum) {
+                    u64 r = rest - (upto - sum);
+                    int k = 0;
+                    u64 mine_k = 0;
+#pragma unroll
+                    for (int q = 0; q < VEC; q++) {
+                        if (k == q && r >= x[q]) {
+                            r -= x[q];
+                            k = q + 1;
+                        } else if (k == q) {
+                            mine_k = x[q];
+                        }
+                    }
+                    a.idx[row] = j0 + i + k - first;
+                    if (a.prob)
+                        a.prob[row] = (float)((double)mine_k / (double)total);
+                }
+                const u64 all = __shfl_sync(0xffffffffu, upto, 31);
+                if (rest < all)
+                    break;
+                rest -= all;
+            }
+        }
+    }
+}
+
+template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t stream)
+{
+    static luce_host::SmemLimit limit;
+    constexpr int VEC = 16 / sizeof(TL), UNIT = VEC * WARPS;
+    const auto kern = k_sample<TL>;
+    // as many CTAs to a row as fill the GPU twice, 2048 logits to a CTA at
+    // least, more where shared memory asks for them
+    int cl = 1;
+    auto slice_of = [&](int n) { return (int)(((a.V + VEC - 1 + n - 1) / n + UNIT - 1) / UNIT * UNIT); };
+    while (cl < CL_MAX && ((int64_t)R * cl < 2 * luce_host::sm_count() && (int64_t)a.V > 2048 * cl))
+        cl *= 2;
+    while (cl < CL_MAX && (size_t)slice_of(cl) * sizeof(TL) > 88 * 1024)
+        cl *= 2;
+    a.slice = slice_of(cl);
+    const size_t smem = (size_t)a.slice * sizeof(TL);
+    if (smem + sizeof(Shared) > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LUCE_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    luce_host::make_config(cfg, attr, dim3((unsigned)cl, (unsigned)R), dim3(THREADS), smem, stream);
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cl;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs].val.clusterDim.z = 1;
+    cfg.numAttrs++;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        limit.forget();
+        return LUCE_ERR_CUDA;
+    }
+    return LUCE_OK;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + nb && q < p + na;
+}
+
+} // namespace
+
+extern "C" luce_status luce_sample(const void *logits, luce_dtype dtype, int R, int64_t V, int64_t ld_logits, const float *u,
+                                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                                   int32_t *idx, float *prob, void *stream)
+{
+    using luce_host::aligned;
+    if (R < 0 || R > 65535 || V < 1 || V >= ((int64_t)1 << 31) || ld_logits < V || ld_logits > ((int64_t)1 << 33) ||
+        (dtype != LUCE_F32 && dtype != LUCE_BF16 && dtype != LUCE_F16))
+        return LUCE_ERR_INVALID_ARG;
+    if (V > V_MAX)
+        return LUCE_ERR_UNSUPPORTED;
+    if (R == 0)
+        return LUCE_OK;
+    const size_t es = dtype == LUCE_F32 ? 4 : 2, n = (size_t)R * 4;
+    if (!logits || !u || !idx || !aligned(logits, es) || !aligned(idx, 4) || (prob && (!aligned(prob, 4) || overlap(prob, n, idx, n))))
+        return LUCE_ERR_INVALID_ARG;
+    const size_t nl = ((size_t)(R - 1) * ld_logits + V) * es;
+    if (overlap(idx, n, logits, nl) || (prob && overlap(prob, n, logits, nl)))
+        return LUCE_ERR_INVALID_ARG;
+    const void *const rows[] = {u, temperature, top_k, top_p, min_p};
+    for (const void *p : rows)
+        if (p && (!aligned(p, 4) || overlap(p, n, idx, n) || (prob && overlap(p, n, prob, n))))
+            return LUCE_ERR_INVALID_ARG;
+    int bits = 0; // ceil(log2 V)
+    while (((int64_t)1 << bits) < V)
+        bits++;
+    SampleArgs a{logits, ld_logits, (int)V, 0, 32 - bits, u, temperature, top_k, top_p, min_p, idx, prob};
+    a.sh = std::min(a.sh, 31);
+    cudaStream_t st = luce_host::as_stream(stream);
+    return dtype == LUCE_F32 ? run_sample<float>(a, R, st)
+         : dtype == LUCE_BF16 ? run_sample<__nv_bfloat16>(a, R, st)
+                              : run_sample<__half>(a, R, st);
+}
