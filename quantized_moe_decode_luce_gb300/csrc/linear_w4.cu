@@ -5,15 +5,25 @@
 //   out[t][n] = (sum_g s[n][g] * S[t][n][g]) (* x_scale[t]) (+ bias[n]),
 //   S[t][n][g] = sum_{k in g} x[t][k] (q[n][k] - z[n][g])   (z = 8 without zero points)
 //
-// Codes are small whole numbers, exact in fp16 and bf16, so a group's sum runs
-// on the tensor cores without rounding an operand: fp16 and int8 activations
-// go in as fp16, bf16 ones as bf16, and fp32 ones as three bf16 numbers (8
-// bits of the mantissa each), three columns that are added at the end.  The
-// products are exact, their sums are fp32, and a group's scale multiplies its
-// fp32 sum.
+// Operands.  The four bits of a code at the low end of an fp16 are the
+// subnormal number q 2^-24, and one place of four bits higher 16 q 2^-24: a
+// code becomes a tensor-core operand by a mask alone.  Products are exact, the
+// factors 2^24 and 16 are put back in fp32 and in the activations, and the zero
+// point is taken off a group's sum.
+// The activations go in as fp16 too, a chunk of 128 of them (a row's packed
+// codes are kept in such chunks) brought to one size by a power of two that
+// multiplies the chunk's sums again in fp32:
+//   whole numbers   int8 codes as they are; fp32, bf16 and fp16 values, where x
+//     or out is fp32, as two columns of twelve bits each, the second 2^-12 of the
+//     first.  What they leave is at most 2^-24 of the chunk's largest value, and
+//     a group's sums (below 2^24) are exact: the tensor cores cut off what they
+//     add, which would cost several of fp32's bits otherwise.
+//   fp16 numbers    bf16 and fp16 values for 16-bit outputs, one column: exact, but
+//     for values so far below the chunk's largest that they end in fp16's
+//     subnormal steps (off by at most 2^-35 of it); the sums are good to about
+//     2^-19, against the outputs' 2^-9 and 2^-12.
 #include <algorithm>
 #include <climits>
-#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -26,11 +36,14 @@ using namespace luce;
 constexpr int CHUNK = 128;             // values of a row that its packed codes keep together
 constexpr int CHUNK_BYTES = CHUNK / 2;
 constexpr int K_MAX = 65536;
+constexpr float UNIT = 16384.0f; // sums are kept 2^-14 of their size, so that no chunk's factor leaves fp32's range
+constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u; // the codes of a word: two as they are, two sixteenfold
 
 struct W4Args {
     const void *x;
     luce_dtype x_dtype;
-    int parts; // columns of a token: three for fp32, else one
+    bool whole;  // activations as whole numbers
+    int parts;   // columns of a token
     int64_t ldx;
     const float *xs;
     const uint8_t *wq;
@@ -51,11 +64,6 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p)
     return v;
 }
 
-__device__ __forceinline__ float scale_of(uint32_t bits16, bool bf)
-{
-    return bf ? __uint_as_float(bits16 << 16) : half_bits_to_float(bits16);
-}
-
 __device__ __forceinline__ void store_as(void *out, luce_dtype t, int64_t i, float v)
 {
     if (t == LUCE_F32)
@@ -66,170 +74,140 @@ __device__ __forceinline__ void store_as(void *out, luce_dtype t, int64_t i, flo
         reinterpret_cast<__half *>(out)[i] = __float2half_rn(v);
 }
 
-// Eight codes of a word -> their differences with the zero point, four pairs
-// in the order of the values (value i of a word has its bits 4 (i / 2) + 16 (i
-// % 2) .. + 3).  A code placed under the exponent of 1024 (fp16) or 128 (bf16)
-// is 1024 + q or 128 + q; z2 holds 1024 + z or 128 + z twice.  Bits 4 to 7 of
-// an fp16 are the code times 16: one exact multiply-add undoes both.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
-    return r;
-}
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b, __half)
-{
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b, __nv_bfloat16)
-{
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t fma2_f16(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-
-// What a group's zero point contributes to the conversion of its codes.
-template <typename E> struct Zero;
-template <> struct Zero<__half> {
-    uint32_t lo, hi; // 1024 + z; -(64 + z)
-    __device__ __forceinline__ explicit Zero(uint32_t z)
-    {
-        lo = (0x6400u + z) * 0x10001u;
-        hi = (0xD400u + 16u * z) * 0x10001u; // 64 .. 79 have steps of 1/16
-    }
-};
-template <> struct Zero<__nv_bfloat16> {
-    uint32_t lo;
-    __device__ __forceinline__ explicit Zero(uint32_t z) { lo = (0x4300u + z) * 0x10001u; }
-};
-
-__device__ __forceinline__ void codes8(uint32_t w, const Zero<__half> &z, uint32_t (&h)[4])
-{
-    const uint32_t w8 = w >> 8;
-    h[0] = sub2(and_or(w, 0x000f000fu, 0x64006400u), z.lo, __half());
-    h[1] = fma2_f16(and_or(w, 0x00f000f0u, 0x64006400u), 0x2C002C00u, z.hi);
-    h[2] = sub2(and_or(w8, 0x000f000fu, 0x64006400u), z.lo, __half());
-    h[3] = fma2_f16(and_or(w8, 0x00f000f0u, 0x64006400u), 0x2C002C00u, z.hi);
-}
-__device__ __forceinline__ void codes8(uint32_t w, const Zero<__nv_bfloat16> &z, uint32_t (&h)[4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        h[i] = sub2(and_or(w >> (4 * i), 0x000f000fu, 0x43004300u), z.lo, __nv_bfloat16());
-}
-
 // ---------------------------------------------------------------------------
-// Eight consecutive activations of a token as one or three operand octets.
-__device__ __forceinline__ uint32_t pair_of(__half a, __half b)
-{
-    return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
-}
-__device__ __forceinline__ void octets(const int8_t *p, uint4 (&o)[1])
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) { // code + 128 under the exponent of 1024, less 1152: exact
-        const uint32_t u = (i < 2 ? v.x : v.y) ^ 0x80808080u;
-        h[i] = sub2(__byte_perm(u, 0x64646464u, (i & 1) ? 0x4342 : 0x4140), 0x64806480u, __half());
-    }
-    o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-}
-__device__ __forceinline__ void octets(const __half *p, uint4 (&o)[1]) { o[0] = *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void octets(const __nv_bfloat16 *p, uint4 (&o)[1]) { o[0] = *reinterpret_cast<const uint4 *>(p); }
-// An fp32 number is the sum of its top, middle and low eight mantissa bits,
-// each a bf16 number (cut off, not rounded: the first cannot overflow, and
-// the rests are exact).  NaN and infinities have no rest.
-__device__ __forceinline__ void octets(const float *p, uint4 (&o)[3])
-{
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t w[3][8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t bits = __float_as_uint(v[i]);
-        const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
-        const float r1 = finite ? __fsub_rn(v[i], __uint_as_float(bits & 0xffff0000u)) : 0.0f;
-        const uint32_t m = __float_as_uint(r1) & 0xffff0000u;
-        w[0][i] = finite || !(bits & 0x007fffffu) ? bits >> 16 : 0x7fffu;
-        w[1][i] = m >> 16;
-        w[2][i] = __float_as_uint(__fsub_rn(r1, __uint_as_float(m))) >> 16;
-    }
-#pragma unroll
-    for (int j = 0; j < 3; j++)
-        o[j] = make_uint4(w[j][0] | w[j][1] << 16, w[j][2] | w[j][3] << 16, w[j][4] | w[j][5] << 16, w[j][6] | w[j][7] << 16);
-}
-
-// Activations k .. k + 7 of token t, as operands of type E (fp16 from fp16 and
-// int8, bf16 from bf16 and fp32): one octet, or three.
-template <typename E> __device__ __forceinline__ void load_octets(const W4Args &a, int t, int k, uint4 (&o)[3])
+// Activations as operands.  Sixteen lanes take a chunk of a token, eight
+// values each.
+__device__ __forceinline__ void load8(const W4Args &a, int t, int k, float (&v)[8])
 {
     const int64_t at = t * a.ldx + k;
-    uint4 one[1];
-    if constexpr (std::is_same<E, __half>::value) {
-        if (a.x_dtype == LUCE_I8)
-            octets(reinterpret_cast<const int8_t *>(a.x) + at, one);
-        else
-            octets(reinterpret_cast<const __half *>(a.x) + at, one);
+    if (a.x_dtype == LUCE_F32) {
+        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.x) + at);
+        const float4 b = p[0], c = p[1];
+        v[0] = b.x, v[1] = b.y, v[2] = b.z, v[3] = b.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
     } else {
-        if (a.x_dtype == LUCE_F32) {
-            octets(reinterpret_cast<const float *>(a.x) + at, o);
-            return;
+        const uint4 b = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(a.x) + at);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+        if (a.x_dtype == LUCE_BF16) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                v[i] = half_bits_to_float(w[i / 2] >> (16 * (i & 1)));
         }
-        octets(reinterpret_cast<const __nv_bfloat16 *>(a.x) + at, one);
     }
-    o[0] = one[0];
+}
+
+// Activations k .. k + 7 of token t (zero unless live) -> operands of one or two
+// columns, the factors of the chunk's sums, and the sum of the group's values
+// (GPC groups to a chunk, 16 / GPC lanes each) in the units of those sums, times
+// eight.  Values 2, 3, 6 and 7 of eight meet codes that count sixteenfold.  A NaN
+// or an infinity stays one, and so do the sums of its group.
+template <int GPC>
+__device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool live, uint4 (&o)[2], float (&factor)[2], float (&sum)[2])
+{
+    if (a.x_dtype == LUCE_I8) {
+        const uint2 b = live ? *reinterpret_cast<const uint2 *>(reinterpret_cast<const int8_t *>(a.x) + t * a.ldx + k) : make_uint2(0, 0);
+        int n = __dp4a((int)b.x, 0x01010101, __dp4a((int)b.y, 0x01010101, 0));
+#pragma unroll
+        for (int d = 1; d < 16 / GPC; d *= 2)
+            n += __shfl_xor_sync(0xffffffffu, n, d);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) { // code + 128 under the exponent of 1024, less 1152: exact
+            const uint32_t u = __byte_perm((i < 2 ? b.x : b.y) ^ 0x80808080u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+            const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __half2half2(__ushort_as_half(0x6480)));
+            const __half2 s = i & 1 ? __hmul2(h, __half2half2(__ushort_as_half(0x2c00))) : h; // 2^-4
+            w[i] = *reinterpret_cast<const uint32_t *>(&s);
+        }
+        o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        factor[0] = 16777216.0f / UNIT;
+        sum[0] = (float)n * (8.0f / UNIT);
+        return;
+    }
+    float v[8] = {};
+    if (live)
+        load8(a, t, k, v);
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        most = fmaxf(most, fabsf(v[i]));
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2)
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    const uint32_t e = max(__float_as_uint(most) >> 23, 15u);                 // 2^(e - 127) <= most < 2^(e - 126)
+    const float up = __uint_as_float(((a.whole ? 264u : 268u) - e) << 23);    // to below 2^11, or 2^15
+    factor[0] = __uint_as_float((a.whole ? e : e - 4u) << 23);                // 2^24 / (up UNIT)
+    factor[1] = __uint_as_float((e - 12u) << 23);
+    uint32_t w[2][4];
+    sum[0] = sum[1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float k16 = i & 2 ? 0.0625f : 1.0f, k1 = i & 2 ? 16.0f : 1.0f;
+        const float x0 = v[i] * up, x1 = v[i + 1] * up;
+        const float p0 = a.whole ? rintf(x0) : x0, p1 = a.whole ? rintf(x1) : x1;
+        const __half2 h = __floats2half2_rn(p0 * k16, p1 * k16), r = __floats2half2_rn(rintf((x0 - p0) * 4096.0f) * k16, rintf((x1 - p1) * 4096.0f) * k16);
+        const float2 f = __half22float2(h), g = __half22float2(r);
+        w[0][i / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        w[1][i / 2] = *reinterpret_cast<const uint32_t *>(&r);
+        sum[0] = fmaf(f.x + f.y, k1, sum[0]);
+        sum[1] = fmaf(g.x + g.y, k1, sum[1]);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+        if (p < a.parts) {
+#pragma unroll
+            for (int d = 1; d < 16 / GPC; d *= 2)
+                sum[p] += __shfl_xor_sync(0xffffffffu, sum[p], d);
+            sum[p] *= factor[p] * (8.0f / 16777216.0f);
+        }
+        o[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // Few columns: a stream of the weights through mma.sync (16 rows x 16 values
 // times 16 values x 8 columns).
 //
-// What bounds it is the weights' way from HBM, and for small matrices the
-// latency of getting there.  A tile is 16 rows; the wk warps of a row group
-// split its chunks among them (every wk-th), so that a tile's rows come as one
-// run of memory, and add their sums through shared memory.  The packed order
-// lets a lane's 16 bytes of a chunk be its operands of eight MMAs: of word j
-// the values 32 j + 8 (lane % 4) .. + 7, whose activations are 16 bytes too,
-// with every group of 32 values in two MMAs.  A warp keeps U chunks' codes in
-// registers and requests a chunk of a later tile as soon as it has used one.
-// The activations stay in shared memory for all tiles of the CTA, converted
-// once, rows 64 bytes off a multiple of 128 so that reads meet no conflict.
-constexpr int S_WARPS = 8;
+// What bounds it is the weights' way from HBM, for small matrices the latency
+// of getting there, and close behind both the instructions: a chunk of 16 rows
+// takes a warp 8 MMAs, 4 reads of activations and 40 instructions for its codes.
+// So everything else is done once for a unit of U chunks: a warp keeps a unit's codes in registers, requests each chunk of its
+// next one as soon as it has used its place, and the wk warps of a row group
+// take every wk-th unit of a row and join their sums through shared memory.
+// The packed order lets a lane's 16 bytes of a chunk be its operands of eight
+// MMAs: of word j the values 32 j + 8 (lane % 4) .. + 7, whose activations are
+// 16 bytes too, with every group of 32 values in two MMAs.  The activations stay
+// in shared memory for all tiles of the CTA, rows 64 bytes off a multiple of 128
+// so that reads meet no conflict; one large CTA to an SM, as each prepares them
+// for itself.
+constexpr int S_WARPS = 24; // warps of a CTA at most
+constexpr int S_SPLIT = 8;  // warps along K at most
 constexpr int ROWS = 16;
-constexpr int U = 4;
+constexpr int PART = 20; // floats between the columns of a warp's sums: no bank is met twice
 
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half)
+__device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (first)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // GPC groups of a row in a chunk: their scales (16 bits each) and zero points
 // (8 bits each), those beyond the row's G as zero.
 template <int GPC> struct Groups {
     uint32_t s[(GPC + 1) / 2], z;
 };
 template <int GPC, bool ZEROS>
-__device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int row, int g0, bool whole)
-{
-    const uint16_t *s = reinterpret_cast<const uint16_t *>(a.ws) + (int64_t)row * a.G + g0;
-    const uint8_t *z = a.zeros + (int64_t)row * a.G + g0;
+__device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int64_t at, int g0, bool whole)
+{ // (group g0 of a row, at `at` among all rows' groups)
+    const uint16_t *s = reinterpret_cast<const uint16_t *>(a.ws) + at;
+    const uint8_t *z = a.zeros + at;
     if constexpr (GPC == 1) {
         g.s[0] = __ldg(s);
         if (ZEROS)
@@ -262,59 +240,78 @@ __device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int
     }
 }
 
-template <typename E, int NT, int GPC, bool ZEROS>
-__global__ void __launch_bounds__(S_WARPS * 32, NT <= 2 ? 2 : 1)
+// Warps of a CTA at most: those whose registers need no spilling.
+template <int NT, int GPC, bool ZEROS, int U> constexpr int S_MOST = NT == 1 && (U == 2 || (GPC == 1 && !ZEROS)) ? S_WARPS : 16;
+
+template <int NT, int GPC, bool ZEROS, int U>
+__global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
     k_linear_w4_stream(const W4Args a, int wk, int tokens, int pitch, int steps, bool whole)
 {
+    constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float4 part[2][S_WARPS][NT][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = (int)blockIdx.y * tokens, nt = min(a.T - t0, tokens), P = a.parts, cols = nt * P;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int P = a.parts, t0 = (int)blockIdx.y * tokens, nt = min(a.T - t0, tokens), cols = nt * P;
     const int chunks = (a.K + CHUNK - 1) / CHUNK, row_bytes = chunks * CHUNK_BYTES;
-    const int groups = S_WARPS / wk, kw = warp % wk, per = (chunks + wk - 1) / wk; // row groups of the CTA; chunks of a warp and tile
+    const int units = (chunks + U - 1) / U, per = (units + wk - 1) / wk; // of a row; of a warp and tile
+    const int group = warp / wk, kw = warp % wk;                         // row group of the CTA, place in it
     const int quad = lane & 3, r8 = lane >> 2;
-    const int rows_step = groups * ROWS; // rows of the CTA at a step
-    const int my_row = (warp / wk) * ROWS + r8;
+    const int rows_step = warps / wk * ROWS; // rows of the CTA at a step
+    // behind the activations: per group and column the factor and the sum of
+    // its activations; then the warps' sums, twice
+    float2 *info = reinterpret_cast<float2 *>(smem + (size_t)tokens * P * pitch);
+    float *part = reinterpret_cast<float *>(info + chunks * GPC * COLS);
 
     pdl_wait(); // (weights too may be the previous kernel's: luce_quantize_w4 writes them)
     pdl_trigger();
 
-    struct Slot {
-        uint4 w[2];
-        Groups<GPC> g[2];
-    } slot[U];
-    auto load = [&](Slot &s, int step, int j) {
-        const int c = kw + j * wk;
-        if (step < steps && c < chunks) {
+    uint4 w[U][2];
+    Groups<GPC> g[U][2];
+    // the unit to request next: its step and place among the tile's, and where
+    // this lane's codes and groups of it are in two rows (those beyond the last repeat it)
+    int ls = blockIdx.x, lj = 0, lc;
+    const uint8_t *lw[2];
+    int64_t lg[2];
+    auto aim = [&]() {
+        lc = ls < steps ? (kw + lj * wk) * U : chunks;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int row = (int)min((int64_t)step * rows_step + my_row + 8 * h, (int64_t)a.N - 1);
-                s.w[h] = ldg_stream(a.wq + (int64_t)row * row_bytes + c * CHUNK_BYTES + 16 * quad);
-                load_groups<GPC, ZEROS>(s.g[h], a, row, c * GPC, whole);
-            }
+        for (int h = 0; h < 2; h++) {
+            const int64_t row = min(ls * rows_step + group * ROWS + r8 + 8 * h, a.N - 1); // (below 2^24 + 2^12)
+            lw[h] = a.wq + row * row_bytes + lc * CHUNK_BYTES + 16 * quad;
+            lg[h] = row * a.G + lc * GPC;
         }
-    };
-    int ls = blockIdx.x, lj = 0; // the chunk to request next
-    auto request = [&](Slot &s) {
-        load(s, ls, lj);
         if (++lj == per)
             lj = 0, ls += gridDim.x;
     };
+    auto request = [&](int u) {
+        if (lc + u < chunks)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                w[u][h] = ldg_stream(lw[h] + u * CHUNK_BYTES);
+                load_groups<GPC, ZEROS>(g[u][h], a, lg[h] + u * GPC, (lc + u) * GPC, whole);
+            }
+    };
+    aim();
 #pragma unroll
     for (int u = 0; u < U; u++)
-        request(slot[u]);
+        request(u);
 
     // activations into shared memory, zero from K to the chunk's end
-    const int units = chunks * (CHUNK / 8);
-    for (int i = threadIdx.x; i < nt * units; i += S_WARPS * 32) {
-        const int t = i / units, k = (i % units) * 8;
-        uint4 o[3] = {};
-        if (k < a.K)
-            load_octets<E>(a, t0 + t, k, o);
+    const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;
+    for (int i0 = 0; i0 < nt * chunks; i0 += 2 * warps) {
+        const int i = i0 + half, t = i / chunks, c = i % chunks, k = c * CHUNK + 8 * l16;
+        const bool live = i < nt * chunks && k < a.K;
+        uint4 o[2];
+        float f[2], sum[2];
+        operands<GPC>(a, t0 + t, k, live, o, f, sum);
+        if (i < nt * chunks) {
 #pragma unroll
-        for (int p = 0; p < 3; p++)
-            if (p < P)
-                *reinterpret_cast<uint4 *>(smem + (size_t)(t * P + p) * pitch + 2 * k) = o[p];
+            for (int p = 0; p < 2; p++)
+                if (p < P) {
+                    *reinterpret_cast<uint4 *>(smem + (size_t)(t * P + p) * pitch + 2 * k) = o[p];
+                    if (l16 % (16 / GPC) == 0)
+                        info[(c * GPC + l16 / (16 / GPC)) * COLS + t * P + p] = make_float2(f[p], sum[p]);
+                }
+        }
     }
     __syncthreads();
 
@@ -322,63 +319,87 @@ __global__ void __launch_bounds__(S_WARPS * 32, NT <= 2 ? 2 : 1)
 #pragma unroll
     for (int n = 0; n < NT; n++)
         xcol[n] = smem + (size_t)min(8 * n + r8, cols - 1) * pitch + 16 * quad;
+    const float2 *const my_info = info + 2 * quad;
 
     float acc[NT][4] = {};
-    int us = blockIdx.x, uj = 0, buf = 0;
-    auto use = [&](const Slot &s) {
-        const int c = kw + uj * wk;
-        if (c >= chunks)
-            return;
-        constexpr int JG = 4 / GPC; // words of a group
+    int buf = 0;
+    for (int step = blockIdx.x; step < steps; step += gridDim.x) {
+        for (int j = 0; j < per; j++) {
+            const int c0 = (kw + j * wk) * U;
+            aim();
 #pragma unroll
-        for (int gi = 0; gi < GPC; gi++) {
-            float sum[NT][4] = {};
-            const Zero<E> z0(ZEROS ? (s.g[0].z >> (8 * gi)) & 15u : 8u), z1(ZEROS ? (s.g[1].z >> (8 * gi)) & 15u : 8u);
+            for (int u = 0; u < U; u++) {
+                if (c0 + u < chunks) {
+                    constexpr int JG = 4 / GPC; // words of a group
+                    float sc[2][GPC];
+                    if (a.ws_bf16) {
 #pragma unroll
-            for (int j = gi * JG; j < (gi + 1) * JG; j++) {
-                uint32_t h0[4], h1[4];
-                codes8(j == 0 ? s.w[0].x : j == 1 ? s.w[0].y : j == 2 ? s.w[0].z : s.w[0].w, z0, h0);
-                codes8(j == 0 ? s.w[1].x : j == 1 ? s.w[1].y : j == 2 ? s.w[1].z : s.w[1].w, z1, h1);
-                const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+                        for (int i = 0; i < 2 * GPC; i++) {
+                            const uint32_t v = g[u][i & 1].s[i >> 2];
+                            sc[i & 1][i >> 1] = __uint_as_float(i & 2 ? v & 0xffff0000u : v << 16);
+                        }
+                    } else {
 #pragma unroll
-                for (int n = 0; n < NT; n++) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(xcol[n] + c * (2 * CHUNK) + j * 64);
-                    mma(sum[n], a0, b.x, b.y, E());
-                    mma(sum[n], a1, b.z, b.w, E());
+                        for (int i = 0; i < 2 * GPC; i++)
+                            sc[i & 1][i >> 1] = half_bits_to_float(g[u][i & 1].s[i >> 2] >> (i & 2 ? 16 : 0));
+                    }
+#pragma unroll
+                    for (int gi = 0; gi < GPC; gi++) {
+                        float sum[NT][4];
+                        // (eight times the activations' sums are known: the zero point counts in eighths)
+                        const float z0 = ZEROS ? (float)((g[u][0].z >> (8 * gi)) & 15u) * -0.125f : -1.0f;
+                        const float z1 = ZEROS ? (float)((g[u][1].z >> (8 * gi)) & 15u) * -0.125f : -1.0f;
+#pragma unroll
+                        for (int q = gi * JG; q < (gi + 1) * JG; q++) {
+                            const uint32_t w0 = q == 0 ? w[u][0].x : q == 1 ? w[u][0].y : q == 2 ? w[u][0].z : w[u][0].w;
+                            const uint32_t w1 = q == 0 ? w[u][1].x : q == 1 ? w[u][1].y : q == 2 ? w[u][1].z : w[u][1].w;
+                            const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+#pragma unroll
+                            for (int n = 0; n < NT; n++) {
+                                const uint4 b = *reinterpret_cast<const uint4 *>(xcol[n] + c0 * (2 * CHUNK) + u * (2 * CHUNK) + q * 64);
+                                mma(sum[n], q == gi * JG, w0 & LO, w1 & LO, w0 & HI, w1 & HI, b.x, b.y);
+                                mma(sum[n], false, v0 & LO, v1 & LO, v0 & HI, v1 & HI, b.z, b.w);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            const float4 f = *reinterpret_cast<const float4 *>(my_info + ((c0 + u) * GPC + gi) * COLS + 8 * n);
+                            acc[n][0] = fmaf(sc[0][gi], fmaf(sum[n][0], f.x, z0 * f.y), acc[n][0]);
+                            acc[n][1] = fmaf(sc[0][gi], fmaf(sum[n][1], f.z, z0 * f.w), acc[n][1]);
+                            acc[n][2] = fmaf(sc[1][gi], fmaf(sum[n][2], f.x, z1 * f.y), acc[n][2]);
+                            acc[n][3] = fmaf(sc[1][gi], fmaf(sum[n][3], f.z, z1 * f.w), acc[n][3]);
+                        }
+                    }
                 }
-            }
-            const float s0 = scale_of((s.g[0].s[gi / 2] >> (16 * (gi & 1))) & 0xffffu, a.ws_bf16);
-            const float s1 = scale_of((s.g[1].s[gi / 2] >> (16 * (gi & 1))) & 0xffffu, a.ws_bf16);
-#pragma unroll
-            for (int n = 0; n < NT; n++) {
-                acc[n][0] = fmaf(s0, sum[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, sum[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, sum[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, sum[n][3], acc[n][3]);
+                request(u);
             }
         }
-    };
-    auto finish = [&]() { // the rows of a step: the warps' sums joined and stored
+        // the warps' sums joined and stored
+        float *const mine = part + (buf * warps + warp) * (COLS * PART);
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            part[buf][warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            float *p = mine + (8 * n + 2 * quad) * PART + r8;
+            p[0] = acc[n][0], p[PART] = acc[n][1], p[8] = acc[n][2], p[PART + 8] = acc[n][3];
             acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
         }
-        __syncthreads();
+        if (wk == 1)
+            __syncwarp();
+        else
+            named_barrier(1 + group, wk * 32);
         // (the next step writes the other half of part, and cannot come back to this one before its own barrier)
-        for (int i = threadIdx.x; i < rows_step * nt; i += S_WARPS * 32) {
-            const int t = i / rows_step, r = i % rows_step, g = r / ROWS, rr = r % ROWS;
-            const int64_t n = (int64_t)us * rows_step + r;
+        for (int i = kw * 32 + lane; i < ROWS * nt; i += wk * 32) {
+            const int t = i / ROWS, r = i % ROWS, n = step * rows_step + group * ROWS + r;
             if (n >= a.N)
                 continue;
             float v = 0.0f;
             for (int p = P - 1; p >= 0; p--) {
-                const int c = t * P + p;
+                const float *q = mine - kw * (COLS * PART) + (t * P + p) * PART + r;
                 float sum = 0.0f;
-                for (int w = 0; w < wk; w++)
-                    sum += reinterpret_cast<const float *>(&part[buf][g * wk + w][c / 8][(rr & 7) * 4 + (c % 8) / 2])[(rr >> 3) * 2 + (c & 1)];
+                for (int k = 0; k < wk; k++)
+                    sum += q[k * (COLS * PART)];
                 v += sum;
             }
+            v *= UNIT;
             if (a.xs)
                 v = __fmul_rn(v, a.xs[t0 + t]);
             if (a.bias)
@@ -386,71 +407,64 @@ __global__ void __launch_bounds__(S_WARPS * 32, NT <= 2 ? 2 : 1)
             store_as(a.out, a.out_dtype, (t0 + t) * a.ldo + n, v);
         }
         buf ^= 1;
-    };
-    while (us < steps) {
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (us < steps) {
-                use(slot[u]);
-                request(slot[u]);
-                if (++uj == per) {
-                    finish();
-                    uj = 0, us += gridDim.x;
-                }
-            }
-        }
     }
 }
 
-constexpr size_t S_SMEM = 190 * 1024; // (32 KB of `part` beside it)
+constexpr size_t S_SMEM = 225 * 1024;
 
-template <typename E, int NT, int GPC, bool ZEROS> luce_status launch_stream(const W4Args &a, int tokens, cudaStream_t stream)
+// Shared memory of the stream for a column's activations.
+int s_pitch(int K) { return (K + CHUNK - 1) / CHUNK * 2 * CHUNK + 64; }
+size_t s_smem(const W4Args &a, int cols, int gpc, int warps)
+{
+    const size_t chunks = (a.K + CHUNK - 1) / CHUNK, padded = (cols + 7) / 8 * 8;
+    return (size_t)cols * s_pitch(a.K) + chunks * gpc * padded * 8 + 2 * warps * padded * PART * 4;
+}
+
+template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4Args &a, int tokens, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
-    const auto kern = k_linear_w4_stream<E, NT, GPC, ZEROS>;
-    const int chunks = (a.K + CHUNK - 1) / CHUNK, pitch = chunks * 2 * CHUNK + 64;
+    const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U>;
+    const int chunks = (a.K + CHUNK - 1) / CHUNK;
     int wk = 1;
-    while (wk < S_WARPS && wk < chunks)
+    while (wk < S_SPLIT && wk * U < chunks)
         wk *= 2;
-    const int rows = S_WARPS / wk * ROWS, steps = (a.N + rows - 1) / rows, blocks = (a.T + tokens - 1) / tokens;
-    const size_t smem = (size_t)std::min(tokens, a.T) * a.parts * pitch;
+    // as many row groups to a CTA as SMs ask for, within its warps
+    const int tiles = (a.N + ROWS - 1) / ROWS, sms = luce_host::sm_count();
+    const int groups = std::max(1, std::min(S_MOST<NT, GPC, ZEROS, U> / wk, (tiles + sms - 1) / sms));
+    const int rows = groups * ROWS, steps = (a.N + rows - 1) / rows, blocks = (a.T + tokens - 1) / tokens;
+    const size_t smem = s_smem(a, tokens * a.parts, GPC, wk * groups);
     const bool whole = a.G % GPC == 0 && luce_host::aligned(a.ws, 2 * GPC) && (!ZEROS || luce_host::aligned(a.zeros, GPC));
-    if (smem + 8192 * NT > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
+    if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
-    const int per_sm = (int)std::max<size_t>(1, std::min<size_t>(2, 220 * 1024 / (smem + 8192 * NT + 1024)));
-    const int grid = std::min(steps, per_sm * luce_host::sm_count());
-    const luce_status st = luce_host::launch(kern, dim3((unsigned)grid, (unsigned)blocks), dim3(S_WARPS * 32), smem, stream,
-                                             a, wk, tokens, pitch, steps, whole);
+    const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms), (unsigned)blocks), dim3(wk * groups * 32), smem,
+                                             stream, a, wk, tokens, s_pitch(a.K), steps, whole);
     if (st != LUCE_OK)
         limit.forget();
     return st;
 }
 
-template <typename E, int GPC, bool ZEROS> luce_status run_w4(const W4Args &a, cudaStream_t stream)
+template <int GPC, bool ZEROS> luce_status run_w4(const W4Args &a, cudaStream_t stream)
 {
-    const int chunks = (a.K + CHUNK - 1) / CHUNK;
-    const size_t column = (size_t)chunks * 2 * CHUNK + 64;
-    const int room = (int)std::min<size_t>(32, S_SMEM / column), most = room / a.parts; // columns that fit; tokens
-    if (most < 1)
+    const size_t chunks = (a.K + CHUNK - 1) / CHUNK;
+    int cols = 16; // that fit
+    while (cols > 0 && s_smem(a, cols, GPC, cols > 8 ? 16 : S_WARPS) > S_SMEM)
+        cols--;
+    const int tokens = std::min(a.T, cols / a.parts);
+    if (tokens < 1)
         return LUCE_ERR_UNSUPPORTED;
-    const int tokens = std::min(a.T, most), nt = (tokens * a.parts + 7) / 8;
-    switch (nt) {
-    case 1:
-        return launch_stream<E, 1, GPC, ZEROS>(a, tokens, stream);
-    case 2:
-        return launch_stream<E, 2, GPC, ZEROS>(a, tokens, stream);
-    default:
-        return launch_stream<E, 4, GPC, ZEROS>(a, tokens, stream);
-    }
+    const bool few = (int64_t)a.N * chunks < (int64_t)1 << 19;
+    if (tokens * a.parts <= 8)
+        return few ? launch_stream<1, GPC, ZEROS, 2>(a, tokens, stream) : launch_stream<1, GPC, ZEROS, 4>(a, tokens, stream);
+    return few ? launch_stream<2, GPC, ZEROS, 2>(a, tokens, stream) : launch_stream<2, GPC, ZEROS, 4>(a, tokens, stream);
 }
 
-template <typename E> luce_status run_type(const W4Args &a, int group, cudaStream_t stream)
+luce_status run_groups(const W4Args &a, int group, cudaStream_t stream)
 {
     if (a.zeros)
-        return group == 32 ? run_w4<E, 4, true>(a, stream) : group == 64 ? run_w4<E, 2, true>(a, stream) : run_w4<E, 1, true>(a, stream);
-    return group == 32 ? run_w4<E, 4, false>(a, stream) : group == 64 ? run_w4<E, 2, false>(a, stream) : run_w4<E, 1, false>(a, stream);
+        return group == 32 ? run_w4<4, true>(a, stream) : group == 64 ? run_w4<2, true>(a, stream) : run_w4<1, true>(a, stream);
+    return group == 32 ? run_w4<4, false>(a, stream) : group == 64 ? run_w4<2, false>(a, stream) : run_w4<1, false>(a, stream);
 }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
@@ -488,7 +502,8 @@ extern "C" luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t
         (zeros && overlap(out, no, zeros, (size_t)N * G)) || (bias && overlap(out, no, bias, (size_t)N * 4)) ||
         (x_scale && overlap(out, no, x_scale, (size_t)T * 4)))
         return LUCE_ERR_INVALID_ARG;
-    const W4Args a{x, x_dtype, x_dtype == LUCE_F32 ? 3 : 1, ld_x, x_scale, wq, w_scale, scale_dtype == LUCE_BF16, zeros, bias, T, N, K, G, out, out_dtype, ld_out};
+    const bool whole = x_dtype == LUCE_I8 || x_dtype == LUCE_F32 || out_dtype == LUCE_F32;
+    const W4Args a{x, x_dtype, whole, whole && x_dtype != LUCE_I8 ? 2 : 1, ld_x, x_scale, wq, w_scale, scale_dtype == LUCE_BF16, zeros, bias, T, N, K, G, out, out_dtype, ld_out};
     cudaStream_t st = luce_host::as_stream(stream);
-    return x_dtype == LUCE_F32 || x_dtype == LUCE_BF16 ? run_type<__nv_bfloat16>(a, group, st) : run_type<__half>(a, group, st);
+    return run_groups(a, group, st);
 }
