@@ -25,53 +25,18 @@
 #include <algorithm>
 #include <climits>
 
-#include <cuda_bf16.h>
-
-#include "common.cuh"
+#include "w4.cuh"
 
 namespace {
 
 using namespace luce;
-
-constexpr int CHUNK = 128;             // values of a row that its packed codes keep together
-constexpr int CHUNK_BYTES = CHUNK / 2;
-constexpr int K_MAX = 65536;
-constexpr float UNIT = 16384.0f; // sums are kept 2^-14 of their size, so that no chunk's factor leaves fp32's range
-constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u; // the codes of a word: two as they are, two sixteenfold
-
-struct W4Args {
-    const void *x;
-    luce_dtype x_dtype;
-    bool whole;  // activations as whole numbers
-    int parts;   // columns of a token
-    int64_t ldx;
-    const float *xs;
-    const uint8_t *wq;
-    const void *ws;
-    bool ws_bf16;
-    const uint8_t *zeros;
-    const float *bias;
-    int T, N, K, G; // G: groups of a row
-    void *out;
-    luce_dtype out_dtype;
-    int64_t ldo;
-};
+using namespace w4;
 
 __device__ __forceinline__ uint4 ldg_stream(const void *p)
 {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
-}
-
-__device__ __forceinline__ void store_as(void *out, luce_dtype t, int64_t i, float v)
-{
-    if (t == LUCE_F32)
-        reinterpret_cast<float *>(out)[i] = v;
-    else if (t == LUCE_BF16)
-        reinterpret_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
-    else
-        reinterpret_cast<__half *>(out)[i] = __float2half_rn(v);
 }
 
 // ---------------------------------------------------------------------------
@@ -183,6 +148,7 @@ __device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool liv
 // so that reads meet no conflict; one large CTA to an SM, as each prepares them
 // for itself.
 constexpr int S_WARPS = 24; // warps of a CTA at most
+constexpr int S_COLS = 16;  // columns at most
 constexpr int S_SPLIT = 8;  // warps along K at most
 constexpr int ROWS = 16;
 constexpr int PART = 20; // floats between the columns of a warp's sums: no bank is met twice
@@ -245,12 +211,12 @@ template <int NT, int GPC, bool ZEROS, int U> constexpr int S_MOST = NT == 1 && 
 
 template <int NT, int GPC, bool ZEROS, int U>
 __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
-    k_linear_w4_stream(const W4Args a, int wk, int tokens, int pitch, int steps, bool whole)
+    k_linear_w4_stream(const W4Args a, int wk, int pitch, int steps, bool whole)
 {
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int P = a.parts, t0 = (int)blockIdx.y * tokens, nt = min(a.T - t0, tokens), cols = nt * P;
+    const int P = a.parts, nt = a.T, cols = nt * P;
     const int chunks = (a.K + CHUNK - 1) / CHUNK, row_bytes = chunks * CHUNK_BYTES;
     const int units = (chunks + U - 1) / U, per = (units + wk - 1) / wk; // of a row; of a warp and tile
     const int group = warp / wk, kw = warp % wk;                         // row group of the CTA, place in it
@@ -258,7 +224,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
     const int rows_step = warps / wk * ROWS; // rows of the CTA at a step
     // behind the activations: per group and column the factor and the sum of
     // its activations; then the warps' sums, twice
-    float2 *info = reinterpret_cast<float2 *>(smem + (size_t)tokens * P * pitch);
+    float2 *info = reinterpret_cast<float2 *>(smem + (size_t)cols * pitch);
     float *part = reinterpret_cast<float *>(info + chunks * GPC * COLS);
 
     pdl_wait(); // (weights too may be the previous kernel's: luce_quantize_w4 writes them)
@@ -302,7 +268,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
         const bool live = i < nt * chunks && k < a.K;
         uint4 o[2];
         float f[2], sum[2];
-        operands<GPC>(a, t0 + t, k, live, o, f, sum);
+        operands<GPC>(a, t, k, live, o, f, sum);
         if (i < nt * chunks) {
 #pragma unroll
             for (int p = 0; p < 2; p++)
@@ -401,10 +367,10 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
             }
             v *= UNIT;
             if (a.xs)
-                v = __fmul_rn(v, a.xs[t0 + t]);
+                v = __fmul_rn(v, a.xs[t]);
             if (a.bias)
                 v = __fadd_rn(v, a.bias[n]);
-            store_as(a.out, a.out_dtype, (t0 + t) * a.ldo + n, v);
+            store_as(a.out, a.out_dtype, t * a.ldo + n, v);
         }
         buf ^= 1;
     }
@@ -420,7 +386,7 @@ size_t s_smem(const W4Args &a, int cols, int gpc, int warps)
     return (size_t)cols * s_pitch(a.K) + chunks * gpc * padded * 8 + 2 * warps * padded * PART * 4;
 }
 
-template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4Args &a, int tokens, cudaStream_t stream)
+template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4Args &a, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
     const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U>;
@@ -431,40 +397,49 @@ template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4
     // as many row groups to a CTA as SMs ask for, within its warps
     const int tiles = (a.N + ROWS - 1) / ROWS, sms = luce_host::sm_count();
     const int groups = std::max(1, std::min(S_MOST<NT, GPC, ZEROS, U> / wk, (tiles + sms - 1) / sms));
-    const int rows = groups * ROWS, steps = (a.N + rows - 1) / rows, blocks = (a.T + tokens - 1) / tokens;
-    const size_t smem = s_smem(a, tokens * a.parts, GPC, wk * groups);
+    const int rows = groups * ROWS, steps = (a.N + rows - 1) / rows;
+    const size_t smem = s_smem(a, a.T * a.parts, GPC, wk * groups);
     const bool whole = a.G % GPC == 0 && luce_host::aligned(a.ws, 2 * GPC) && (!ZEROS || luce_host::aligned(a.zeros, GPC));
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
-    const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms), (unsigned)blocks), dim3(wk * groups * 32), smem,
-                                             stream, a, wk, tokens, s_pitch(a.K), steps, whole);
+    const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms)), dim3(wk * groups * 32), smem, stream, a, wk,
+                                             s_pitch(a.K), steps, whole);
     if (st != LUCE_OK)
         limit.forget();
     return st;
 }
 
-template <int GPC, bool ZEROS> luce_status run_w4(const W4Args &a, cudaStream_t stream)
+// Whether the stream serves a call.  Each of its CTAs prepares the activations
+// for itself, 0.022 us a column and chunk (int8 half of that); the tensor cores
+// are later to start, and read the codes of large matrices more slowly: 4.2 us
+// at 4096 x 4096, 5.3 at 4096 x 14336, 12.5 at 28672 x 4096, 28 at 129280 x 4096.
+// (Four tokens, bf16, groups of 128: 4096 x 4096 8.2 us, tensor cores 9.7;
+// 4096 x 14336 20.4 and 16.7; eight tokens: 4096 x 4096 11.0 and 9.8, 28672 x
+// 4096 20.7 and 28.5.)
+bool stream_serves(const W4Args &a, int gpc)
 {
-    const size_t chunks = (a.K + CHUNK - 1) / CHUNK;
-    int cols = 16; // that fit
-    while (cols > 0 && s_smem(a, cols, GPC, cols > 8 ? 16 : S_WARPS) > S_SMEM)
-        cols--;
-    const int tokens = std::min(a.T, cols / a.parts);
-    if (tokens < 1)
-        return LUCE_ERR_UNSUPPORTED;
-    const bool few = (int64_t)a.N * chunks < (int64_t)1 << 19;
-    if (tokens * a.parts <= 8)
-        return few ? launch_stream<1, GPC, ZEROS, 2>(a, tokens, stream) : launch_stream<1, GPC, ZEROS, 4>(a, tokens, stream);
-    return few ? launch_stream<2, GPC, ZEROS, 2>(a, tokens, stream) : launch_stream<2, GPC, ZEROS, 4>(a, tokens, stream);
+    const int64_t chunks = (a.K + CHUNK - 1) / CHUNK, cols = (int64_t)a.T * a.parts;
+    if (cols > S_COLS || s_smem(a, (int)cols, gpc, cols > 8 ? 16 : S_WARPS) > S_SMEM)
+        return false;
+    return cols * chunks / (a.x_dtype == LUCE_I8 ? 2 : 1) <= 140 + 4 * ((int64_t)a.N * chunks / (128 * 152));
+}
+
+template <int GPC, bool ZEROS> luce_status run_stream(const W4Args &a, cudaStream_t stream)
+{
+    // units of two chunks where there are not enough of four for all SMs
+    const bool few = (int64_t)a.N * ((a.K + CHUNK - 1) / CHUNK) < (int64_t)1 << 19;
+    if (a.T * a.parts <= 8)
+        return few ? launch_stream<1, GPC, ZEROS, 2>(a, stream) : launch_stream<1, GPC, ZEROS, 4>(a, stream);
+    return few ? launch_stream<2, GPC, ZEROS, 2>(a, stream) : launch_stream<2, GPC, ZEROS, 4>(a, stream);
 }
 
 luce_status run_groups(const W4Args &a, int group, cudaStream_t stream)
 {
     if (a.zeros)
-        return group == 32 ? run_w4<4, true>(a, stream) : group == 64 ? run_w4<2, true>(a, stream) : run_w4<1, true>(a, stream);
-    return group == 32 ? run_w4<4, false>(a, stream) : group == 64 ? run_w4<2, false>(a, stream) : run_w4<1, false>(a, stream);
+        return group == 32 ? run_stream<4, true>(a, stream) : group == 64 ? run_stream<2, true>(a, stream) : run_stream<1, true>(a, stream);
+    return group == 32 ? run_stream<4, false>(a, stream) : group == 64 ? run_stream<2, false>(a, stream) : run_stream<1, false>(a, stream);
 }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
@@ -505,5 +480,5 @@ extern "C" luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t
     const bool whole = x_dtype == LUCE_I8 || x_dtype == LUCE_F32 || out_dtype == LUCE_F32;
     const W4Args a{x, x_dtype, whole, whole && x_dtype != LUCE_I8 ? 2 : 1, ld_x, x_scale, wq, w_scale, scale_dtype == LUCE_BF16, zeros, bias, T, N, K, G, out, out_dtype, ld_out};
     cudaStream_t st = luce_host::as_stream(stream);
-    return run_groups(a, group, st);
+    return stream_serves(a, CHUNK / group) ? run_groups(a, group, st) : tc_product(a, group, st);
 }
