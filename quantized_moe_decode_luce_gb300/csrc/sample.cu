@@ -4,14 +4,22 @@
 //
 // A cluster of CTAs takes a row: every CTA keeps a slice of it in shared
 // memory, in the logits' own type, so the row is read from memory once and
-// everything after the first pass runs on the chip.  Both filters come down to
-// a key (a logit as a whole number of the same order) that divides those that
-// stay from the rest, and a count of ties that stay, in the order of ids.  The
-// key is found digit by digit: a histogram of the keys in question, ten bits of
-// them at a time, holds counts (top-k) or weights (top-p); the CTAs' histograms
-// are added through distributed shared memory by every CTA for itself, so a
-// level costs one cluster barrier.  The draw adds the weights that stay in the
-// order of ids: lanes, warps, CTAs.
+// everything after the first pass runs on the chip.
+//
+// Both filters come down to a few candidates, as a rule.  For top-k the warps'
+// largest lanes bound the key (a logit as a whole number of the same order) of
+// the k-th token from below: with W warps in the cluster, k tokens are at or
+// above the least of the warps' ceil(k / W)-th largest lane maxima.  For top-p
+// the pass that adds all weights also adds those at four distances from the
+// largest, and the first that reaches the share bounds the set.  Up to MOST
+// candidates go to the first CTA, in the order of ids, which sorts them by
+// logit, cuts, and draws.
+// Larger sets are cut where they are: the key that divides those that stay from
+// the rest is found digit by digit, a histogram of counts or weights over ten bits
+// of the keys in question at a time, the CTAs' histograms added through
+// distributed shared memory by every CTA for itself (one cluster barrier a
+// level); ties at that key stay in the order of ids.  The draw then adds the
+// weights that stay in the order of ids: lanes, warps, CTAs.
 //
 // Weights are whole numbers.  2^-z is looked up for the first eight bits
 // behind the binary point of z = (M - l) log2(e) / temperature and corrected by
@@ -34,7 +42,8 @@ using namespace luce;
 namespace cg = cooperative_groups;
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
-constexpr int CL_MAX = 8;                // CTAs of a cluster at most (the portable limit)
+constexpr int CL_MAX = 16, CL_PORTABLE = 8; // CTAs of a cluster at most, and without asking for more
+constexpr int MOST = 2 * THREADS;        // candidates that one CTA sorts
 constexpr int DIGIT = 10, BINS = 1 << DIGIT;
 constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
 typedef unsigned long long u64;
@@ -159,19 +168,50 @@ template <typename T> __device__ __forceinline__ T warp_scan(T v, int lane) // i
     return v;
 }
 
+constexpr int LEVELS = 4; // distances from the largest logit at which weights are added, in octaves of weight
+__device__ constexpr float OCTAVES[LEVELS] = {3.0f, 6.0f, 10.0f, 16.0f};
+
 struct Shared {
     uint2 table[256];
-    u64 hist[2][BINS];       // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
-    u64 gather[2][CL_MAX];
+    union {
+        u64 hist[2][BINS];                  // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
+        struct {
+            u64 sorted[MOST];               // key and place of candidates, largest key first
+            uint32_t key[MOST];             // candidates in the order of ids
+            int id[MOST];
+        } few;
+    };
+    u64 gather[2][CL_MAX][2 * LEVELS + 2]; // (alternating, for the same reason)
     u64 warp[WARPS];
     u64 found[4];
-    uint32_t top[CL_MAX], bad[CL_MAX];
-    uint32_t wtop[WARPS];
+    uint32_t wtop[WARPS], wbound[WARPS];
     uint32_t tie;
 };
 
+// The largest key of a warp's lanes, and their j-th largest (j from 1; 0 where j is not asked for).
+__device__ __forceinline__ uint32_t largest(uint32_t key, int j, int lane, uint32_t &jth)
+{
+    jth = 0;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    if (j == 1) {
+        jth = top;
+    } else if (j > 1) { // (warp-uniform)
+        // bitonic, falling
+#pragma unroll
+        for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+            for (int d = k / 2; d > 0; d /= 2) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, key, d);
+                const bool low = (lane & d) == 0, falling = (lane & k) == 0;
+                key = low == falling ? max(key, other) : min(key, other);
+            }
+        jth = __shfl_sync(0xffffffffu, key, j - 1);
+    }
+    return top;
+}
+
 template <typename TL>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 2)
     k_sample(const SampleArgs a)
 {
     constexpr int VEC = 16 / sizeof(TL);
@@ -186,6 +226,10 @@ __global__ void __launch_bounds__(THREADS)
         s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
     pdl_wait();
     pdl_trigger();
+    const float temp = a.temperature ? a.temperature[row] : 1.0f;
+    const int top_k = a.top_k ? a.top_k[row] : 0;
+    const float top_p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f, u = a.u[row];
+    const bool greedy = !(temp > 0.0f), by_k = !greedy && top_k > 0 && top_k < a.V, by_p = !greedy && top_p < 1.0f;
 
     // The row's slice.  Place j of the row is its element j - first, so that
     // vectors of places start 16-byte aligned; places without an element hold -infinity.
@@ -213,20 +257,46 @@ __global__ void __launch_bounds__(THREADS)
             top = max(top, Key<TL>::of(v.v[k]));
         }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
+    const int nth = by_k ? (top_k + WARPS * CL - 1) / (WARPS * CL) : 0; // lane of every warp, by size, that bounds the k-th token
+    uint32_t bound;
+    top = largest(top, nth <= 32 ? nth : 0, lane, bound);
     bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0)
+    if (lane == 0) {
         s.wtop[warp] = bad ? 0xffffffffu : top; // (no logit of a good row has this key)
+        s.wbound[warp] = bound;
+    }
     __syncthreads();
     cl.sync(); // every CTA runs: its shared memory may be written
-    if (warp == 0) {
-        const uint32_t t = __reduce_max_sync(0xffffffffu, lane < WARPS ? s.wtop[lane] : 0u);
-        if (lane < CL)
-            cl.map_shared_rank(s.top, lane)[rank] = t;
+
+    // Values of each CTA to all of them; `mine` of a thread below N is its value number.
+    int phase = 0, level = 0;
+    auto exchange = [&](int n, auto &&value) {
+        phase ^= 1;
+        if (tid < CL * n)
+            cl.map_shared_rank(&s.gather[phase][rank][0], tid / n)[tid % n] = value(tid % n);
+        cl.sync();
+    };
+    // The sum over the CTAs of value i of each, and of those before this one.
+    auto sum_of = [&](int i, u64 &before) {
+        u64 all = 0;
+        before = 0;
+        for (int c = 0; c < CL; c++) {
+            if (c == rank)
+                before = all;
+            all += s.gather[phase][c][i];
+        }
+        return all;
+    };
+    {
+        uint32_t t = __reduce_max_sync(0xffffffffu, s.wtop[lane % WARPS]), b = __reduce_min_sync(0xffffffffu, s.wbound[lane % WARPS]);
+        exchange(1, [&](int) { return (u64)t << 32 | b; });
+        t = 0, b = 0xffffffffu;
+        for (int c = 0; c < CL; c++) {
+            t = max(t, (uint32_t)(s.gather[phase][c][0] >> 32));
+            b = min(b, (uint32_t)s.gather[phase][c][0]);
+        }
+        top = t, bound = b;
     }
-    cl.sync();
-    for (int i = 0; i < CL; i++)
-        top = i == 0 ? s.top[0] : max(top, s.top[i]);
     if (top == 0xffffffffu || top <= Key<TL>::NONE) {
         if (rank == 0 && tid == 0) {
             a.idx[row] = 0;
@@ -237,10 +307,8 @@ __global__ void __launch_bounds__(THREADS)
     }
 
     const float M = Key<TL>::value(top);
-    const float temp = a.temperature ? a.temperature[row] : 1.0f;
-    const bool greedy = !(temp > 0.0f);
     Weigh weigh{0.25f * M, 0.0f, 0.0f, a.sh, s.table};
-    uint32_t low = Key<TL>::NONE + 1; // keys below weigh nothing, or do not stay
+    uint32_t low = Key<TL>::NONE + 1, least = 0; // keys below weigh nothing; those below `least` fail min-p
     if (!greedy) {
         const double c = fmin(4.0 * 1.4426950408889634 / (double)temp, 1e38);
         weigh.c_hi = (float)c;
@@ -248,24 +316,13 @@ __global__ void __launch_bounds__(THREADS)
         const double reach = (double)M - 44.5 * (double)temp; // 44.5 > 64 ln(2)
         if (reach > -3e38)
             low = max(low, Key<TL>::at_least(__double2float_rd(reach)));
+        if (min_p > 0.0f) {
+            const double l = (double)M + (double)temp * log(fmin((double)min_p, 1.0));
+            if (l > -3e38)
+                least = min(top, Key<TL>::at_least(__double2float_ru(l)));
+        }
     }
 
-    int phase = 0, level = 0;
-    // The sum over the CTAs of a value of each, and of those before this one.
-    auto gather = [&](u64 v, u64 &before) {
-        phase ^= 1;
-        if (tid < CL)
-            cl.map_shared_rank(s.gather[phase], tid)[rank] = v;
-        cl.sync();
-        u64 all = 0;
-        before = 0;
-        for (int i = 0; i < CL; i++) {
-            if (i == rank)
-                before = all;
-            all += s.gather[phase][i];
-        }
-        return all;
-    };
     auto block_sum = [&](u64 v) { // of the warps' sums, which stay in s.warp
         v = warp_add(v);
         __syncthreads();
@@ -291,13 +348,129 @@ __global__ void __launch_bounds__(THREADS)
         }
     };
 
+    // The draw from n candidates of the first CTA, in the order of ids, where the
+    // weights to reach are `want` of (0: top_p of those that top-k leaves).
+    auto draw_few = [&](int n, u64 want) {
+        int size = 64; // a power of two, candidates two to a thread
+        while (size < n)
+            size *= 2;
+        for (int i = tid; i < size; i += THREADS)
+            s.few.sorted[i] = i < n ? (u64)s.few.key[i] << 32 | (0xffffffffu - (uint32_t)i) : 0;
+        __syncthreads();
+        for (int k = 2; k <= size; k *= 2)
+            for (int d = k / 2; d > 0; d /= 2) {
+                if (tid < size / 2) {
+                    const int i = 2 * tid - (tid & (d - 1)); // (its partner is d further on)
+                    const u64 x = s.few.sorted[i], y = s.few.sorted[i + d];
+                    if ((x < y) == ((i & k) == 0)) {
+                        s.few.sorted[i] = y;
+                        s.few.sorted[i + d] = x;
+                    }
+                }
+                if (d > 32 || (d == 1 && k >= 64)) // (up to a distance of 32 a warp stays within its 64 places)
+                    __syncthreads();
+                else
+                    __syncwarp();
+            }
+        // two neighbours a thread
+        auto scan = [&](u64 x, u64 y, u64 &before) {
+            const u64 upto = warp_scan(x + y, lane);
+            __syncthreads();
+            if (lane == 31)
+                s.warp[warp] = upto;
+            __syncthreads();
+            u64 total = 0;
+            before = upto - x - y;
+            for (int i = 0; i < WARPS; i++) {
+                if (i < warp)
+                    before += s.warp[i];
+                total += s.warp[i];
+            }
+            return total;
+        };
+        const int keep = by_k ? min(top_k, n) : n, p0 = 2 * tid;
+        u64 w[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            w[i] = p0 + i < keep ? weigh(Key<TL>::value((uint32_t)(s.few.sorted[p0 + i] >> 32))) : 0;
+        u64 before;
+        const u64 all = scan(w[0], w[1], before);
+        if (by_p && want == 0)
+            want = top_p > 0.0f ? min(max((u64)ceil((double)top_p * (double)all), (u64)1), all) : (u64)1;
+        int stay = 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const bool in = p0 + i < keep && (!by_p || before + (i ? w[0] : 0) < want) &&
+                            ((uint32_t)(s.few.sorted[min(p0 + i, MOST - 1)] >> 32) >= least || p0 + i == 0);
+            stay += __syncthreads_count(in);
+        }
+        const u64 line = s.few.sorted[stay - 1]; // (the first one always stays)
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            w[i] = 0;
+            if (p0 + i < n && ((u64)s.few.key[p0 + i] << 32 | (0xffffffffu - (uint32_t)(p0 + i))) >= line)
+                w[i] = weigh(Key<TL>::value(s.few.key[p0 + i]));
+        }
+        const u64 total = scan(w[0], w[1], before);
+        const double at = u > 0.0f ? floor((double)u * (double)total) : 0.0;
+        const u64 target = at >= (double)total ? total - 1 : min((u64)at, total - 1);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (target >= before && target < before + w[i]) {
+                a.idx[row] = s.few.id[p0 + i];
+                if (a.prob)
+                    a.prob[row] = (float)((double)w[i] / (double)total);
+            }
+            before += w[i];
+        }
+    };
+    // Candidates with keys of `lo` and more to the first CTA, if they are few, and
+    // the draw there.  (Their number in this CTA is `mine`, with the warps' in s.warp.)
+    auto few = [&](uint32_t lo, u64 all, u64 before, u64 want) {
+        if (all > MOST)
+            return false;
+        int at = (int)before;
+        for (int w = 0; w < warp; w++)
+            at += (int)s.warp[w];
+        // (no histogram has been made yet where they go)
+        uint32_t *keys = cl.map_shared_rank(s.few.key, 0);
+        int *ids = cl.map_shared_rank(s.few.id, 0);
+        for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
+            uint32_t key[VEC], n = 0;
+            if (i < i1) {
+                const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+#pragma unroll
+                for (int k = 0; k < VEC; k++)
+                    n += (key[k] = Key<TL>::of(v.v[k])) >= lo;
+            }
+            const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
+            if (any) {
+                const uint32_t upto = warp_scan(n, lane);
+                int to = at + (int)(upto - n);
+                if (n > 0)
+#pragma unroll
+                    for (int k = 0; k < VEC; k++)
+                        if (key[k] >= lo) {
+                            keys[to] = key[k];
+                            ids[to++] = j0 + i + k - first;
+                        }
+                at += (int)__shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        cl.sync();
+        if (rank == 0)
+            draw_few((int)all, want);
+        return true;
+    };
+
     // The place of tie number m (from 1) at the key `cut`.
     auto locate = [&](u64 m) {
         uint32_t n = 0;
         each([&](TL v, int) { n += Key<TL>::of(v) == cut; });
         u64 before;
         const u64 mine = block_sum(n);
-        gather(mine, before);
+        exchange(1, [&](int) { return mine; });
+        sum_of(0, before);
         if (m > before && m <= before + mine) {
             u64 rest = m - before; // among this CTA's
             int w = 0;
@@ -324,12 +497,11 @@ __global__ void __launch_bounds__(THREADS)
             }
         }
         cl.sync();
-        const int at = (int)s.tie;
-        return at;
+        return (int)s.tie;
     };
 
     // The key at which the tokens that stay, in the order of falling logits,
-    // reach a count (top-k) or a share p of their weight (top-p): `cut` and
+    // reach a count (top-k) or weight (top-p; 0: a share p of theirs): `cut` and
     // `last` move there.
     auto search = [&](bool by_weight, u64 want, float p) {
         uint32_t hi = top, lo = cut;
@@ -368,10 +540,8 @@ __global__ void __launch_bounds__(THREADS)
             }
             if (first_level) {
                 first_level = false;
-                if (by_weight) {
-                    const u64 w = (u64)ceil((double)p * (double)total); // the first one always stays
-                    want = p > 0.0f ? min(max(w, (u64)1), total) : (u64)1;
-                }
+                if (want == 0) // (the first one always stays)
+                    want = p > 0.0f ? min(max((u64)ceil((double)p * (double)total), (u64)1), total) : (u64)1;
                 if (want > total)
                     return; // all stay
             }
@@ -407,21 +577,75 @@ __global__ void __launch_bounds__(THREADS)
     if (greedy) {
         cut = top;
         last = locate(1);
-    } else {
-        const int k = a.top_k ? a.top_k[row] : 0;
-        const float p = a.top_p ? a.top_p[row] : 1.0f;
-        if (k > 0 && k < a.V)
-            search(false, (u64)k, 0.0f);
-        if (p < 1.0f)
-            search(true, 0, p);
-        const float q = a.min_p ? a.min_p[row] : 0.0f;
-        if (q > 0.0f) {
-            const double least = (double)M + (double)temp * log(fmin((double)q, 1.0));
-            const uint32_t key = least > -3e38 ? min(top, Key<TL>::at_least(__double2float_ru(least))) : 0u;
-            if (key > cut)
-                cut = key, last = INT_MAX;
+    } else if (by_k) {
+        cut = max(low, bound);
+        uint32_t n = 0;
+        each([&](TL v, int) { n += Key<TL>::of(v) >= cut; });
+        const u64 mine = block_sum(n);
+        exchange(1, [&](int) { return mine; });
+        u64 before;
+        const u64 all = sum_of(0, before);
+        if (few(cut, all, before, 0))
+            return;
+        search(false, (u64)top_k, 0.0f);
+        if (by_p)
+            search(true, 0, top_p);
+    } else if (by_p) {
+        // the weights, and those within a few octaves of the largest, with their counts
+        uint32_t line[LEVELS];
+        u64 sum[LEVELS + 1] = {};
+        uint32_t n[LEVELS] = {};
+#pragma unroll
+        for (int i = 0; i < LEVELS; i++)
+            line[i] = max(low, Key<TL>::at_least(M - OCTAVES[i] * 0.69314718f * fminf(temp, 1e30f)));
+        each([&](TL v, int) {
+            const uint32_t key = Key<TL>::of(v);
+            if (key >= low) {
+                const u64 w = weigh(to_float(v));
+                sum[LEVELS] += w;
+#pragma unroll
+                for (int i = 0; i < LEVELS; i++)
+                    if (key >= line[i]) {
+                        sum[i] += w;
+                        n[i]++;
+                    }
+            }
+        });
+        u64 mine[2 * LEVELS + 1];
+#pragma unroll
+        for (int i = 0; i < LEVELS; i++)
+            mine[LEVELS + 1 + i] = block_sum(n[i]);
+#pragma unroll
+        for (int i = LEVELS; i >= 0; i--)
+            mine[i] = block_sum(sum[i]);
+        exchange(2 * LEVELS + 1, [&](int i) {
+            u64 v = 0;
+#pragma unroll
+            for (int k = 0; k < 2 * LEVELS + 1; k++)
+                v = i == k ? mine[k] : v;
+            return v;
+        });
+        u64 before;
+        const u64 all = sum_of(LEVELS, before);
+        const u64 want = top_p > 0.0f ? min(max((u64)ceil((double)top_p * (double)all), (u64)1), all) : (u64)1;
+        for (int i = 0; i < LEVELS; i++) {
+            if (sum_of(i, before) >= want) {
+                cut = line[i];
+                const u64 cands = sum_of(LEVELS + 1 + i, before);
+                uint32_t count = n[0];
+#pragma unroll
+                for (int k = 1; k < LEVELS; k++)
+                    count = i == k ? n[k] : count;
+                block_sum(count);
+                if (few(cut, cands, before, want))
+                    return;
+                break;
+            }
         }
+        search(true, want, top_p);
     }
+    if (least > cut)
+        cut = least, last = INT_MAX;
 
     // The draw.
     u64 mine = 0, before;
@@ -433,8 +657,8 @@ __global__ void __launch_bounds__(THREADS)
                 mine += weigh(to_float(v));
         });
     const u64 here = block_sum(mine);
-    const u64 total = gather(here, before);
-    const float u = a.u[row];
+    exchange(1, [&](int) { return here; });
+    const u64 total = sum_of(0, before);
     const double at = u > 0.0f ? floor((double)u * (double)total) : 0.0;
     const u64 target = at >= (double)total ? total - 1 : min((u64)at, total - 1); // of the whole numbers 0 .. total - 1
     if (target >= before && target < before + here) {
@@ -488,9 +712,9 @@ template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t 
     // least, more where shared memory asks for them
     int cl = 1;
     auto slice_of = [&](int n) { return (int)(((a.V + VEC - 1 + n - 1) / n + UNIT - 1) / UNIT * UNIT); };
-    while (cl < CL_MAX && ((int64_t)R * cl < 2 * luce_host::sm_count() && (int64_t)a.V > 2048 * cl))
+    while (cl < CL_PORTABLE && ((int64_t)R * cl < 2 * luce_host::sm_count() && (int64_t)a.V > 2048 * cl))
         cl *= 2;
-    while (cl < CL_MAX && (size_t)slice_of(cl) * sizeof(TL) > 88 * 1024)
+    while (cl < CL_PORTABLE && (size_t)slice_of(cl) * sizeof(TL) > 88 * 1024)
         cl *= 2;
     a.slice = slice_of(cl);
     const size_t smem = (size_t)a.slice * sizeof(TL);
