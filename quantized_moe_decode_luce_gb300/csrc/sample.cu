@@ -6,20 +6,20 @@
 // memory, in the logits' own type, so the row is read from memory once and
 // everything after the first pass runs on the chip.
 //
-// Both filters come down to a few candidates, as a rule.  For top-k the warps'
-// largest lanes bound the key (a logit as a whole number of the same order) of
-// the k-th token from below: with W warps in the cluster, k tokens are at or
-// above the least of the warps' ceil(k / W)-th largest lane maxima.  For top-p
-// the pass that adds all weights also adds those at four distances from the
-// largest, and the first that reaches the share bounds the set.  Up to MOST
-// candidates go to the first CTA, in the order of ids, which sorts them by
-// logit, cuts, and draws.
-// Larger sets are cut where they are: the key that divides those that stay from
-// the rest is found digit by digit, a histogram of counts or weights over ten bits
-// of the keys in question at a time, the CTAs' histograms added through
-// distributed shared memory by every CTA for itself (one cluster barrier a
-// level); ties at that key stay in the order of ids.  The draw then adds the
-// weights that stay in the order of ids: lanes, warps, CTAs.
+// Both filters look for the token at which those before it, by falling logits,
+// reach a count (top-k) or a weight (top-p).  A histogram over the logits'
+// distance from the largest finds the bin that holds it: ten bits of the
+// distance at a time, the CTAs' histograms added through distributed shared
+// memory by every CTA for itself.  Few logits enter it.  For top-k the warps'
+// largest lanes bound the k-th from below: with W warps in the cluster, k tokens
+// are at or above the least of the warps' ceil(k / W)-th largest lane maxima.
+// For top-p only those within 2^-16 of the largest weight are binned; if they do
+// not reach the share, all are.  Up to MOST tokens up to the bin's end go to the
+// first CTA, which sorts them, cuts, and draws.  More than those stay where they
+// are: the bin's own tokens go to the first CTA, which finds the last to stay,
+// and the draw adds the weights that stay in the order of ids: lanes, warps,
+// CTAs.  A bin with too many tokens is divided further; what three rounds do not
+// tell apart, by the bits of the logits, and equal ones by id.
 //
 // Weights are whole numbers.  2^-z is looked up for the first eight bits
 // behind the binary point of z = (M - l) log2(e) / temperature and corrected by
@@ -43,8 +43,10 @@ namespace cg = cooperative_groups;
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int CL_MAX = 16, CL_PORTABLE = 8; // CTAs of a cluster at most, and without asking for more
-constexpr int MOST = 2 * THREADS;        // candidates that one CTA sorts
+constexpr int MOST = 2 * THREADS;        // tokens that one CTA sorts
 constexpr int DIGIT = 10, BINS = 1 << DIGIT;
+constexpr int QBITS = 30;                // of a distance from the largest logit
+constexpr float NEAR = 16.0f;            // octaves of weight whose tokens are binned for top-p at first
 constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
 typedef unsigned long long u64;
 
@@ -168,25 +170,36 @@ template <typename T> __device__ __forceinline__ T warp_scan(T v, int lane) // i
     return v;
 }
 
-constexpr int LEVELS = 4; // distances from the largest logit at which weights are added, in octaves of weight
-__device__ constexpr float OCTAVES[LEVELS] = {3.0f, 6.0f, 10.0f, 16.0f};
-
+struct Hist {
+    uint32_t lo[BINS], hi[BINS], n[BINS]; // weights in two halves, counts
+};
 struct Shared {
     uint2 table[256];
-    union {
-        u64 hist[2][BINS];                  // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
-        struct {
-            u64 sorted[MOST];               // key and place of candidates, largest key first
-            uint32_t key[MOST];             // candidates in the order of ids
-            int id[MOST];
-        } few;
-    };
-    u64 gather[2][CL_MAX][2 * LEVELS + 2]; // (alternating, for the same reason)
-    u64 warp[WARPS];
-    u64 found[4];
+    Hist hist[2];                // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
+    u64 list[MOST], sorted[MOST]; // tokens: key, and id from the last; the first CTA's
+    u64 exchange[2][CL_MAX];     // (alternating, for the same reason)
+    u64 warp[WARPS], part[32];
+    u64 found[5];
+    u64 sum[2];                  // (alternating with the histograms)
     uint32_t wtop[WARPS], wbound[WARPS];
-    uint32_t tie;
+    uint32_t count, cut;
+    int last;
 };
+
+// f x, f in [0, 1), rounded down, or up: exact.
+__device__ __forceinline__ u64 share(float f, u64 x, bool up)
+{
+    const uint32_t b = __float_as_uint(f), e = b >> 23;
+    const u64 m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+    const int s = 150 - (int)max(e, 1u); // f = m 2^-s, s >= 24
+    const u64 hi = __umul64hi(x, m), lo = x * m;
+    u64 q = s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0;
+    if (up) { // the ceiling
+        const u64 back_lo = s < 64 ? q << s : 0, back_hi = s < 64 ? q >> (64 - s) : s < 128 ? q << (s - 64) : 0;
+        q += back_lo != lo || back_hi != hi;
+    }
+    return q;
+}
 
 // The largest key of a warp's lanes, and their j-th largest (j from 1; 0 where j is not asked for).
 __device__ __forceinline__ uint32_t largest(uint32_t key, int j, int lane, uint32_t &jth)
@@ -222,8 +235,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks(), row = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < 256; i += THREADS)
-        s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
+    cl.barrier_arrive(); // (waited for before the first write to another CTA: every CTA runs)
     pdl_wait();
     pdl_trigger();
     const float temp = a.temperature ? a.temperature[row] : 1.0f;
@@ -235,28 +247,43 @@ __global__ void __launch_bounds__(THREADS, 2)
     // vectors of places start 16-byte aligned; places without an element hold -infinity.
     const TL *logits = reinterpret_cast<const TL *>(a.logits) + (int64_t)row * a.ld;
     const int first = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(TL));
-    const int seg = a.slice / WARPS, j0 = rank * a.slice; // places of a warp; the CTA's first
-    const int i0 = warp * seg, i1 = i0 + seg;             // this warp's places, counted from the CTA's first
+    const int seg = a.slice / WARPS, id0 = rank * a.slice - first; // places of a warp; the id at the CTA's first place
+    const int i0 = warp * seg, i1 = i0 + seg;                      // this warp's places, counted from the CTA's first
     uint32_t top = 0;
     bool bad = false;
-#pragma unroll 4
-    for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
-        const int e = j0 + i - first; // (element)
-        Vec v;
-        if (e >= 0 && e + VEC <= a.V) {
-            v = *reinterpret_cast<const Vec *>(logits + e);
-        } else {
+    constexpr int BATCH = 8; // vectors requested together
+    for (int ib = i0; ib < i1; ib += BATCH * 32 * VEC) {
+        Vec v[BATCH];
 #pragma unroll
-            for (int k = 0; k < VEC; k++)
-                v.v[k] = e + k >= 0 && e + k < a.V ? logits[e + k] : minus_infinity<TL>();
+        for (int x = 0; x < BATCH; x++) {
+            const int i = ib + (x * 32 + lane) * VEC, e = id0 + i;
+            if (i < i1) {
+                if (e >= 0 && e + VEC <= a.V) {
+                    v[x] = *reinterpret_cast<const Vec *>(logits + e);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VEC; k++)
+                        v[x].v[k] = e + k >= 0 && e + k < a.V ? logits[e + k] : minus_infinity<TL>();
+                }
+            }
         }
-        *reinterpret_cast<Vec *>(buf + i) = v;
 #pragma unroll
-        for (int k = 0; k < VEC; k++) {
-            bad |= !(to_float(v.v[k]) < INFINITY); // NaN or +infinity
-            top = max(top, Key<TL>::of(v.v[k]));
+        for (int x = 0; x < BATCH; x++) {
+            const int i = ib + (x * 32 + lane) * VEC;
+            if (i < i1) {
+                *reinterpret_cast<Vec *>(buf + i) = v[x];
+#pragma unroll
+                for (int k = 0; k < VEC; k++) {
+                    bad |= !(to_float(v[x].v[k]) < INFINITY); // NaN or +infinity
+                    top = max(top, Key<TL>::of(v[x].v[k]));
+                }
+            }
         }
     }
+    for (int i = tid; i < 256; i += THREADS)
+        s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
+    if (tid == 0)
+        s.count = 0;
     const int nth = by_k ? (top_k + WARPS * CL - 1) / (WARPS * CL) : 0; // lane of every warp, by size, that bounds the k-th token
     uint32_t bound;
     top = largest(top, nth <= 32 ? nth : 0, lane, bound);
@@ -266,34 +293,34 @@ __global__ void __launch_bounds__(THREADS, 2)
         s.wbound[warp] = bound;
     }
     __syncthreads();
-    cl.sync(); // every CTA runs: its shared memory may be written
+    cl.barrier_wait();
 
-    // Values of each CTA to all of them; `mine` of a thread below N is its value number.
+    // A value of each CTA to all of them; their sum, and the sum of those before this one.
     int phase = 0, level = 0;
-    auto exchange = [&](int n, auto &&value) {
+    auto send = [&](u64 v) {
         phase ^= 1;
-        if (tid < CL * n)
-            cl.map_shared_rank(&s.gather[phase][rank][0], tid / n)[tid % n] = value(tid % n);
+        if (tid < CL)
+            cl.map_shared_rank(s.exchange[phase], tid)[rank] = v;
         cl.sync();
     };
-    // The sum over the CTAs of value i of each, and of those before this one.
-    auto sum_of = [&](int i, u64 &before) {
+    auto add_up = [&](u64 v, u64 &before) {
+        send(v);
         u64 all = 0;
         before = 0;
         for (int c = 0; c < CL; c++) {
             if (c == rank)
                 before = all;
-            all += s.gather[phase][c][i];
+            all += s.exchange[phase][c];
         }
         return all;
     };
     {
         uint32_t t = __reduce_max_sync(0xffffffffu, s.wtop[lane % WARPS]), b = __reduce_min_sync(0xffffffffu, s.wbound[lane % WARPS]);
-        exchange(1, [&](int) { return (u64)t << 32 | b; });
+        send((u64)t << 32 | b);
         t = 0, b = 0xffffffffu;
         for (int c = 0; c < CL; c++) {
-            t = max(t, (uint32_t)(s.gather[phase][c][0] >> 32));
-            b = min(b, (uint32_t)s.gather[phase][c][0]);
+            t = max(t, (uint32_t)(s.exchange[phase][c] >> 32));
+            b = min(b, (uint32_t)s.exchange[phase][c]);
         }
         top = t, bound = b;
     }
@@ -306,22 +333,43 @@ __global__ void __launch_bounds__(THREADS, 2)
         return;
     }
 
-    const float M = Key<TL>::value(top);
-    Weigh weigh{0.25f * M, 0.0f, 0.0f, a.sh, s.table};
-    uint32_t low = Key<TL>::NONE + 1, least = 0; // keys below weigh nothing; those below `least` fail min-p
-    if (!greedy) {
-        const double c = fmin(4.0 * 1.4426950408889634 / (double)temp, 1e38);
-        weigh.c_hi = (float)c;
-        weigh.c_lo = (float)(c - (double)weigh.c_hi);
-        const double reach = (double)M - 44.5 * (double)temp; // 44.5 > 64 ln(2)
-        if (reach > -3e38)
-            low = max(low, Key<TL>::at_least(__double2float_rd(reach)));
-        if (min_p > 0.0f) {
-            const double l = (double)M + (double)temp * log(fmin((double)min_p, 1.0));
-            if (l > -3e38)
-                least = min(top, Key<TL>::at_least(__double2float_ru(l)));
+    auto each = [&](auto &&f) {
+        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
+            const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+#pragma unroll
+            for (int k = 0; k < VEC; k++)
+                f(v.v[k], id0 + i + k);
         }
+    };
+    if (greedy) {
+        uint32_t id = 0xffffffffu;
+        each([&](TL v, int i) { id = Key<TL>::of(v) == top ? min(id, (uint32_t)i) : id; });
+        id = __reduce_min_sync(0xffffffffu, id);
+        if (lane == 0)
+            s.wtop[warp] = id;
+        __syncthreads();
+        id = __reduce_min_sync(0xffffffffu, s.wtop[lane % WARPS]);
+        send(id);
+        if (rank == 0 && tid == 0) {
+            for (int c = 0; c < CL; c++)
+                id = min(id, (uint32_t)s.exchange[phase][c]);
+            a.idx[row] = (int)id;
+            if (a.prob)
+                a.prob[row] = 1.0f;
+        }
+        return;
     }
+
+    const float M = Key<TL>::value(top);
+    // 4 log2(e) / temperature in two floats (temperatures below 1e-37 count as that)
+    const float t = fmaxf(temp, 1e-37f), c_hi = __fdiv_rn(5.77078009f, t);
+    const float c_lo = t < INFINITY ? __fdiv_rn(fmaf(-c_hi, t, 5.77078009f) + 7.703852e-08f, t) : 0.0f;
+    const Weigh weigh{0.25f * M, c_hi, c_lo, a.sh, s.table};
+    // keys below `low` weigh nothing (46 > 64 ln(2), by more than the roundings); weights below `least` fail min-p
+    const float reach = M - 46.0f * t;
+    const uint32_t low = reach > -3e38f ? max(Key<TL>::NONE + 1, Key<TL>::at_least(reach)) : Key<TL>::NONE + 1;
+    const u64 most = (u64)1 << (31 + a.sh);
+    const u64 least = min_p > 0.0f ? (min_p < 1.0f ? share(min_p, most, true) : most) : 0;
 
     auto block_sum = [&](u64 v) { // of the warps' sums, which stay in s.warp
         v = warp_add(v);
@@ -335,36 +383,45 @@ __global__ void __launch_bounds__(THREADS, 2)
         return t;
     };
 
-    // What stays: keys above `cut`, and of those at it the places up to `last`.
+    // What stays: keys above `cut`, and of those at it the ids up to `last`.
     uint32_t cut = low;
     int last = INT_MAX;
-    auto stays = [&](uint32_t key, int i) { return key > cut || (key == cut && j0 + i <= last); };
-    auto each = [&](auto &&f) {
-        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
-            const Vec v = *reinterpret_cast<const Vec *>(buf + i);
-#pragma unroll
-            for (int k = 0; k < VEC; k++)
-                f(v.v[k], i + k);
-        }
-    };
+    auto stays = [&](uint32_t key, int id) { return key > cut || (key == cut && id <= last); };
 
-    // The draw from n candidates of the first CTA, in the order of ids, where the
-    // weights to reach are `want` of (0: top_p of those that top-k leaves).
-    auto draw_few = [&](int n, u64 want) {
-        int size = 64; // a power of two, candidates two to a thread
+    // -------------------------------------------------------------- the first CTA's part
+    // s.list, n entries, by size into s.sorted, the largest first (no two are equal).
+    auto sort = [&](int n) {
+        __syncthreads();
+        if (n <= THREADS / 2) { // the place of each is the number of larger ones
+            int parts = 1;      // threads to an entry
+            while (2 * parts * n <= THREADS && parts < 32)
+                parts *= 2;
+            const int e = tid / parts;
+            const u64 mine = e < n ? s.list[e] : 0;
+            int larger = 0;
+            for (int j = tid % parts; j < n; j += parts)
+                larger += s.list[j] > mine;
+            for (int d = 1; d < parts; d *= 2)
+                larger += __shfl_xor_sync(0xffffffffu, larger, d);
+            if (e < n && tid % parts == 0)
+                s.sorted[larger] = mine;
+            __syncthreads();
+            return;
+        }
+        int size = THREADS;
         while (size < n)
             size *= 2;
         for (int i = tid; i < size; i += THREADS)
-            s.few.sorted[i] = i < n ? (u64)s.few.key[i] << 32 | (0xffffffffu - (uint32_t)i) : 0;
+            s.sorted[i] = i < n ? s.list[i] : 0;
         __syncthreads();
         for (int k = 2; k <= size; k *= 2)
             for (int d = k / 2; d > 0; d /= 2) {
                 if (tid < size / 2) {
                     const int i = 2 * tid - (tid & (d - 1)); // (its partner is d further on)
-                    const u64 x = s.few.sorted[i], y = s.few.sorted[i + d];
+                    const u64 x = s.sorted[i], y = s.sorted[i + d];
                     if ((x < y) == ((i & k) == 0)) {
-                        s.few.sorted[i] = y;
-                        s.few.sorted[i + d] = x;
+                        s.sorted[i] = y;
+                        s.sorted[i + d] = x;
                     }
                 }
                 if (d > 32 || (d == 1 && k >= 64)) // (up to a distance of 32 a warp stays within its 64 places)
@@ -372,105 +429,143 @@ __global__ void __launch_bounds__(THREADS, 2)
                 else
                     __syncwarp();
             }
-        // two neighbours a thread
-        auto scan = [&](u64 x, u64 y, u64 &before) {
-            const u64 upto = warp_scan(x + y, lane);
-            __syncthreads();
-            if (lane == 31)
-                s.warp[warp] = upto;
-            __syncthreads();
-            u64 total = 0;
-            before = upto - x - y;
-            for (int i = 0; i < WARPS; i++) {
-                if (i < warp)
-                    before += s.warp[i];
-                total += s.warp[i];
-            }
-            return total;
-        };
-        const int keep = by_k ? min(top_k, n) : n, p0 = 2 * tid;
-        u64 w[2];
+    };
+    auto key_of = [&](u64 entry) { return (uint32_t)(entry >> 32); };
+    auto id_of = [&](u64 entry) { return (int)(0xffffffffu - (uint32_t)entry); };
+    // Values of two neighbours a thread: what stands before the first, and the total.
+    auto scan = [&](u64 x, u64 y, u64 &before) {
+        const u64 upto = warp_scan(x + y, lane);
+        __syncthreads();
+        if (lane == 31)
+            s.warp[warp] = upto;
+        __syncthreads();
+        u64 total = 0;
+        before = upto - x - y;
+        for (int i = 0; i < WARPS; i++) {
+            if (i < warp)
+                before += s.warp[i];
+            total += s.warp[i];
+        }
+        return total;
+    };
+    // The draw from the n tokens of the list, of which the first `keep` and those that
+    // reach a weight of `want` stay (0: top_p of theirs).
+    auto draw_few = [&](int n, int keep, u64 want) {
+        sort(n);
+        const int p0 = 2 * tid;
+        u64 w[2], before;
+        uint32_t key[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 2; i++)
-            w[i] = p0 + i < keep ? weigh(Key<TL>::value((uint32_t)(s.few.sorted[p0 + i] >> 32))) : 0;
-        u64 before;
+        for (int i = 0; i < 2; i++) {
+            if (p0 + i < keep)
+                key[i] = key_of(s.sorted[p0 + i]);
+            w[i] = p0 + i < keep ? weigh(Key<TL>::value(key[i])) : 0;
+        }
         const u64 all = scan(w[0], w[1], before);
         if (by_p && want == 0)
-            want = top_p > 0.0f ? min(max((u64)ceil((double)top_p * (double)all), (u64)1), all) : (u64)1;
+            want = top_p > 0.0f ? max(share(top_p, all, true), (u64)1) : (u64)1;
         int stay = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const bool in = p0 + i < keep && (!by_p || before + (i ? w[0] : 0) < want) &&
-                            ((uint32_t)(s.few.sorted[min(p0 + i, MOST - 1)] >> 32) >= least || p0 + i == 0);
-            stay += __syncthreads_count(in);
+            const bool in = p0 + i < keep && (!by_p || before + (i ? w[0] : 0) < want) && w[i] >= least;
+            stay += __syncthreads_count(in); // (the first one always stays)
         }
-        const u64 line = s.few.sorted[stay - 1]; // (the first one always stays)
+        // those that stay, in the order of ids: the id, and the weight's place
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (p0 + i < stay)
+                s.list[p0 + i] = (u64)(uint32_t)s.sorted[p0 + i] << 32 | (uint32_t)(p0 + i);
+        sort(stay);
+        int at[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 2; i++) {
+            at[i] = p0 + i < stay ? (int)(uint32_t)s.sorted[p0 + i] : -1;
             w[i] = 0;
-            if (p0 + i < n && ((u64)s.few.key[p0 + i] << 32 | (0xffffffffu - (uint32_t)(p0 + i))) >= line)
-                w[i] = weigh(Key<TL>::value(s.few.key[p0 + i]));
         }
+        // (the sort has taken the places of the tokens: their keys come back from the threads that hold them)
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (p0 + i < stay)
+                s.list[p0 + i] = key[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (at[i] >= 0)
+                w[i] = weigh(Key<TL>::value((uint32_t)s.list[at[i]]));
         const u64 total = scan(w[0], w[1], before);
-        const double at = u > 0.0f ? floor((double)u * (double)total) : 0.0;
-        const u64 target = at >= (double)total ? total - 1 : min((u64)at, total - 1);
+        const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             if (target >= before && target < before + w[i]) {
-                a.idx[row] = s.few.id[p0 + i];
+                a.idx[row] = (int)(0xffffffffu - (uint32_t)(s.sorted[p0 + i] >> 32));
                 if (a.prob)
-                    a.prob[row] = (float)((double)w[i] / (double)total);
+                    a.prob[row] = __fdiv_rn(__ull2float_rn(w[i]), __ull2float_rn(total));
             }
             before += w[i];
         }
     };
-    // Candidates with keys of `lo` and more to the first CTA, if they are few, and
-    // the draw there.  (Their number in this CTA is `mine`, with the warps' in s.warp.)
-    auto few = [&](uint32_t lo, u64 all, u64 before, u64 want) {
-        if (all > MOST)
-            return false;
-        int at = (int)before;
-        for (int w = 0; w < warp; w++)
-            at += (int)s.warp[w];
-        // (no histogram has been made yet where they go)
-        uint32_t *keys = cl.map_shared_rank(s.few.key, 0);
-        int *ids = cl.map_shared_rank(s.few.id, 0);
+
+    // -------------------------------------------------------------- sets of tokens
+    // Tokens that `in` says yes to, into the first CTA's list (at most MOST).
+    auto collect = [&](auto &&in) {
+        u64 *list = cl.map_shared_rank(s.list, 0);
+        uint32_t *count = cl.map_shared_rank(&s.count, 0);
         for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
-            uint32_t key[VEC], n = 0;
+            uint32_t mask = 0;
+            Vec v;
             if (i < i1) {
-                const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+                v = *reinterpret_cast<const Vec *>(buf + i);
 #pragma unroll
                 for (int k = 0; k < VEC; k++)
-                    n += (key[k] = Key<TL>::of(v.v[k])) >= lo;
+                    mask |= (uint32_t)in(v.v[k], id0 + i + k) << k;
             }
-            const uint32_t any = __ballot_sync(0xffffffffu, n > 0);
-            if (any) {
-                const uint32_t upto = warp_scan(n, lane);
-                int to = at + (int)(upto - n);
-                if (n > 0)
+            if (mask) {
+                uint32_t at = atomicAdd(count, (uint32_t)__popc(mask));
 #pragma unroll
-                    for (int k = 0; k < VEC; k++)
-                        if (key[k] >= lo) {
-                            keys[to] = key[k];
-                            ids[to++] = j0 + i + k - first;
-                        }
-                at += (int)__shfl_sync(0xffffffffu, upto, 31);
+                for (int k = 0; k < VEC; k++)
+                    if (mask >> k & 1)
+                        list[min(at++, (uint32_t)MOST - 1)] = (u64)Key<TL>::of(v.v[k]) << 32 | (0xffffffffu - (uint32_t)(id0 + i + k));
             }
         }
         cl.sync();
-        if (rank == 0)
-            draw_few((int)all, want);
-        return true;
     };
-
-    // The place of tie number m (from 1) at the key `cut`.
+    // Of the tokens in the first CTA's list, the last to stay where `above` stands
+    // before them and `want` is to be reached: `cut` and `last`, in every CTA.
+    auto cut_list = [&](bool by_weight, u64 above, u64 want) {
+        if (rank == 0) {
+            const int n = (int)s.count;
+            sort(n);
+            const int p0 = 2 * tid;
+            u64 w[2], before;
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+                w[i] = p0 + i >= n ? 0 : by_weight ? weigh(Key<TL>::value(key_of(s.sorted[p0 + i]))) : (u64)1;
+            scan(w[0], w[1], before);
+            before += above;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                if (before < want && want <= before + w[i])
+                    for (int c = 0; c < CL; c++) {
+                        *cl.map_shared_rank(&s.cut, c) = key_of(s.sorted[p0 + i]);
+                        *cl.map_shared_rank(&s.last, c) = id_of(s.sorted[p0 + i]);
+                    }
+                before += w[i];
+            }
+            if (tid == 0)
+                s.count = 0;
+        }
+        cl.sync();
+        cut = s.cut;
+        last = s.last;
+    };
+    // The id of tie number m (from 1) at the key `cut`, in the order of ids.
     auto locate = [&](u64 m) {
         uint32_t n = 0;
         each([&](TL v, int) { n += Key<TL>::of(v) == cut; });
         u64 before;
         const u64 mine = block_sum(n);
-        exchange(1, [&](int) { return mine; });
-        sum_of(0, before);
+        add_up(mine, before);
         if (m > before && m <= before + mine) {
             u64 rest = m - before; // among this CTA's
             int w = 0;
@@ -487,7 +582,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                         for (u64 t = rest - (upto - __popc(mask)); t > 1; t--)
                             mask &= mask - 1;
                         for (int c = 0; c < CL; c++)
-                            *cl.map_shared_rank(&s.tie, c) = (uint32_t)(j0 + i + __ffs(mask) - 1);
+                            *cl.map_shared_rank(&s.last, c) = id0 + i + __ffs(mask) - 1;
                     }
                     const u64 here = __shfl_sync(0xffffffffu, upto, 31);
                     if (here >= rest)
@@ -497,207 +592,250 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
         }
         cl.sync();
-        return (int)s.tie;
+        return s.last;
     };
 
-    // The key at which the tokens that stay, in the order of falling logits,
-    // reach a count (top-k) or weight (top-p; 0: a share p of theirs): `cut` and
-    // `last` move there.
-    auto search = [&](bool by_weight, u64 want, float p) {
-        uint32_t hi = top, lo = cut;
-        u64 above = 0;
-        bool first_level = true;
-        while (true) {
-            const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
-            u64 *hist = s.hist[level & 1];
-            level++;
-            for (int i = tid; i < BINS; i += THREADS)
-                hist[i] = 0;
-            __syncthreads();
-            each([&](TL v, int i) {
-                const uint32_t key = Key<TL>::of(v);
-                if (key - lo <= hi - lo && stays(key, i))
-                    atomicAdd(hist + ((hi - key) >> shift), by_weight ? weigh(to_float(v)) : (u64)1);
-            });
-            cl.sync();
-            u64 bin[BINS / THREADS], sum = 0;
-#pragma unroll
-            for (int i = 0; i < BINS / THREADS; i++) {
-                bin[i] = 0;
-                for (int c = 0; c < CL; c++)
-                    bin[i] += cl.map_shared_rank(hist, c)[tid * (BINS / THREADS) + i];
-                sum += bin[i];
-            }
-            const u64 in_warp = warp_scan(sum, lane);
-            if (lane == 31)
-                s.warp[warp] = in_warp;
-            __syncthreads();
-            u64 upto = in_warp, total = 0;
-            for (int i = 0; i < WARPS; i++) {
-                if (i < warp)
-                    upto += s.warp[i];
-                total += s.warp[i];
-            }
-            if (first_level) {
-                first_level = false;
-                if (want == 0) // (the first one always stays)
-                    want = p > 0.0f ? min(max((u64)ceil((double)p * (double)total), (u64)1), total) : (u64)1;
-                if (want > total)
-                    return; // all stay
-            }
-            u64 at = above + upto - sum;
-#pragma unroll
-            for (int i = 0; i < BINS / THREADS; i++) {
-                if (at < want && want <= at + bin[i]) {
-                    s.found[0] = tid * (BINS / THREADS) + i;
-                    s.found[1] = at;
-                    s.found[2] = bin[i];
-                }
-                at += bin[i];
-            }
-            __syncthreads();
-            const uint32_t b = (uint32_t)s.found[0];
-            above = s.found[1];
-            const u64 in_bin = s.found[2];
-            hi -= b << shift;
-            if (shift == 0) { // one key: how many of its ties stay
-                const u64 each_one = by_weight ? weigh(Key<TL>::value(hi)) : (u64)1;
-                const u64 need = (want - above + each_one - 1) / each_one;
-                if (hi != cut) // (at the same key, those that stayed so far do)
-                    last = INT_MAX;
-                cut = hi;
-                if (need * each_one < in_bin)
-                    last = locate(need);
-                return;
-            }
-            lo = max(lo, hi - min(hi, (1u << shift) - 1));
-        }
+    // A histogram over the tokens that stay (bin: a bin, or none below zero), and in
+    // it the bin at which what stands before it reaches `want`.
+    struct Found {
+        uint32_t bin;
+        u64 above, in; // before the bin, in it
+        uint32_t n_above, n_in;
+        u64 total;     // in all bins
     };
-
-    if (greedy) {
-        cut = top;
-        last = locate(1);
-    } else if (by_k) {
-        cut = max(low, bound);
-        uint32_t n = 0;
-        each([&](TL v, int) { n += Key<TL>::of(v) >= cut; });
-        const u64 mine = block_sum(n);
-        exchange(1, [&](int) { return mine; });
-        u64 before;
-        const u64 all = sum_of(0, before);
-        if (few(cut, all, before, 0))
-            return;
-        search(false, (u64)top_k, 0.0f);
-        if (by_p)
-            search(true, 0, top_p);
-    } else if (by_p) {
-        // the weights, and those within a few octaves of the largest, with their counts
-        uint32_t line[LEVELS];
-        u64 sum[LEVELS + 1] = {};
-        uint32_t n[LEVELS] = {};
-#pragma unroll
-        for (int i = 0; i < LEVELS; i++)
-            line[i] = max(low, Key<TL>::at_least(M - OCTAVES[i] * 0.69314718f * fminf(temp, 1e30f)));
-        each([&](TL v, int) {
+    auto find = [&](bool by_weight, u64 above, auto &&want_of, auto &&bin) {
+        level ^= 1;
+        Hist &h = s.hist[level];
+        for (int i = tid; i < BINS; i += THREADS)
+            h.lo[i] = h.hi[i] = h.n[i] = 0;
+        __syncthreads();
+        u64 sum = 0;
+        each([&](TL v, int id) {
             const uint32_t key = Key<TL>::of(v);
-            if (key >= low) {
-                const u64 w = weigh(to_float(v));
-                sum[LEVELS] += w;
-#pragma unroll
-                for (int i = 0; i < LEVELS; i++)
-                    if (key >= line[i]) {
-                        sum[i] += w;
-                        n[i]++;
+            if (stays(key, id)) {
+                const float l = to_float(v);
+                u64 w = 1;
+                if (by_weight) {
+                    w = weigh(l);
+                    sum += w;
+                }
+                const int b = bin(key, l);
+                if (b >= 0) {
+                    atomicAdd(&h.n[b], 1u);
+                    if (by_weight) {
+                        const uint32_t wl = (uint32_t)w, old = atomicAdd(&h.lo[b], wl);
+                        const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
+                        if (wh)
+                            atomicAdd(&h.hi[b], wh);
                     }
+                }
             }
         });
-        u64 mine[2 * LEVELS + 1];
+        if (by_weight) {
+            sum = block_sum(sum);
+            if (tid == 0)
+                s.sum[level] = sum;
+        }
+        cl.sync();
+        u64 w[BINS / THREADS], all = 0;
+        uint32_t n[BINS / THREADS] = {}, count = 0;
+        sum = 0;
 #pragma unroll
-        for (int i = 0; i < LEVELS; i++)
-            mine[LEVELS + 1 + i] = block_sum(n[i]);
+        for (int i = 0; i < BINS / THREADS; i++)
+            w[i] = 0;
+        for (int c = 0; c < CL; c++) {
+            const Hist *r = cl.map_shared_rank(&h, c);
 #pragma unroll
-        for (int i = LEVELS; i >= 0; i--)
-            mine[i] = block_sum(sum[i]);
-        exchange(2 * LEVELS + 1, [&](int i) {
-            u64 v = 0;
+            for (int i = 0; i < BINS / THREADS; i++) {
+                const int b = tid * (BINS / THREADS) + i;
+                n[i] += r->n[b];
+                if (by_weight)
+                    w[i] += (u64)r->hi[b] << 32 | r->lo[b];
+            }
+            if (by_weight)
+                sum += *cl.map_shared_rank(&s.sum[level], c);
+        }
 #pragma unroll
-            for (int k = 0; k < 2 * LEVELS + 1; k++)
-                v = i == k ? mine[k] : v;
-            return v;
-        });
-        u64 before;
-        const u64 all = sum_of(LEVELS, before);
-        const u64 want = top_p > 0.0f ? min(max((u64)ceil((double)top_p * (double)all), (u64)1), all) : (u64)1;
-        for (int i = 0; i < LEVELS; i++) {
-            if (sum_of(i, before) >= want) {
-                cut = line[i];
-                const u64 cands = sum_of(LEVELS + 1 + i, before);
-                uint32_t count = n[0];
+        for (int i = 0; i < BINS / THREADS; i++) {
+            if (!by_weight)
+                w[i] = n[i];
+            all += w[i];
+            count += n[i];
+        }
+        const u64 in_warp = warp_scan(all, lane);
+        const uint32_t n_warp = warp_scan(count, lane);
+        if (lane == 31) {
+            s.warp[warp] = in_warp;
+            s.part[warp] = n_warp;
+        }
+        __syncthreads();
+        u64 at = in_warp - all, total = 0;
+        uint32_t n_at = n_warp - count;
+        for (int i = 0; i < WARPS; i++) {
+            if (i < warp) {
+                at += s.warp[i];
+                n_at += (uint32_t)s.part[i];
+            }
+            total += s.warp[i];
+        }
+        const u64 want = want_of(sum);
+        at += above;
 #pragma unroll
-                for (int k = 1; k < LEVELS; k++)
-                    count = i == k ? n[k] : count;
-                block_sum(count);
-                if (few(cut, cands, before, want))
-                    return;
-                break;
+        for (int i = 0; i < BINS / THREADS; i++) {
+            if (at < want && want <= at + w[i]) {
+                s.found[0] = tid * (BINS / THREADS) + i;
+                s.found[1] = at;
+                s.found[2] = w[i];
+                s.found[3] = n_at;
+                s.found[4] = n[i];
+            }
+            at += w[i];
+            n_at += n[i];
+        }
+        __syncthreads();
+        return Found{(uint32_t)s.found[0], s.found[1], s.found[2], (uint32_t)s.found[3], (uint32_t)s.found[4], total};
+    };
+    // The cut at which the tokens that stay reach `want` (a weight of 0: a share top_p of
+    // theirs).  True: they were few, and the first CTA has drawn from them.
+    auto search = [&](bool by_weight, u64 want) {
+        bool all_in = !by_weight; // whether every token that stays is binned
+        while (true) {
+            // distances as whole numbers of QBITS bits, the same order as the keys' (equal for logits that are near)
+            const float range = all_in ? weigh.M4 - 0.25f * Key<TL>::value(cut) : NEAR * 0.69314718f * 0.25f * fminf(temp, 1e30f);
+            const float scale = range > 0.0f ? fminf(1073741824.0f / range, 1e38f) : 0.0f;
+            auto place = [&](float l) {
+                const float x = (weigh.M4 - 0.25f * l) * scale;
+                return x < 1073741824.0f ? (int)x : all_in ? (1 << QBITS) - 1 : -1;
+            };
+            uint32_t prefix = 0;
+            u64 above = 0;
+            bool again = false;
+            for (int bits = QBITS - DIGIT; bits >= 0; bits -= DIGIT) {
+                const bool fresh = bits == QBITS - DIGIT;
+                const Found f = find(by_weight, above,
+                                     [&](u64 sum) {
+                                         if (by_weight && want == 0)
+                                             want = top_p > 0.0f ? max(share(top_p, sum, true), (u64)1) : (u64)1;
+                                         return want;
+                                     },
+                                     [&](uint32_t, float l) {
+                                         const int q = place(l);
+                                         return q < 0 || (!fresh && (uint32_t)q >> (bits + DIGIT) != prefix) ? -1 : q >> bits & (BINS - 1);
+                                     });
+                if (fresh && want > f.total) {
+                    if (all_in)
+                        return false; // all stay
+                    again = all_in = true;
+                    break;
+                }
+                if (fresh && f.n_above + f.n_in <= MOST) {
+                    collect([&](TL v, int id) {
+                        const uint32_t key = Key<TL>::of(v);
+                        const int q = place(to_float(v));
+                        return stays(key, id) && q >= 0 && (uint32_t)q >> bits <= f.bin;
+                    });
+                    if (rank == 0) {
+                        const int n = (int)(f.n_above + f.n_in);
+                        draw_few(n, by_weight ? n : min(top_k, n), by_weight ? want : 0);
+                    }
+                    return true;
+                }
+                prefix = prefix << DIGIT | f.bin;
+                above = f.above;
+                if (f.n_in <= MOST) {
+                    collect([&](TL v, int id) {
+                        const uint32_t key = Key<TL>::of(v);
+                        const int q = place(to_float(v));
+                        return stays(key, id) && q >= 0 && (uint32_t)q >> bits == prefix;
+                    });
+                    cut_list(by_weight, above, want);
+                    return false;
+                }
+            }
+            if (again)
+                continue;
+            // many logits of one distance: by their bits, then by id
+            uint32_t hi = top, lo = cut;
+            while (true) {
+                const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
+                const Found f = find(by_weight, above, [&](u64) { return want; },
+                                     [&](uint32_t key, float l) {
+                                         return key - lo <= hi - lo && (uint32_t)place(l) == prefix ? (int)((hi - key) >> shift) : -1;
+                                     });
+                above = f.above;
+                hi -= f.bin << shift;
+                if (shift == 0) { // one key: how many of its ties stay
+                    const u64 each_one = by_weight ? weigh(Key<TL>::value(hi)) : (u64)1;
+                    const u64 need = (want - above + each_one - 1) / each_one;
+                    if (hi != cut) // (at the same key, those that stayed so far do)
+                        last = INT_MAX;
+                    cut = hi;
+                    if (need < f.n_in)
+                        last = locate(need);
+                    return false;
+                }
+                lo = max(lo, hi - min(hi, (1u << shift) - 1));
             }
         }
-        search(true, want, top_p);
-    }
-    if (least > cut)
-        cut = least, last = INT_MAX;
+    };
 
-    // The draw.
+    if (by_k) {
+        cut = max(low, bound);
+        if (search(false, (u64)top_k))
+            return;
+    }
+    if (by_p && search(true, 0))
+        return;
+
+    // -------------------------------------------------------------- the draw
+    auto weight_of = [&](TL v, int id) {
+        const u64 w = stays(Key<TL>::of(v), id) ? weigh(to_float(v)) : 0;
+        return w >= least ? w : 0;
+    };
     u64 mine = 0, before;
-    if (greedy)
-        each([&](TL v, int i) { mine += stays(Key<TL>::of(v), i); });
-    else
-        each([&](TL v, int i) {
-            if (stays(Key<TL>::of(v), i))
-                mine += weigh(to_float(v));
-        });
+    each([&](TL v, int id) { mine += weight_of(v, id); });
     const u64 here = block_sum(mine);
-    exchange(1, [&](int) { return here; });
-    const u64 total = sum_of(0, before);
-    const double at = u > 0.0f ? floor((double)u * (double)total) : 0.0;
-    const u64 target = at >= (double)total ? total - 1 : min((u64)at, total - 1); // of the whole numbers 0 .. total - 1
+    const u64 total = add_up(here, before);
+    const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
     if (target >= before && target < before + here) {
         u64 rest = target - before;
         int w = 0;
         while (rest >= s.warp[w])
             rest -= s.warp[w++];
-        if (warp == w) {
-            for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
-                u64 x[VEC], sum = 0;
+        // that warp's places again, a warp for every 32 vectors
+        const int steps = (seg + 32 * VEC - 1) / (32 * VEC);
+        for (int x = warp; x < steps; x += WARPS) {
+            const int i = w * seg + (x * 32 + lane) * VEC;
+            u64 sum = 0;
+            if (i < (w + 1) * seg)
 #pragma unroll
-                for (int k = 0; k < VEC; k++) {
-                    x[k] = 0;
-                    if (i < i1 && stays(Key<TL>::of(buf[i + k]), i + k))
-                        x[k] = greedy ? (u64)1 : weigh(to_float(buf[i + k]));
-                    sum += x[k];
-                }
-                const u64 upto = warp_scan(sum, lane);
-                if (rest < upto && rest >= upto - sum) {
-                    u64 r = rest - (upto - sum);
-                    int k = 0;
-                    u64 mine_k = 0;
+                for (int k = 0; k < VEC; k++)
+                    sum += weight_of(buf[i + k], id0 + i + k);
+            sum = warp_add(sum);
+            if (lane == 0)
+                s.part[x] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int x = 0;
+            while (rest >= s.part[x])
+                rest -= s.part[x++];
+            const int i = w * seg + (x * 32 + lane) * VEC;
+            u64 part[VEC], sum = 0;
 #pragma unroll
-                    for (int q = 0; q < VEC; q++) {
-                        if (k == q && r >= x[q]) {
-                            r -= x[q];
-                            k = q + 1;
-                        } else if (k == q) {
-                            mine_k = x[q];
-                        }
-                    }
-                    a.idx[row] = j0 + i + k - first;
+            for (int k = 0; k < VEC; k++) {
+                part[k] = i < (w + 1) * seg ? weight_of(buf[i + k], id0 + i + k) : 0;
+                sum += part[k];
+            }
+            u64 upto = warp_scan(sum, lane) - sum;
+#pragma unroll
+            for (int k = 0; k < VEC; k++) {
+                if (rest >= upto && rest < upto + part[k]) {
+                    a.idx[row] = id0 + i + k;
                     if (a.prob)
-                        a.prob[row] = (float)((double)mine_k / (double)total);
+                        a.prob[row] = __fdiv_rn(__ull2float_rn(part[k]), __ull2float_rn(total));
                 }
-                const u64 all = __shfl_sync(0xffffffffu, upto, 31);
-                if (rest < all)
-                    break;
-                rest -= all;
+                upto += part[k];
             }
         }
     }
@@ -708,13 +846,13 @@ template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t 
     static luce_host::SmemLimit limit;
     constexpr int VEC = 16 / sizeof(TL), UNIT = VEC * WARPS;
     const auto kern = k_sample<TL>;
-    // as many CTAs to a row as fill the GPU twice, 2048 logits to a CTA at
-    // least, more where shared memory asks for them
-    int cl = 1;
     auto slice_of = [&](int n) { return (int)(((a.V + VEC - 1 + n - 1) / n + UNIT - 1) / UNIT * UNIT); };
-    while (cl < CL_PORTABLE && ((int64_t)R * cl < 2 * luce_host::sm_count() && (int64_t)a.V > 2048 * cl))
+    // as many CTAs to a row as fill the GPU twice, 2048 logits to a CTA at
+    // least, more where two of them would not fit an SM's shared memory
+    int cl = 1;
+    while (cl < CL_PORTABLE && (int64_t)R * cl < 2 * luce_host::sm_count() && a.V > 2048 * cl)
         cl *= 2;
-    while (cl < CL_PORTABLE && (size_t)slice_of(cl) * sizeof(TL) > 88 * 1024)
+    while (cl < CL_PORTABLE && (size_t)slice_of(cl) * sizeof(TL) > 110 * 1024 - sizeof(Shared))
         cl *= 2;
     a.slice = slice_of(cl);
     const size_t smem = (size_t)a.slice * sizeof(TL);
