@@ -8,12 +8,12 @@
 //
 // Both filters look for the token at which those before it, by falling logits,
 // reach a count (top-k) or a weight (top-p).  A histogram over the logits'
-// distance from the largest finds the bin that holds it: ten bits of the
+// distance from the largest finds the bin that holds it: nine bits of the
 // distance at a time, the CTAs' histograms added through distributed shared
 // memory by every CTA for itself.  Few logits enter it.  For top-k the warps'
 // largest lanes bound the k-th from below: with W warps in the cluster, k tokens
 // are at or above the least of the warps' ceil(k / W)-th largest lane maxima.
-// For top-p only those within 2^-16 of the largest weight are binned; if they do
+// For top-p only those within 2^-24 of the largest weight are binned; if they do
 // not reach the share, all are.  Up to MOST tokens up to the bin's end go to the
 // first CTA, which sorts them, cuts, and draws.  More than those stay where they
 // are: the bin's own tokens go to the first CTA, which finds the last to stay,
@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -41,12 +42,12 @@ namespace {
 using namespace luce;
 namespace cg = cooperative_groups;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int CL_MAX = 16, CL_PORTABLE = 8; // CTAs of a cluster at most, and without asking for more
 constexpr int MOST = 2 * THREADS;        // tokens that one CTA sorts
-constexpr int DIGIT = 10, BINS = 1 << DIGIT;
-constexpr int QBITS = 30;                // of a distance from the largest logit
-constexpr float NEAR = 16.0f;            // octaves of weight whose tokens are binned for top-p at first
+constexpr int DIGIT = 9, BINS = 1 << DIGIT;
+constexpr int QBITS = 3 * DIGIT;         // of a distance from the largest logit
+constexpr float NEAR = 24.0f;            // octaves of weight whose tokens are binned for top-p at first
 constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
 typedef unsigned long long u64;
 
@@ -124,31 +125,55 @@ template <> struct Key<__nv_bfloat16> : Key16 {
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+// The greatest of logits; NaN where one is.
+__device__ __forceinline__ float greatest(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ __half greatest(__half a, __half b) { return __hmax_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat16 greatest(__nv_bfloat16 a, __nv_bfloat16 b) { return __hmax_nan(a, b); }
+__device__ __forceinline__ float greatest(const float (&v)[4]) { return greatest(greatest(v[0], v[1]), greatest(v[2], v[3])); }
+template <typename TL> __device__ __forceinline__ TL greatest(const TL (&v)[8]) // two at a time
+{
+    using T2 = typename std::conditional<std::is_same<TL, __half>::value, __half2, __nv_bfloat162>::type;
+    const T2 *p = reinterpret_cast<const T2 *>(v);
+    const T2 m = __hmax2_nan(__hmax2_nan(p[0], p[1]), __hmax2_nan(p[2], p[3]));
+    return __hmax_nan(m.x, m.y);
+}
 template <typename TL> __device__ __forceinline__ TL minus_infinity();
 template <> __device__ __forceinline__ float minus_infinity<float>() { return -INFINITY; }
 template <> __device__ __forceinline__ __half minus_infinity<__half>() { return __ushort_as_half(0xfc00); }
 template <> __device__ __forceinline__ __nv_bfloat16 minus_infinity<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
 
-// The weight of a logit: 2^(31 + sh - z), z = (M - l) c, in whole numbers.
-// (M and l are taken as quarters, so that their difference cannot overflow.)
-struct Weigh {
+// The weight of a logit at most 66 octaves of weight below M: 2^(31 + sh - z),
+// z = (M - l) c, in whole numbers.  (M and l are taken as quarters, so that their
+// difference cannot overflow.  That of fp32 numbers is kept in two floats; 16-bit
+// ones leave no more of it than 2^-25 of logits close to zero.)
+template <bool WIDE> struct Weigh {
     float M4, c_hi, c_lo; // M / 4, 4 c in two floats
     int sh;
     const uint2 *table; // 2^(31 - j / 256) as a whole number and as a float
     __device__ __forceinline__ u64 operator()(float l) const
     {
         const float b = -0.25f * l, d = M4 + b;
-        const float bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
-        const float zh = fminf(d * c_hi, 64.0f);
-        const float zl = fmaf(d, c_hi, -zh) + fmaf(d, c_lo, e * c_hi);
+        const float zh = d * c_hi;
+        float zl = fmaf(d, c_hi, -zh) + d * c_lo;
+        if (WIDE) {
+            const float bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
+            zl = fmaf(e, c_hi, zl);
+        }
         const float magic = 49152.0f; // steps of 2^-8 at 2^15
         const float t = zh + magic;
-        const int n = __float_as_int(t) - __float_as_int(magic);
+        const uint32_t n = __float_as_uint(t); // (the last eight bits of magic, and ten before them, are zero)
         const float r = (zh - (t - magic)) + zl;
         const float p = r * fmaf(r, fmaf(r, -0.055504109f, 0.24022651f), -0.69314718f); // ln(2)^3 / 6, ln(2)^2 / 2, ln(2)
         const uint2 q = table[n & 255];
         const uint32_t m = q.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(q.y), p, 12582912.0f)) - 0x4B400000);
-        return n < 64 * 256 ? ((u64)m << sh) >> (n >> 8) : 0;
+        u64 w;
+        asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"((u64)m << sh), "r"(n >> 8 & 1023)); // (by 64 and more: zero)
+        return w;
     }
 };
 
@@ -171,14 +196,14 @@ template <typename T> __device__ __forceinline__ T warp_scan(T v, int lane) // i
 }
 
 struct Hist {
-    uint32_t lo[BINS], hi[BINS], n[BINS]; // weights in two halves, counts
+    uint32_t lo[BINS], hi[BINS]; // weights in two halves, or counts
 };
 struct Shared {
     uint2 table[256];
     Hist hist[2];                // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
     u64 list[MOST], sorted[MOST]; // tokens: key, and id from the last; the first CTA's
     u64 exchange[2][CL_MAX];     // (alternating, for the same reason)
-    u64 warp[WARPS], part[32];
+    u64 warp[WARPS], part[64];
     u64 found[5];
     u64 sum[2];                  // (alternating with the histograms)
     uint32_t wtop[WARPS], wbound[WARPS];
@@ -224,7 +249,7 @@ __device__ __forceinline__ uint32_t largest(uint32_t key, int j, int lane, uint3
 }
 
 template <typename TL>
-__global__ void __launch_bounds__(THREADS, 2)
+__global__ void __launch_bounds__(THREADS, 4)
     k_sample(const SampleArgs a)
 {
     constexpr int VEC = 16 / sizeof(TL);
@@ -249,9 +274,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int first = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(TL));
     const int seg = a.slice / WARPS, id0 = rank * a.slice - first; // places of a warp; the id at the CTA's first place
     const int i0 = warp * seg, i1 = i0 + seg;                      // this warp's places, counted from the CTA's first
-    uint32_t top = 0;
-    bool bad = false;
-    constexpr int BATCH = 8; // vectors requested together
+    TL most_v = minus_infinity<TL>(); // (NaN where there is one)
+    constexpr int BATCH = 8;          // vectors requested together
     for (int ib = i0; ib < i1; ib += BATCH * 32 * VEC) {
         Vec v[BATCH];
 #pragma unroll
@@ -272,14 +296,12 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int i = ib + (x * 32 + lane) * VEC;
             if (i < i1) {
                 *reinterpret_cast<Vec *>(buf + i) = v[x];
-#pragma unroll
-                for (int k = 0; k < VEC; k++) {
-                    bad |= !(to_float(v[x].v[k]) < INFINITY); // NaN or +infinity
-                    top = max(top, Key<TL>::of(v[x].v[k]));
-                }
+                most_v = greatest(most_v, greatest(v[x].v));
             }
         }
     }
+    const bool bad = __any_sync(0xffffffffu, !(to_float(most_v) < INFINITY)); // NaN or +infinity
+    uint32_t top = bad ? 0xffffffffu : Key<TL>::of(most_v);                    // (no logit of a good row has this key)
     for (int i = tid; i < 256; i += THREADS)
         s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
     if (tid == 0)
@@ -287,9 +309,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int nth = by_k ? (top_k + WARPS * CL - 1) / (WARPS * CL) : 0; // lane of every warp, by size, that bounds the k-th token
     uint32_t bound;
     top = largest(top, nth <= 32 ? nth : 0, lane, bound);
-    bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
-        s.wtop[warp] = bad ? 0xffffffffu : top; // (no logit of a good row has this key)
+        s.wtop[warp] = top;
         s.wbound[warp] = bound;
     }
     __syncthreads();
@@ -333,17 +354,24 @@ __global__ void __launch_bounds__(THREADS, 2)
         return;
     }
 
-    auto each = [&](auto &&f) {
+    // Logits of `least` and more, with their ids.
+    auto each = [&](float least, auto &&f) {
+#pragma unroll 2
         for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
             const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+            if (to_float(greatest(v.v)) >= least) {
 #pragma unroll
-            for (int k = 0; k < VEC; k++)
-                f(v.v[k], id0 + i + k);
+                for (int k = 0; k < VEC; k++) {
+                    const float l = to_float(v.v[k]);
+                    if (l >= least)
+                        f(l, id0 + i + k);
+                }
+            }
         }
     };
     if (greedy) {
         uint32_t id = 0xffffffffu;
-        each([&](TL v, int i) { id = Key<TL>::of(v) == top ? min(id, (uint32_t)i) : id; });
+        each(Key<TL>::value(top), [&](float, int i) { id = min(id, (uint32_t)i); });
         id = __reduce_min_sync(0xffffffffu, id);
         if (lane == 0)
             s.wtop[warp] = id;
@@ -364,10 +392,9 @@ __global__ void __launch_bounds__(THREADS, 2)
     // 4 log2(e) / temperature in two floats (temperatures below 1e-37 count as that)
     const float t = fmaxf(temp, 1e-37f), c_hi = __fdiv_rn(5.77078009f, t);
     const float c_lo = t < INFINITY ? __fdiv_rn(fmaf(-c_hi, t, 5.77078009f) + 7.703852e-08f, t) : 0.0f;
-    const Weigh weigh{0.25f * M, c_hi, c_lo, a.sh, s.table};
-    // keys below `low` weigh nothing (46 > 64 ln(2), by more than the roundings); weights below `least` fail min-p
-    const float reach = M - 46.0f * t;
-    const uint32_t low = reach > -3e38f ? max(Key<TL>::NONE + 1, Key<TL>::at_least(reach)) : Key<TL>::NONE + 1;
+    const Weigh<sizeof(TL) == 4> weigh{0.25f * M, c_hi, c_lo, a.sh, s.table};
+    // logits below `low` weigh nothing (45 > 64 ln(2), by more than the roundings); weights below `least` fail min-p
+    const float low = fmaxf(M - 45.0f * t, -3.4028235e38f);
     const u64 most = (u64)1 << (31 + a.sh);
     const u64 least = min_p > 0.0f ? (min_p < 1.0f ? share(min_p, most, true) : most) : 0;
 
@@ -383,10 +410,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         return t;
     };
 
-    // What stays: keys above `cut`, and of those at it the ids up to `last`.
-    uint32_t cut = low;
+    // What stays: logits above `cut`, and of those at it the ids up to `last`.
+    float cut = low;
     int last = INT_MAX;
-    auto stays = [&](uint32_t key, int id) { return key > cut || (key == cut && id <= last); };
+    auto stays = [&](float l, int id) { return l > cut || (l == cut && id <= last); };
 
     // -------------------------------------------------------------- the first CTA's part
     // s.list, n entries, by size into s.sorted, the largest first (no two are equal).
@@ -507,18 +534,21 @@ __global__ void __launch_bounds__(THREADS, 2)
     };
 
     // -------------------------------------------------------------- sets of tokens
-    // Tokens that `in` says yes to, into the first CTA's list (at most MOST).
+    // Tokens that stay and that `in` says yes to, into the first CTA's list (at most MOST).
     auto collect = [&](auto &&in) {
         u64 *list = cl.map_shared_rank(s.list, 0);
         uint32_t *count = cl.map_shared_rank(&s.count, 0);
-        for (int i = i0 + lane * VEC; i - lane * VEC < i1; i += 32 * VEC) {
+        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
             uint32_t mask = 0;
             Vec v;
-            if (i < i1) {
+            {
                 v = *reinterpret_cast<const Vec *>(buf + i);
+                if (to_float(greatest(v.v)) >= cut)
 #pragma unroll
-                for (int k = 0; k < VEC; k++)
-                    mask |= (uint32_t)in(v.v[k], id0 + i + k) << k;
+                    for (int k = 0; k < VEC; k++) {
+                        const float l = to_float(v.v[k]);
+                        mask |= (uint32_t)(stays(l, id0 + i + k) && in(l)) << k;
+                    }
             }
             if (mask) {
                 uint32_t at = atomicAdd(count, (uint32_t)__popc(mask));
@@ -534,7 +564,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // before them and `want` is to be reached: `cut` and `last`, in every CTA.
     auto cut_list = [&](bool by_weight, u64 above, u64 want) {
         if (rank == 0) {
-            const int n = (int)s.count;
+            const int n = min((int)s.count, MOST);
             sort(n);
             const int p0 = 2 * tid;
             u64 w[2], before;
@@ -556,13 +586,13 @@ __global__ void __launch_bounds__(THREADS, 2)
                 s.count = 0;
         }
         cl.sync();
-        cut = s.cut;
+        cut = Key<TL>::value(s.cut);
         last = s.last;
     };
-    // The id of tie number m (from 1) at the key `cut`, in the order of ids.
+    // The id of tie number m (from 1) at `cut`, in the order of ids.
     auto locate = [&](u64 m) {
         uint32_t n = 0;
-        each([&](TL v, int) { n += Key<TL>::of(v) == cut; });
+        each(cut, [&](float l, int) { n += l == cut; });
         u64 before;
         const u64 mine = block_sum(n);
         add_up(mine, before);
@@ -576,7 +606,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     uint32_t mask = 0;
                     if (i < i1)
                         for (int k = 0; k < VEC; k++)
-                            mask |= (uint32_t)(Key<TL>::of(buf[i + k]) == cut) << k;
+                            mask |= (uint32_t)(to_float(buf[i + k]) == cut) << k;
                     const u64 upto = warp_scan((uint32_t)__popc(mask), lane);
                     if (upto >= rest && upto - __popc(mask) < rest) {
                         for (u64 t = rest - (upto - __popc(mask)); t > 1; t--)
@@ -600,34 +630,32 @@ __global__ void __launch_bounds__(THREADS, 2)
     struct Found {
         uint32_t bin;
         u64 above, in; // before the bin, in it
-        uint32_t n_above, n_in;
         u64 total;     // in all bins
+        uint32_t upto, inside; // tokens up to the bin's end, and in it, at most
     };
-    auto find = [&](bool by_weight, u64 above, auto &&want_of, auto &&bin) {
+    auto find = [&](bool by_weight, u64 above, auto &&want_of, auto &&bin, auto &&lightest) {
         level ^= 1;
         Hist &h = s.hist[level];
         for (int i = tid; i < BINS; i += THREADS)
-            h.lo[i] = h.hi[i] = h.n[i] = 0;
+            h.lo[i] = h.hi[i] = 0;
         __syncthreads();
         u64 sum = 0;
-        each([&](TL v, int id) {
-            const uint32_t key = Key<TL>::of(v);
-            if (stays(key, id)) {
-                const float l = to_float(v);
-                u64 w = 1;
+        each(cut, [&](float l, int id) {
+            if (l > cut || id <= last) {
                 if (by_weight) {
-                    w = weigh(l);
+                    const u64 w = weigh(l);
                     sum += w;
-                }
-                const int b = bin(key, l);
-                if (b >= 0) {
-                    atomicAdd(&h.n[b], 1u);
-                    if (by_weight) {
+                    const int b = bin(l);
+                    if (b >= 0) {
                         const uint32_t wl = (uint32_t)w, old = atomicAdd(&h.lo[b], wl);
                         const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
                         if (wh)
                             atomicAdd(&h.hi[b], wh);
                     }
+                } else {
+                    const int b = bin(l);
+                    if (b >= 0)
+                        atomicAdd(&h.lo[b], 1u);
                 }
             }
         });
@@ -637,33 +665,41 @@ __global__ void __launch_bounds__(THREADS, 2)
                 s.sum[level] = sum;
         }
         cl.sync();
-        u64 w[BINS / THREADS], all = 0;
-        uint32_t n[BINS / THREADS] = {}, count = 0;
+        constexpr int PER = BINS / THREADS; // neighbouring bins of a thread
+        static_assert(PER == 2, "two bins a thread");
+        u64 w[PER] = {0, 0};
         sum = 0;
+        for (int c0 = 0; c0 < CL; c0 += 4) { // (four CTAs' in flight)
+            uint2 lo[4], hi[4];
+            u64 one[4];
 #pragma unroll
-        for (int i = 0; i < BINS / THREADS; i++)
-            w[i] = 0;
-        for (int c = 0; c < CL; c++) {
-            const Hist *r = cl.map_shared_rank(&h, c);
-#pragma unroll
-            for (int i = 0; i < BINS / THREADS; i++) {
-                const int b = tid * (BINS / THREADS) + i;
-                n[i] += r->n[b];
-                if (by_weight)
-                    w[i] += (u64)r->hi[b] << 32 | r->lo[b];
+            for (int c = 0; c < 4; c++) {
+                lo[c] = hi[c] = make_uint2(0, 0);
+                one[c] = 0;
+                if (c0 + c < CL) {
+                    const Hist *r = cl.map_shared_rank(&h, c0 + c);
+                    lo[c] = reinterpret_cast<const uint2 *>(r->lo)[tid];
+                    if (by_weight) {
+                        hi[c] = reinterpret_cast<const uint2 *>(r->hi)[tid];
+                        one[c] = *cl.map_shared_rank(&s.sum[level], c0 + c);
+                    }
+                }
             }
-            if (by_weight)
-                sum += *cl.map_shared_rank(&s.sum[level], c);
-        }
 #pragma unroll
-        for (int i = 0; i < BINS / THREADS; i++) {
-            if (!by_weight)
-                w[i] = n[i];
-            all += w[i];
-            count += n[i];
+            for (int c = 0; c < 4; c++) {
+                w[0] += (u64)hi[c].x << 32 | lo[c].x;
+                w[1] += (u64)hi[c].y << 32 | lo[c].y;
+                sum += one[c];
+            }
         }
-        const u64 in_warp = warp_scan(all, lane);
-        const uint32_t n_warp = warp_scan(count, lane);
+        // (the tokens of a bin: no more than its weight in the lightest of them)
+        uint32_t n[PER] = {(uint32_t)w[0], (uint32_t)w[1]};
+        if (by_weight)
+#pragma unroll
+            for (int i = 0; i < PER; i++)
+                n[i] = w[i] == 0 ? 0u : (uint32_t)fminf(__ull2float_ru(w[i]) * lightest(tid * PER + i) + 1.0f, 4194304.0f);
+        const u64 all = w[0] + w[1], in_warp = warp_scan(all, lane);
+        const uint32_t count = n[0] + n[1], n_warp = warp_scan(count, lane);
         if (lane == 31) {
             s.warp[warp] = in_warp;
             s.part[warp] = n_warp;
@@ -671,6 +707,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         __syncthreads();
         u64 at = in_warp - all, total = 0;
         uint32_t n_at = n_warp - count;
+#pragma unroll
         for (int i = 0; i < WARPS; i++) {
             if (i < warp) {
                 at += s.warp[i];
@@ -681,19 +718,19 @@ __global__ void __launch_bounds__(THREADS, 2)
         const u64 want = want_of(sum);
         at += above;
 #pragma unroll
-        for (int i = 0; i < BINS / THREADS; i++) {
+        for (int i = 0; i < PER; i++) {
+            n_at += n[i];
             if (at < want && want <= at + w[i]) {
-                s.found[0] = tid * (BINS / THREADS) + i;
+                s.found[0] = tid * PER + i;
                 s.found[1] = at;
                 s.found[2] = w[i];
                 s.found[3] = n_at;
                 s.found[4] = n[i];
             }
             at += w[i];
-            n_at += n[i];
         }
         __syncthreads();
-        return Found{(uint32_t)s.found[0], s.found[1], s.found[2], (uint32_t)s.found[3], (uint32_t)s.found[4], total};
+        return Found{(uint32_t)s.found[0], s.found[1], s.found[2], total, (uint32_t)s.found[3], (uint32_t)s.found[4]};
     };
     // The cut at which the tokens that stay reach `want` (a weight of 0: a share top_p of
     // theirs).  True: they were few, and the first CTA has drawn from them.
@@ -701,11 +738,17 @@ __global__ void __launch_bounds__(THREADS, 2)
         bool all_in = !by_weight; // whether every token that stays is binned
         while (true) {
             // distances as whole numbers of QBITS bits, the same order as the keys' (equal for logits that are near)
-            const float range = all_in ? weigh.M4 - 0.25f * Key<TL>::value(cut) : NEAR * 0.69314718f * 0.25f * fminf(temp, 1e30f);
-            const float scale = range > 0.0f ? fminf(1073741824.0f / range, 1e38f) : 0.0f;
+            const float range = all_in ? weigh.M4 - 0.25f * cut : NEAR * 0.69314718f * 0.25f * fminf(temp, 1e30f);
+            constexpr float FULL = (float)(1 << QBITS);
+            const float scale = range > 0.0f ? fminf(FULL / range, 1e38f) : 0.0f;
             auto place = [&](float l) {
                 const float x = (weigh.M4 - 0.25f * l) * scale;
-                return x < 1073741824.0f ? (int)x : all_in ? (1 << QBITS) - 1 : -1;
+                return x < FULL ? (int)x : all_in ? (1 << QBITS) - 1 : -1;
+            };
+            // one over the weight at the end of a stretch of `bits` bits (and a hundredth, for all roundings)
+            const float octaves = scale > 0.0f ? c_hi / scale : 0.0f;
+            auto over_end = [&](uint32_t stretch, int bits) {
+                return scale > 0.0f ? 1.01f * exp2f(fminf(octaves * ((float)stretch + 1.0f) * (float)(1 << bits) - (float)(31 + a.sh), 120.0f)) : 1.0f;
             };
             uint32_t prefix = 0;
             u64 above = 0;
@@ -718,35 +761,34 @@ __global__ void __launch_bounds__(THREADS, 2)
                                              want = top_p > 0.0f ? max(share(top_p, sum, true), (u64)1) : (u64)1;
                                          return want;
                                      },
-                                     [&](uint32_t, float l) {
+                                     [&](float l) {
                                          const int q = place(l);
                                          return q < 0 || (!fresh && (uint32_t)q >> (bits + DIGIT) != prefix) ? -1 : q >> bits & (BINS - 1);
-                                     });
+                                     },
+                                     [&](uint32_t b) { return over_end(prefix << DIGIT | b, bits); });
                 if (fresh && want > f.total) {
                     if (all_in)
                         return false; // all stay
                     again = all_in = true;
                     break;
                 }
-                if (fresh && f.n_above + f.n_in <= MOST) {
-                    collect([&](TL v, int id) {
-                        const uint32_t key = Key<TL>::of(v);
-                        const int q = place(to_float(v));
-                        return stays(key, id) && q >= 0 && (uint32_t)q >> bits <= f.bin;
+                if (fresh && f.upto <= MOST) {
+                    collect([&](float l) {
+                        const int q = place(l);
+                        return q >= 0 && (uint32_t)q >> bits <= f.bin;
                     });
                     if (rank == 0) {
-                        const int n = (int)(f.n_above + f.n_in);
+                        const int n = min((int)s.count, MOST);
                         draw_few(n, by_weight ? n : min(top_k, n), by_weight ? want : 0);
                     }
                     return true;
                 }
                 prefix = prefix << DIGIT | f.bin;
                 above = f.above;
-                if (f.n_in <= MOST) {
-                    collect([&](TL v, int id) {
-                        const uint32_t key = Key<TL>::of(v);
-                        const int q = place(to_float(v));
-                        return stays(key, id) && q >= 0 && (uint32_t)q >> bits == prefix;
+                if (f.inside <= MOST) {
+                    collect([&](float l) {
+                        const int q = place(l);
+                        return q >= 0 && (uint32_t)q >> bits == prefix;
                     });
                     cut_list(by_weight, above, want);
                     return false;
@@ -755,22 +797,24 @@ __global__ void __launch_bounds__(THREADS, 2)
             if (again)
                 continue;
             // many logits of one distance: by their bits, then by id
-            uint32_t hi = top, lo = cut;
+            uint32_t hi = top, lo = Key<TL>::at_least(cut);
             while (true) {
                 const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
                 const Found f = find(by_weight, above, [&](u64) { return want; },
-                                     [&](uint32_t key, float l) {
+                                     [&](float l) {
+                                         const uint32_t key = Key<TL>::at_least(l);
                                          return key - lo <= hi - lo && (uint32_t)place(l) == prefix ? (int)((hi - key) >> shift) : -1;
-                                     });
+                                     },
+                                     [&](uint32_t) { return 1.0f; });
                 above = f.above;
                 hi -= f.bin << shift;
                 if (shift == 0) { // one key: how many of its ties stay
-                    const u64 each_one = by_weight ? weigh(Key<TL>::value(hi)) : (u64)1;
-                    const u64 need = (want - above + each_one - 1) / each_one;
-                    if (hi != cut) // (at the same key, those that stayed so far do)
+                    const float at = Key<TL>::value(hi);
+                    const u64 each_one = by_weight ? weigh(at) : (u64)1, need = (want - above + each_one - 1) / each_one;
+                    if (at != cut) // (at the same one, those that stayed so far do)
                         last = INT_MAX;
-                    cut = hi;
-                    if (need < f.n_in)
+                    cut = at;
+                    if (need * each_one < f.in)
                         last = locate(need);
                     return false;
                 }
@@ -780,7 +824,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     };
 
     if (by_k) {
-        cut = max(low, bound);
+        cut = bound > Key<TL>::NONE ? fmaxf(low, Key<TL>::value(bound)) : low;
         if (search(false, (u64)top_k))
             return;
     }
@@ -789,11 +833,15 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     // -------------------------------------------------------------- the draw
     auto weight_of = [&](TL v, int id) {
-        const u64 w = stays(Key<TL>::of(v), id) ? weigh(to_float(v)) : 0;
+        const float l = to_float(v);
+        const u64 w = stays(l, id) ? weigh(l) : 0;
         return w >= least ? w : 0;
     };
     u64 mine = 0, before;
-    each([&](TL v, int id) { mine += weight_of(v, id); });
+    each(cut, [&](float l, int id) {
+        const u64 w = l > cut || id <= last ? weigh(l) : 0;
+        mine += w >= least ? w : 0;
+    });
     const u64 here = block_sum(mine);
     const u64 total = add_up(here, before);
     const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
@@ -847,12 +895,28 @@ template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t 
     constexpr int VEC = 16 / sizeof(TL), UNIT = VEC * WARPS;
     const auto kern = k_sample<TL>;
     auto slice_of = [&](int n) { return (int)(((a.V + VEC - 1 + n - 1) / n + UNIT - 1) / UNIT * UNIT); };
-    // as many CTAs to a row as fill the GPU twice, 2048 logits to a CTA at
-    // least, more where two of them would not fit an SM's shared memory
+    // as many CTAs to a row as fill the GPU's SMs four times, 1024 logits to a CTA at
+    // least, more where four of them would not fit an SM's shared memory
+    static std::atomic<int> wide[64]; // whether a device takes clusters of CL_MAX: 1 yes, -1 no
+    int dev = 0, most = CL_PORTABLE;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LUCE_ERR_CUDA;
+    }
+    if (dev >= 0 && dev < 64) {
+        int w = wide[dev].load(std::memory_order_acquire);
+        if (w == 0) {
+            w = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
+            if (w < 0)
+                (void)cudaGetLastError();
+            wide[dev].store(w, std::memory_order_release);
+        }
+        most = w > 0 ? CL_MAX : CL_PORTABLE;
+    }
     int cl = 1;
-    while (cl < CL_PORTABLE && (int64_t)R * cl < 2 * luce_host::sm_count() && a.V > 2048 * cl)
+    while (cl < most && (int64_t)R * cl < 4 * luce_host::sm_count() && a.V > 1024 * cl)
         cl *= 2;
-    while (cl < CL_PORTABLE && (size_t)slice_of(cl) * sizeof(TL) > 110 * 1024 - sizeof(Shared))
+    while (cl < most && (size_t)slice_of(cl) * sizeof(TL) > 56 * 1024 - sizeof(Shared))
         cl *= 2;
     a.slice = slice_of(cl);
     const size_t smem = (size_t)a.slice * sizeof(TL);
