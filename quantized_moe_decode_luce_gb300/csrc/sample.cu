@@ -42,11 +42,7 @@ namespace {
 using namespace luce;
 namespace cg = cooperative_groups;
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int CL_MAX = 16, CL_PORTABLE = 8; // CTAs of a cluster at most, and without asking for more
-constexpr int MOST = 2 * THREADS;        // tokens that one CTA sorts
-constexpr int DIGIT = 9, BINS = 1 << DIGIT;
-constexpr int QBITS = 3 * DIGIT;         // of a distance from the largest logit
 constexpr float NEAR = 24.0f;            // octaves of weight whose tokens are binned for top-p at first
 constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
 typedef unsigned long long u64;
@@ -148,26 +144,33 @@ template <> __device__ __forceinline__ __half minus_infinity<__half>() { return 
 template <> __device__ __forceinline__ __nv_bfloat16 minus_infinity<__nv_bfloat16>() { return __ushort_as_bfloat16(0xff80); }
 
 // The weight of a logit at most 66 octaves of weight below M: 2^(31 + sh - z),
-// z = (M - l) c, in whole numbers.  (M and l are taken as quarters, so that their
-// difference cannot overflow.  That of fp32 numbers is kept in two floats; 16-bit
-// ones leave no more of it than 2^-25 of logits close to zero.)
-template <bool WIDE> struct Weigh {
-    float M4, c_hi, c_lo; // M / 4, 4 c in two floats
+// z = (M - l) c, c = log2(e) / temperature, in whole numbers.  z is split into a
+// multiple n of 2^-8 and a rest r.  Where c M is below 2^14, n is c M - c l
+// rounded, and r = (A1 - n) - l c + A2, with c M = A1 + A2 and A1 a multiple of
+// 2^-8: A1 - n is exact, and the difference with l c, below 2^-7, is rounded
+// once.  Beyond (small temperatures) M - l is kept in two floats (as quarters, so
+// that it cannot overflow).
+struct Weigh {
+    float c_hi, c_lo; // c in two floats
+    float cM, A1, A2;
+    float M4, c4_hi, c4_lo; // M / 4, 4 c
     int sh;
+    bool small;
     const uint2 *table; // 2^(31 - j / 256) as a whole number and as a float
     __device__ __forceinline__ u64 operator()(float l) const
     {
-        const float b = -0.25f * l, d = M4 + b;
-        const float zh = d * c_hi;
-        float zl = fmaf(d, c_hi, -zh) + d * c_lo;
-        if (WIDE) {
-            const float bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
-            zl = fmaf(e, c_hi, zl);
-        }
         const float magic = 49152.0f; // steps of 2^-8 at 2^15
-        const float t = zh + magic;
+        float t, r;
+        if (!small) {
+            t = fmaf(-l, c_hi, cM) + magic;
+            r = fmaf(-l, c_hi, A1 - (t - magic)) + fmaf(-l, c_lo, A2);
+        } else {
+            const float b = -0.25f * l, d = M4 + b, bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
+            const float zh = d * c4_hi, zl = fmaf(d, c4_hi, -zh) + fmaf(d, c4_lo, e * c4_hi);
+            t = zh + magic;
+            r = (zh - (t - magic)) + zl;
+        }
         const uint32_t n = __float_as_uint(t); // (the last eight bits of magic, and ten before them, are zero)
-        const float r = (zh - (t - magic)) + zl;
         const float p = r * fmaf(r, fmaf(r, -0.055504109f, 0.24022651f), -0.69314718f); // ln(2)^3 / 6, ln(2)^2 / 2, ln(2)
         const uint2 q = table[n & 255];
         const uint32_t m = q.x + (uint32_t)(__float_as_int(fmaf(__uint_as_float(q.y), p, 12582912.0f)) - 0x4B400000);
@@ -195,14 +198,21 @@ template <typename T> __device__ __forceinline__ T warp_scan(T v, int lane) // i
     return v;
 }
 
-struct Hist {
-    uint32_t lo[BINS], hi[BINS]; // weights in two halves, or counts
-};
-struct Shared {
+template <int THREADS> struct Shared {
+    static constexpr int WARPS = THREADS / 32;
+    static constexpr int BINS = 2 * THREADS, DIGIT = THREADS == 256 ? 9 : 10;
+    static constexpr int MOST = 2 * THREADS; // tokens that one CTA sorts
+    static_assert(BINS == 1 << DIGIT, "bins");
+    struct Hist {
+        uint32_t lo[BINS], hi[BINS]; // weights in two halves, or counts
+    };
     uint2 table[256];
-    Hist hist[2];                // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
-    u64 list[MOST], sorted[MOST]; // tokens: key, and id from the last; the first CTA's
-    u64 exchange[2][CL_MAX];     // (alternating, for the same reason)
+    union {
+        Hist hist[2];     // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
+        u64 sorted[MOST]; // (while no histogram is in use)
+    };
+    u64 list[MOST];          // the first CTA's tokens: key, and id from the last
+    u64 exchange[2][CL_MAX]; // (alternating, for the same reason)
     u64 warp[WARPS], part[64];
     u64 found[5];
     u64 sum[2];                  // (alternating with the histograms)
@@ -248,14 +258,16 @@ __device__ __forceinline__ uint32_t largest(uint32_t key, int j, int lane, uint3
     return top;
 }
 
-template <typename TL>
-__global__ void __launch_bounds__(THREADS, 4)
+template <typename TL, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     k_sample(const SampleArgs a)
 {
-    constexpr int VEC = 16 / sizeof(TL);
+    using S = Shared<THREADS>;
+    constexpr int VEC = 16 / sizeof(TL), WARPS = S::WARPS, BINS = S::BINS, DIGIT = S::DIGIT, MOST = S::MOST;
+    constexpr int QBITS = 3 * DIGIT; // of a distance from the largest logit
     struct __align__(16) Vec { TL v[VEC]; };
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ Shared s;
+    __shared__ S s;
     TL *buf = reinterpret_cast<TL *>(smem_raw);
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), CL = (int)cl.num_blocks(), row = blockIdx.y;
@@ -369,6 +381,15 @@ __global__ void __launch_bounds__(THREADS, 4)
             }
         }
     };
+    // All logits, with their ids.
+    auto every = [&](auto &&f) {
+        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
+            const Vec v = *reinterpret_cast<const Vec *>(buf + i);
+#pragma unroll
+            for (int k = 0; k < VEC; k++)
+                f(to_float(v.v[k]), id0 + i + k);
+        }
+    };
     if (greedy) {
         uint32_t id = 0xffffffffu;
         each(Key<TL>::value(top), [&](float, int i) { id = min(id, (uint32_t)i); });
@@ -392,10 +413,17 @@ __global__ void __launch_bounds__(THREADS, 4)
     // 4 log2(e) / temperature in two floats (temperatures below 1e-37 count as that)
     const float t = fmaxf(temp, 1e-37f), c_hi = __fdiv_rn(5.77078009f, t);
     const float c_lo = t < INFINITY ? __fdiv_rn(fmaf(-c_hi, t, 5.77078009f) + 7.703852e-08f, t) : 0.0f;
-    const Weigh<sizeof(TL) == 4> weigh{0.25f * M, c_hi, c_lo, a.sh, s.table};
+    Weigh weigh;
+    weigh.c4_hi = c_hi, weigh.c4_lo = c_lo, weigh.c_hi = 0.25f * c_hi, weigh.c_lo = 0.25f * c_lo;
+    weigh.M4 = 0.25f * M, weigh.sh = a.sh, weigh.table = s.table;
+    weigh.cM = M * weigh.c_hi;
+    weigh.small = !(fabsf(weigh.cM) < 16384.0f) || c_hi < 1e-30f;
+    weigh.A1 = (weigh.cM + 98304.0f) - 98304.0f; // (a multiple of 2^-7)
+    weigh.A2 = (weigh.cM - weigh.A1) + fmaf(M, weigh.c_lo, fmaf(M, weigh.c_hi, -weigh.cM));
+    const u64 most = weigh(M); // 2^(31 + sh), or a few units of 2^sh off
+
     // logits below `low` weigh nothing (45 > 64 ln(2), by more than the roundings); weights below `least` fail min-p
     const float low = fmaxf(M - 45.0f * t, -3.4028235e38f);
-    const u64 most = (u64)1 << (31 + a.sh);
     const u64 least = min_p > 0.0f ? (min_p < 1.0f ? share(min_p, most, true) : most) : 0;
 
     auto block_sum = [&](u64 v) { // of the warps' sums, which stay in s.warp
@@ -626,40 +654,48 @@ __global__ void __launch_bounds__(THREADS, 4)
     };
 
     // A histogram over the tokens that stay (bin: a bin, or none below zero), and in
-    // it the bin at which what stands before it reaches `want`.
+    // it the bin at which what stands before it reaches `want`.  (fresh: and the weight
+    // of all of them, for want_of.)
     struct Found {
         uint32_t bin;
         u64 above, in; // before the bin, in it
         u64 total;     // in all bins
         uint32_t upto, inside; // tokens up to the bin's end, and in it, at most
     };
-    auto find = [&](bool by_weight, u64 above, auto &&want_of, auto &&bin, auto &&lightest) {
+    auto find = [&](bool by_weight, bool fresh, u64 above, auto &&want_of, auto &&bin, auto &&lightest) {
         level ^= 1;
-        Hist &h = s.hist[level];
+        auto &h = s.hist[level];
         for (int i = tid; i < BINS; i += THREADS)
             h.lo[i] = h.hi[i] = 0;
         __syncthreads();
         u64 sum = 0;
-        each(cut, [&](float l, int id) {
-            if (l > cut || id <= last) {
-                if (by_weight) {
-                    const u64 w = weigh(l);
-                    sum += w;
-                    const int b = bin(l);
-                    if (b >= 0) {
-                        const uint32_t wl = (uint32_t)w, old = atomicAdd(&h.lo[b], wl);
-                        const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
-                        if (wh)
-                            atomicAdd(&h.hi[b], wh);
-                    }
-                } else {
-                    const int b = bin(l);
-                    if (b >= 0)
+        auto into = [&](int b, u64 w) {
+            const uint32_t wl = (uint32_t)w, old = atomicAdd(&h.lo[b], wl);
+            const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old);
+            if (wh)
+                atomicAdd(&h.hi[b], wh);
+        };
+        if (by_weight && fresh) {
+            every([&](float l, int id) {
+                const bool in = stays(l, id);
+                const u64 w = weigh(in ? l : cut);
+                sum += in ? w : 0;
+                const int b = bin(l);
+                if (in && b >= 0)
+                    into(b, w);
+            });
+        } else {
+            each(cut, [&](float l, int id) {
+                const int b = bin(l);
+                if (b >= 0 && (l > cut || id <= last)) {
+                    if (by_weight)
+                        into(b, weigh(l));
+                    else
                         atomicAdd(&h.lo[b], 1u);
                 }
-            }
-        });
-        if (by_weight) {
+            });
+        }
+        if (by_weight && fresh) {
             sum = block_sum(sum);
             if (tid == 0)
                 s.sum[level] = sum;
@@ -677,11 +713,12 @@ __global__ void __launch_bounds__(THREADS, 4)
                 lo[c] = hi[c] = make_uint2(0, 0);
                 one[c] = 0;
                 if (c0 + c < CL) {
-                    const Hist *r = cl.map_shared_rank(&h, c0 + c);
+                    const auto *r = cl.map_shared_rank(&h, c0 + c);
                     lo[c] = reinterpret_cast<const uint2 *>(r->lo)[tid];
                     if (by_weight) {
                         hi[c] = reinterpret_cast<const uint2 *>(r->hi)[tid];
-                        one[c] = *cl.map_shared_rank(&s.sum[level], c0 + c);
+                        if (fresh)
+                            one[c] = *cl.map_shared_rank(&s.sum[level], c0 + c);
                     }
                 }
             }
@@ -755,9 +792,9 @@ __global__ void __launch_bounds__(THREADS, 4)
             bool again = false;
             for (int bits = QBITS - DIGIT; bits >= 0; bits -= DIGIT) {
                 const bool fresh = bits == QBITS - DIGIT;
-                const Found f = find(by_weight, above,
+                const Found f = find(by_weight, fresh, above,
                                      [&](u64 sum) {
-                                         if (by_weight && want == 0)
+                                         if (fresh && by_weight && want == 0)
                                              want = top_p > 0.0f ? max(share(top_p, sum, true), (u64)1) : (u64)1;
                                          return want;
                                      },
@@ -800,7 +837,7 @@ __global__ void __launch_bounds__(THREADS, 4)
             uint32_t hi = top, lo = Key<TL>::at_least(cut);
             while (true) {
                 const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
-                const Found f = find(by_weight, above, [&](u64) { return want; },
+                const Found f = find(by_weight, false, above, [&](u64) { return want; },
                                      [&](float l) {
                                          const uint32_t key = Key<TL>::at_least(l);
                                          return key - lo <= hi - lo && (uint32_t)place(l) == prefix ? (int)((hi - key) >> shift) : -1;
@@ -838,10 +875,15 @@ __global__ void __launch_bounds__(THREADS, 4)
         return w >= least ? w : 0;
     };
     u64 mine = 0, before;
-    each(cut, [&](float l, int id) {
-        const u64 w = l > cut || id <= last ? weigh(l) : 0;
-        mine += w >= least ? w : 0;
-    });
+    auto add = [&](float l, int id) {
+        const bool in = stays(l, id);
+        const u64 w = weigh(in ? l : cut);
+        mine += in && w >= least ? w : 0;
+    };
+    if (by_k || by_p)
+        each(cut, add);
+    else
+        every(add);
     const u64 here = block_sum(mine);
     const u64 total = add_up(here, before);
     const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
@@ -889,38 +931,12 @@ __global__ void __launch_bounds__(THREADS, 4)
     }
 }
 
-template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t stream)
+template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int R, int cl, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
-    constexpr int VEC = 16 / sizeof(TL), UNIT = VEC * WARPS;
-    const auto kern = k_sample<TL>;
-    auto slice_of = [&](int n) { return (int)(((a.V + VEC - 1 + n - 1) / n + UNIT - 1) / UNIT * UNIT); };
-    // as many CTAs to a row as fill the GPU's SMs four times, 1024 logits to a CTA at
-    // least, more where four of them would not fit an SM's shared memory
-    static std::atomic<int> wide[64]; // whether a device takes clusters of CL_MAX: 1 yes, -1 no
-    int dev = 0, most = CL_PORTABLE;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return LUCE_ERR_CUDA;
-    }
-    if (dev >= 0 && dev < 64) {
-        int w = wide[dev].load(std::memory_order_acquire);
-        if (w == 0) {
-            w = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
-            if (w < 0)
-                (void)cudaGetLastError();
-            wide[dev].store(w, std::memory_order_release);
-        }
-        most = w > 0 ? CL_MAX : CL_PORTABLE;
-    }
-    int cl = 1;
-    while (cl < most && (int64_t)R * cl < 4 * luce_host::sm_count() && a.V > 1024 * cl)
-        cl *= 2;
-    while (cl < most && (size_t)slice_of(cl) * sizeof(TL) > 56 * 1024 - sizeof(Shared))
-        cl *= 2;
-    a.slice = slice_of(cl);
+    const auto kern = k_sample<TL, THREADS>;
     const size_t smem = (size_t)a.slice * sizeof(TL);
-    if (smem + sizeof(Shared) > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
+    if (smem + sizeof(Shared<THREADS>) > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
@@ -938,6 +954,51 @@ template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t 
         return LUCE_ERR_CUDA;
     }
     return LUCE_OK;
+}
+
+// Whether the current device takes clusters of CL_MAX CTAs (asked once per device).
+template <typename TL> bool wide_clusters()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    int w = known[dev].load(std::memory_order_acquire);
+    if (w == 0) {
+        w = cudaFuncSetAttribute(k_sample<TL, 256>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaFuncSetAttribute(k_sample<TL, 512>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
+                ? 1
+                : -1;
+        if (w < 0)
+            (void)cudaGetLastError();
+        known[dev].store(w, std::memory_order_release);
+    }
+    return w > 0;
+}
+
+template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t stream)
+{
+    constexpr int VEC = 16 / sizeof(TL);
+    auto slice_of = [&](int n, int unit) { return (int)(((int64_t)a.V + VEC - 1 + n - 1) / n + unit - 1) / unit * unit; };
+    // Few rows: as many CTAs to a row as there are SMs for, 1024 logits to a CTA at
+    // least.  More: as many as fill every SM four times, or keep a slice small enough
+    // for that; but clusters of more than eight CTAs find less room (at most 21
+    // of 16 of them at once).  Slices too large for four CTAs to an SM get CTAs of
+    // twice the threads (128 x 151936 fp32).
+    const int sms = luce_host::sm_count();
+    int cl = 1;
+    while (cl < CL_PORTABLE && (int64_t)R * cl < 4 * sms && a.V > 1024 * cl)
+        cl *= 2;
+    if (cl == CL_PORTABLE && R * CL_MAX <= sms && a.V > 1024 * cl && wide_clusters<TL>())
+        cl = CL_MAX;
+    constexpr size_t QUARTER = 56 * 1024; // of an SM's shared memory
+    while (cl < CL_PORTABLE && slice_of(cl, VEC * 8) * sizeof(TL) > QUARTER - sizeof(Shared<256>))
+        cl *= 2;
+    const bool narrow = slice_of(cl, VEC * 8) * sizeof(TL) <= QUARTER - sizeof(Shared<256>);
+    a.slice = slice_of(cl, VEC * (narrow ? 8 : 16)); // whole vectors of every warp
+    return narrow ? launch_sample<TL, 256>(a, R, cl, stream) : launch_sample<TL, 512>(a, R, cl, stream);
 }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb)
