@@ -212,12 +212,13 @@ template <int THREADS> struct Shared {
         u64 sorted[MOST]; // (while no histogram is in use)
     };
     u64 list[MOST];          // the first CTA's tokens: key, and id from the last
+    u64 near[THREADS];       // this CTA's candidates for top-k, the same
     u64 exchange[2][CL_MAX]; // (alternating, for the same reason)
     u64 warp[WARPS], part[64];
     u64 found[5];
     u64 sum[2];                  // (alternating with the histograms)
     uint32_t wtop[WARPS], wbound[WARPS];
-    uint32_t count, cut;
+    uint32_t count, near_count, cut;
     int last;
 };
 
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     for (int i = tid; i < 256; i += THREADS)
         s.table[i] = make_uint2(POWERS.v[i], __float_as_uint((float)POWERS.v[i]));
     if (tid == 0)
-        s.count = 0;
+        s.count = s.near_count = 0;
     const int nth = by_k ? (top_k + WARPS * CL - 1) / (WARPS * CL) : 0; // lane of every warp, by size, that bounds the k-th token
     uint32_t bound;
     top = largest(top, nth <= 32 ? nth : 0, lane, bound);
@@ -444,11 +445,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     auto stays = [&](float l, int id) { return l > cut || (l == cut && id <= last); };
 
     // -------------------------------------------------------------- the first CTA's part
+    // Each part is made for the whole CTA and (ONE) for one warp, which takes up to 64
+    // tokens without a barrier.
     // s.list, n entries, by size into s.sorted, the largest first (no two are equal).
-    auto sort = [&](int n) {
+    auto sort = [&](auto one, int n) {
+        constexpr bool ONE = decltype(one)::value;
+        if constexpr (ONE) { // the place of each is the number of larger ones
+            __syncwarp();
+            const u64 x = lane < n ? s.list[lane] : 0, y = lane + 32 < n ? s.list[lane + 32] : 0;
+            int to_x = 0, to_y = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; j++) {
+                const u64 v = s.list[j];
+                to_x += v > x;
+                to_y += v > y;
+            }
+            if (lane < n)
+                s.sorted[to_x] = x;
+            if (lane + 32 < n)
+                s.sorted[to_y] = y;
+            __syncwarp();
+            return;
+        }
         __syncthreads();
-        if (n <= THREADS / 2) { // the place of each is the number of larger ones
-            int parts = 1;      // threads to an entry
+        if (n <= THREADS / 2) { // the same, with several threads to an entry
+            int parts = 1;
             while (2 * parts * n <= THREADS && parts < 32)
                 parts *= 2;
             const int e = tid / parts;
@@ -487,15 +508,24 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     };
     auto key_of = [&](u64 entry) { return (uint32_t)(entry >> 32); };
     auto id_of = [&](u64 entry) { return (int)(0xffffffffu - (uint32_t)entry); };
+    auto sync = [&](auto one) {
+        if constexpr (decltype(one)::value)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
     // Values of two neighbours a thread: what stands before the first, and the total.
-    auto scan = [&](u64 x, u64 y, u64 &before) {
+    auto scan = [&](auto one, u64 x, u64 y, u64 &before) {
         const u64 upto = warp_scan(x + y, lane);
+        before = upto - x - y;
+        if constexpr (decltype(one)::value)
+            return __shfl_sync(0xffffffffu, upto, 31);
         __syncthreads();
         if (lane == 31)
             s.warp[warp] = upto;
         __syncthreads();
         u64 total = 0;
-        before = upto - x - y;
+#pragma unroll
         for (int i = 0; i < WARPS; i++) {
             if (i < warp)
                 before += s.warp[i];
@@ -505,8 +535,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     };
     // The draw from the n tokens of the list, of which the first `keep` and those that
     // reach a weight of `want` stay (0: top_p of theirs).
-    auto draw_few = [&](int n, int keep, u64 want) {
-        sort(n);
+    auto draw_few = [&](auto one, int n, int keep, u64 want) {
+        sort(one, n);
         const int p0 = 2 * tid;
         u64 w[2], before;
         uint32_t key[2] = {0, 0};
@@ -516,39 +546,39 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 key[i] = key_of(s.sorted[p0 + i]);
             w[i] = p0 + i < keep ? weigh(Key<TL>::value(key[i])) : 0;
         }
-        const u64 all = scan(w[0], w[1], before);
+        const u64 all = scan(one, w[0], w[1], before);
         if (by_p && want == 0)
             want = top_p > 0.0f ? max(share(top_p, all, true), (u64)1) : (u64)1;
         int stay = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             const bool in = p0 + i < keep && (!by_p || before + (i ? w[0] : 0) < want) && w[i] >= least;
-            stay += __syncthreads_count(in); // (the first one always stays)
+            if constexpr (decltype(one)::value) // (the first one always stays)
+                stay += __popc(__ballot_sync(0xffffffffu, in));
+            else
+                stay += __syncthreads_count(in);
         }
         // those that stay, in the order of ids: the id, and the weight's place
 #pragma unroll
         for (int i = 0; i < 2; i++)
             if (p0 + i < stay)
                 s.list[p0 + i] = (u64)(uint32_t)s.sorted[p0 + i] << 32 | (uint32_t)(p0 + i);
-        sort(stay);
-        int at[2] = {0, 0};
+        sort(one, stay);
+        int at[2];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < 2; i++)
             at[i] = p0 + i < stay ? (int)(uint32_t)s.sorted[p0 + i] : -1;
-            w[i] = 0;
-        }
-        // (the sort has taken the places of the tokens: their keys come back from the threads that hold them)
-        __syncthreads();
+        // (the weights come from the threads that hold them)
+        sync(one);
 #pragma unroll
         for (int i = 0; i < 2; i++)
             if (p0 + i < stay)
-                s.list[p0 + i] = key[i];
-        __syncthreads();
+                s.list[p0 + i] = w[i];
+        sync(one);
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            if (at[i] >= 0)
-                w[i] = weigh(Key<TL>::value((uint32_t)s.list[at[i]]));
-        const u64 total = scan(w[0], w[1], before);
+            w[i] = at[i] >= 0 ? s.list[at[i]] : 0;
+        const u64 total = scan(one, w[0], w[1], before);
         const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -560,62 +590,67 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             before += w[i];
         }
     };
+    // Of the n tokens in the list, the last to stay where `above` stands before them and
+    // `want` is to be reached: `cut` and `last`, to every CTA.
+    auto cut_list = [&](auto one, int n, bool by_weight, u64 above, u64 want) {
+        sort(one, n);
+        const int p0 = 2 * tid;
+        u64 w[2], before;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            w[i] = p0 + i >= n ? 0 : by_weight ? weigh(Key<TL>::value(key_of(s.sorted[p0 + i]))) : (u64)1;
+        scan(one, w[0], w[1], before);
+        before += above;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            if (before < want && want <= before + w[i])
+                for (int c = 0; c < CL; c++) {
+                    *cl.map_shared_rank(&s.cut, c) = key_of(s.sorted[p0 + i]);
+                    *cl.map_shared_rank(&s.last, c) = id_of(s.sorted[p0 + i]);
+                }
+            before += w[i];
+        }
+    };
+    // f(whether one warp is to do it) in the first CTA, for n tokens.
+    auto by_first = [&](int n, auto &&f) {
+        if (n > 64)
+            f(std::integral_constant<bool, false>());
+        else if (warp == 0)
+            f(std::integral_constant<bool, true>());
+    };
 
     // -------------------------------------------------------------- sets of tokens
-    // Tokens that stay and that `in` says yes to, into the first CTA's list (at most MOST).
-    auto collect = [&](auto &&in) {
+    // Tokens that stay and that `in` says yes to, into the first CTA's list (at most
+    // MOST).  `noted`: this CTA's candidates are in s.near, unless there are too many.
+    auto collect = [&](bool noted, auto &&in) {
         u64 *list = cl.map_shared_rank(s.list, 0);
         uint32_t *count = cl.map_shared_rank(&s.count, 0);
-        for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
-            uint32_t mask = 0;
-            Vec v;
-            {
-                v = *reinterpret_cast<const Vec *>(buf + i);
+        const int near = noted ? (int)s.near_count : INT_MAX;
+        if (near <= THREADS) {
+            const u64 entry = tid < near ? s.near[tid] : 0;
+            const bool yes = tid < near && in(Key<TL>::value((uint32_t)(entry >> 32)));
+            if (yes)
+                list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = entry;
+        } else {
+            for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
+                uint32_t mask = 0;
+                const Vec v = *reinterpret_cast<const Vec *>(buf + i);
                 if (to_float(greatest(v.v)) >= cut)
 #pragma unroll
                     for (int k = 0; k < VEC; k++) {
                         const float l = to_float(v.v[k]);
                         mask |= (uint32_t)(stays(l, id0 + i + k) && in(l)) << k;
                     }
-            }
-            if (mask) {
-                uint32_t at = atomicAdd(count, (uint32_t)__popc(mask));
+                if (mask) {
+                    uint32_t at = atomicAdd(count, (uint32_t)__popc(mask));
 #pragma unroll
-                for (int k = 0; k < VEC; k++)
-                    if (mask >> k & 1)
-                        list[min(at++, (uint32_t)MOST - 1)] = (u64)Key<TL>::of(v.v[k]) << 32 | (0xffffffffu - (uint32_t)(id0 + i + k));
+                    for (int k = 0; k < VEC; k++)
+                        if (mask >> k & 1)
+                            list[min(at++, (uint32_t)MOST - 1)] = (u64)Key<TL>::of(v.v[k]) << 32 | (0xffffffffu - (uint32_t)(id0 + i + k));
+                }
             }
         }
         cl.sync();
-    };
-    // Of the tokens in the first CTA's list, the last to stay where `above` stands
-    // before them and `want` is to be reached: `cut` and `last`, in every CTA.
-    auto cut_list = [&](bool by_weight, u64 above, u64 want) {
-        if (rank == 0) {
-            const int n = min((int)s.count, MOST);
-            sort(n);
-            const int p0 = 2 * tid;
-            u64 w[2], before;
-#pragma unroll
-            for (int i = 0; i < 2; i++)
-                w[i] = p0 + i >= n ? 0 : by_weight ? weigh(Key<TL>::value(key_of(s.sorted[p0 + i]))) : (u64)1;
-            scan(w[0], w[1], before);
-            before += above;
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                if (before < want && want <= before + w[i])
-                    for (int c = 0; c < CL; c++) {
-                        *cl.map_shared_rank(&s.cut, c) = key_of(s.sorted[p0 + i]);
-                        *cl.map_shared_rank(&s.last, c) = id_of(s.sorted[p0 + i]);
-                    }
-                before += w[i];
-            }
-            if (tid == 0)
-                s.count = 0;
-        }
-        cl.sync();
-        cut = Key<TL>::value(s.cut);
-        last = s.last;
     };
     // The id of tie number m (from 1) at `cut`, in the order of ids.
     auto locate = [&](u64 m) {
@@ -692,6 +727,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                         into(b, weigh(l));
                     else
                         atomicAdd(&h.lo[b], 1u);
+                    if (fresh) { // (noted for collect; counts only)
+                        const uint32_t at = atomicAdd(&s.near_count, 1u);
+                        if (at < THREADS)
+                            s.near[at] = (u64)Key<TL>::at_least(l) << 32 | (0xffffffffu - (uint32_t)id);
+                    }
                 }
             });
         }
@@ -810,24 +850,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                     break;
                 }
                 if (fresh && f.upto <= MOST) {
-                    collect([&](float l) {
+                    collect(!by_weight && fresh, [&](float l) {
                         const int q = place(l);
                         return q >= 0 && (uint32_t)q >> bits <= f.bin;
                     });
                     if (rank == 0) {
                         const int n = min((int)s.count, MOST);
-                        draw_few(n, by_weight ? n : min(top_k, n), by_weight ? want : 0);
+                        by_first(n, [&](auto one) { draw_few(one, n, by_weight ? n : min(top_k, n), by_weight ? want : 0); });
                     }
                     return true;
                 }
                 prefix = prefix << DIGIT | f.bin;
                 above = f.above;
                 if (f.inside <= MOST) {
-                    collect([&](float l) {
+                    collect(!by_weight && fresh, [&](float l) {
                         const int q = place(l);
                         return q >= 0 && (uint32_t)q >> bits == prefix;
                     });
-                    cut_list(by_weight, above, want);
+                    if (rank == 0) {
+                        const int n = min((int)s.count, MOST);
+                        by_first(n, [&](auto one) { cut_list(one, n, by_weight, above, want); });
+                        __syncthreads();
+                        if (tid == 0)
+                            s.count = 0;
+                    }
+                    cl.sync();
+                    cut = Key<TL>::value(s.cut);
+                    last = s.last;
                     return false;
                 }
             }
