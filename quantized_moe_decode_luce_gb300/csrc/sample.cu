@@ -157,11 +157,12 @@ struct Weigh {
     int sh;
     bool small;
     const uint2 *table; // 2^(31 - j / 256) as a whole number and as a float
-    __device__ __forceinline__ u64 operator()(float l) const
+    __device__ __forceinline__ u64 operator()(float l) const { return small ? of<true>(l) : of<false>(l); }
+    template <bool SMALL> __device__ __forceinline__ u64 of(float l) const
     {
         const float magic = 49152.0f; // steps of 2^-8 at 2^15
         float t, r;
-        if (!small) {
+        if constexpr (!SMALL) {
             t = fmaf(-l, c_hi, cM) + magic;
             r = fmaf(-l, c_hi, A1 - (t - magic)) + fmaf(-l, c_lo, A2);
         } else {
@@ -217,6 +218,7 @@ template <int THREADS> struct Shared {
     u64 warp[WARPS], part[64];
     u64 found[5];
     u64 sum[2];                  // (alternating with the histograms)
+    float edge[2];
     uint32_t wtop[WARPS], wbound[WARPS];
     uint32_t count, near_count, cut;
     int last;
@@ -339,24 +341,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     };
     auto add_up = [&](u64 v, u64 &before) {
         send(v);
-        u64 all = 0;
-        before = 0;
-        for (int c = 0; c < CL; c++) {
-            if (c == rank)
-                before = all;
-            all += s.exchange[phase][c];
-        }
-        return all;
+        const u64 x = lane < CL ? s.exchange[phase][lane] : 0, upto = warp_scan(x, lane);
+        before = __shfl_sync(0xffffffffu, upto - x, rank);
+        return __shfl_sync(0xffffffffu, upto, 31);
     };
     {
         uint32_t t = __reduce_max_sync(0xffffffffu, s.wtop[lane % WARPS]), b = __reduce_min_sync(0xffffffffu, s.wbound[lane % WARPS]);
         send((u64)t << 32 | b);
-        t = 0, b = 0xffffffffu;
-        for (int c = 0; c < CL; c++) {
-            t = max(t, (uint32_t)(s.exchange[phase][c] >> 32));
-            b = min(b, (uint32_t)s.exchange[phase][c]);
-        }
-        top = t, bound = b;
+        const u64 x = s.exchange[phase][lane % CL]; // (a power of two)
+        top = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32));
+        bound = __reduce_min_sync(0xffffffffu, (uint32_t)x);
     }
     if (top == 0xffffffffu || top <= Key<TL>::NONE) {
         if (rank == 0 && tid == 0) {
@@ -433,10 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (lane == 0)
             s.warp[warp] = v;
         __syncthreads();
-        u64 t = 0;
-        for (int i = 0; i < WARPS; i++)
-            t += s.warp[i];
-        return t;
+        return warp_add(lane < WARPS ? s.warp[lane] : 0);
     };
 
     // What stays: logits above `cut`, and of those at it the ids up to `last`.
@@ -524,14 +515,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         if (lane == 31)
             s.warp[warp] = upto;
         __syncthreads();
-        u64 total = 0;
-#pragma unroll
-        for (int i = 0; i < WARPS; i++) {
-            if (i < warp)
-                before += s.warp[i];
-            total += s.warp[i];
-        }
-        return total;
+        const u64 v = lane < WARPS ? s.warp[lane] : 0, sums = warp_scan(v, lane);
+        before += __shfl_sync(0xffffffffu, sums - v, warp);
+        return __shfl_sync(0xffffffffu, sums, 31);
     };
     // The draw from the n tokens of the list, of which the first `keep` and those that
     // reach a weight of `want` stay (0: top_p of theirs).
@@ -620,35 +606,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     };
 
     // -------------------------------------------------------------- sets of tokens
-    // Tokens that stay and that `in` says yes to, into the first CTA's list (at most
-    // MOST).  `noted`: this CTA's candidates are in s.near, unless there are too many.
-    auto collect = [&](bool noted, auto &&in) {
+    // Tokens that stay, of logits from `from` to below `to`, into the first CTA's list (at
+    // most MOST).  `noted`: this CTA's candidates are in s.near, unless there are too many.
+    auto collect = [&](bool noted, float from, float to) {
         u64 *list = cl.map_shared_rank(s.list, 0);
         uint32_t *count = cl.map_shared_rank(&s.count, 0);
         const int near = noted ? (int)s.near_count : INT_MAX;
         if (near <= THREADS) {
             const u64 entry = tid < near ? s.near[tid] : 0;
-            const bool yes = tid < near && in(Key<TL>::value((uint32_t)(entry >> 32)));
-            if (yes)
+            const float l = Key<TL>::value((uint32_t)(entry >> 32));
+            if (tid < near && l >= from && l < to)
                 list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = entry;
         } else {
-            for (int i = i0 + lane * VEC; i < i1; i += 32 * VEC) {
-                uint32_t mask = 0;
-                const Vec v = *reinterpret_cast<const Vec *>(buf + i);
-                if (to_float(greatest(v.v)) >= cut)
-#pragma unroll
-                    for (int k = 0; k < VEC; k++) {
-                        const float l = to_float(v.v[k]);
-                        mask |= (uint32_t)(stays(l, id0 + i + k) && in(l)) << k;
-                    }
-                if (mask) {
-                    uint32_t at = atomicAdd(count, (uint32_t)__popc(mask));
-#pragma unroll
-                    for (int k = 0; k < VEC; k++)
-                        if (mask >> k & 1)
-                            list[min(at++, (uint32_t)MOST - 1)] = (u64)Key<TL>::of(v.v[k]) << 32 | (0xffffffffu - (uint32_t)(id0 + i + k));
-                }
-            }
+            each(from, [&](float l, int id) {
+                if (l < to && (l > cut || id <= last))
+                    list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = (u64)Key<TL>::at_least(l) << 32 | (0xffffffffu - (uint32_t)id);
+            });
         }
         cl.sync();
     };
@@ -688,16 +661,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         return s.last;
     };
 
-    // A histogram over the tokens that stay (bin: a bin, or none below zero), and in
-    // it the bin at which what stands before it reaches `want`.  (fresh: and the weight
-    // of all of them, for want_of.)
+    // A histogram over the tokens that stay, of logits from `from` to below `to`, and in
+    // it the bin at which what stands before it reaches `want`.  (fresh: over all that stay,
+    // those of a bin below zero apart; and the weight of all, for want_of.)
     struct Found {
         uint32_t bin;
         u64 above, in; // before the bin, in it
         u64 total;     // in all bins
         uint32_t upto, inside; // tokens up to the bin's end, and in it, at most
     };
-    auto find = [&](bool by_weight, bool fresh, u64 above, auto &&want_of, auto &&bin, auto &&lightest) {
+    auto find = [&](bool by_weight, bool fresh, float from, float to, u64 above, auto &&want_of, auto &&bin, auto &&lightest) {
         level ^= 1;
         auto &h = s.hist[level];
         for (int i = tid; i < BINS; i += THREADS)
@@ -711,27 +684,44 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 atomicAdd(&h.hi[b], wh);
         };
         if (by_weight && fresh) {
-            every([&](float l, int id) {
-                const bool in = stays(l, id);
-                const u64 w = weigh(in ? l : cut);
-                sum += in ? w : 0;
-                const int b = bin(l);
-                if (in && b >= 0)
-                    into(b, w);
+            auto pass = [&](auto small, auto ties) {
+                every([&](float l, int id) {
+                    const bool in = decltype(ties)::value ? stays(l, id) : l >= cut;
+                    const u64 w = weigh.template of<decltype(small)::value>(in ? l : cut);
+                    sum += in ? w : 0;
+                    const int b = bin(l);
+                    if (in && b >= 0)
+                        into(b, w);
+                });
+            };
+            if (weigh.small)
+                pass(std::true_type(), std::true_type());
+            else if (last != INT_MAX)
+                pass(std::false_type(), std::true_type());
+            else
+                pass(std::false_type(), std::false_type());
+        } else if (fresh) { // (few, where the k-th is bounded well: noted, then counted)
+            each(from, [&](float l, int id) {
+                const uint32_t at = atomicAdd(&s.near_count, 1u);
+                if (at < THREADS)
+                    s.near[at] = (u64)Key<TL>::at_least(l) << 32 | (0xffffffffu - (uint32_t)id);
             });
+            __syncthreads();
+            const int near = (int)s.near_count;
+            if (near <= THREADS) {
+                if (tid < near)
+                    atomicAdd(&h.lo[bin(Key<TL>::value((uint32_t)(s.near[tid] >> 32)))], 1u);
+            } else {
+                each(from, [&](float l, int) { atomicAdd(&h.lo[bin(l)], 1u); });
+            }
         } else {
-            each(cut, [&](float l, int id) {
-                const int b = bin(l);
-                if (b >= 0 && (l > cut || id <= last)) {
+            each(from, [&](float l, int id) {
+                if (l < to && (l > cut || id <= last)) {
+                    const int b = bin(l);
                     if (by_weight)
                         into(b, weigh(l));
                     else
                         atomicAdd(&h.lo[b], 1u);
-                    if (fresh) { // (noted for collect; counts only)
-                        const uint32_t at = atomicAdd(&s.near_count, 1u);
-                        if (at < THREADS)
-                            s.near[at] = (u64)Key<TL>::at_least(l) << 32 | (0xffffffffu - (uint32_t)id);
-                    }
                 }
             });
         }
@@ -782,16 +772,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             s.part[warp] = n_warp;
         }
         __syncthreads();
-        u64 at = in_warp - all, total = 0;
-        uint32_t n_at = n_warp - count;
-#pragma unroll
-        for (int i = 0; i < WARPS; i++) {
-            if (i < warp) {
-                at += s.warp[i];
-                n_at += (uint32_t)s.part[i];
-            }
-            total += s.warp[i];
-        }
+        const u64 v = lane < WARPS ? s.warp[lane] : 0, sums = warp_scan(v, lane);
+        const uint32_t vn = lane < WARPS ? (uint32_t)s.part[lane] : 0, sums_n = warp_scan(vn, lane);
+        u64 at = in_warp - all + __shfl_sync(0xffffffffu, sums - v, warp);
+        const u64 total = __shfl_sync(0xffffffffu, sums, 31);
+        uint32_t n_at = n_warp - count + __shfl_sync(0xffffffffu, sums_n - vn, warp);
         const u64 want = want_of(sum);
         at += above;
 #pragma unroll
@@ -827,12 +812,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             auto over_end = [&](uint32_t stretch, int bits) {
                 return scale > 0.0f ? 1.01f * exp2f(fminf(octaves * ((float)stretch + 1.0f) * (float)(1 << bits) - (float)(31 + a.sh), 120.0f)) : 1.0f;
             };
+            // the smallest logits at a distance below q0 (from 1), and below q1 (0: none):
+            // two warps find them, 32 keys at a time
+            auto edges = [&](int q0, int q1, float &l0, float &l1) {
+                if (warp < 2) {
+                    const int q = warp ? q1 : q0;
+                    uint32_t lo = Key<TL>::at_least(cut), hi = top; // hi is near enough
+                    while (q > 0 && lo < hi) {
+                        const uint32_t step = (hi - lo + 31) / 32, k = lo + (uint32_t)lane * step;
+                        const int at = k < hi ? place(Key<TL>::value(k)) : 0;
+                        const int f = __ffs((int)__ballot_sync(0xffffffffu, at >= 0 && at < q)) - 1; // the first lane that is (none: hi)
+                        if (f >= 0)
+                            hi = min(hi, lo + (uint32_t)f * step);
+                        lo = f == 0 ? hi : min(hi, lo + (uint32_t)(f < 0 ? 31 : f - 1) * step + 1);
+                    }
+                    if (lane == 0)
+                        s.edge[warp] = q > 0 ? Key<TL>::value(hi) : INFINITY;
+                }
+                __syncthreads();
+                l0 = s.edge[0], l1 = s.edge[1]; // (written again behind find's barriers)
+            };
             uint32_t prefix = 0;
             u64 above = 0;
+            float from = cut, to = INFINITY;
             bool again = false;
             for (int bits = QBITS - DIGIT; bits >= 0; bits -= DIGIT) {
                 const bool fresh = bits == QBITS - DIGIT;
-                const Found f = find(by_weight, fresh, above,
+                const Found f = find(by_weight, fresh, from, to, above,
                                      [&](u64 sum) {
                                          if (fresh && by_weight && want == 0)
                                              want = top_p > 0.0f ? max(share(top_p, sum, true), (u64)1) : (u64)1;
@@ -840,7 +846,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                                      },
                                      [&](float l) {
                                          const int q = place(l);
-                                         return q < 0 || (!fresh && (uint32_t)q >> (bits + DIGIT) != prefix) ? -1 : q >> bits & (BINS - 1);
+                                         return q < 0 ? -1 : q >> bits & (BINS - 1);
                                      },
                                      [&](uint32_t b) { return over_end(prefix << DIGIT | b, bits); });
                 if (fresh && want > f.total) {
@@ -849,24 +855,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                     again = all_in = true;
                     break;
                 }
+                prefix = prefix << DIGIT | f.bin;
+                above = f.above;
+                edges((int)((prefix + 1) << bits), (int)(prefix << bits), from, to);
                 if (fresh && f.upto <= MOST) {
-                    collect(!by_weight && fresh, [&](float l) {
-                        const int q = place(l);
-                        return q >= 0 && (uint32_t)q >> bits <= f.bin;
-                    });
+                    collect(!by_weight, from, INFINITY);
                     if (rank == 0) {
                         const int n = min((int)s.count, MOST);
                         by_first(n, [&](auto one) { draw_few(one, n, by_weight ? n : min(top_k, n), by_weight ? want : 0); });
                     }
                     return true;
                 }
-                prefix = prefix << DIGIT | f.bin;
-                above = f.above;
                 if (f.inside <= MOST) {
-                    collect(!by_weight && fresh, [&](float l) {
-                        const int q = place(l);
-                        return q >= 0 && (uint32_t)q >> bits == prefix;
-                    });
+                    collect(!by_weight && fresh, from, to);
                     if (rank == 0) {
                         const int n = min((int)s.count, MOST);
                         by_first(n, [&](auto one) { cut_list(one, n, by_weight, above, want); });
@@ -883,14 +884,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             if (again)
                 continue;
             // many logits of one distance: by their bits, then by id
-            uint32_t hi = top, lo = Key<TL>::at_least(cut);
+            uint32_t hi = to < INFINITY ? Key<TL>::at_least(to) - 1 : top, lo = Key<TL>::at_least(from);
             while (true) {
                 const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
-                const Found f = find(by_weight, false, above, [&](u64) { return want; },
-                                     [&](float l) {
-                                         const uint32_t key = Key<TL>::at_least(l);
-                                         return key - lo <= hi - lo && (uint32_t)place(l) == prefix ? (int)((hi - key) >> shift) : -1;
-                                     },
+                const Found f = find(by_weight, false, Key<TL>::value(lo), hi == top ? INFINITY : Key<TL>::value(hi + 1), above,
+                                     [&](u64) { return want; }, [&](float l) { return (int)((hi - Key<TL>::at_least(l)) >> shift); },
                                      [&](uint32_t) { return 1.0f; });
                 above = f.above;
                 hi -= f.bin << shift;
@@ -924,15 +922,21 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         return w >= least ? w : 0;
     };
     u64 mine = 0, before;
-    auto add = [&](float l, int id) {
-        const bool in = stays(l, id);
-        const u64 w = weigh(in ? l : cut);
-        mine += in && w >= least ? w : 0;
+    auto pass = [&](auto small) {
+        auto add = [&](float l, int id) {
+            const bool in = stays(l, id);
+            const u64 w = weigh.template of<decltype(small)::value>(in ? l : cut);
+            mine += in && w >= least ? w : 0;
+        };
+        if (by_k || by_p)
+            each(cut, add);
+        else
+            every(add);
     };
-    if (by_k || by_p)
-        each(cut, add);
+    if (weigh.small)
+        pass(std::true_type());
     else
-        every(add);
+        pass(std::false_type());
     const u64 here = block_sum(mine);
     const u64 total = add_up(here, before);
     const u64 target = u > 0.0f ? (u < 1.0f ? share(u, total, false) : total - 1) : 0;
