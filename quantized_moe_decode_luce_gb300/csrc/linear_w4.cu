@@ -5,25 +5,27 @@
 //   out[t][n] = (sum_g s[n][g] * S[t][n][g]) (* x_scale[t]) (+ bias[n]),
 //   S[t][n][g] = sum_{k in g} x[t][k] (q[n][k] - z[n][g])   (z = 8 without zero points)
 //
-// Operands.  The four bits of a code at the low end of an fp16 are the
-// subnormal number q 2^-24, and one place of four bits higher 16 q 2^-24: a
-// code becomes a tensor-core operand by a mask alone.  Products are exact, the
-// factors 2^24 and 16 are put back in fp32 and in the activations, and the zero
-// point is taken off a group's sum.
-// The activations go in as fp16 too, a chunk of 128 of them (a row's packed
+// Operands.  The activations go in as fp16, a chunk of 128 of them (a row's packed
 // codes are kept in such chunks) brought to one size by a power of two that
 // multiplies the chunk's sums again in fp32:
-//   whole numbers   int8 codes as they are; fp32, bf16 and fp16 values, where x
-//     or out is fp32, as two columns of twelve bits each, the second 2^-12 of the
-//     first.  What they leave is at most 2^-24 of the chunk's largest value, and
-//     a group's sums (below 2^24) are exact: the tensor cores cut off what they
-//     add, which would cost several of fp32's bits otherwise.
-//   fp16 numbers    bf16 and fp16 values for 16-bit outputs, one column: exact, but
-//     for values so far below the chunk's largest that they end in fp16's
-//     subnormal steps (off by at most 2^-35 of it); the sums are good to about
-//     2^-19, against the outputs' 2^-9 and 2^-12.
+//   whole numbers   int8 codes as they are; others as two columns of twelve bits
+//     each, the second 2^-12 of the first.  What they leave is at most 2^-23 of
+//     the chunk's largest value, and a group's sums (below 2^24) are exact: the
+//     tensor cores cut off what they add.
+//   fp16 numbers    bf16 and fp16 values for 16-bit outputs, where two columns a
+//     token would not fit one MMA: exact, but for values so far below the
+//     chunk's largest that they end in fp16's subnormal steps (off by at most
+//     2^-39 of it).
+// With whole numbers a code becomes an operand by a mask alone: its four bits at the
+// low end of an fp16 are the subnormal number q 2^-24, and four places higher
+// 16 q 2^-24.  The factors 2^24 and 16 are put back in fp32 and in the
+// activations, and the zero point is taken off a group's sum.  With fp16 numbers
+// that would lose digits (the sums are aligned to the largest exponent, and
+// subnormal ones are up to ten bits below theirs), so the codes become normal
+// numbers, less their zero points: four instructions more for eight of them.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "w4.cuh"
 
@@ -67,8 +69,8 @@ __device__ __forceinline__ void load8(const W4Args &a, int t, int k, float (&v)[
 // Activations k .. k + 7 of token t (zero unless live) -> operands of one or two
 // columns, the factors of the chunk's sums, and the sum of the group's values
 // (GPC groups to a chunk, 16 / GPC lanes each) in the units of those sums, times
-// eight.  Values 2, 3, 6 and 7 of eight meet codes that count sixteenfold.  A NaN
-// or an infinity stays one, and so do the sums of its group.
+// eight.  As whole numbers values 2, 3, 6 and 7 of eight meet codes that count
+// sixteenfold.  A NaN or an infinity stays one, and so do the sums of its group.
 template <int GPC>
 __device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool live, uint4 (&o)[2], float (&factor)[2], float (&sum)[2])
 {
@@ -101,15 +103,15 @@ __device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool liv
 #pragma unroll
     for (int d = 1; d < 16; d *= 2)
         most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-    const uint32_t e = max(__float_as_uint(most) >> 23, 15u);                 // 2^(e - 127) <= most < 2^(e - 126)
+    const uint32_t e = max(__float_as_uint(most) >> 23, a.whole ? 15u : 29u); // 2^(e - 127) <= most < 2^(e - 126)
     const float up = __uint_as_float(((a.whole ? 264u : 268u) - e) << 23);    // to below 2^11, or 2^15
-    factor[0] = __uint_as_float((a.whole ? e : e - 4u) << 23);                // 2^24 / (up UNIT)
+    factor[0] = __uint_as_float((a.whole ? e : e - 28u) << 23);               // 2^24 / (up UNIT), 1 / (up UNIT)
     factor[1] = __uint_as_float((e - 12u) << 23);
     uint32_t w[2][4];
     sum[0] = sum[1] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        const float k16 = i & 2 ? 0.0625f : 1.0f, k1 = i & 2 ? 16.0f : 1.0f;
+        const float k16 = a.whole && (i & 2) ? 0.0625f : 1.0f, k1 = a.whole && (i & 2) ? 16.0f : 1.0f;
         const float x0 = v[i] * up, x1 = v[i + 1] * up;
         const float p0 = a.whole ? rintf(x0) : x0, p1 = a.whole ? rintf(x1) : x1;
         const __half2 h = __floats2half2_rn(p0 * k16, p1 * k16), r = __floats2half2_rn(rintf((x0 - p0) * 4096.0f) * k16, rintf((x1 - p1) * 4096.0f) * k16);
@@ -137,7 +139,8 @@ __device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool liv
 //
 // What bounds it is the weights' way from HBM, for small matrices the latency
 // of getting there, and close behind both the instructions: a chunk of 16 rows
-// takes a warp 8 MMAs, 4 reads of activations and 40 instructions for its codes.
+// takes a warp 8 MMAs, 4 reads of activations and 40 instructions for its codes
+// (72 for normal numbers).
 // So everything else is done once for a unit of U chunks: a warp keeps a unit's codes in registers, requests each chunk of its
 // next one as soon as it has used its place, and the wk warps of a row group
 // take every wk-th unit of a row and join their sums through shared memory.
@@ -164,6 +167,18 @@ __device__ __forceinline__ void mma(float (&d)[4], bool first, uint32_t a0, uint
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Masked codes (of a word's four pairs) less their zero point, as normal fp16
+// numbers, exact: under the exponent of 1024 a code is 1024 + q, or 1024 + 16 q.
+__device__ __forceinline__ void normal(uint32_t (&h)[4], uint32_t zero)
+{
+    const uint32_t zl = (0x6400u + zero) * 0x10001u, zh = (0xD400u + 16u * zero) * 0x10001u; // 1024 + z, -(64 + z)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(h[i]) : "r"(h[i] | 0x64006400u), "r"(zl));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[i + 1]) : "r"(h[i + 1] | 0x64006400u), "r"(0x2C002C00u), "r"(zh)); // a sixteenth
+    }
+}
+
 // GPC groups of a row in a chunk: their scales (16 bits each) and zero points
 // (8 bits each), those beyond the row's G as zero.
 template <int GPC> struct Groups {
@@ -209,7 +224,8 @@ __device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int
 // Warps of a CTA at most: those whose registers need no spilling.
 template <int NT, int GPC, bool ZEROS, int U> constexpr int S_MOST = NT == 1 && (U == 2 || (GPC == 1 && !ZEROS)) ? S_WARPS : 16;
 
-template <int NT, int GPC, bool ZEROS, int U>
+// WHOLE: activations as whole numbers, codes as they are.
+template <int NT, int GPC, bool ZEROS, int U, bool WHOLE>
 __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
     k_linear_w4_stream(const W4Args a, int wk, int pitch, int steps, bool whole)
 {
@@ -312,28 +328,40 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
 #pragma unroll
                     for (int gi = 0; gi < GPC; gi++) {
                         float sum[NT][4];
+                        const uint32_t zero0 = ZEROS ? (g[u][0].z >> (8 * gi)) & 15u : 8u, zero1 = ZEROS ? (g[u][1].z >> (8 * gi)) & 15u : 8u;
                         // (eight times the activations' sums are known: the zero point counts in eighths)
-                        const float z0 = ZEROS ? (float)((g[u][0].z >> (8 * gi)) & 15u) * -0.125f : -1.0f;
-                        const float z1 = ZEROS ? (float)((g[u][1].z >> (8 * gi)) & 15u) * -0.125f : -1.0f;
+                        const float z0 = ZEROS ? (float)zero0 * -0.125f : -1.0f, z1 = ZEROS ? (float)zero1 * -0.125f : -1.0f;
 #pragma unroll
                         for (int q = gi * JG; q < (gi + 1) * JG; q++) {
                             const uint32_t w0 = q == 0 ? w[u][0].x : q == 1 ? w[u][0].y : q == 2 ? w[u][0].z : w[u][0].w;
                             const uint32_t w1 = q == 0 ? w[u][1].x : q == 1 ? w[u][1].y : q == 2 ? w[u][1].z : w[u][1].w;
-                            const uint32_t v0 = w0 >> 8, v1 = w1 >> 8;
+                            uint32_t h0[4] = {w0 & LO, w0 & HI, (w0 >> 8) & LO, (w0 >> 8) & HI};
+                            uint32_t h1[4] = {w1 & LO, w1 & HI, (w1 >> 8) & LO, (w1 >> 8) & HI};
+                            if constexpr (!WHOLE) {
+                                normal(h0, zero0);
+                                normal(h1, zero1);
+                            }
 #pragma unroll
                             for (int n = 0; n < NT; n++) {
                                 const uint4 b = *reinterpret_cast<const uint4 *>(xcol[n] + c0 * (2 * CHUNK) + u * (2 * CHUNK) + q * 64);
-                                mma(sum[n], q == gi * JG, w0 & LO, w1 & LO, w0 & HI, w1 & HI, b.x, b.y);
-                                mma(sum[n], false, v0 & LO, v1 & LO, v0 & HI, v1 & HI, b.z, b.w);
+                                mma(sum[n], q == gi * JG, h0[0], h1[0], h0[1], h1[1], b.x, b.y);
+                                mma(sum[n], false, h0[2], h1[2], h0[3], h1[3], b.z, b.w);
                             }
                         }
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
                             const float4 f = *reinterpret_cast<const float4 *>(my_info + ((c0 + u) * GPC + gi) * COLS + 8 * n);
-                            acc[n][0] = fmaf(sc[0][gi], fmaf(sum[n][0], f.x, z0 * f.y), acc[n][0]);
-                            acc[n][1] = fmaf(sc[0][gi], fmaf(sum[n][1], f.z, z0 * f.w), acc[n][1]);
-                            acc[n][2] = fmaf(sc[1][gi], fmaf(sum[n][2], f.x, z1 * f.y), acc[n][2]);
-                            acc[n][3] = fmaf(sc[1][gi], fmaf(sum[n][3], f.z, z1 * f.w), acc[n][3]);
+                            if constexpr (WHOLE) {
+                                acc[n][0] = fmaf(sc[0][gi], fmaf(sum[n][0], f.x, z0 * f.y), acc[n][0]);
+                                acc[n][1] = fmaf(sc[0][gi], fmaf(sum[n][1], f.z, z0 * f.w), acc[n][1]);
+                                acc[n][2] = fmaf(sc[1][gi], fmaf(sum[n][2], f.x, z1 * f.y), acc[n][2]);
+                                acc[n][3] = fmaf(sc[1][gi], fmaf(sum[n][3], f.z, z1 * f.w), acc[n][3]);
+                            } else {
+                                acc[n][0] = fmaf(sc[0][gi] * f.x, sum[n][0], acc[n][0]);
+                                acc[n][1] = fmaf(sc[0][gi] * f.z, sum[n][1], acc[n][1]);
+                                acc[n][2] = fmaf(sc[1][gi] * f.x, sum[n][2], acc[n][2]);
+                                acc[n][3] = fmaf(sc[1][gi] * f.z, sum[n][3], acc[n][3]);
+                            }
                         }
                     }
                 }
@@ -386,10 +414,10 @@ size_t s_smem(const W4Args &a, int cols, int gpc, int warps)
     return (size_t)cols * s_pitch(a.K) + chunks * gpc * padded * 8 + 2 * warps * padded * PART * 4;
 }
 
-template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4Args &a, cudaStream_t stream)
+template <int NT, int GPC, bool ZEROS, int U, bool WHOLE> luce_status launch_stream(const W4Args &a, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
-    const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U>;
+    const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U, WHOLE>;
     const int chunks = (a.K + CHUNK - 1) / CHUNK;
     int wk = 1;
     while (wk < S_SPLIT && wk * U < chunks)
@@ -412,7 +440,7 @@ template <int NT, int GPC, bool ZEROS, int U> luce_status launch_stream(const W4
 }
 
 // Whether the stream serves a call.  Each of its CTAs prepares the activations
-// for itself, 0.022 us a column and chunk (int8 half of that); the tensor cores
+// for itself, 0.022 us a token and chunk (int8 half of that); the tensor cores
 // are later to start, and read the codes of large matrices more slowly: 4.2 us
 // at 4096 x 4096, 5.3 at 4096 x 14336, 12.5 at 28672 x 4096, 28 at 129280 x 4096.
 // (Four tokens, bf16, groups of 128: 4096 x 4096 8.2 us, tensor cores 9.7;
@@ -423,16 +451,23 @@ bool stream_serves(const W4Args &a, int gpc)
     const int64_t chunks = (a.K + CHUNK - 1) / CHUNK, cols = (int64_t)a.T * a.parts;
     if (cols > S_COLS || s_smem(a, (int)cols, gpc, cols > 8 ? 16 : S_WARPS) > S_SMEM)
         return false;
-    return cols * chunks / (a.x_dtype == LUCE_I8 ? 2 : 1) <= 140 + 4 * ((int64_t)a.N * chunks / (128 * 152));
+    return (int64_t)a.T * chunks / (a.x_dtype == LUCE_I8 ? 2 : 1) <= 140 + 4 * ((int64_t)a.N * chunks / (128 * 152));
 }
 
 template <int GPC, bool ZEROS> luce_status run_stream(const W4Args &a, cudaStream_t stream)
 {
     // units of two chunks where there are not enough of four for all SMs
     const bool few = (int64_t)a.N * ((a.K + CHUNK - 1) / CHUNK) < (int64_t)1 << 19;
+    auto run = [&](auto nt, auto whole) {
+        constexpr int NT = decltype(nt)::value;
+        constexpr bool WHOLE = decltype(whole)::value;
+        return few ? launch_stream<NT, GPC, ZEROS, 2, WHOLE>(a, stream) : launch_stream<NT, GPC, ZEROS, 4, WHOLE>(a, stream);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     if (a.T * a.parts <= 8)
-        return few ? launch_stream<1, GPC, ZEROS, 2>(a, stream) : launch_stream<1, GPC, ZEROS, 4>(a, stream);
-    return few ? launch_stream<2, GPC, ZEROS, 2>(a, stream) : launch_stream<2, GPC, ZEROS, 4>(a, stream);
+        return a.whole ? run(One(), std::true_type()) : run(One(), std::false_type());
+    return a.whole ? run(Two(), std::true_type()) : run(Two(), std::false_type());
 }
 
 luce_status run_groups(const W4Args &a, int group, cudaStream_t stream)
@@ -477,7 +512,7 @@ extern "C" luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t
         (zeros && overlap(out, no, zeros, (size_t)N * G)) || (bias && overlap(out, no, bias, (size_t)N * 4)) ||
         (x_scale && overlap(out, no, x_scale, (size_t)T * 4)))
         return LUCE_ERR_INVALID_ARG;
-    const bool whole = x_dtype == LUCE_I8 || x_dtype == LUCE_F32 || out_dtype == LUCE_F32;
+    const bool whole = x_dtype == LUCE_I8 || x_dtype == LUCE_F32 || out_dtype == LUCE_F32 || 2 * T <= 8;
     const W4Args a{x, x_dtype, whole, whole && x_dtype != LUCE_I8 ? 2 : 1, ld_x, x_scale, wq, w_scale, scale_dtype == LUCE_BF16, zeros, bias, T, N, K, G, out, out_dtype, ld_out};
     cudaStream_t st = luce_host::as_stream(stream);
     return stream_serves(a, CHUNK / group) ? run_groups(a, group, st) : tc_product(a, group, st);

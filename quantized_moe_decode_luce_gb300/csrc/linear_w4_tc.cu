@@ -8,10 +8,7 @@
 // the epilogue multiplies by the channel's scale and adds in fp32 registers.
 // What a chunk needs of each kind of activations:
 //   bf16, and fp16 for 16-bit outputs   nothing: TMA puts them where B is.
-//     With bf16 the codes become bf16 (placed under the exponent of 128, less 128 +
-//     z), with fp16 subnormal fp16 numbers, (q - z) 2^-24.  Sums of eight-bit by
-//     four-bit numbers hardly lose anything to the tensor cores' cutting off;
-//     those of fp16 numbers are good to about 2^-19.
+//     The codes less their zero points become numbers of the same type.
 //   int8                                converted to fp16, exact sums.
 //   fp32, and fp16 for fp32 outputs     two columns of whole numbers and a
 //     factor per chunk (see linear_w4.cu), exact sums.
@@ -237,8 +234,9 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// The eight codes of a word less z, in their order: bf16 numbers, or fp16
-// numbers times 2^-24.  All exact.
+// The eight codes of a word less z, in their order, exact.  A code placed under
+// the exponent of 128 (bf16) or 1024 (fp16) is 128 + q or 1024 + q; four places
+// higher in an fp16 it counts sixteenfold.
 template <bool BF> __device__ __forceinline__ void centred(uint32_t w, uint32_t z, uint32_t *h)
 {
     if constexpr (BF) {
@@ -247,11 +245,11 @@ template <bool BF> __device__ __forceinline__ void centred(uint32_t w, uint32_t 
         for (int i = 0; i < 4; i++)
             h[i] = sub_bf16x2(and_or(w >> (4 * i), LO, 0x43004300u), zz);
     } else {
-        const uint32_t zz = z * 0x10001u, w8 = w >> 8; // z 2^-24
-        h[0] = sub_f16x2(w & LO, zz);
-        h[1] = fma_f16x2(w & HI, 0x2C002C00u, zz ^ 0x80008000u); // a sixteenth
-        h[2] = sub_f16x2(w8 & LO, zz);
-        h[3] = fma_f16x2(w8 & HI, 0x2C002C00u, zz ^ 0x80008000u);
+        const uint32_t zl = (0x6400u + z) * 0x10001u, zh = (0xD400u + 16u * z) * 0x10001u, w8 = w >> 8; // 1024 + z, -(64 + z)
+        h[0] = sub_f16x2(and_or(w, LO, 0x64006400u), zl);
+        h[1] = fma_f16x2(and_or(w, HI, 0x64006400u), 0x2C002C00u, zh); // a sixteenth
+        h[2] = sub_f16x2(and_or(w8, LO, 0x64006400u), zl);
+        h[3] = fma_f16x2(and_or(w8, HI, 0x64006400u), 0x2C002C00u, zh);
     }
 }
 
@@ -275,8 +273,7 @@ __device__ __forceinline__ void codes16(const uint4 &v, uint4 (&h)[2])
 __device__ __forceinline__ float nearest(float v) { return __fadd_rn(__fadd_rn(v, 12582912.0f), -12582912.0f); }
 
 // Four values of a chunk that a warp holds -> two columns of whole numbers of
-// twelve bits, the second 2^-12 of the first, and the factor of the chunk's
-// sums (of 2^-24 q, to units of 1 / UNIT).
+// twelve bits, the second 2^-12 of the first, and the factor of the chunk's sums.
 __device__ __forceinline__ float whole4(const float4 &v, uint2 &o0, uint2 &o1)
 {
     const uint32_t most = __reduce_max_sync(0xffffffffu, max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
@@ -293,7 +290,7 @@ __device__ __forceinline__ float whole4(const float4 &v, uint2 &o0, uint2 &o1)
     const __half2 h[4] = {__floats2half2_rn(p[0], p[1]), __floats2half2_rn(p[2], p[3]), __floats2half2_rn(r[0], r[1]), __floats2half2_rn(r[2], r[3])};
     o0 = make_uint2(*reinterpret_cast<const uint32_t *>(&h[0]), *reinterpret_cast<const uint32_t *>(&h[1]));
     o1 = make_uint2(*reinterpret_cast<const uint32_t *>(&h[2]), *reinterpret_cast<const uint32_t *>(&h[3]));
-    return __uint_as_float(e << 23);
+    return __uint_as_float((e - 10u) << 23); // 2^(e - 137)
 }
 
 // The scales (16 bits each) and zero points (8 bits each) of a row's groups in
@@ -697,7 +694,6 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
             }
             if (!ok)
                 break;
-            constexpr float BACK = MODE == BF16 ? 1.0f : MODE == WHOLE ? UNIT : 16777216.0f;
             const int nt = min(t.tokens, t.a.T - token0);
             if (t.sk > 1) { // (one tile per cluster) the sums, where the stages were
 #pragma unroll
@@ -706,7 +702,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
                     for (int j = 0; j < BT; j++) {
                         const int tok = (2 * i + e) * BT + j;
                         if (tok < nt)
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sm + (uint32_t)(tok * PITCH + row) * 4u), "f"(acc[i][j] * BACK) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(sm + (uint32_t)(tok * PITCH + row) * 4u), "f"(acc[i][j]) : "memory");
                     }
             } else {
                 const float bn = live && t.a.bias ? t.a.bias[chan] : 0.0f;
@@ -716,7 +712,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
                     for (int j = 0; j < BT; j++) {
                         const int tok = (2 * i + e) * BT + j;
                         if (tok < nt && live) {
-                            float v = acc[i][j] * BACK;
+                            float v = acc[i][j];
                             if (MODE == I8)
                                 v = __fmul_rn(v, t.a.xs[token0 + tok]);
                             if (t.a.bias)
@@ -815,7 +811,7 @@ bool map_rows(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_
 
 Mode mode_of(const W4Args &a)
 {
-    return a.x_dtype == LUCE_I8 ? I8 : a.x_dtype == LUCE_BF16 ? BF16 : a.x_dtype == LUCE_F16 && !a.whole ? F16 : WHOLE;
+    return a.x_dtype == LUCE_I8 ? I8 : a.x_dtype == LUCE_BF16 ? BF16 : a.x_dtype == LUCE_F16 && a.out_dtype != LUCE_F32 ? F16 : WHOLE;
 }
 
 template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStream_t stream)
