@@ -116,6 +116,7 @@ def _load_call_module(L) -> None:
         return
     module.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
         "luce_quantize_i8", "luce_rmsnorm_i8", "luce_add_rmsnorm_i8", "luce_linear_i8", "luce_logits_process")))
+    module.bind_more(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in ("luce_linear_w4", "luce_sample")))
     _fast = module
 
 
@@ -534,6 +535,10 @@ def luce_linear_w4(x, x_scale, wq, scale, zeros, group: int, bias, out, stream=N
     """x [T, K] fp32, bf16, fp16 (x_scale None), or int8 with x_scale [T] fp32; wq, scale, zeros (or None) as
     luce_quantize_w4 leaves them; bias [N] fp32 or None -> out [T, N] fp32, bf16 or fp16.  The rows of x and out
     may be apart (slices of wider rows)."""
+    if stream is None and _fast is not None:
+        status = _fast.linear_w4(x, x_scale, wq, scale, zeros, group, bias, out)
+        if status >= 0:
+            return _check("luce_linear_w4", status)
     T, K, dev = _matrix(x, "x")
     N, G = _matrix(wq, "wq")[0], _groups(K, group)
     xp, ldx = _rows(x, _XS, (T, K), dev, "x")
@@ -552,6 +557,10 @@ def luce_sample(logits, u, idx, prob=None, temperature=None, top_k=None, top_p=N
     """logits [R, V] fp32, bf16 or fp16 (rows may be apart) -> idx [R] int32, a token per row drawn with u [R] fp32 in
     [0, 1), and prob [R] fp32 (or None), its probability among those left by top_k [R] int32, top_p and min_p
     [R] fp32 at temperature [R] fp32.  Each of the four may be left out."""
+    if stream is None and _fast is not None:
+        status = _fast.sample(logits, u, idx, prob, temperature, top_k, top_p, min_p)
+        if status >= 0:
+            return _check("luce_sample", status)
     R, V, dev = _matrix(logits, "logits")
     lp, ld = _rows(logits, _FLOATS, (R, V), dev, "logits")
 

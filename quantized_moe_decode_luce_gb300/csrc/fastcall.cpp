@@ -1,4 +1,4 @@
-// fastcall.cpp -- the common call of the int8 decode head's bindings in one
+// fastcall.cpp -- the common call of the decode head's bindings in one
 // step: tensors checked, device and stream looked up and the library's C
 // function called from here instead of from Python (a call's overhead from 6 to 12 us to
 // 3 us; the kernels of one token take 2 to 4).
@@ -28,6 +28,8 @@ decltype(&luce_rmsnorm_i8) f_rmsnorm;
 decltype(&luce_add_rmsnorm_i8) f_add_rmsnorm;
 decltype(&luce_linear_i8) f_linear;
 decltype(&luce_logits_process) f_logits;
+decltype(&luce_linear_w4) f_linear_w4;
+decltype(&luce_sample) f_sample;
 
 // The arguments of one call: `ok` turns false at the first that is not the common kind.
 struct Args {
@@ -270,7 +272,61 @@ PyObject *logits_process(PyObject *, PyObject *const *p, Py_ssize_t n)
     });
 }
 
-// bind(addresses): the library's functions, in the order of the pointers above
+// x, x_scale, wq, scale, zeros, group, bias, out
+PyObject *linear_w4(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return result([&] {
+        if (n != 8 || !f_linear_w4 || !PyLong_Check(p[5]))
+            return -1;
+        const long group = PyLong_AsLong(p[5]);
+        if (group != 32 && group != 64 && group != 128) {
+            PyErr_Clear(); // (of a number beyond a long)
+            return -1;
+        }
+        Args a;
+        const at::Tensor *x = a.tensor(p[0], 2), *w = a.tensor(p[2], 2), *s = a.tensor(p[3], 2), *o = a.tensor(p[7], 2);
+        const int64_t T = a.size(x, 0), K = a.size(x, 1), N = a.size(w, 0), G = (K + group - 1) / group;
+        int64_t ldx = 0, ldo = 0;
+        a.ok = a.ok && o->size(0) == T && o->size(1) == N;
+        const bool i8 = a.ok && x->scalar_type() == ScalarType::Char;
+        const luce_dtype xt = i8 ? LUCE_I8 : a.dtype(x), st = a.dtype(s), ot = a.dtype(o);
+        a.ok = a.ok && st != LUCE_F32 && i8 == (p[1] != Py_None);
+        void *xp = a.rows(x, ldx), *out = a.rows(o, ldo), *xs = a.data_or_none(p[1], ScalarType::Float, T),
+             *wq = a.data(p[2], ScalarType::Byte, N, (K + 127) / 128 * 64),
+             *ws = a.data(p[3], st == LUCE_F16 ? ScalarType::Half : ScalarType::BFloat16, N, G),
+             *z = a.data_or_none(p[4], ScalarType::Byte, N, G), *b = a.data_or_none(p[6], ScalarType::Float, N);
+        const int t = a.small(T), nn = a.small(N), k = a.small(K);
+        void *stream = a.stream();
+        return a.ok ? unlocked(f_linear_w4, (const void *)xp, xt, ldx, (const float *)xs, (const uint8_t *)wq, (const void *)ws, st,
+                               (const uint8_t *)z, (int)group, (const float *)b, t, nn, k, out, ot, ldo, stream)
+                    : -1;
+    });
+}
+
+// logits, u, idx, prob, temperature, top_k, top_p, min_p
+PyObject *sample(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    return result([&] {
+        if (n != 8 || !f_sample)
+            return -1;
+        Args a;
+        const at::Tensor *l = a.tensor(p[0], 2);
+        const int64_t R = a.size(l, 0), V = a.size(l, 1);
+        int64_t ld = 0;
+        const luce_dtype dt = a.dtype(l);
+        void *lp = a.rows(l, ld), *u = a.data(p[1], ScalarType::Float, R), *idx = a.data(p[2], ScalarType::Int, R),
+             *prob = a.data_or_none(p[3], ScalarType::Float, R), *t = a.data_or_none(p[4], ScalarType::Float, R),
+             *k = a.data_or_none(p[5], ScalarType::Int, R), *tp = a.data_or_none(p[6], ScalarType::Float, R),
+             *mp = a.data_or_none(p[7], ScalarType::Float, R);
+        const int r = a.small(R);
+        void *stream = a.stream();
+        return a.ok ? unlocked(f_sample, (const void *)lp, dt, r, V, ld, (const float *)u, (const float *)t, (const int32_t *)k,
+                               (const float *)tp, (const float *)mp, (int32_t *)idx, (float *)prob, stream)
+                    : -1;
+    });
+}
+
+// bind(addresses): the library's functions, in the order of the pointers above; bind_more: the last two
 PyObject *bind(PyObject *, PyObject *const *p, Py_ssize_t n)
 {
     if (n != 5) {
@@ -294,9 +350,30 @@ PyObject *bind(PyObject *, PyObject *const *p, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+PyObject *bind_more(PyObject *, PyObject *const *p, Py_ssize_t n)
+{
+    if (n != 2) {
+        PyErr_SetString(PyExc_TypeError, "bind_more takes two addresses");
+        return nullptr;
+    }
+    void *at[2];
+    for (int i = 0; i < 2; i++) {
+        at[i] = PyLong_AsVoidPtr(p[i]);
+        if (!at[i]) {
+            if (!PyErr_Occurred())
+                PyErr_SetString(PyExc_ValueError, "bind_more takes addresses that are not null");
+            return nullptr;
+        }
+    }
+    f_linear_w4 = reinterpret_cast<decltype(f_linear_w4)>(at[0]);
+    f_sample = reinterpret_cast<decltype(f_sample)>(at[1]);
+    Py_RETURN_NONE;
+}
+
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),      METHOD(quantize_i8),    METHOD(rmsnorm_i8), METHOD(add_rmsnorm_i8),
-                         METHOD(linear_i8), METHOD(logits_process), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(linear_i8), METHOD(logits_process), METHOD(bind_more),  METHOD(linear_w4),
+                         METHOD(sample),    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "luce_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 } // namespace
