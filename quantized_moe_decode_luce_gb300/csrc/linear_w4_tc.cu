@@ -54,14 +54,22 @@ constexpr int STAGE = RM * 128;          // bytes of a stage of codes: two chunk
 constexpr int NS_MAX = 12, XS = 2, RS = 2, DS_MAX = 8, FR = 32;
 constexpr int NB_MAX = 96;               // columns of a tile
 constexpr int SK_MAX = 8;                // CTAs of one cluster at most
-constexpr int W_WARP = 0, MMA_WARP = 1, X_WARP = 2, CONV_WARP0 = 4, B_WARP0 = 12, EPI_WARP0 = 16, WARPS = 24;
-constexpr int THREADS = WARPS * 32, EPI_THREADS = THREADS - EPI_WARP0 * 32;
+constexpr int W_WARP = 0, MMA_WARP = 1, X_WARP = 2, CONV_WARP0 = 4;
+constexpr int EPI_THREADS = 256;
 constexpr uint32_t TMEM_COLS = 512, ACOLS = CHUNK / 2, D_COL = RS * 2 * ACOLS;
-constexpr int LAUNCH_REGS = 80, REGS_MISC = 40, REGS_CONV = 56, REGS_B = 88, REGS_EPI = 120;
-static_assert(128 * REGS_MISC + 2 * 128 * REGS_CONV + 128 * REGS_B + 256 * REGS_EPI <= THREADS * LAUNCH_REGS && THREADS * LAUNCH_REGS <= 65536,
-              "register shares");
 constexpr int PITCH = RM + 4;            // floats between the columns of a tile's sums in shared memory
 constexpr size_t SMEM = 224 * 1024;
+
+// Warps of a kind of activations, and their registers (the launch's, which the
+// warpgroups share out again).
+template <int MODE> struct Roles {
+    static constexpr bool RAW = MODE == BF16 || MODE == F16; // operands as they come
+    static constexpr int GROUPS = RAW ? 4 : 2;               // of four warps that convert codes
+    static constexpr int B_WARP0 = CONV_WARP0 + 4 * GROUPS, EPI_WARP0 = B_WARP0 + (RAW ? 0 : 4), WARPS = EPI_WARP0 + EPI_THREADS / 32;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int LAUNCH = RAW ? 72 : 80, MISC = 40, CONV = 56, B = 88, EPI = 120;
+    static_assert(128 * (MISC + GROUPS * CONV + (RAW ? 0 : B)) + EPI_THREADS * EPI <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "register shares");
+};
 
 struct TcArgs {
     CUtensorMap tw, tx;
@@ -335,9 +343,11 @@ __device__ __forceinline__ float scale_of(uint32_t bits16, bool bf)
 template <int GPC, int NBLK> constexpr int GB = NBLK == 1 ? (GPC == 1 ? 2 : 4) : NBLK == 2 ? 2 : 1;
 
 // GPC: groups of a chunk.  NBLK: blocks of 16 columns of an epilogue warp, at most.
-template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS, 1) k_linear_w4_tc(const __grid_constant__ TcArgs t)
+template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<MODE>::THREADS, 1) k_linear_w4_tc(const __grid_constant__ TcArgs t)
 {
-    constexpr bool RAW = MODE == BF16 || MODE == F16;
+    using R = Roles<MODE>;
+    constexpr bool RAW = R::RAW;
+    constexpr int B_WARP0 = R::B_WARP0, EPI_WARP0 = R::EPI_WARP0;
     constexpr int GROUPS = 2 * GPC; // of a stage
     extern __shared__ uint8_t smraw[];
     __shared__ uint64_t wfull[NS_MAX], wfree[NS_MAX], full[RS], freed[RS], xfull[XS], xfree[XS], dfull[DS_MAX], dfree[DS_MAX], drain;
@@ -394,7 +404,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
     const int total = my_tiles * (st1 - st0); // stages of all tiles, in order (the host keeps sk <= stages)
 
     if (warp < CONV_WARP0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_MISC));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::MISC));
         if (warp == W_WARP) {
             Ring r;
             int issued = 0;
@@ -503,54 +513,71 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
         }
     } else if (warp < B_WARP0) {
         // ------------------------------------------------------------ codes
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_CONV));
-        const int q = warp & 3, g = (warp - CONV_WARP0) >> 2, row = 32 * q + lane; // lane quarter, chunk of a stage, row
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CONV));
+        // (a group takes one chunk of every stage, or of every second one: each slot of codes then has
+        // the same group's every time, their number being even)
+        constexpr int EVERY = R::GROUPS / 2;
+        const int q = warp & 3, g = ((warp - CONV_WARP0) >> 2) & 1, row = 32 * q + lane; // lane quarter, chunk of a stage, row
         const uint32_t ta = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)g * ACOLS;
+        uint32_t n = (uint32_t)(warp - CONV_WARP0) >> 3;
+        int tile = first, st = st0;
+        auto advance = [&](int by) { // by stages
+            st += by;
+            while (st >= st1) {
+                st -= st1 - st0;
+                tile += step;
+            }
+        };
+        advance((int)n);
         Ring r;
-        uint32_t n = 0;
-        bool ok = true;
-        auto zeros_of = [&](int tile, int st) {
+        r.slot = n;
+        auto zeros_of = [&] {
             return load_zeros<GPC>(t, min((int64_t)(tile / t.tt) * RM + row, (int64_t)t.a.N - 1), 2 * st + g);
         };
-        uint32_t z = first < tiles ? zeros_of(first, st0) : 0u;
-        for (int tile = first; tile < tiles && ok; tile += step) {
-            for (int st = st0; st < st1; st++, n++, r.next(t.ns)) {
-                if (!(ok = wait_warp(&wfull[r.slot], r.phase, abort_flag)))
-                    break;
-                uint4 v[4];
-                const uint32_t raw = sm + r.slot * STAGE + (uint32_t)row * 128u;
+        uint32_t z = (int)n < total ? zeros_of() : 0u;
+        for (; (int)n < total; n += EVERY) {
+            if (!wait_warp(&wfull[r.slot], r.phase, abort_flag))
+                break;
+            uint4 v[4];
+            const uint32_t raw = sm + r.slot * STAGE + (uint32_t)row * 128u;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                v[i] = lds128(raw + (((uint32_t)(4 * g + i) ^ (uint32_t)(row & 7)) << 4));
+            const uint32_t zc = z;
+            if (t.a.zeros && (int)n + EVERY < total) { // the next chunk's, requested early
+                advance(EVERY);
+                z = zeros_of();
+            }
+            const uint32_t slot = n % RS;
+            if (!wait_warp(&freed[slot], (n / RS & 1) ^ 1, abort_flag))
+                break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t zg = (zc >> (8 * (GPC == 4 ? j : GPC == 2 ? j >> 1 : 0))) & 255u;
+                uint32_t h[16];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    v[i] = lds128(raw + (((uint32_t)(4 * g + i) ^ (uint32_t)(row & 7)) << 4));
-                const uint32_t zc = z;
-                if (t.a.zeros && (st + 1 < st1 || tile + step < tiles)) // the next chunk's, requested early
-                    z = st + 1 < st1 ? zeros_of(tile, st + 1) : zeros_of(tile + step, st0);
-                const uint32_t slot = n % RS;
-                if (!(ok = wait_warp(&freed[slot], (n / RS & 1) ^ 1, abort_flag)))
-                    break;
-                tc_fence_after();
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const uint32_t zg = (zc >> (8 * (GPC == 4 ? j : GPC == 2 ? j >> 1 : 0))) & 255u;
-                    uint32_t h[16];
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        centred<MODE == BF16>(j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w, zg, h + 4 * i);
-                    tmem_st16(ta + slot * (2 * ACOLS) + 16 * j, h);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&full[slot]);
-                    mbar_arrive(&wfree[r.slot]);
-                }
+                    centred<MODE == BF16>(j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w, zg, h + 4 * i);
+                tmem_st16(ta + slot * (2 * ACOLS) + 16 * j, h);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full[slot]);
+                mbar_arrive(&wfree[r.slot]);
+            }
+            r.slot += EVERY;
+            if ((int)r.slot >= t.ns) {
+                r.slot -= (uint32_t)t.ns;
+                r.phase ^= 1;
             }
         }
     } else if (warp < EPI_WARP0) {
         // ------------------------------------------------------------ activations
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_B));
         if constexpr (!RAW) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::B));
             const int q = warp - B_WARP0;
             bool ok = true;
             for (int n = 0; n < total && ok; n++) {
@@ -617,7 +644,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(THREADS
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::EPI));
         constexpr int BT = MODE == WHOLE ? 8 : 16; // tokens of a block of 16 columns
         const int q = warp & 3, e = (warp - EPI_WARP0) >> 2, row = 32 * q + lane;
         const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + D_COL;
@@ -819,7 +846,14 @@ template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStre
     static luce_host::SmemLimit limit;
     static std::atomic<int> resident[64][SK_MAX + 1]; // clusters of a size that a device holds at once, plus one
     const auto kern = k_linear_w4_tc<MODE, GPC, NBLK>;
-    if (limit.raise(kern, SMEM) != cudaSuccess) {
+    // (warpgroups take registers up from the launch's: with fewer of those they would wait for ever)
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, kern) == cudaSuccess)
+            regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < Roles<MODE>::LAUNCH || limit.raise(kern, SMEM) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
@@ -830,7 +864,7 @@ template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStre
     }
     const int sms = luce_host::sm_count(), tiles = t.rt * t.tt;
     auto config = [&](cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int sk) {
-        luce_host::make_config(cfg, attr, dim3((unsigned)grid), dim3(THREADS), SMEM, stream);
+        luce_host::make_config(cfg, attr, dim3((unsigned)grid), dim3(Roles<MODE>::THREADS), SMEM, stream);
         if (sk > 1) {
             cudaLaunchAttribute &cluster = attr[cfg.numAttrs++];
             cluster.id = cudaLaunchAttributeClusterDimension;
@@ -910,7 +944,7 @@ luce_status tc_product(const W4Args &a, int group, cudaStream_t stream)
     const int box = mode == WHOLE ? t.nb / 2 : t.nb;
     t.xbytes = mode == I8 || mode == WHOLE ? (uint32_t)box * CHUNK * es : 0;
     const uint32_t rest = b + XS * t.xbytes + (mode == WHOLE ? FR * (NB_MAX / 2) * 4 : 0); // (every part a multiple of 1024)
-    t.ns = (int)std::min<uint32_t>(NS_MAX, ((uint32_t)SMEM - 1024 - rest) / STAGE);
+    t.ns = (int)std::min<uint32_t>(NS_MAX, ((uint32_t)SMEM - 1024 - rest) / STAGE) & ~1;
     t.off_b = (uint32_t)t.ns * STAGE;
     t.off_x = t.off_b + b;
     t.off_f = t.off_x + XS * t.xbytes;
