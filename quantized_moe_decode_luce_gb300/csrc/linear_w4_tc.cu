@@ -55,26 +55,28 @@ constexpr int NS_MAX = 12, XS = 2, RS = 2, DS_MAX = 8, FR = 32;
 constexpr int NB_MAX = 96;               // columns of a tile
 constexpr int SK_MAX = 8;                // CTAs of one cluster at most
 constexpr int W_WARP = 0, MMA_WARP = 1, X_WARP = 2, CONV_WARP0 = 4;
-constexpr int EPI_THREADS = 256;
 constexpr uint32_t TMEM_COLS = 512, ACOLS = CHUNK / 2, D_COL = RS * 2 * ACOLS;
 constexpr int PITCH = RM + 4;            // floats between the columns of a tile's sums in shared memory
 constexpr size_t SMEM = 224 * 1024;
 
-// Warps of a kind of activations, and their registers (the launch's, which the
-// warpgroups share out again).
-template <int MODE> struct Roles {
+// Warps of a kind of activations (NBLK: pairs of blocks of 16 columns in a
+// tile, at most), and their registers, which the warpgroups share out again.
+// Where TMA writes B, no warps do: few columns leave the conversion of codes the
+// longest part, more the epilogue, and the warps go there.
+template <int MODE, int NBLK> struct Roles {
     static constexpr bool RAW = MODE == BF16 || MODE == F16; // operands as they come
-    static constexpr int GROUPS = RAW ? 4 : 2;               // of four warps that convert codes
-    static constexpr int B_WARP0 = CONV_WARP0 + 4 * GROUPS, EPI_WARP0 = B_WARP0 + (RAW ? 0 : 4), WARPS = EPI_WARP0 + EPI_THREADS / 32;
-    static constexpr int THREADS = WARPS * 32;
-    static constexpr int LAUNCH = RAW ? 72 : 80, MISC = 40, CONV = 56, B = 88, EPI = 120;
-    static_assert(128 * (MISC + GROUPS * CONV + (RAW ? 0 : B)) + EPI_THREADS * EPI <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "register shares");
+    static constexpr int GROUPS = RAW && NBLK == 1 ? 4 : 2;  // of four warps that convert codes
+    static constexpr int EPI = RAW && NBLK > 1 ? 4 : 2;      // of the epilogue
+    static constexpr int B_WARP0 = CONV_WARP0 + 4 * GROUPS, EPI_WARP0 = B_WARP0 + (RAW ? 0 : 4), WARPS = EPI_WARP0 + 4 * EPI;
+    static constexpr int THREADS = WARPS * 32, EPI_THREADS = EPI * 128;
+    static constexpr int LAUNCH = RAW ? 72 : 80, REGS_MISC = 40, REGS_CONV = 56, REGS_B = 88, REGS_EPI = EPI == 4 ? 88 : 120;
+    static_assert(128 * (REGS_MISC + GROUPS * REGS_CONV + (RAW ? 0 : REGS_B) + EPI * REGS_EPI) <= THREADS * LAUNCH && THREADS * LAUNCH <= 65536, "register shares");
 };
 
 struct TcArgs {
     CUtensorMap tw, tx;
     W4Args a;
-    bool whole_groups;     // every row's groups are whole chunks, aligned
+    int whole_groups;      // groups of a row that one load may take: 8, 2 or 1
     int nb, tokens;        // columns (a multiple of 16) and tokens of a tile
     int rt, tt;            // tiles of channels, of tokens (fastest)
     int chunks, stages;    // of a row
@@ -301,37 +303,43 @@ __device__ __forceinline__ float whole4(const float4 &v, uint2 &o0, uint2 &o1)
     return __uint_as_float((e - 10u) << 23); // 2^(e - 137)
 }
 
-// The scales (16 bits each) and zero points (8 bits each) of a row's groups in
-// chunk c (which may be one behind the last), those beyond the row's G as zero.
-template <int GPC> __device__ __forceinline__ uint2 load_scales(const TcArgs &t, int64_t row, int c)
+// The scales and zero points of a row's groups 8 b .. 8 b + 7 (16 and 8 bits
+// each), those beyond the row's G as zero.  Lanes hold rows, so that a load
+// touches 32 lines however little it reads: one for eight groups where rows are
+// aligned for it (28672 x 4096, 64 tokens: one a chunk kept the load units busy
+// for 2/3 of a stage).
+__device__ __forceinline__ uint4 load_scales(const TcArgs &t, int64_t row, int b)
 {
-    const int64_t at = row * t.a.G + c * GPC;
-    const uint16_t *s = reinterpret_cast<const uint16_t *>(t.a.ws) + at;
-    if (c >= t.chunks)
-        return make_uint2(0, 0);
-    if (GPC == 1)
-        return make_uint2(__ldg(s), 0);
-    if (t.whole_groups)
-        return GPC == 2 ? make_uint2(__ldg(reinterpret_cast<const uint32_t *>(s)), 0) : __ldg(reinterpret_cast<const uint2 *>(s));
+    const uint16_t *s = reinterpret_cast<const uint16_t *>(t.a.ws) + row * t.a.G + 8 * b;
+    const int left = t.a.G - 8 * b;
+    if (t.whole_groups == 8)
+        return left > 0 ? __ldg(reinterpret_cast<const uint4 *>(s)) : make_uint4(0, 0, 0, 0);
     uint32_t v[4] = {};
-    for (int i = 0; i < 4; i++)
-        if (i < GPC && c * GPC + i < t.a.G)
-            v[i] = __ldg(s + i);
-    return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-}
-template <int GPC> __device__ __forceinline__ uint32_t load_zeros(const TcArgs &t, int64_t row, int c)
-{
-    if (!t.a.zeros)
-        return 0x08080808u;
-    const int64_t at = row * t.a.G + c * GPC;
-    uint32_t z = 0;
-    if (t.whole_groups && GPC == 4 && c < t.chunks)
-        z = __ldg(reinterpret_cast<const uint32_t *>(t.a.zeros + at));
-    else
+    if (t.whole_groups == 2) {
+#pragma unroll
         for (int i = 0; i < 4; i++)
-            if (i < GPC && c * GPC + i < t.a.G)
-                z |= (uint32_t)__ldg(t.a.zeros + at + i) << (8 * i);
-    return z & 0x0f0f0f0fu;
+            if (2 * i < left)
+                v[i] = __ldg(reinterpret_cast<const uint32_t *>(s) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (i < left)
+                v[i / 2] |= (uint32_t)__ldg(s + i) << (16 * (i & 1));
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint2 load_zeros(const TcArgs &t, int64_t row, int b)
+{
+    const uint8_t *z = t.a.zeros + row * t.a.G + 8 * b;
+    const int left = t.a.G - 8 * b;
+    if (t.whole_groups == 8)
+        return left > 0 ? __ldg(reinterpret_cast<const uint2 *>(z)) : make_uint2(0, 0);
+    uint32_t v[2] = {};
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        if (i < left)
+            v[i / 4] |= (uint32_t)__ldg(z + i) << (8 * (i & 3));
+    return make_uint2(v[0], v[1]);
 }
 __device__ __forceinline__ float scale_of(uint32_t bits16, bool bf)
 {
@@ -342,12 +350,13 @@ __device__ __forceinline__ float scale_of(uint32_t bits16, bool bf)
 // columns per epilogue warp.
 template <int GPC, int NBLK> constexpr int GB = NBLK == 1 ? (GPC == 1 ? 2 : 4) : NBLK == 2 ? 2 : 1;
 
-// GPC: groups of a chunk.  NBLK: blocks of 16 columns of an epilogue warp, at most.
-template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<MODE>::THREADS, 1) k_linear_w4_tc(const __grid_constant__ TcArgs t)
+// GPC: groups of a chunk.  NBLK: pairs of blocks of 16 columns, at most.
+template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<MODE, NBLK>::THREADS, 1) k_linear_w4_tc(const __grid_constant__ TcArgs t)
 {
-    using R = Roles<MODE>;
+    using R = Roles<MODE, NBLK>;
     constexpr bool RAW = R::RAW;
-    constexpr int B_WARP0 = R::B_WARP0, EPI_WARP0 = R::EPI_WARP0;
+    constexpr int B_WARP0 = R::B_WARP0, EPI_WARP0 = R::EPI_WARP0, EPI_THREADS = R::EPI_THREADS;
+    constexpr int EB = (2 * NBLK + R::EPI - 1) / R::EPI; // blocks of an epilogue warp, at most
     constexpr int GROUPS = 2 * GPC; // of a stage
     extern __shared__ uint8_t smraw[];
     __shared__ uint64_t wfull[NS_MAX], wfree[NS_MAX], full[RS], freed[RS], xfull[XS], xfree[XS], dfull[DS_MAX], dfree[DS_MAX], drain;
@@ -404,7 +413,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
     const int total = my_tiles * (st1 - st0); // stages of all tiles, in order (the host keeps sk <= stages)
 
     if (warp < CONV_WARP0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::MISC));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::REGS_MISC));
         if (warp == W_WARP) {
             Ring r;
             int issued = 0;
@@ -480,30 +489,26 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
                 const uint32_t as = tm + slot * (2 * ACOLS);
                 const uint64_t bd = desc0 + (slot * bslot >> 4);
 #pragma unroll
-                for (int g = 0; g < GROUPS; g++) {
-                    const int in = g & (gb - 1); // place in its slot of D
-                    if (in == 0) {
-                        if (!(ok = wait_warp(&dfree[rd.slot], rd.phase ^ 1, abort_flag)))
-                            break;
-                        tc_fence_after();
-                    }
-                    const uint32_t dd = tm + D_COL + (rd.slot * (uint32_t)gb + (uint32_t)in) * nb;
-                    const bool closes = in == gb - 1;
+                for (int g = 0; g < GROUPS; g += gb) { // a slot of D
+                    if (!(ok = wait_warp(&dfree[rd.slot], rd.phase ^ 1, abort_flag)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t dd = tm + D_COL + rd.slot * (uint32_t)gb * nb;
                     if (elect_one()) {
+                        // (the groups in turn: an MMA waits for the sums of the one before it)
 #pragma unroll
-                        for (int k = 0; k < STEPS; k++) {
-                            const int kk = g * STEPS + k;
-                            mma_ts(dd, as + 8 * kk, bd + (kk >> 2) * atom + 2 * (kk & 3), idesc, k > 0);
-                        }
-                        if (g == GROUPS - 1)
+                        for (int k = 0; k < STEPS; k++)
+#pragma unroll
+                            for (int i = 0; i < gb; i++) {
+                                const int kk = (g + i) * STEPS + k;
+                                mma_ts(dd + (uint32_t)i * nb, as + 8 * kk, bd + (kk >> 2) * atom + 2 * (kk & 3), idesc, k > 0);
+                            }
+                        if (g + gb == GROUPS)
                             mma_commit(&freed[slot]);
-                        if (closes) {
-                            mma_commit(&dfull[rd.slot]);
-                            mbar_arrive(&dfull[rd.slot]);
-                        }
+                        mma_commit(&dfull[rd.slot]);
+                        mbar_arrive(&dfull[rd.slot]);
                     }
-                    if (closes)
-                        rd.next(t.ds);
+                    rd.next(t.ds);
                 }
             }
             // every MMA issued has completed before the tensor memory is freed
@@ -513,7 +518,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
         }
     } else if (warp < B_WARP0) {
         // ------------------------------------------------------------ codes
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::CONV));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::REGS_CONV));
         // (a group takes one chunk of every stage, or of every second one: each slot of codes then has
         // the same group's every time, their number being even)
         constexpr int EVERY = R::GROUPS / 2;
@@ -531,10 +536,19 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
         advance((int)n);
         Ring r;
         r.slot = n;
+        // the zero points of eight groups, of the chunk to come; loaded early
+        uint2 zs = make_uint2(0x08080808u, 0x08080808u);
+        int held = -1, held_tile = -1;
         auto zeros_of = [&] {
-            return load_zeros<GPC>(t, min((int64_t)(tile / t.tt) * RM + row, (int64_t)t.a.N - 1), 2 * st + g);
+            const int block = (2 * st + g) * GPC / 8;
+            if (t.a.zeros && (block != held || tile != held_tile)) {
+                zs = load_zeros(t, min((int64_t)(tile / t.tt) * RM + row, (int64_t)t.a.N - 1), block);
+                held = block;
+                held_tile = tile;
+            }
         };
-        uint32_t z = (int)n < total ? zeros_of() : 0u;
+        if ((int)n < total)
+            zeros_of();
         for (; (int)n < total; n += EVERY) {
             if (!wait_warp(&wfull[r.slot], r.phase, abort_flag))
                 break;
@@ -543,10 +557,11 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 v[i] = lds128(raw + (((uint32_t)(4 * g + i) ^ (uint32_t)(row & 7)) << 4));
-            const uint32_t zc = z;
-            if (t.a.zeros && (int)n + EVERY < total) { // the next chunk's, requested early
+            const int at = (2 * st + g) * GPC % 8;
+            const uint32_t zc = (at & 4 ? zs.y : zs.x) >> (8 * (at & 3));
+            if ((int)n + EVERY < total) {
                 advance(EVERY);
-                z = zeros_of();
+                zeros_of();
             }
             const uint32_t slot = n % RS;
             if (!wait_warp(&freed[slot], (n / RS & 1) ^ 1, abort_flag))
@@ -554,7 +569,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const uint32_t zg = (zc >> (8 * (GPC == 4 ? j : GPC == 2 ? j >> 1 : 0))) & 255u;
+                const uint32_t zg = (zc >> (8 * (GPC == 4 ? j : GPC == 2 ? j >> 1 : 0))) & 15u;
                 uint32_t h[16];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -577,7 +592,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
     } else if (warp < EPI_WARP0) {
         // ------------------------------------------------------------ activations
         if constexpr (!RAW) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::B));
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::REGS_B));
             const int q = warp - B_WARP0;
             bool ok = true;
             for (int n = 0; n < total && ok; n++) {
@@ -644,7 +659,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::EPI));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::REGS_EPI));
         constexpr int BT = MODE == WHOLE ? 8 : 16; // tokens of a block of 16 columns
         const int q = warp & 3, e = (warp - EPI_WARP0) >> 2, row = 32 * q + lane;
         const uint32_t td = tmem + ((uint32_t)(32 * q) << 16) + D_COL;
@@ -652,7 +667,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
         Ring rd;
         bool ok = true;
         uint32_t n = 0;
-        float acc[NBLK][BT];
+        float acc[EB][BT];
         // a block's sums of a group into the tokens'
         auto add = [&](float (&to)[BT], const uint32_t (&v)[16], float s, const float *f) {
             if constexpr (MODE == WHOLE) {
@@ -674,9 +689,20 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
             const int chan = tile / t.tt * RM + row, token0 = tile % t.tt * t.tokens;
             const int64_t crow = min(chan, t.a.N - 1);
             const bool live = chan < t.a.N;
-            uint2 sc[2] = {load_scales<GPC>(t, crow, 2 * st0), load_scales<GPC>(t, crow, 2 * st0 + 1)};
+            constexpr int PER = 8 / GROUPS; // stages of eight groups
+            uint4 sc = load_scales(t, crow, st0 / PER), next = make_uint4(0, 0, 0, 0);
+            if (st0 / PER < (st1 - 1) / PER)
+                next = load_scales(t, crow, st0 / PER + 1);
+            auto shift = [&] { // a stage's scales out of sc
+                if constexpr (GPC == 1)
+                    sc = make_uint4(sc.y, sc.z, sc.w, 0);
+                else
+                    sc = make_uint4(sc.z, sc.w, 0, 0);
+            };
+            for (int i = 0; i < st0 % PER; i++)
+                shift();
 #pragma unroll
-            for (int i = 0; i < NBLK; i++)
+            for (int i = 0; i < EB; i++)
 #pragma unroll
                 for (int j = 0; j < BT; j++)
                     acc[i][j] = 0.0f;
@@ -684,12 +710,15 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
                 float s[GROUPS];
 #pragma unroll
                 for (int g = 0; g < GROUPS; g++) {
-                    const uint2 v = sc[g / GPC];
-                    s[g] = scale_of(((g % GPC & 2 ? v.y : v.x) >> (16 * (g % GPC & 1))) & 0xffffu, t.a.ws_bf16);
+                    const uint32_t v = g < 2 ? sc.x : g < 4 ? sc.y : g < 6 ? sc.z : sc.w;
+                    s[g] = scale_of(g & 1 ? v >> 16 : v & 0xffffu, t.a.ws_bf16);
                 }
-                if (st + 1 < st1) {
-                    sc[0] = load_scales<GPC>(t, crow, 2 * st + 2);
-                    sc[1] = load_scales<GPC>(t, crow, 2 * st + 3);
+                if ((st + 1) % PER != 0) {
+                    shift();
+                } else {
+                    sc = next;
+                    if ((st + 1) / PER < (st1 - 1) / PER)
+                        next = load_scales(t, crow, (st + 1) / PER + 1);
                 }
                 const float *f[2] = {factors + 2 * n % FR * (NB_MAX / 2), factors + (2 * n + 1) % FR * (NB_MAX / 2)};
 #pragma unroll
@@ -698,13 +727,13 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
                         break;
                     tc_fence_after();
                     // the slot's sums into registers, and the slot back
-                    uint32_t v[gb][NBLK][16];
+                    uint32_t v[gb][EB][16];
 #pragma unroll
                     for (int i = 0; i < gb; i++)
 #pragma unroll
-                        for (int b = 0; b < NBLK; b++)
-                            if (2 * b + e < blocks)
-                                tmem_ld16(td + (rd.slot * gb + i) * (uint32_t)t.nb + 16 * (2 * b + e), v[i][b]);
+                        for (int b = 0; b < EB; b++)
+                            if (R::EPI * b + e < blocks)
+                                tmem_ld16(td + (rd.slot * gb + i) * (uint32_t)t.nb + 16 * (R::EPI * b + e), v[i][b]);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
@@ -712,11 +741,11 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
                         mbar_arrive(&dfree[rd.slot]);
                     rd.next(t.ds);
 #pragma unroll
-                    for (int b = 0; b < NBLK; b++)
-                        if (2 * b + e < blocks)
+                    for (int b = 0; b < EB; b++)
+                        if (R::EPI * b + e < blocks)
 #pragma unroll
                             for (int i = 0; i < gb; i++)
-                                add(acc[b], v[i][b], s[g + i], f[(g + i) / GPC] + BT * (2 * b + e));
+                                add(acc[b], v[i][b], s[g + i], f[(g + i) / GPC] + BT * (R::EPI * b + e));
                 }
             }
             if (!ok)
@@ -724,20 +753,20 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
             const int nt = min(t.tokens, t.a.T - token0);
             if (t.sk > 1) { // (one tile per cluster) the sums, where the stages were
 #pragma unroll
-                for (int i = 0; i < NBLK; i++)
+                for (int i = 0; i < EB; i++)
 #pragma unroll
                     for (int j = 0; j < BT; j++) {
-                        const int tok = (2 * i + e) * BT + j;
+                        const int tok = (R::EPI * i + e) * BT + j;
                         if (tok < nt)
                             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sm + (uint32_t)(tok * PITCH + row) * 4u), "f"(acc[i][j]) : "memory");
                     }
             } else {
                 const float bn = live && t.a.bias ? t.a.bias[chan] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < NBLK; i++)
+                for (int i = 0; i < EB; i++)
 #pragma unroll
                     for (int j = 0; j < BT; j++) {
-                        const int tok = (2 * i + e) * BT + j;
+                        const int tok = (R::EPI * i + e) * BT + j;
                         if (tok < nt && live) {
                             float v = acc[i][j];
                             if (MODE == I8)
@@ -853,7 +882,7 @@ template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStre
         if (cudaFuncGetAttributes(&at, kern) == cudaSuccess)
             regs.store(at.numRegs, std::memory_order_relaxed);
     }
-    if (regs.load(std::memory_order_relaxed) < Roles<MODE>::LAUNCH || limit.raise(kern, SMEM) != cudaSuccess) {
+    if (regs.load(std::memory_order_relaxed) < Roles<MODE, NBLK>::LAUNCH || limit.raise(kern, SMEM) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
@@ -864,7 +893,7 @@ template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStre
     }
     const int sms = luce_host::sm_count(), tiles = t.rt * t.tt;
     auto config = [&](cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int sk) {
-        luce_host::make_config(cfg, attr, dim3((unsigned)grid), dim3(Roles<MODE>::THREADS), SMEM, stream);
+        luce_host::make_config(cfg, attr, dim3((unsigned)grid), dim3(Roles<MODE, NBLK>::THREADS), SMEM, stream);
         if (sk > 1) {
             cudaLaunchAttribute &cluster = attr[cfg.numAttrs++];
             cluster.id = cudaLaunchAttributeClusterDimension;
@@ -929,7 +958,8 @@ luce_status tc_product(const W4Args &a, int group, cudaStream_t stream)
     const Mode mode = mode_of(a);
     t.a = a;
     const int gpc = CHUNK / group;
-    t.whole_groups = a.G % gpc == 0 && luce_host::aligned(a.ws, 2 * gpc) && (!a.zeros || luce_host::aligned(a.zeros, gpc));
+    t.whole_groups = a.G % 8 == 0 && luce_host::aligned(a.ws, 16) && (!a.zeros || luce_host::aligned(a.zeros, 8)) ? 8
+                     : a.G % 2 == 0 && luce_host::aligned(a.ws, 4) ? 2 : 1;
     t.chunks = (a.K + CHUNK - 1) / CHUNK;
     t.stages = (t.chunks + 1) / 2;
     const int parts = mode == WHOLE ? 2 : 1, most = NB_MAX / parts;
