@@ -226,17 +226,17 @@ template <int NT, int GPC, bool ZEROS, int U> constexpr int S_MOST = NT == 1 && 
 // WHOLE: activations as whole numbers, codes as they are.
 template <int NT, int GPC, bool ZEROS, int U, bool WHOLE>
 __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
-    k_linear_w4_stream(const W4Args a, int wk, int pitch, int steps, bool whole)
+    k_linear_w4_stream(const W4Args a, int wk, int groups, int pitch, int steps, bool whole)
 {
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = groups * wk;
     const int P = a.parts, nt = a.T, cols = nt * P;
     const int chunks = (a.K + CHUNK - 1) / CHUNK, row_bytes = chunks * CHUNK_BYTES;
     const int units = (chunks + U - 1) / U, per = (units + wk - 1) / wk; // of a row; of a warp and tile
     const int group = warp / wk, kw = warp % wk;                         // row group of the CTA, place in it
     const int quad = lane & 3, r8 = lane >> 2;
-    const int rows_step = warps / wk * ROWS; // rows of the CTA at a step
+    const int rows_step = groups * ROWS; // rows of the CTA at a step (warps beyond them prepare activations only)
     // behind the activations: per group and column the factor and the sum of
     // its activations; then the warps' sums, twice
     float2 *info = reinterpret_cast<float2 *>(smem + (size_t)cols * pitch);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
     Groups<GPC> g[U][2];
     // the unit to request next: its step and place among the tile's, and where
     // this lane's codes and groups of it are in two rows (those beyond the last repeat it)
-    int ls = blockIdx.x, lj = 0, lc;
+    int ls = warp < warps ? blockIdx.x : steps, lj = 0, lc;
     const uint8_t *lw[2];
     int64_t lg[2];
     auto aim = [&]() {
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
 
     // activations into shared memory, zero from K to the chunk's end
     const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;
-    for (int i0 = 0; i0 < nt * chunks; i0 += 2 * warps) {
+    for (int i0 = 0; i0 < nt * chunks; i0 += blockDim.x / 16) {
         const int i = i0 + half, t = i / chunks, c = i % chunks, k = c * CHUNK + 8 * l16;
         const bool live = i < nt * chunks && k < a.K;
         uint4 o[2];
@@ -295,6 +295,8 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
         }
     }
     __syncthreads();
+    if (warp >= warps)
+        return;
 
     const uint8_t *xcol[NT]; // (columns beyond the last repeat it; their sums are not stored)
 #pragma unroll
@@ -432,12 +434,13 @@ template <int NT, int GPC, bool ZEROS, int U, bool WHOLE> luce_status launch_str
     }
     const int rows = groups * ROWS, steps = (a.N + rows - 1) / rows;
     const size_t smem = s_smem(a, a.T * a.parts, GPC, wk * groups);
+    const int warps = std::max(wk * groups, std::min(S_MOST<NT, GPC, ZEROS, U>, (a.T * chunks + 1) / 2)); // two chunks a warp to prepare
     const bool whole = a.G % GPC == 0 && luce_host::aligned(a.ws, 2 * GPC) && (!ZEROS || luce_host::aligned(a.zeros, GPC));
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
-    const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms)), dim3(wk * groups * 32), smem, stream, a, wk,
+    const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms)), dim3(warps * 32), smem, stream, a, wk, groups,
                                              s_pitch(a.K), steps, whole);
     if (st != LUCE_OK)
         limit.forget();
@@ -445,18 +448,24 @@ template <int NT, int GPC, bool ZEROS, int U, bool WHOLE> luce_status launch_str
 }
 
 // Whether the stream serves a call.  Each of its CTAs prepares the activations
-// for itself, 0.022 us a token and chunk (int8 half of that); the tensor cores
-// are later to start, and read the codes of large matrices more slowly: 4.2 us
-// at 4096 x 4096, 5.3 at 4096 x 14336, 12.5 at 28672 x 4096, 28 at 129280 x 4096.
-// (Four tokens, bf16, groups of 128: 4096 x 4096 8.2 us, tensor cores 9.7;
-// 4096 x 14336 20.4 and 16.7; eight tokens: 4096 x 4096 11.0 and 9.8, 28672 x
-// 4096 20.7 and 28.5.)
+// for itself, 0.02 us a token and chunk (int8 half of that); the tensor cores
+// are later to start, and read the codes of large matrices more slowly, most of
+// all where they have activations to convert.  In tokens times chunks, with the
+// stages of codes that an SM takes:
+//   fp32      170 + 9 stages   (8192 x 8192, 5 tokens 23.4 us, tensor cores 25.0; 4096 x 4096, 8 tokens 12.2 and 10.7)
+//   int8      290 + 12 stages  (8192 x 8192, 8 tokens 19.4 us and 21.6; 4096 x 4096, 12 tokens 11.2 and 10.5)
+//   16 bits   140 + 4 stages   (4096 x 4096, 4 tokens 8.4 us and 9.4; 8192 x 8192, 4 tokens 17.5 and 16.4)
+// and for more than four tokens of 16 bits, whose codes take the stream twice the
+// instructions, 166 + 2 stages, but 260 at most (4096 x 4096, 5 tokens 9.0 us and
+// 9.5, 8 tokens 10.8 and 9.6; 129280 x 4096, 8 tokens 67.4 and 68.2, 12 tokens
+// 82.3 and 69.5).
 bool stream_serves(const W4Args &a, int gpc)
 {
     const int64_t chunks = (a.K + CHUNK - 1) / CHUNK, cols = (int64_t)a.T * a.parts;
     if (cols > S_COLS || s_smem(a, (int)cols, gpc, cols > 8 ? 16 : S_WARPS) > S_SMEM)
         return false;
-    return (int64_t)a.T * chunks / (a.x_dtype == LUCE_I8 ? 2 : 1) <= 140 + 4 * ((int64_t)a.N * chunks / (128 * 152));
+    const int64_t stages = (int64_t)a.N * chunks / (128 * 152), work = a.T * chunks;
+    return work <= (a.x_dtype == LUCE_F32 ? 170 + 9 * stages : a.x_dtype == LUCE_I8 ? 290 + 12 * stages : a.whole ? 140 + 4 * stages : std::min<int64_t>(166 + 2 * stages, 260));
 }
 
 template <int GPC, bool ZEROS> luce_status run_stream(const W4Args &a, cudaStream_t stream)
