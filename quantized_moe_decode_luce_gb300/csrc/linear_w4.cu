@@ -183,8 +183,10 @@ __device__ __forceinline__ void normal(uint32_t (&h)[4], uint32_t zero)
 template <int GPC> struct Groups {
     uint32_t s[(GPC + 1) / 2], z;
 };
-template <int GPC, bool ZEROS>
-__device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int64_t at, int g0, bool whole)
+// EVEN: every row's groups are whole chunks, aligned.  (A choice at run time would
+// cost a wait for the loads at its end: 129280 x 4096 in groups of 64 75 us.)
+template <int GPC, bool ZEROS, bool EVEN>
+__device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int64_t at, int g0)
 { // (group g0 of a row, at `at` among all rows' groups)
     const uint16_t *s = reinterpret_cast<const uint16_t *>(a.ws) + at;
     const uint8_t *z = a.zeros + at;
@@ -193,7 +195,7 @@ __device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int
         if (ZEROS)
             g.z = __ldg(z);
     } else {
-        if (whole) { // (every row's groups are whole chunks, aligned)
+        if constexpr (EVEN) {
             if constexpr (GPC == 2) {
                 g.s[0] = __ldg(reinterpret_cast<const uint32_t *>(s));
                 if (ZEROS)
@@ -224,9 +226,9 @@ __device__ __forceinline__ void load_groups(Groups<GPC> &g, const W4Args &a, int
 template <int NT, int GPC, bool ZEROS, int U> constexpr int S_MOST = NT == 1 && (U == 2 || (GPC == 1 && !ZEROS)) ? S_WARPS : 16;
 
 // WHOLE: activations as whole numbers, codes as they are.
-template <int NT, int GPC, bool ZEROS, int U, bool WHOLE>
+template <int NT, int GPC, bool ZEROS, int U, bool WHOLE, bool EVEN>
 __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
-    k_linear_w4_stream(const W4Args a, int wk, int groups, int pitch, int steps, bool whole)
+    k_linear_w4_stream(const W4Args a, int wk, int groups, int pitch, int steps)
 {
     constexpr int COLS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 w[u][h] = ldg_stream(lw[h] + u * CHUNK_BYTES);
-                load_groups<GPC, ZEROS>(g[u][h], a, lg[h] + u * GPC, (lc + u) * GPC, whole);
+                load_groups<GPC, ZEROS, EVEN>(g[u][h], a, lg[h] + u * GPC, (lc + u) * GPC);
             }
     };
     aim();
@@ -415,10 +417,10 @@ size_t s_smem(const W4Args &a, int cols, int gpc, int warps)
     return (size_t)cols * s_pitch(a.K) + chunks * gpc * padded * 8 + 2 * warps * padded * PART * 4;
 }
 
-template <int NT, int GPC, bool ZEROS, int U, bool WHOLE> luce_status launch_stream(const W4Args &a, cudaStream_t stream)
+template <int NT, int GPC, bool ZEROS, int U, bool WHOLE, bool EVEN> luce_status launch_stream(const W4Args &a, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
-    const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U, WHOLE>;
+    const auto kern = k_linear_w4_stream<NT, GPC, ZEROS, U, WHOLE, EVEN>;
     const int chunks = (a.K + CHUNK - 1) / CHUNK;
     // wk warps along a row, and as many row groups to a CTA as SMs ask for, within its warps: those
     // with the fewest units one after another; a step's joining counts as a quarter of a unit (of two
@@ -435,13 +437,12 @@ template <int NT, int GPC, bool ZEROS, int U, bool WHOLE> luce_status launch_str
     const int rows = groups * ROWS, steps = (a.N + rows - 1) / rows;
     const size_t smem = s_smem(a, a.T * a.parts, GPC, wk * groups);
     const int warps = std::max(wk * groups, std::min(S_MOST<NT, GPC, ZEROS, U>, (a.T * chunks + 1) / 2)); // two chunks a warp to prepare
-    const bool whole = a.G % GPC == 0 && luce_host::aligned(a.ws, 2 * GPC) && (!ZEROS || luce_host::aligned(a.zeros, GPC));
     if (smem > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
     const luce_status st = luce_host::launch(kern, dim3((unsigned)std::min(steps, sms)), dim3(warps * 32), smem, stream, a, wk, groups,
-                                             s_pitch(a.K), steps, whole);
+                                             s_pitch(a.K), steps);
     if (st != LUCE_OK)
         limit.forget();
     return st;
@@ -475,7 +476,10 @@ template <int GPC, bool ZEROS> luce_status run_stream(const W4Args &a, cudaStrea
     auto run = [&](auto nt, auto whole) {
         constexpr int NT = decltype(nt)::value;
         constexpr bool WHOLE = decltype(whole)::value;
-        return few ? launch_stream<NT, GPC, ZEROS, 2, WHOLE>(a, stream) : launch_stream<NT, GPC, ZEROS, 4, WHOLE>(a, stream);
+        const bool even = a.G % GPC == 0 && luce_host::aligned(a.ws, 2 * GPC) && (!ZEROS || luce_host::aligned(a.zeros, GPC));
+        if (GPC > 1 && !even)
+            return launch_stream<NT, GPC, ZEROS, 2, WHOLE, GPC == 1>(a, stream);
+        return few ? launch_stream<NT, GPC, ZEROS, 2, WHOLE, true>(a, stream) : launch_stream<NT, GPC, ZEROS, 4, WHOLE, true>(a, stream);
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
