@@ -210,10 +210,11 @@ template <int THREADS> struct Shared {
     uint2 table[256];
     union {
         Hist hist[2];     // (alternating: a level's readers have passed the next level's barrier before it is zeroed)
-        u64 sorted[MOST]; // (while no histogram is in use)
+        alignas(16) u64 sorted[MOST]; // (while no histogram is in use)
     };
-    u64 list[MOST];          // the first CTA's tokens: key, and id from the last
-    u64 near[THREADS];       // this CTA's candidates for top-k, the same
+    alignas(16) u64 list[MOST]; // the first CTA's tokens: key, and id from the last
+    static constexpr int NEAR_MOST = 2 * THREADS;
+    u64 near[NEAR_MOST];     // this CTA's candidates for top-k, the same
     u64 exchange[2][CL_MAX]; // (alternating, for the same reason)
     u64 warp[WARPS], part[64];
     u64 found[5];
@@ -475,27 +476,46 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
             __syncthreads();
             return;
         }
-        int size = THREADS;
-        while (size < n)
-            size *= 2;
-        for (int i = tid; i < size; i += THREADS)
-            s.sorted[i] = i < n ? s.list[i] : 0;
-        __syncthreads();
-        for (int k = 2; k <= size; k *= 2)
-            for (int d = k / 2; d > 0; d /= 2) {
-                if (tid < size / 2) {
-                    const int i = 2 * tid - (tid & (d - 1)); // (its partner is d further on)
-                    const u64 x = s.sorted[i], y = s.sorted[i + d];
-                    if ((x < y) == ((i & k) == 0)) {
-                        s.sorted[i] = y;
-                        s.sorted[i + d] = x;
-                    }
-                }
-                if (d > 32 || (d == 1 && k >= 64)) // (up to a distance of 32 a warp stays within its 64 places)
+        // bitonic, falling, two neighbours a thread: exchanged by shuffles within 64 places, beyond through
+        // shared memory (s.list and s.sorted in turn)
+        const int size = n <= THREADS ? THREADS : 2 * THREADS, p0 = 2 * tid;
+        const bool live = p0 < size; // (whole warps)
+        ulonglong2 *at = reinterpret_cast<ulonglong2 *>(s.sorted), *next = reinterpret_cast<ulonglong2 *>(s.list);
+        u64 e[2] = {p0 < n ? s.list[p0] : 0, p0 + 1 < n ? s.list[p0 + 1] : 0};
+        for (int k = 2; k <= size; k *= 2) {
+            const bool falling = (p0 & k) == 0;
+            for (int d = k / 2; d > 1; d /= 2) {
+                u64 o[2] = {0, 0};
+                if (d <= 32) {
+                    if (live)
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+                            o[i] = __shfl_xor_sync(0xffffffffu, e[i], d / 2);
+                } else { // (a buffer's readers have passed the next one's barrier before it is written again)
+                    if (live)
+                        at[tid] = make_ulonglong2(e[0], e[1]);
                     __syncthreads();
-                else
-                    __syncwarp();
+                    if (live) {
+                        const ulonglong2 v = at[tid ^ (d / 2)];
+                        o[0] = v.x, o[1] = v.y;
+                    }
+                    ulonglong2 *const was = at;
+                    at = next, next = was;
+                }
+                const bool larger = ((p0 & d) == 0) == falling;
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    e[i] = larger == (o[i] > e[i]) ? o[i] : e[i];
             }
+            if (falling == (e[0] < e[1])) {
+                const u64 x = e[0];
+                e[0] = e[1], e[1] = x;
+            }
+        }
+        __syncthreads(); // (s.list's and s.sorted's last readers)
+        if (live)
+            reinterpret_cast<ulonglong2 *>(s.sorted)[tid] = make_ulonglong2(e[0], e[1]);
+        __syncthreads();
     };
     auto key_of = [&](u64 entry) { return (uint32_t)(entry >> 32); };
     auto id_of = [&](u64 entry) { return (int)(0xffffffffu - (uint32_t)entry); };
@@ -612,11 +632,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         u64 *list = cl.map_shared_rank(s.list, 0);
         uint32_t *count = cl.map_shared_rank(&s.count, 0);
         const int near = noted ? (int)s.near_count : INT_MAX;
-        if (near <= THREADS) {
-            const u64 entry = tid < near ? s.near[tid] : 0;
-            const float l = Key<TL>::value((uint32_t)(entry >> 32));
-            if (tid < near && l >= from && l < to)
-                list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = entry;
+        if (near <= S::NEAR_MOST) {
+            for (int i = tid; i < near; i += THREADS) {
+                const u64 entry = s.near[i];
+                const float l = Key<TL>::value((uint32_t)(entry >> 32));
+                if (l >= from && l < to)
+                    list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = entry;
+            }
         } else {
             each(from, [&](float l, int id) {
                 if (l < to && (l > cut || id <= last))
@@ -703,14 +725,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         } else if (fresh) { // (few, where the k-th is bounded well: noted, then counted)
             each(from, [&](float l, int id) {
                 const uint32_t at = atomicAdd(&s.near_count, 1u);
-                if (at < THREADS)
+                if (at < S::NEAR_MOST)
                     s.near[at] = (u64)Key<TL>::at_least(l) << 32 | (0xffffffffu - (uint32_t)id);
             });
             __syncthreads();
             const int near = (int)s.near_count;
-            if (near <= THREADS) {
-                if (tid < near)
-                    atomicAdd(&h.lo[bin(Key<TL>::value((uint32_t)(s.near[tid] >> 32)))], 1u);
+            if (near <= S::NEAR_MOST) {
+                for (int i = tid; i < near; i += THREADS)
+                    atomicAdd(&h.lo[bin(Key<TL>::value((uint32_t)(s.near[i] >> 32)))], 1u);
             } else {
                 each(from, [&](float l, int) { atomicAdd(&h.lo[bin(l)], 1u); });
             }
