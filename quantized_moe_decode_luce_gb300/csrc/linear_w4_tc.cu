@@ -79,6 +79,7 @@ struct TcArgs {
     int whole_groups;      // groups of a row that one load may take: 8, 2 or 1
     int nb, tokens;        // columns (a multiple of 16) and tokens of a tile
     int rt, tt;            // tiles of channels, of tokens (fastest)
+    int tile0, tiles;      // of this launch: the first, and the end
     int chunks, stages;    // of a row
     int sk;
     int ns, ds;            // stages of codes, slots of D
@@ -407,7 +408,7 @@ template <int MODE, int GPC, int NBLK> __global__ void __launch_bounds__(Roles<M
     // of K: stages st0 .. st1 - 1.  A last stage's second chunk may lie behind the
     // row: it reads as zeros and has scales of zero.
     const int kg = t.sk > 1 ? (int)cluster_rank() : 0;
-    const int first = (int)(blockIdx.x / (unsigned)t.sk), step = (int)(gridDim.x / (unsigned)t.sk), tiles = t.rt * t.tt;
+    const int first = t.tile0 + (int)(blockIdx.x / (unsigned)t.sk), step = (int)(gridDim.x / (unsigned)t.sk), tiles = t.tiles;
     const int st0 = (int)((long long)t.stages * kg / t.sk), st1 = (int)((long long)t.stages * (kg + 1) / t.sk);
     const int my_tiles = first < tiles ? (tiles - first + step - 1) / step : 0;
     const int total = my_tiles * (st1 - st0); // stages of all tiles, in order (the host keeps sk <= stages)
@@ -870,6 +871,28 @@ Mode mode_of(const W4Args &a)
     return a.x_dtype == LUCE_I8 ? I8 : a.x_dtype == LUCE_BF16 ? BF16 : a.x_dtype == LUCE_F16 && a.out_dtype != LUCE_F32 ? F16 : WHOLE;
 }
 
+// Clocks of a stage, about (8192 x 4096 in groups of 64: 64 columns 2000, 80, whose slots of D take one group, 2900).
+int stage_cost(int gpc, int nb) { return 1000 + nb * (gpc == 1 ? 7 : gpc == 2 ? 16 : 30) + (gpc > 1 && nb > 64 ? 500 : 0); }
+constexpr int LAUNCH_COST = 8000; // clocks of a launch
+// CTAs along K that `tiles` tiles, fewer than SMs, leave room for.
+int split(int tiles, int stages, int sms) { return std::min({SK_MAX, stages, sms / tiles}); }
+// Whether the tiles behind the last whole round get a launch of their own, split along K.
+bool tail_apart(int tiles, int stages, int cost, int sms)
+{
+    const int rest = tiles % sms, sk = rest ? split(rest, stages, sms) : 1;
+    return tiles > sms && sk > 1 && (stages + sk - 1) / sk * (int64_t)cost + LAUNCH_COST < stages * (int64_t)cost;
+}
+int64_t tiles_cost(int64_t tiles, int stages, int cost, int sms)
+{
+    const int rest = (int)(tiles % sms), sk = rest ? split(rest, stages, sms) : 1;
+    const int64_t whole = tiles / sms * stages * (int64_t)cost;
+    if (rest == 0)
+        return whole;
+    if (tiles < sms)
+        return (stages + sk - 1) / sk * (int64_t)cost;
+    return whole + (tail_apart((int)tiles, stages, cost, sms) ? (stages + sk - 1) / sk * (int64_t)cost + LAUNCH_COST : stages * (int64_t)cost);
+}
+
 template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStream_t stream)
 {
     static luce_host::SmemLimit limit;
@@ -891,7 +914,7 @@ template <int MODE, int GPC, int NBLK> luce_status launch_tc(TcArgs &t, cudaStre
         (void)cudaGetLastError();
         return LUCE_ERR_CUDA;
     }
-    const int sms = luce_host::sm_count(), tiles = t.rt * t.tt;
+    const int sms = luce_host::sm_count(), tiles = t.tiles - t.tile0;
     auto config = [&](cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int grid, int sk) {
         luce_host::make_config(cfg, attr, dim3((unsigned)grid), dim3(Roles<MODE, NBLK>::THREADS), SMEM, stream);
         if (sk > 1) {
@@ -938,6 +961,18 @@ template <int MODE, int GPC> luce_status launch_blocks(TcArgs &t, cudaStream_t s
     auto run = [&](auto nblk) {
         constexpr int NBLK = decltype(nblk)::value;
         t.ds = std::min(DS_MAX, (int)(TMEM_COLS - D_COL) / (GB<GPC, NBLK> * t.nb));
+        // whole rounds of tiles, and what is left
+        t.tile0 = 0;
+        t.tiles = t.rt * t.tt;
+        const int sms = luce_host::sm_count(), rest = t.tiles % sms;
+        if (tail_apart(t.tiles, t.stages, stage_cost(GPC, t.nb), sms)) {
+            t.tiles -= rest;
+            const luce_status st = launch_tc<MODE, GPC, NBLK>(t, stream);
+            if (st != LUCE_OK)
+                return st;
+            t.tile0 = t.tiles;
+            t.tiles += rest;
+        }
         return launch_tc<MODE, GPC, NBLK>(t, stream);
     };
     return t.nb <= 32 ? run(std::integral_constant<int, 1>()) : t.nb <= 64 ? run(std::integral_constant<int, 2>()) : run(std::integral_constant<int, 3>());
@@ -963,12 +998,19 @@ luce_status tc_product(const W4Args &a, int group, cudaStream_t stream)
     t.chunks = (a.K + CHUNK - 1) / CHUNK;
     t.stages = (t.chunks + 1) / 2;
     const int parts = mode == WHOLE ? 2 : 1, most = NB_MAX / parts;
-    t.tt = (a.T + most - 1) / most;
-    t.tokens = (a.T + t.tt - 1) / t.tt;
-    t.nb = (t.tokens * parts + 15) / 16 * 16;
     t.rt = (a.N + RM - 1) / RM;
-    if ((int64_t)t.rt * t.tt > INT_MAX / 2)
+    const int fewest = (a.T + most - 1) / most, sms = luce_host::sm_count();
+    if ((int64_t)t.rt * (2 * fewest) > INT_MAX / 2)
         return LUCE_ERR_UNSUPPORTED;
+    // the tokens' tiles that take the least time (300 tokens of 8192 x 4096 in groups of 64: four of 75 54 us)
+    int64_t best = INT64_MAX;
+    for (int tt = fewest; tt <= 2 * fewest && tt <= a.T; tt++) {
+        const int tokens = (a.T + tt - 1) / tt, nb = (tokens * parts + 15) / 16 * 16;
+        const int64_t cost = tiles_cost((int64_t)t.rt * tt, t.stages, stage_cost(gpc, nb), sms);
+        if (cost < best)
+            best = cost, t.tt = tt, t.tokens = tokens, t.nb = nb;
+    }
+    t.tt = (a.T + t.tokens - 1) / t.tokens;
     // shared memory: stages of codes, operands of columns, activations as they come, factors
     const uint32_t es = a.x_dtype == LUCE_F32 ? 4 : a.x_dtype == LUCE_I8 ? 1 : 2, b = RS * (uint32_t)t.nb * 512u;
     const int box = mode == WHOLE ? t.nb / 2 : t.nb;
