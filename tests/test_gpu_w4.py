@@ -178,6 +178,15 @@ def test_many_tiles(T, N, K, group, zero_points, x_dtype):
         same(check_linear(T, N, K, group, zero_points, x_dtype, f32, device_oracle=True), first)
 
 
+# more tiles than SMs, so that those of the last round may be split along K by a second launch
+@pytest.mark.parametrize("T,N,K,group,zero_points,x_dtype", [
+    (200, 4096, 4112, 64, True, bf16), (210, 14001, 1040, 64, False, f16), (515, 4000, 1552, 32, True, bf16), (161, 10000, 2064, 32, True, f32),
+    (300, 8100, 2048, 64, False, i8), (700, 3000, 2080, 128, True, bf16), (97, 20479, 1056, 64, True, bf16), (2049, 1300, 528, 128, False, i8)])
+def test_the_last_tiles(T, N, K, group, zero_points, x_dtype):
+    first = check_linear(T, N, K, group, zero_points, x_dtype, f32, bias=True, gap=5, device_oracle=True)
+    same(check_linear(T, N, K, group, zero_points, x_dtype, f32, bias=True, gap=5, device_oracle=True), first)
+
+
 @pytest.mark.parametrize("T,K", [(1, 16384), (4, 16384), (2, 65536), (20, 65536), (64, 14336), (1, 65520)])
 @pytest.mark.parametrize("x_dtype", [f32, bf16, i8])
 def test_long_rows(T, K, x_dtype):
