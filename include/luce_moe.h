@@ -512,8 +512,13 @@ LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, i
  * z is 8 where there are no zero points.  The products of a group are added in
  * fp32 (exact for int8 activations) and multiplied by the group's scale, the
  * groups' products are added in fp32, the factor and the bias are rounded to
- * fp32 each, then the sum to out_dtype.  The order of the sums depends on the
- * sizes and types alone: a call gives the same bits whenever it is made.
+ * fp32 each, then the sum to out_dtype.  fp32 activations (and fp16 and bf16
+ * ones in small batches, or fp16 for fp32 outputs) enter in fixed point, less at
+ * most 2^-23 of the largest among 128 neighbours of their row.
+ * The order of the sums depends on the sizes, the types and the scales'
+ * alignment alone: a call gives the same bits whenever it is made.  A token with
+ * a NaN or an infinity among its activations has NaN or infinite outputs only;
+ * other tokens' are unaffected, and so are channels by others' scales.
  *
  * A row of codes is kept in chunks of 128 values, 64 bytes: word 4 t + j of a
  * chunk (t, j in 0..3; 32 bits, little-endian) holds the values 32 j + 8 t + i
@@ -542,7 +547,8 @@ LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, i
  *     lies between the rows is left as it was), aligned to the element
  *   w [N][K] fp32, bf16 or fp16, aligned to the element    codes [N][K] bytes
  * Requires K % 16 == 0, 16 <= K <= 65536, group 32, 64 or 128, N >= 1 (N >= 0
- * where a matrix is made), T >= 0, N and T below 2^24; no output may overlap
+ * where a matrix is made), T >= 0, N and T below 2^24 (it may be
+ * LUCE_ERR_UNSUPPORTED where N / 128 times T / 24 exceeds 2^30); no output may overlap
  * an input or another output.  No workspace.  Under programmatic launch
  * nothing is read before the previous kernel is over.
  */
@@ -568,7 +574,8 @@ LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t l
  *   at which the weights that stay, up to and including it, exceed u[r] * Z;
  *   prob[r] = its weight / Z
  * A temperature that is not above zero picks the first token (prob 1), as
- * luce_argmax does.  An infinite one weighs all tokens above -infinity alike.
+ * luce_argmax does; one below 1e-37 counts as 1e-37.  An infinite one weighs all
+ * tokens above -infinity alike.  prob is good to 2^-21 of itself, and 2^-40.
  * Tokens at -infinity have no weight and are never drawn.  A row of them alone
  * has idx 0 and prob 0; a row with a NaN or +infinity has idx 0 and prob NaN.
  * u[r] is taken as within [0, 1): NaN as 0, 1 and more as the last token.

@@ -999,18 +999,18 @@ luce_status tc_product(const W4Args &a, int group, cudaStream_t stream)
     t.stages = (t.chunks + 1) / 2;
     const int parts = mode == WHOLE ? 2 : 1, most = NB_MAX / parts;
     t.rt = (a.N + RM - 1) / RM;
-    const int fewest = (a.T + most - 1) / most, sms = luce_host::sm_count();
-    if ((int64_t)t.rt * (2 * fewest) > INT_MAX / 2)
+    const int sms = luce_host::sm_count();
+    if ((int64_t)t.rt * ((a.T + most / 2 - 1) / (most / 2)) > INT_MAX / 2)
         return LUCE_ERR_UNSUPPORTED;
-    // the tokens' tiles that take the least time (300 tokens of 8192 x 4096 in groups of 64: four of 75 54 us)
+    // the tokens' tiles that take the least time (300 tokens of 8192 x 4096 in groups of 64: four of 75 53.6 us, five of 60 48.7)
     int64_t best = INT64_MAX;
-    for (int tt = fewest; tt <= 2 * fewest && tt <= a.T; tt++) {
-        const int tokens = (a.T + tt - 1) / tt, nb = (tokens * parts + 15) / 16 * 16;
+    for (int cols = NB_MAX; cols >= NB_MAX / 2; cols -= 16) {
+        const int tt = (a.T + cols / parts - 1) / (cols / parts), tokens = (a.T + tt - 1) / tt, nb = (tokens * parts + 15) / 16 * 16;
         const int64_t cost = tiles_cost((int64_t)t.rt * tt, t.stages, stage_cost(gpc, nb), sms);
         if (cost < best)
             best = cost, t.tt = tt, t.tokens = tokens, t.nb = nb;
     }
-    t.tt = (a.T + t.tokens - 1) / t.tokens;
+    t.tt = (a.T + t.tokens - 1) / t.tokens; // (none empty)
     // shared memory: stages of codes, operands of columns, activations as they come, factors
     const uint32_t es = a.x_dtype == LUCE_F32 ? 4 : a.x_dtype == LUCE_I8 ? 1 : 2, b = RS * (uint32_t)t.nb * 512u;
     const int box = mode == WHOLE ? t.nb / 2 : t.nb;

@@ -213,7 +213,7 @@ template <int THREADS> struct Shared {
         alignas(16) u64 sorted[MOST]; // (while no histogram is in use)
     };
     alignas(16) u64 list[MOST]; // the first CTA's tokens: key, and id from the last
-    static constexpr int NEAR_MOST = 2 * THREADS;
+    static constexpr int NEAR_MOST = 512;
     u64 near[NEAR_MOST];     // this CTA's candidates for top-k, the same
     u64 exchange[2][CL_MAX]; // (alternating, for the same reason)
     u64 warp[WARPS], part[64];
@@ -1005,6 +1005,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
         }
     }
 }
+
+constexpr size_t SMEM_CTA = 227 * 1024;
+static_assert(sizeof(Shared<512>) + (V_MAX / CL_PORTABLE + 64) * sizeof(float) <= SMEM_CTA, "a slice of the longest rows");
 
 template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int R, int cl, cudaStream_t stream)
 {

@@ -413,6 +413,8 @@ def test_draws_from_the_largest_vocabularies(V, dtype):
     l, u = logits_of("normal", 3, V, 2).to(dtype), torch.tensor([0.1, 0.5, 0.999])
     for prm in (dict(t=0.8), dict(t=0.8, k=50, p=0.9), dict(t=1.2, p=0.9), dict(k=200000, p=0.99)):
         assert check_draws(l, u, **prm) <= 1
+    l, u = logits_of("normal", 20, V, 3).to(dtype), torch.rand(20, generator=gen(3))  # (rows for clusters of eight CTAs)
+    assert check_draws(l, u, t=0.9, k=40, p=0.95) <= 1
     with pytest.raises(B.LuceError) as e:
         B.luce_sample(torch.zeros((1, 393217), device="cuda"), torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
     assert e.value.status == B.LUCE_ERR_UNSUPPORTED
