@@ -137,13 +137,16 @@ __device__ __forceinline__ void operands(const W4Args &a, int t, int k, bool liv
 // Few columns: a stream of the weights through mma.sync (16 rows x 16 values
 // times 16 values x 8 columns).
 //
-// What bounds it is the weights' way from HBM, for small matrices the latency
-// of getting there, and close behind both the instructions: a chunk of 16 rows
-// takes a warp 8 MMAs, 4 reads of activations and 40 instructions for its codes
-// (72 for normal numbers).
-// So everything else is done once for a unit of U chunks: a warp keeps a unit's codes in registers, requests each chunk of its
-// next one as soon as it has used its place, and the wk warps of a row group
-// take every wk-th unit of a row and join their sums through shared memory.
+// What bounds it is the weights' way from HBM (one int8 token of 129280 x 4096 in
+// groups of 128: 52.1 us, 5.2 TB/s), for small matrices the latency of getting
+// there (2048 x 2048: 3.8 us), and close behind both the instructions: a chunk of
+// 16 rows takes a warp 8 MMAs, 4 reads of activations and 40 instructions for its
+// codes (72 for normal numbers), and twice the MMAs and reads for more than eight
+// columns (five fp32 tokens, groups of 64 with zero points: 97 us).
+// So everything else is done once for a unit of U chunks: a warp keeps a unit's
+// codes in registers, requests each chunk of its next one as soon as it has used
+// its place, and the wk warps of a row group take every wk-th unit of a row and
+// join their sums through shared memory.
 // The packed order lets a lane's 16 bytes of a chunk be its operands of eight
 // MMAs: of word j the values 32 j + 8 (lane % 4) .. + 7, whose activations are
 // 16 bytes too, with every group of 32 values in two MMAs.  The activations stay

@@ -17,12 +17,17 @@
 // columns the weights' way from HBM.
 //
 // Few tiles: sk CTAs of a cluster split K and add their sums through
-// distributed shared memory, in the order of their ranks.
+// distributed shared memory, in the order of their ranks.  Where the last round
+// of many tiles leaves most SMs without one, its tiles are split in that way too,
+// by a launch of their own.
+// 300 bf16 tokens of 8192 x 4096 in groups of 64: 48.7 us; 61 fp16 ones of 4096 x
+// 14336 in groups of 128: 18.5 us.
 //
 // Roles: warp 0 issues the TMA tiles of codes, warp 1 the MMAs, warp 2 the TMA
-// tiles of activations; two groups of four warps convert codes, a chunk of each
-// stage of two; four warps convert activations; eight warps are the epilogue
-// (lane quarter w & 3, every second block of 16 columns).  A wait costs the
+// tiles of activations; groups of four warps convert codes, a chunk of each
+// stage of two (or of every second stage); four warps convert activations where
+// they need it; eight or sixteen warps are the epilogue (lane quarter w & 3, every
+// second or fourth block of 16 columns).  A wait costs the
 // warp that issues the MMAs some 250 clocks even where there is nothing to wait
 // for, and a stage of two chunks about 700 in all: so operands change hands by
 // the stage, A and B behind one barrier, and as many groups' sums as tensor

@@ -40,7 +40,16 @@ __device__ __forceinline__ float scale_value(uint16_t b, bool bf)
 // Value i of a word has its bits 4 (i / 2) + 16 (i % 2) .. + 3.
 __device__ __forceinline__ uint32_t place(uint32_t code, int i) { return code << (4 * (i >> 1) + 16 * (i & 1)); }
 
-template <typename TW>
+// A chunk's row and place in it (64-bit division only for matrices that need it).
+__device__ __forceinline__ int row_of(int64_t c, int chunks, int &at)
+{
+    const int64_t row = c >> 32 ? c / chunks : (uint32_t)c / (uint32_t)chunks;
+    at = (int)(c - row * chunks);
+    return (int)row;
+}
+
+// WIDE: eight values of a row in one or two loads (w 16-byte aligned).
+template <typename TW, bool WIDE>
 __global__ void __launch_bounds__(THREADS)
     k_quantize_w4(const TW *w, int N, int K, int chunks, int group, uint32_t *wq, uint16_t *scale, bool bf, uint8_t *zeros)
 {
@@ -48,13 +57,26 @@ __global__ void __launch_bounds__(THREADS)
     pdl_trigger();
     const int64_t c = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 4; // chunk of the matrix
     const bool live = c < (int64_t)N * chunks;
-    const int row = live ? (int)(c / chunks) : 0, i0 = threadIdx.x & 15;
-    const int k = live ? (int)(c % chunks) * CHUNK + 8 * i0 : K; // first value of this thread
+    int at = 0;
+    const int row = live ? row_of(c, chunks, at) : 0, i0 = threadIdx.x & 15;
+    const int k = live ? at * CHUNK + 8 * i0 : K; // first value of this thread (K is a multiple of 16)
+    struct __align__(16) Eight { TW v[8]; };
+    Eight x = {};
+    if (k < K) {
+        const TW *p = w + (int64_t)row * K + k;
+        if constexpr (WIDE) {
+            x = *reinterpret_cast<const Eight *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x.v[i] = p[i];
+        }
+    }
     float v[8], lo = 0.0f, hi = 0.0f;
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        v[i] = k + i < K ? to_float(w[(int64_t)row * K + k + i]) : 0.0f;
+        v[i] = to_float(x.v[i]);
         odd |= !isfinite(v[i]);
         lo = fminf(lo, v[i]);
         hi = fmaxf(hi, v[i]);
@@ -70,12 +92,33 @@ __global__ void __launch_bounds__(THREADS)
     if (odd)
         s = bf ? 0x7fffu : 0x7fffu; // NaN in either type
     const float z = !zeros ? 8.0f : flat ? 0.0f : fminf(roundf(__fdiv_rn(-lo, d)), 15.0f);
-    uint32_t word = 0;
+    // round(fl(v / d)) is the whole number nearest v rinv wherever that is not within 1e-4 of half way between
+    // two (up to 64 rinv = fl(1 / d) moves it by less than 2e-5): the sum with
+    // 1.5 2^23 leaves it in the low bits.  Threads with a value near half way, or a larger one (of a d that its type
+    // keeps from being what it should, or whose reciprocal overflows), divide.
+    const float rinv = __frcp_rn(d);
+    constexpr float MAGIC = 12582912.0f;
+    int n[8];
+    bool near_half = false;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const float q = flat ? z : roundf(__fdiv_rn(v[i], d)) + z;
-        word |= place((uint32_t)fminf(fmaxf(q, zeros ? 0.0f : 1.0f), 15.0f), i);
+        const float r = fmaf(v[i], rinv, MAGIC), whole = __fsub_rn(r, MAGIC);
+        n[i] = __float_as_int(r) - 0x4B400000;
+        near_half |= !(fabsf(fmaf(v[i], rinv, -whole)) <= 0.4999f && fabsf(whole) <= 64.0f);
     }
+    if (flat) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            n[i] = 0;
+    } else if (near_half) {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            n[i] = (int)fminf(fmaxf(roundf(__fdiv_rn(v[i], d)), -64.0f), 64.0f);
+    }
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+        word |= place((uint32_t)min(max(n[i] + (int)z, zeros ? 0 : 1), 15), i);
     if (!live)
         return;
     wq[c * (CHUNK / 8) + 4 * (i0 & 3) + (i0 >> 2)] = word;
@@ -87,6 +130,7 @@ __global__ void __launch_bounds__(THREADS)
     }
 }
 
+template <bool WIDE> // (codes 8-byte aligned)
 __global__ void __launch_bounds__(THREADS) k_pack_w4(const uint8_t *codes, int N, int K, int chunks, uint32_t *wq)
 {
     pdl_wait();
@@ -94,12 +138,24 @@ __global__ void __launch_bounds__(THREADS) k_pack_w4(const uint8_t *codes, int N
     const int64_t c = ((int64_t)blockIdx.x * THREADS + threadIdx.x) >> 4;
     if (c >= (int64_t)N * chunks)
         return;
-    const int row = (int)(c / chunks), i0 = threadIdx.x & 15, k = (int)(c % chunks) * CHUNK + 8 * i0;
+    int at;
+    const int row = row_of(c, chunks, at), i0 = threadIdx.x & 15, k = at * CHUNK + 8 * i0;
+    struct __align__(8) Eight { uint8_t v[8]; };
+    Eight x = {};
+    if (k < K) {
+        const uint8_t *p = codes + (int64_t)row * K + k;
+        if constexpr (WIDE) {
+            x = *reinterpret_cast<const Eight *>(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                x.v[i] = p[i];
+        }
+    }
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++)
-        if (k + i < K)
-            word |= place(codes[(int64_t)row * K + k + i] & 15u, i);
+        word |= place(x.v[i] & 15u, i);
     wq[c * (CHUNK / 8) + 4 * (i0 & 3) + (i0 >> 2)] = word;
 }
 
@@ -134,7 +190,7 @@ extern "C" luce_status luce_quantize_w4(const void *w, luce_dtype dtype, int N, 
         return LUCE_ERR_INVALID_ARG;
     auto run = [&](auto element) {
         using TW = decltype(element);
-        return luce_host::launch(k_quantize_w4<TW>, dim3(blocks_of(N, chunks)), dim3(THREADS), 0, luce_host::as_stream(stream),
+        return luce_host::launch(aligned(w, 16) ? k_quantize_w4<TW, true> : k_quantize_w4<TW, false>, dim3(blocks_of(N, chunks)), dim3(THREADS), 0, luce_host::as_stream(stream),
                                  (const TW *)w, N, K, chunks, group, (uint32_t *)wq, (uint16_t *)w_scale,
                                  scale_dtype == LUCE_BF16, zeros);
     };
@@ -151,6 +207,6 @@ extern "C" luce_status luce_pack_w4(const uint8_t *codes, int N, int K, uint8_t 
     if (!codes || !wq || !luce_host::aligned(wq, 16) ||
         overlap(codes, (size_t)N * K, wq, (size_t)N * chunks * CHUNK_BYTES))
         return LUCE_ERR_INVALID_ARG;
-    return luce_host::launch(k_pack_w4, dim3(blocks_of(N, chunks)), dim3(THREADS), 0, luce_host::as_stream(stream), codes, N,
+    return luce_host::launch(luce_host::aligned(codes, 8) ? k_pack_w4<true> : k_pack_w4<false>, dim3(blocks_of(N, chunks)), dim3(THREADS), 0, luce_host::as_stream(stream), codes, N,
                              K, chunks, (uint32_t *)wq);
 }

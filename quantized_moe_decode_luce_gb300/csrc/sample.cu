@@ -4,7 +4,11 @@
 //
 // A cluster of CTAs takes a row: every CTA keeps a slice of it in shared
 // memory, in the logits' own type, so the row is read from memory once and
-// everything after the first pass runs on the chip.
+// everything after the first pass runs on the chip.  What bounds a row is the
+// way from barrier to barrier (top-k 50 with top-p of 129280 logits, clusters of
+// 16: 11.2 us; 64 rows of 32000, all kinds: 40.4), for many rows how many clusters
+// run at once and the passes over all logits (256 bf16 rows of 129280 with top-k
+// 64 and top-p: 51 us; 128 fp32 rows of 151936 with top-p alone: 140).
 //
 // Both filters look for the token at which those before it, by falling logits,
 // reach a count (top-k) or a weight (top-p).  A histogram over the logits'

@@ -86,6 +86,32 @@ def test_quantize_of_unusual_groups(sdt, zero_points):
         check_quantize(w, group, sdt, zero_points)
 
 
+# codes at and beside half way between two, of rows aligned for wide loads and not, and of scales that their type holds down
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("dt,shift", [(f32, 0), (f32, 1), (bf16, 0), (bf16, 1), (f16, 0), (f16, 8)])
+def test_quantize_half_way(dt, shift, zero_points):
+    N, K = 65, 272
+    half = torch.randint(-14, 15, (N, K), generator=gen(5)).float() * 0.5
+    half[:, ::16] = 7.0
+    w = half * 2.0 ** torch.randint(-12, 5, (N, 1), generator=gen(6)).float()
+    w[::5] *= 1.0 + 2.0 ** -9
+    w[1::5] *= torch.rand((13, K), generator=gen(7)) * 2.0 ** -7 + 1.0
+    w = w.to(dt)
+    if dt != f16:
+        w[2::5] *= 2.0 ** torch.randint(16, 48, (13, K), generator=gen(8)).to(dt)
+    for group in (32, 64, 128):
+        for sdt in (f16, bf16):
+            check_quantize(w, group, sdt, zero_points, shift)
+
+
+@pytest.mark.parametrize("N,K", [(1, 32), (17, 144)])
+def test_pack_aligned(N, K):
+    q = torch.randint(0, 16, (N, K), generator=gen(K), dtype=torch.uint8)
+    wq = torch.full((N, O.row_bytes(K)), 77, dtype=torch.uint8, device="cuda")
+    B.luce_pack_w4(q.cuda(), wq)
+    same(wq, O.pack(q))
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (9, 112), (40, 400)])
 def test_pack(N, K):
     q = torch.randint(0, 256, (N, K), generator=gen(K), dtype=torch.uint8)  # (of other bits the low four count)
