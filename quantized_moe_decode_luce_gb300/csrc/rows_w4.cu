@@ -4,7 +4,10 @@
 // A half-warp takes a chunk of 128 values of a row, a thread eight of them:
 // thread 4 j + t the values 32 j + 8 t .. + 7, which are word 4 t + j of the
 // chunk.  A group of 32, 64 or 128 values is 4, 8 or 16 threads, which join
-// their extremes by shuffles.  Made once for a matrix; bound by reading it.
+// their extremes by shuffles.  Made once for a matrix; bound by instructions, a
+// group's extremes and divisions for eight values a thread (4096 x 4096 bf16
+// 29.8 us, floor 6.2; packing 9.8, floor 3.7).  Four chunks to a thread at once,
+// whose waits overlap but which need 125 registers, took 51.8.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -96,6 +99,7 @@ __global__ void __launch_bounds__(THREADS)
     // two (up to 64 rinv = fl(1 / d) moves it by less than 2e-5): the sum with
     // 1.5 2^23 leaves it in the low bits.  Threads with a value near half way, or a larger one (of a d that its type
     // keeps from being what it should, or whose reciprocal overflows), divide.
+    // (8192 x 4144 fp16 in groups of 32: 57 us, with divisions and narrow loads 68.)
     const float rinv = __frcp_rn(d);
     constexpr float MAGIC = 12582912.0f;
     int n[8];
