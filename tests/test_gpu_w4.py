@@ -213,6 +213,30 @@ def test_the_last_tiles(T, N, K, group, zero_points, x_dtype):
     same(check_linear(T, N, K, group, zero_points, x_dtype, f32, bias=True, gap=5, device_oracle=True), first)
 
 
+def test_the_last_tiles_started_early():
+    # each product's activations are the one's before, two launches each: the same bits with programmatic launch as without
+    T, N = 200, 4096
+    q, s, z = weights(N, N, 64, True, f16, 3)
+    w = LinearW4(O.pack(q).cuda(), (s * 0.05).cuda(), N, 64, z.cuda())
+    x = activations(T, N, bf16, 4).cuda()
+
+    def chain():
+        outs = [x] + [torch.zeros((T, N), dtype=bf16, device="cuda") for _ in range(4)]
+        for a, b in zip(outs, outs[1:]):
+            w.run(a, None, b)
+        torch.cuda.synchronize()
+        return outs[1:]
+
+    want = chain()
+    B.luce_set_pdl(True)
+    try:
+        for _ in range(10):
+            for a, b in zip(chain(), want):
+                same(a, b)
+    finally:
+        B.luce_set_pdl(False)
+
+
 @pytest.mark.parametrize("T,K", [(1, 16384), (4, 16384), (2, 65536), (20, 65536), (64, 14336), (1, 65520)])
 @pytest.mark.parametrize("x_dtype", [f32, bf16, i8])
 def test_long_rows(T, K, x_dtype):
