@@ -631,16 +631,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 
     // -------------------------------------------------------------- sets of tokens
     // Tokens that stay, of logits from `from` to below `to`, into the first CTA's list (at
-    // most MOST).  `noted`: this CTA's candidates are in s.near, unless there are too many.
-    auto collect = [&](bool noted, float from, float to) {
+    // most MOST).  `noted`: those of this CTA are all in s.near, and `among` says which they are.
+    auto collect = [&](bool noted, auto &&among, float from, float to) {
         u64 *list = cl.map_shared_rank(s.list, 0);
         uint32_t *count = cl.map_shared_rank(&s.count, 0);
-        const int near = noted ? (int)s.near_count : INT_MAX;
-        if (near <= S::NEAR_MOST) {
+        if (noted) {
+            const int near = (int)s.near_count;
             for (int i = tid; i < near; i += THREADS) {
                 const u64 entry = s.near[i];
-                const float l = Key<TL>::value((uint32_t)(entry >> 32));
-                if (l >= from && l < to)
+                if (among(Key<TL>::value((uint32_t)(entry >> 32))))
                     list[min(atomicAdd(count, 1u), (uint32_t)MOST - 1)] = entry;
             }
         } else {
@@ -883,9 +882,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 }
                 prefix = prefix << DIGIT | f.bin;
                 above = f.above;
-                edges((int)((prefix + 1) << bits), (int)(prefix << bits), from, to);
-                if (fresh && f.upto <= MOST) {
-                    collect(!by_weight, from, INFINITY);
+                // (a CTA that has noted its candidates tells them by their distance)
+                const bool few = fresh && f.upto <= MOST, noted = fresh && !by_weight && s.near_count <= S::NEAR_MOST;
+                auto among = [&](float l) {
+                    const uint32_t b = (uint32_t)place(l) >> bits;
+                    return few ? b <= prefix : b == prefix;
+                };
+                if (!noted || !(few || f.inside <= MOST))
+                    edges((int)((prefix + 1) << bits), (int)(prefix << bits), from, to);
+                if (few) {
+                    collect(noted, among, from, INFINITY);
                     if (rank == 0) {
                         const int n = min((int)s.count, MOST);
                         by_first(n, [&](auto one) { draw_few(one, n, by_weight ? n : min(top_k, n), by_weight ? want : 0); });
@@ -893,7 +899,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                     return true;
                 }
                 if (f.inside <= MOST) {
-                    collect(!by_weight && fresh, from, to);
+                    collect(noted, among, from, to);
                     if (rank == 0) {
                         const int n = min((int)s.count, MOST);
                         by_first(n, [&](auto one) { cut_list(one, n, by_weight, above, want); });
