@@ -6,9 +6,9 @@
 // memory, in the logits' own type, so the row is read from memory once and
 // everything after the first pass runs on the chip.  What bounds a row is the
 // way from barrier to barrier (top-k 50 with top-p of 129280 logits, clusters of
-// 16: 11.2 us; 64 rows of 32000, all kinds: 40.4), for many rows how many clusters
+// 16: 10.6 us; 64 rows of 32000, all kinds: 40.5), for many rows how many clusters
 // run at once and the passes over all logits (256 bf16 rows of 129280 with top-k
-// 64 and top-p: 51 us; 128 fp32 rows of 151936 with top-p alone: 140).
+// 64 and top-p: 50.3 us; 128 fp32 rows of 151936 with top-p alone: 140).
 //
 // Both filters look for the token at which those before it, by falling logits,
 // reach a count (top-k) or a weight (top-p).  A histogram over the logits'
