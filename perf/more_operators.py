@@ -129,8 +129,7 @@ def prepare(case, seed):
     l = torch.randn((R, V), generator=g, device="cuda") * 2.0
     # the plausible continuations stand out of the rest, as in a trained model's logits
     n = min(40, V // 4)
-    # (each id once, of a stretch of its own: of two writes to one place either may win)
-    ids = torch.arange(n, device="cuda") * V // n + torch.randint(0, V // n, (R, n), generator=g, device="cuda")
+    ids = torch.randint(0, V, (R, n), generator=g, device="cuda")
     l.scatter_(1, ids, 14.0 - torch.rand((R, n), generator=g, device="cuda").pow_(0.5) * 8.0)
     l[:, 7::13] = -math.inf  # what a grammar has masked
     s["logits"] = l.to(DTYPES[case["dtype"]])
