@@ -49,6 +49,7 @@ namespace cg = cooperative_groups;
 constexpr int CL_MAX = 16, CL_PORTABLE = 8; // CTAs of a cluster at most, and without asking for more
 constexpr float NEAR = 24.0f;            // octaves of weight whose tokens are binned for top-p at first
 constexpr int64_t V_MAX = 393216;        // fp32 slices of eight CTAs within shared memory
+constexpr uint32_t TOO_MANY = 1u << 20;  // tokens: above V_MAX, and for 1024 bins below 2^32
 typedef unsigned long long u64;
 
 struct SampleArgs {
@@ -784,12 +785,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 sum += one[c];
             }
         }
-        // (the tokens of a bin: no more than its weight in the lightest of them)
+        // The tokens of a bin: no more than its weight over the lightest of them, which the rounding to whole units may
+        // leave one below its real weight.  Where that is no unit at all they may be any number, and the bin is divided
+        // further.
         uint32_t n[PER] = {(uint32_t)w[0], (uint32_t)w[1]};
         if (by_weight)
 #pragma unroll
-            for (int i = 0; i < PER; i++)
-                n[i] = w[i] == 0 ? 0u : (uint32_t)fminf(__ull2float_ru(w[i]) * lightest(tid * PER + i) + 1.0f, 4194304.0f);
+            for (int i = 0; i < PER; i++) {
+                const float units = lightest(tid * PER + i) - 1.0f;
+                n[i] = w[i] == 0 ? 0u : units >= 1.0f ? (uint32_t)fminf(__fmul_ru(__ull2float_ru(w[i]), __frcp_ru(units)), (float)TOO_MANY) : TOO_MANY;
+            }
         const u64 all = w[0] + w[1], in_warp = warp_scan(all, lane);
         const uint32_t count = n[0] + n[1], n_warp = warp_scan(count, lane);
         if (lane == 31) {
@@ -832,10 +837,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 const float x = (weigh.M4 - 0.25f * l) * scale;
                 return x < FULL ? (int)x : all_in ? (1 << QBITS) - 1 : -1;
             };
-            // one over the weight at the end of a stretch of `bits` bits (and a hundredth, for all roundings)
+            // the weight at the end of a stretch of `bits` bits (less a hundredth, for all roundings), not yet in whole units
             const float octaves = scale > 0.0f ? c_hi / scale : 0.0f;
-            auto over_end = [&](uint32_t stretch, int bits) {
-                return scale > 0.0f ? 1.01f * exp2f(fminf(octaves * ((float)stretch + 1.0f) * (float)(1 << bits) - (float)(31 + a.sh), 120.0f)) : 1.0f;
+            auto end_weight = [&](uint32_t stretch, int bits) {
+                return scale > 0.0f ? 0.99f * exp2f((float)(31 + a.sh) - octaves * ((float)stretch + 1.0f) * (float)(1 << bits)) : 0.0f;
             };
             // the smallest logits at a distance below q0 (from 1), and below q1 (0: none):
             // two warps find them, 32 keys at a time
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                                          const int q = place(l);
                                          return q < 0 ? -1 : q >> bits & (BINS - 1);
                                      },
-                                     [&](uint32_t b) { return over_end(prefix << DIGIT | b, bits); });
+                                     [&](uint32_t b) { return end_weight(prefix << DIGIT | b, bits); });
                 if (fresh && want > f.total) {
                     if (all_in)
                         return false; // all stay
@@ -921,7 +926,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
                 const int shift = max(0, 32 - __clz(hi - lo) - DIGIT);
                 const Found f = find(by_weight, false, Key<TL>::value(lo), hi == top ? INFINITY : Key<TL>::value(hi + 1), above,
                                      [&](u64) { return want; }, [&](float l) { return (int)((hi - Key<TL>::at_least(l)) >> shift); },
-                                     [&](uint32_t) { return 1.0f; });
+                                     [&](uint32_t) { return 0.0f; });
                 above = f.above;
                 hi -= f.bin << shift;
                 if (shift == 0) { // one key: how many of its ties stay

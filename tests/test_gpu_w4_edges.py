@@ -1,0 +1,102 @@
+"""GPU: draws at the ends of their ranges: top-p just below 1 over long flat tails."""
+import math
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+from quantized_moe_decode_luce_gb300 import binding as B
+from test_gpu_head import _lib, _no_device_faults, bf16, f16, f32, gen  # noqa: F401 (the fixtures hold here)
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------- draws in whole units
+# The weights of a row whose largest logit is 0, at temperature 1, are whole multiples of 2^-L, rounded down: 2^L for the
+# largest. Where no weight is near a whole number (the library's are within 2^-29 of theirs) every sum is known, and so is
+# every decision: nothing is left to a margin.
+def units_of(l):
+    V = l.size
+    L = min(62, 63 - (V - 1).bit_length())
+    with np.errstate(divide="ignore"):
+        w = np.exp2(L + l.astype(np.float64) / math.log(2.0))
+    rest = np.abs(w - np.rint(w))
+    assert np.all((l == 0) | (w == 0) | (rest > 1e-6 * np.maximum(w, 1.0)))
+    return np.where(l == 0, 1 << L, np.floor(w).astype(np.int64)).astype(np.int64)
+
+
+def draw_in_units(l, us, top_p, top_k=0):
+    """[(id, weight / total)] for every u."""
+    w = units_of(l)
+    order = np.lexsort((np.arange(l.size), -l))
+    if 0 < top_k < l.size:
+        order = order[:top_k]
+    upto = np.cumsum(w[order])
+    want = max(1, math.ceil(Fraction(float(np.float32(top_p))) * int(upto[-1])))
+    ids = np.sort(order[upto - w[order] < want])
+    upto = np.cumsum(w[ids])
+    total, out = int(upto[-1]), []
+    for u in us:
+        f = float(np.float32(u))
+        target = total - 1 if f >= 1 else math.floor(Fraction(f) * total)
+        i = int(np.searchsorted(upto, target, side="right"))
+        out.append((int(ids[i]), int(w[ids[i]]) / total))
+    return out
+
+
+def check_units(row, top_p, top_k=0, copies=1):
+    """One row for every random number, and that `copies` times over, in one call; the same bits in ten calls."""
+    us = [0.0, 0.25, 0.5, 0.999, 1.0 - 2.0 ** -23, 1.0 - 2.0 ** -24, 1.0] * copies
+    want = draw_in_units(row.float().numpy(), us[:7], top_p, top_k) * copies
+    R = len(us)
+    l, u = row.cuda().expand(R, -1).contiguous(), torch.tensor(us, device="cuda")
+    p = torch.full((R,), top_p, device="cuda")
+    k = torch.full((R,), top_k, dtype=torch.int32, device="cuda") if top_k else None
+    for _ in range(10):
+        idx, prob = torch.full((R,), -9, dtype=torch.int32, device="cuda"), torch.full((R,), -9.0, device="cuda")
+        B.luce_sample(l, u, idx, prob, None, k, p)
+        torch.cuda.synchronize()
+        assert idx.tolist() == [i for i, _ in want]
+        # the weight and the total are rounded to fp32, and so is their quotient: 3 2^-24
+        assert all(abs(a - q) <= q * 2.0 ** -22 for a, (_, q) in zip(prob.tolist(), want))
+
+
+def tail_row(V, parts, first_at, seed):
+    """A token at 0, and for each (n, w) n tokens whose weight is w units, at places of their own; no others."""
+    L = min(62, 63 - (V - 1).bit_length())
+    l = torch.full((V,), -math.inf)
+    places = torch.randperm(V, generator=gen(seed))
+    places = places[places != first_at]
+    at = 0
+    for n, w in parts:
+        l[places[at:at + n]] = math.log(w) - L * math.log(2.0)
+        at += n
+    l[first_at] = 0.0
+    return l
+
+
+# The weights stand a little below whole numbers: counted by their real size, a bin holds fewer tokens than it does.
+# (Clusters of 16 CTAs and of eight; CTAs of 512 threads for the first two, of 256 for the last two.)
+@pytest.mark.parametrize("copies", [1, 3])
+@pytest.mark.parametrize("first_at", [0, 77777, -1])
+@pytest.mark.parametrize("V,parts,top_p", [
+    (393216, [(1200, 3.95), (349000, 3.1)], 1.0 - 2.0 ** -24), (393216, [(1500, 3.97), (349400, 3.1)], 1.0 - 2.0 ** -24),
+    (129280, [(518, 33.95), (127000, 33.05)], 1.0 - 2.0 ** -24), (129280, [(3000, 34.9), (125000, 33.9)], 1.0 - 2.0 ** -24)])
+def test_top_p_over_a_flat_tail(V, parts, top_p, first_at, copies):
+    check_units(tail_row(V, parts, first_at % V, 1), top_p, copies=copies)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16, f16])
+@pytest.mark.parametrize("most", [1.9, 8.0, 100.0])
+@pytest.mark.parametrize("bits", [20, 22, 23, 24])
+@pytest.mark.parametrize("V", [393216, 250000, 129280])
+def test_top_p_over_a_tail_of_few_units(V, bits, most, dtype):
+    L = 63 - (V - 1).bit_length()
+    units = torch.exp(torch.rand(V, generator=gen(bits)) * math.log(most)) * 1.01
+    l = (units.log() - L * math.log(2.0)).to(dtype)
+    w = np.exp2(L + l.double().numpy() / math.log(2.0))
+    l[torch.from_numpy(np.abs(w - np.rint(w)) < 1e-4)] = -math.inf
+    l[V // 3] = 0.0
+    check_units(l, 1.0 - 2.0 ** -bits)
+    check_units(l, 1.0 - 2.0 ** -bits, top_k=V // 2)
