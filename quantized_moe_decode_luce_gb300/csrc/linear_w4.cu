@@ -363,10 +363,11 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
                                 acc[n][2] = fmaf(sc[1][gi], fmaf(sum[n][2], f.x, z1 * f.y), acc[n][2]);
                                 acc[n][3] = fmaf(sc[1][gi], fmaf(sum[n][3], f.z, z1 * f.w), acc[n][3]);
                             } else {
-                                acc[n][0] = fmaf(sc[0][gi] * f.x, sum[n][0], acc[n][0]);
-                                acc[n][1] = fmaf(sc[0][gi] * f.z, sum[n][1], acc[n][1]);
-                                acc[n][2] = fmaf(sc[1][gi] * f.x, sum[n][2], acc[n][2]);
-                                acc[n][3] = fmaf(sc[1][gi] * f.z, sum[n][3], acc[n][3]);
+                                // (the factor first: its product with a scale may leave fp32's range, 2^26 times it cannot)
+                                acc[n][0] = fmaf(sc[0][gi], sum[n][0] * f.x, acc[n][0]);
+                                acc[n][1] = fmaf(sc[0][gi], sum[n][1] * f.z, acc[n][1]);
+                                acc[n][2] = fmaf(sc[1][gi], sum[n][2] * f.x, acc[n][2]);
+                                acc[n][3] = fmaf(sc[1][gi], sum[n][3] * f.z, acc[n][3]);
                             }
                         }
                     }

@@ -1,4 +1,5 @@
-"""GPU: draws at the ends of their ranges: top-p just below 1 over long flat tails."""
+"""GPU: draws and 4-bit products at the ends of their ranges: top-p just below 1 over long flat tails, activations and
+scales near fp32's smallest numbers."""
 import math
 from fractions import Fraction
 
@@ -6,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import w4 as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from test_gpu_head import _lib, _no_device_faults, bf16, f16, f32, gen  # noqa: F401 (the fixtures hold here)
 
@@ -100,3 +102,23 @@ def test_top_p_over_a_tail_of_few_units(V, bits, most, dtype):
     l[V // 3] = 0.0
     check_units(l, 1.0 - 2.0 ** -bits)
     check_units(l, 1.0 - 2.0 ** -bits, top_k=V // 2)
+
+
+# ----------------------------------------------------------------------------- products
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("T", [5, 8, 12, 40])
+@pytest.mark.parametrize("x_dtype,x_size,s_size", [(bf16, -98, -20), (bf16, -100, -16), (f16, -16, -96)])
+def test_small_activations_and_scales(T, x_dtype, x_size, s_size, zero_points):
+    N, K, group = 60, 512, 64
+    x = (torch.randn((T, K), generator=gen(T)).clamp(-4, 4) * 2.0 ** x_size).to(x_dtype)
+    q = torch.randint(0, 16, (N, K), generator=gen(1), dtype=torch.uint8)
+    s = ((torch.rand((N, K // group), generator=gen(2)) + 0.5) * 2.0 ** s_size).to(bf16)
+    z = torch.randint(0, 16, (N, K // group), generator=gen(3), dtype=torch.uint8) if zero_points else None
+    out = torch.empty((T, N), dtype=bf16, device="cuda")
+    B.luce_linear_w4(x.cuda(), None, O.pack(q).cuda(), s.cuda(), None if z is None else z.cuda(), group, None, out)
+    torch.cuda.synchronize()
+    y, terms, _ = O.linear(x, None, q, s, z, group)
+    # the output's rounding, half a step of 2^-7 of it; 2^-19 of the terms for the tensor cores' sums, 2^-24 for each of
+    # eight groups and 24 further operations; sums of groups are kept 2^-14 of their size, good to 2^-150 2^14 each
+    tol = 1.001 * 2.0 ** -8 * y.abs() + (2.0 ** -19 + 32 * 2.0 ** -24) * terms + 8 * 2.0 ** -136
+    assert terms.max() < 2.0 ** -90 and torch.all((out.cpu().double() - y).abs() <= tol)
