@@ -172,7 +172,7 @@ struct Weigh {
             r = fmaf(-l, c_hi, A1 - (t - magic)) + fmaf(-l, c_lo, A2);
         } else {
             const float b = -0.25f * l, d = M4 + b, bp = d - M4, e = (M4 - (d - bp)) + (b - bp); // M4 + b = d + e
-            const float zh = d * c4_hi, zl = fmaf(d, c4_hi, -zh) + fmaf(d, c4_lo, e * c4_hi);
+            const float zh = __fmul_rn(d, c4_hi), zl = fmaf(d, c4_hi, -zh) + fmaf(d, c4_lo, e * c4_hi);
             t = zh + magic;
             r = (zh - (t - magic)) + zl;
         }

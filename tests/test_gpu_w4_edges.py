@@ -1,5 +1,5 @@
-"""GPU: draws and 4-bit products at the ends of their ranges: top-p just below 1 over long flat tails, activations and
-scales near fp32's smallest numbers."""
+"""GPU: draws and 4-bit products at the ends of their ranges: top-p just below 1 over long flat tails, small
+temperatures, activations and scales near fp32's smallest numbers."""
 import math
 from fractions import Fraction
 
@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import draw as D
 from oracle import w4 as O
 from quantized_moe_decode_luce_gb300 import binding as B
 from test_gpu_head import _lib, _no_device_faults, bf16, f16, f32, gen  # noqa: F401 (the fixtures hold here)
@@ -102,6 +103,24 @@ def test_top_p_over_a_tail_of_few_units(V, bits, most, dtype):
     l[V // 3] = 0.0
     check_units(l, 1.0 - 2.0 ** -bits)
     check_units(l, 1.0 - 2.0 ** -bits, top_k=V // 2)
+
+
+# ----------------------------------------------------------------------------- small temperatures
+@pytest.mark.parametrize("M,t", [(100.0, 1e-3), (-37.0, 1e-3), (5.0, 1e-4), (3e4, 0.5), (12345.0, 1e-1)])
+def test_probabilities_at_small_temperatures(M, t):
+    # two tokens 1 to 38 octaves of weight apart; u = 1 draws the second
+    R = 64
+    l = torch.empty((R, 2))
+    l[:, 0] = M
+    l[:, 1] = torch.from_numpy(M - np.linspace(1.0, 38.0, R) * math.log(2.0) * t).float()
+    assert torch.all(l[:, 1] < M)
+    idx, prob = torch.empty(R, dtype=torch.int32, device="cuda"), torch.empty(R, device="cuda")
+    B.luce_sample(l.cuda(), torch.ones(R, device="cuda"), idx, prob, torch.full((R,), t, device="cuda"))
+    torch.cuda.synchronize()
+    for r in range(R):
+        i, q, _ = D.draw(l[r].double().numpy(), 1.0, float(np.float32(t)))
+        # weights within 2^-29 of theirs, or a unit of 2^-62 of weights above 2^-39; three roundings to fp32 of 2^-24
+        assert int(idx[r]) == i == 1 and abs(prob[r].item() - q) <= q * 2.0 ** -22, (r, prob[r].item() / q - 1)
 
 
 # ----------------------------------------------------------------------------- products
