@@ -144,6 +144,8 @@ class LinearW4:
 
     def run(self, x, x_scale, out, stream=None) -> torch.Tensor:
         """x [T, K] int8 with x_scale [T], or fp32, bf16 or fp16 with None."""
+        if x.shape[-1] != self.K:  # (rows of packed codes do not tell K: they are whole chunks)
+            raise ValueError(f"the projection takes {self.K} values, got {x.shape[-1]}")
         B.luce_linear_w4(x, x_scale, self.wq, self.w_scale, self.zeros, self.group, self.bias, out, stream)
         return out
 
