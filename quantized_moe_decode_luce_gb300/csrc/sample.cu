@@ -1024,9 +1024,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 constexpr size_t SMEM_CTA = 227 * 1024;
 static_assert(sizeof(Shared<512>) + (V_MAX / CL_PORTABLE + 64) * sizeof(float) <= SMEM_CTA, "a slice of the longest rows");
 
-template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int R, int cl, cudaStream_t stream)
+template <typename TL, int THREADS> luce_host::SmemLimit &smem_limit()
 {
     static luce_host::SmemLimit limit;
+    return limit;
+}
+
+void cluster_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int cl, int R, int threads, size_t smem, cudaStream_t stream)
+{
+    luce_host::make_config(cfg, attr, dim3((unsigned)cl, (unsigned)R), dim3((unsigned)threads), smem, stream);
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cl;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs].val.clusterDim.z = 1;
+    cfg.numAttrs++;
+}
+
+template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int R, int cl, cudaStream_t stream)
+{
+    luce_host::SmemLimit &limit = smem_limit<TL, THREADS>();
     const auto kern = k_sample<TL, THREADS>;
     const size_t smem = (size_t)a.slice * sizeof(TL);
     if (smem + sizeof(Shared<THREADS>) > 48 * 1024 && limit.raise(kern, smem) != cudaSuccess) {
@@ -1035,12 +1051,7 @@ template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int 
     }
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    luce_host::make_config(cfg, attr, dim3((unsigned)cl, (unsigned)R), dim3(THREADS), smem, stream);
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cl;
-    attr[cfg.numAttrs].val.clusterDim.y = 1;
-    attr[cfg.numAttrs].val.clusterDim.z = 1;
-    cfg.numAttrs++;
+    cluster_config(cfg, attr, cl, R, THREADS, smem, stream);
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
         (void)cudaGetLastError();
         limit.forget();
@@ -1049,7 +1060,32 @@ template <typename TL, int THREADS> luce_status launch_sample(SampleArgs a, int 
     return LUCE_OK;
 }
 
-// Whether the current device takes clusters of CL_MAX CTAs (asked once per device).
+// Places of a CTA where n of them share a row of V logits, in whole vectors of every warp.
+template <typename TL> int slice_of(int64_t V, int n, int warps)
+{
+    constexpr int VEC = 16 / sizeof(TL);
+    const int unit = VEC * warps;
+    return (int)((V + VEC - 1 + n - 1) / n + unit - 1) / unit * unit;
+}
+constexpr size_t QUARTER = 56 * 1024; // of an SM's shared memory
+
+// Whether the current device holds a cluster of CL_MAX CTAs with so much shared memory.
+template <typename TL, int THREADS> bool holds_wide(size_t smem)
+{
+    const auto kern = k_sample<TL, THREADS>;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    cluster_config(cfg, attr, CL_MAX, 1, THREADS, smem, nullptr);
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        smem_limit<TL, THREADS>().raise(kern, smem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    return n > 0;
+}
+
+// Whether it takes them with the largest slices that they may have (asked once per device).
 template <typename TL> bool wide_clusters()
 {
     static std::atomic<int> known[64];
@@ -1060,12 +1096,7 @@ template <typename TL> bool wide_clusters()
     }
     int w = known[dev].load(std::memory_order_acquire);
     if (w == 0) {
-        w = cudaFuncSetAttribute(k_sample<TL, 256>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                    cudaFuncSetAttribute(k_sample<TL, 512>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess
-                ? 1
-                : -1;
-        if (w < 0)
-            (void)cudaGetLastError();
+        w = holds_wide<TL, 256>(QUARTER - sizeof(Shared<256>)) && holds_wide<TL, 512>(slice_of<TL>(V_MAX, CL_MAX, 16) * sizeof(TL)) ? 1 : -1;
         known[dev].store(w, std::memory_order_release);
     }
     return w > 0;
@@ -1073,8 +1104,6 @@ template <typename TL> bool wide_clusters()
 
 template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t stream)
 {
-    constexpr int VEC = 16 / sizeof(TL);
-    auto slice_of = [&](int n, int unit) { return (int)(((int64_t)a.V + VEC - 1 + n - 1) / n + unit - 1) / unit * unit; };
     // Few rows: as many CTAs to a row as there are SMs for, 1024 logits to a CTA at
     // least.  More: as many as fill every SM four times, or keep a slice small enough
     // for that; but clusters of more than eight CTAs find less room (at most 21
@@ -1086,11 +1115,10 @@ template <typename TL> luce_status run_sample(SampleArgs a, int R, cudaStream_t 
         cl *= 2;
     if (cl == CL_PORTABLE && R * CL_MAX <= sms && a.V > 1024 * cl && wide_clusters<TL>())
         cl = CL_MAX;
-    constexpr size_t QUARTER = 56 * 1024; // of an SM's shared memory
-    while (cl < CL_PORTABLE && slice_of(cl, VEC * 8) * sizeof(TL) > QUARTER - sizeof(Shared<256>))
+    while (cl < CL_PORTABLE && slice_of<TL>(a.V, cl, 8) * sizeof(TL) > QUARTER - sizeof(Shared<256>))
         cl *= 2;
-    const bool narrow = slice_of(cl, VEC * 8) * sizeof(TL) <= QUARTER - sizeof(Shared<256>);
-    a.slice = slice_of(cl, VEC * (narrow ? 8 : 16)); // whole vectors of every warp
+    const bool narrow = slice_of<TL>(a.V, cl, 8) * sizeof(TL) <= QUARTER - sizeof(Shared<256>);
+    a.slice = slice_of<TL>(a.V, cl, narrow ? 8 : 16);
     return narrow ? launch_sample<TL, 256>(a, R, cl, stream) : launch_sample<TL, 512>(a, R, cl, stream);
 }
 
