@@ -469,7 +469,7 @@ bool stream_serves(const W4Args &a, int gpc)
     const int64_t chunks = (a.K + CHUNK - 1) / CHUNK, cols = (int64_t)a.T * a.parts;
     if (cols > S_COLS || s_smem(a, (int)cols, gpc, cols > 8 ? 16 : S_WARPS) > S_SMEM)
         return false;
-    const int64_t stages = (int64_t)a.N * chunks / (128 * 152), work = a.T * chunks;
+    const int64_t stages = (int64_t)a.N * chunks / (128 * luce_host::sm_count()), work = a.T * chunks;
     return work <= (a.x_dtype == LUCE_F32 ? 170 + 9 * stages : a.x_dtype == LUCE_I8 ? 290 + 12 * stages : a.whole ? 140 + 4 * stages : std::min<int64_t>(166 + 2 * stages, 260));
 }
 
