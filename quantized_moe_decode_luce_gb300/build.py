@@ -38,6 +38,25 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+# Sources whose warpgroups trade registers: a kernel there is launched with as many a thread as the first pattern finds in
+# the source for the template argument that stands first in its name (the last two of the four modes take the second).
+TRADING = {"linear_w4_tc.cu": (r"LAUNCH = RAW \? (\d+) : (\d+)", r"k_linear_w4_tcILi(\d)E")}
+
+
+def check_registers(src: str, text: str, log: str) -> None:
+    """Raises where the compiler gave a kernel of `src` fewer registers a thread (`log` is what -Xptxas -v printed) than
+    its warpgroups share out (`text` is the source): the library would refuse to launch it."""
+    share, entry = TRADING[src]
+    needs = [int(n) for n in re.search(share, text).groups()]
+    seen = re.findall(r"Compiling entry function '([^']*)'.*?Used (\d+) registers", log, re.S)
+    modes = [(name, re.search(entry, name), int(regs)) for name, regs in seen]
+    if not any(m for _, m, _ in modes):
+        raise RuntimeError(f"{src}: the compiler told no kernel's registers")
+    for name, m, regs in modes:
+        if m and regs < needs[int(m.group(1)) // 2]:
+            raise RuntimeError(f"{src}: {name} has {regs} registers a thread, its warpgroups share {needs[int(m.group(1)) // 2]}")
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -78,7 +97,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
         objs.append(o)
         if force or _stale(o, [s] + headers + [__file__]):
-            jobs.append([nvcc(), *ARCH, *NVCC_FLAGS, "-c", s, "-o", o])
+            jobs.append((src, s, o))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -87,6 +106,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             sys.stderr.write(r.stderr)
         return r
+
+    def compile_one(job):
+        src, s, o = job
+        if src not in TRADING:
+            return run([nvcc(), *ARCH, *NVCC_FLAGS, "-c", s, "-o", o])
+        tmp = o + f".tmp{os.getpid()}.o"
+        r = run([nvcc(), *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", "-c", s, "-o", tmp])
+        with open(s) as f:
+            check_registers(src, f.read(), r.stderr + r.stdout)
+        os.replace(tmp, o)
 
     def build_call():
         # (no torch, no headers, no compiler: the library does without the module)
@@ -106,7 +135,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         call = ex.submit(build_call)
-        list(ex.map(run, jobs))
+        list(ex.map(compile_one, jobs))
         call.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
