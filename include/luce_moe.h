@@ -509,12 +509,20 @@ LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, i
  * per group of 32, 64 or 128 values of a row (an output channel):
  *   w[n][k] = scale[n][k / group] * (q[n][k] - z[n][k / group])
  *   out[t][n] = (sum_k x[t][k] * w[n][k]) (* x_scale[t]) (+ bias[n])
- * z is 8 where there are no zero points.  The products of a group are added in
- * fp32 (exact for int8 activations) and multiplied by the group's scale, the
- * groups' products are added in fp32, the factor and the bias are rounded to
- * fp32 each, then the sum to out_dtype.  fp32 activations (and fp16 and bf16
- * ones in small batches, or fp16 for fp32 outputs) enter in fixed point, less at
- * most 2^-23 of the largest among 128 neighbours of their row.
+ * z is 8 where there are no zero points.  The products of a group are added,
+ * their sum is multiplied by the group's scale, the groups' products are added in
+ * fp32, the factor and the bias are rounded to fp32 each, then the sum to
+ * out_dtype.  A group's sum is
+ *   exact for int8 activations;
+ *   exact for fp32 ones, for fp16 ones with fp32 outputs, and for other fp16 and
+ *     bf16 ones in small batches, but these enter in fixed point, less at most
+ *     2^-23 of the largest among 128 neighbours of their row (one that is a
+ *     thousand times the others costs them ten of their 24 bits, whatever its code);
+ *   the tensor cores' for fp16 and bf16 ones in larger batches (bf16 with fp32
+ *     outputs among them): up to eight steps in fp32, each of which may cut off
+ *     2^-22 of the sizes added so far.  The sizes alone decide which it is.
+ * Among fp32's smallest numbers an activation in fixed point is off by up to
+ * 2^-135, and for scales up to 1 a result by up to 2^-127 for each of its groups.
  * The order of the sums depends on the sizes, the types and the scales'
  * alignment alone: a call gives the same bits whenever it is made.  A token with
  * a NaN or an infinity among its activations has NaN or infinite outputs only;
@@ -538,13 +546,13 @@ LUCE_API luce_status luce_logits_process(const void *logits, luce_dtype dtype, i
  * scale NaN.
  *
  *   x [T][K] fp32, bf16, fp16 (x_scale NULL), or int8 with x_scale [T] fp32;
- *     rows ld_x elements apart (ld_x >= K), every row 16-byte aligned
+ *     rows ld_x elements apart (K <= ld_x <= 2^33), every row 16-byte aligned
  *   wq [N][ceil(K / 128)][64] bytes, 16-byte aligned
  *   scale [N][ceil(K / group)] fp16 or bf16
  *   zeros [N][ceil(K / group)] bytes 0..15 (of others the low four bits), or NULL
  *   bias [N] fp32 or NULL
- *   out [T][N] of out_dtype, its rows ld_out elements apart (ld_out >= N; what
- *     lies between the rows is left as it was), aligned to the element
+ *   out [T][N] of out_dtype, its rows ld_out elements apart (N <= ld_out <= 2^33;
+ *     what lies between the rows is left as it was), aligned to the element
  *   w [N][K] fp32, bf16 or fp16, aligned to the element    codes [N][K] bytes
  * Requires K % 16 == 0, 16 <= K <= 65536, group 32, 64 or 128, N >= 1 (N >= 0
  * where a matrix is made), T >= 0, N and T below 2^24 (it may be
@@ -569,7 +577,8 @@ LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t l
  *   top_p:  of those, a token stays if the weights before it add up to less than
  *           top_p[r] times the weights of all of them (the first one always;
  *           all if top_p[r] >= 1 or NaN)
- *   min_p:  of those, a token stays if w_v >= min_p[r] (the first one always)
+ *   min_p:  of those, a token stays if w_v >= min_p[r] (the first one always;
+ *           all if min_p[r] <= 0 or NaN)
  *   Z = the weights that stay;  idx[r] = the first token, in the order of ids,
  *   at which the weights that stay, up to and including it, exceed u[r] * Z;
  *   prob[r] = its weight / Z
@@ -580,12 +589,12 @@ LUCE_API luce_status luce_linear_w4(const void *x, luce_dtype x_dtype, int64_t l
  * has idx 0 and prob 0; a row with a NaN or +infinity has idx 0 and prob NaN.
  * u[r] is taken as within [0, 1): NaN as 0, 1 and more as the last token.
  * Weights are whole multiples of 2^-L of the row's largest (L = 63 -
- * ceil(log2 V), at least 44), each within 2^-29 of its value relative to it or
- * one such unit: their sums have no order, and the result is the same bits
- * whenever the call is made.
+ * ceil(log2 V), at least 44 and at most 62), each within 2^-29 of its value
+ * relative to it and then rounded down: their sums have no order, and the result
+ * is the same bits whenever the call is made.
  *
- *   logits [R][V] of `dtype`, rows ld_logits elements apart (ld_logits >= V),
- *     aligned to the element
+ *   logits [R][V] of `dtype`, rows ld_logits elements apart (V <= ld_logits <=
+ *     2^33), aligned to the element
  *   u [R] fp32    temperature, top_p, min_p [R] fp32, top_k [R] int32, each
  *     NULL for none (temperature 1)
  *   idx [R] int32 out    prob [R] fp32 out, or NULL; neither may overlap an

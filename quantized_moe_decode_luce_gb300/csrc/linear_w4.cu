@@ -10,8 +10,8 @@
 // multiplies the chunk's sums again in fp32:
 //   whole numbers   int8 codes as they are; others as two columns of twelve bits
 //     each, the second 2^-12 of the first.  What they leave is at most 2^-23 of
-//     the chunk's largest value, and a group's sums (below 2^24) are exact: the
-//     tensor cores cut off what they add.
+//     the chunk's largest value (2^-135 where all are below 2^-112), and a group's
+//     sums (below 2^24) are exact: the tensor cores cut off what they add.
 //   fp16 numbers    bf16 and fp16 values for 16-bit outputs, where two columns a
 //     token would not fit one MMA: exact, but for values so far below the
 //     chunk's largest that they end in fp16's subnormal steps (off by at most
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(S_MOST<NT, GPC, ZEROS, U> * 32)
         lc = ls < steps ? (kw + lj * wk) * U : chunks;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int64_t row = min(ls * rows_step + group * ROWS + r8 + 8 * h, a.N - 1); // (below 2^24 + 2^12)
+            const int64_t row = min(ls * rows_step + group * ROWS + r8 + 8 * h, a.N - 1); // (below 2^24 + 2^16)
             lw[h] = a.wq + row * row_bytes + lc * CHUNK_BYTES + 16 * quad;
             lg[h] = row * a.G + lc * GPC;
         }

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(THREADS)
     const float d = scale_value(s, bf);
     const bool flat = odd || d == 0.0f;
     if (odd)
-        s = bf ? 0x7fffu : 0x7fffu; // NaN in either type
+        s = 0x7fffu; // NaN in either type
     const float z = !zeros ? 8.0f : flat ? 0.0f : fminf(roundf(__fdiv_rn(-lo, d)), 15.0f);
     // round(fl(v / d)) is the whole number nearest v rinv wherever that is not within 1e-4 of half way between
     // two (up to 64 rinv = fl(1 / d) moves it by less than 2e-5): the sum with

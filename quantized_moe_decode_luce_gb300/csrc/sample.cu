@@ -13,8 +13,8 @@
 // Both filters look for the token at which those before it, by falling logits,
 // reach a count (top-k) or a weight (top-p).  A histogram over the logits'
 // distance from the largest finds the bin that holds it: nine bits of the
-// distance at a time, the CTAs' histograms added through distributed shared
-// memory by every CTA for itself.  Few logits enter it.  For top-k the warps'
+// distance at a time (ten in CTAs of 512 threads), the CTAs' histograms added
+// through distributed shared memory by every CTA for itself.  Few logits enter it.  For top-k the warps'
 // largest lanes bound the k-th from below: with W warps in the cluster, k tokens
 // are at or above the least of the warps' ceil(k / W)-th largest lane maxima.
 // For top-p only those within 2^-24 of the largest weight are binned; if they do
@@ -152,7 +152,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 minus_infinity<__nv_bfloat1
 // z = (M - l) c, c = log2(e) / temperature, in whole numbers.  z is split into a
 // multiple n of 2^-8 and a rest r.  Where c M is below 2^14, n is c M - c l
 // rounded, and r = (A1 - n) - l c + A2, with c M = A1 + A2 and A1 a multiple of
-// 2^-8: A1 - n is exact, and the difference with l c, below 2^-7, is rounded
+// 2^-7: A1 - n is exact, and the difference with l c, below 2^-7, is rounded
 // once.  Beyond (small temperatures) M - l is kept in two floats (as quarters, so
 // that it cannot overflow).
 struct Weigh {

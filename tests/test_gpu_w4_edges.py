@@ -1,5 +1,5 @@
 """GPU: draws and 4-bit products at the ends of their ranges: top-p just below 1 over long flat tails, small
-temperatures, activations and scales near fp32's smallest numbers."""
+temperatures, activations and scales near fp32's smallest numbers, sums of bf16 activations for fp32 outputs."""
 import math
 from fractions import Fraction
 
@@ -141,3 +141,25 @@ def test_small_activations_and_scales(T, x_dtype, x_size, s_size, zero_points):
     # eight groups and 24 further operations; sums of groups are kept 2^-14 of their size, good to 2^-150 2^14 each
     tol = 1.001 * 2.0 ** -8 * y.abs() + (2.0 ** -19 + 32 * 2.0 ** -24) * terms + 8 * 2.0 ** -136
     assert terms.max() < 2.0 ** -90 and torch.all((out.cpu().double() - y).abs() <= tol)
+
+
+# Sums of bf16 activations for fp32 outputs: without the fixed point of others, so that nothing is left of an activation
+# itself. Eight steps of the tensor cores may each cut off 2^-22 of the sizes added so far, 2^-19 of a group's terms; a
+# rounding of 2^-24 for each of G groups and for 24 further additions, factors and conversions; the output's, 2^-24.
+@pytest.mark.parametrize("zero_points", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,N,K", [(20, 300, 128), (70, 200, 2064), (300, 1000, 4096)])
+def test_sums_of_bf16_for_fp32_outputs(T, N, K, group, zero_points):
+    # activations over forty octaves, and some that outweigh their chunk a thousandfold
+    x = torch.randn((T, K), generator=gen(T)) * 2.0 ** torch.randint(-20, 21, (T, K), generator=gen(T + 1))
+    x = torch.where(torch.rand((T, K), generator=gen(T + 2)) < 0.6, torch.randn((T, K), generator=gen(T + 3)), x).to(bf16)
+    G = -(-K // group)
+    q = torch.randint(0, 16, (N, K), generator=gen(1), dtype=torch.uint8)
+    s = (torch.rand((N, G), generator=gen(2)) + 0.5).to(f16)
+    z = torch.randint(0, 16, (N, G), generator=gen(3), dtype=torch.uint8) if zero_points else None
+    out = torch.empty((T, N), device="cuda")
+    B.luce_linear_w4(x.cuda(), None, O.pack(q).cuda(), s.cuda(), None if z is None else z.cuda(), group, None, out)
+    torch.cuda.synchronize()
+    y, terms, _ = O.linear(x.cuda(), None, q.cuda(), s.cuda(), None if z is None else z.cuda(), group)
+    tol = 1.001 * 2.0 ** -24 * y.abs() + (2.0 ** -19 + (G + 24) * 2.0 ** -24) * terms
+    assert torch.all((out.double() - y).abs() <= tol)
